@@ -23,7 +23,8 @@ __all__ = [
     "HS_DEVERR_STATE", "HostBuffer", "PoolBuffers", "hs_probe_link", "hs_gather", "hs_gather_history",
     "hs_resolve_shared", "hs_resolve_tiered", "hs_mla_decode", "hs_mla_decode_history", "HS_DEVERR_TIMEOUT",
     "MLA_HEADS", "MLA_D_QK", "MLA_D_V", "hs_probe_launch", "hs_debug_attention", "hs_step_begin_fused", "hs_probe_link_static", "HS_ERR_TOO_LARGE",
-    "hs_resolve_ids", "hs_prefetch_ids",
+    "hs_resolve_ids", "hs_prefetch_ids", "hs_append", "hs_append_desc", "append_desc", "hs_paged_rows", "paged_rows",
+    "hs_mla_prefix", "hs_mla_prefix_workspace", "HS_TYPE_BF16", "HS_TYPE_F16", "HS_TYPE_F32",
 ]
 
 HS_OK = 0
@@ -37,6 +38,7 @@ HS_DEVERR_RANGE = 1
 HS_DEVERR_DUP = 2
 HS_DEVERR_STATE = 4
 HS_DEVERR_TIMEOUT = 8
+HS_TYPE_BF16, HS_TYPE_F16, HS_TYPE_F32 = 0, 1, 2
 MLA_HEADS, MLA_D_QK, MLA_D_V = 128, 576, 512  # shape of the sparse MLA decode consumer
 
 LIB_PATH = _build_mod.LIB_PATH
@@ -62,6 +64,22 @@ class hs_pool_desc(ctypes.Structure):
 class hs_meta_layout(ctypes.Structure):
     _fields_ = [(n, ctypes.c_size_t) for n in
                 ("step", "error", "counters", "tok2slot", "slot_tok", "slot_stamp", "total")]
+
+
+class hs_paged_rows(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_void_p), ("count", ctypes.c_int64), ("pages", ctypes.c_void_p),
+                ("page_stride", ctypes.c_int64), ("page_rows", ctypes.c_int32)]
+
+
+class hs_append_desc(ctypes.Structure):
+    _fields_ = [
+        ("type", ctypes.c_int32), ("interleaved", ctypes.c_int32), ("kv", ctypes.c_void_p),
+        ("kv_stride", ctypes.c_int64), ("norm_weight", ctypes.c_void_p), ("inv_freq", ctypes.c_void_p),
+        ("req_ids", ctypes.c_void_p), ("positions", ctypes.c_void_p), ("q_rope", ctypes.c_void_p),
+        ("q_rope_token_stride", ctypes.c_int64), ("q_rope_head_stride", ctypes.c_int64), ("q", ctypes.c_void_p),
+        ("q_token_stride", ctypes.c_int64), ("q_head_stride", ctypes.c_int64), ("q_heads", ctypes.c_int32),
+        ("norm_eps", ctypes.c_float),
+    ]
 
 
 def load():
@@ -102,6 +120,10 @@ def load():
             "hs_probe_launch": (ctypes.c_int, [vp, i32, i32, i32, i32, vp]),
             "hs_probe_link_static": (ctypes.c_int, [vp, sz, i32, vp, P(ctypes.c_double), P(ctypes.c_double)]),
             "hs_debug_attention": (ctypes.c_int, [ctypes.c_uint32, i32, P(i32)]),
+            "hs_append": (ctypes.c_int, [vp, i32, i32, P(hs_append_desc), P(hs_paged_rows), i32, vp]),
+            "hs_mla_prefix": (ctypes.c_int, [vp, i32, vp, P(hs_paged_rows), i32, vp, ctypes.c_float, vp, vp, vp, i32, vp,
+                                             vp, sz, vp]),
+            "hs_mla_prefix_workspace": (sz, [vp, i32, i32]),
         }
         for name, (res, args) in sig.items():
             fn = getattr(lib, name)
@@ -245,6 +267,67 @@ def hs_mla_decode_history(pool: int, layer: int, batch: int, q, topk_idx, k: int
 def hs_gather_history(pool: int, layer: int, batch: int, topk_idx, k: int, dst, stream=None) -> None:
     _check(load().hs_gather_history(pool, layer, batch, _addr(topk_idx), k, _addr(dst), _stream(stream)),
            "hs_gather_history")
+
+
+def paged_rows(rows, pages, page_rows: int) -> hs_paged_rows:
+    """The struct of an ordinary paged pool: `rows` a tensor [count][...] of contiguous rows, `pages` int32 [lists][entries]
+    (or [entries], one list). It keeps both tensors alive; build it once and pass it to every call."""
+    if not rows.is_contiguous() or not pages.is_contiguous():
+        raise ValueError("paged_rows takes contiguous tensors")
+    p = hs_paged_rows(rows.data_ptr(), rows.shape[0], pages.data_ptr(), pages.shape[-1], page_rows)
+    p._keep = (rows, pages)
+    return p
+
+
+def append_desc(kv, inv_freq, positions, req_ids=None, norm_weight=None, norm_eps: float = 0.0,
+                interleaved: bool = True, q_rope=None, q=None) -> hs_append_desc:
+    """The struct of one append, from torch tensors: kv [n][576], inv_freq fp32 [32], positions and req_ids int32 [n],
+    norm_weight fp32 [512], q_rope [n][heads][64] of kv's type, q bf16 [n][heads][576]; the last dimension of each is
+    contiguous. It keeps the tensors alive; build it once and refill them between calls."""
+    import torch
+
+    types = {torch.bfloat16: HS_TYPE_BF16, torch.float16: HS_TYPE_F16, torch.float32: HS_TYPE_F32}
+    if kv.dtype not in types or (q_rope is not None and q_rope.dtype != kv.dtype):
+        raise ValueError("kv and q_rope are bf16, fp16 or fp32, both the same")
+    for t, want in ((inv_freq, torch.float32), (positions, torch.int32), (req_ids, torch.int32),
+                    (norm_weight, torch.float32), (q, torch.bfloat16)):
+        if t is not None and t.dtype != want:
+            raise ValueError(f"append_desc takes {want} there, not {t.dtype}")
+    if any(t is not None and t.stride(-1) != 1 for t in (kv, inv_freq, positions, req_ids, norm_weight, q_rope, q)):
+        raise ValueError("the last dimension of every tensor is contiguous")
+    if (q_rope is None) != (q is None):
+        raise ValueError("q_rope and q go together")
+    n, width, rope = positions.shape[0], MLA_D_QK, MLA_D_QK - MLA_D_V
+    heads = 0 if q is None else q.shape[1]
+    for name, t, shape in (("kv", kv, (n, width)), ("inv_freq", inv_freq, (rope // 2,)), ("req_ids", req_ids, (n,)),
+                           ("norm_weight", norm_weight, (MLA_D_V,)), ("q_rope", q_rope, (n, heads, rope)),
+                           ("q", q, (n, heads, width))):
+        if t is not None and tuple(t.shape) != shape:
+            raise ValueError(f"{name} is {tuple(t.shape)}, not {shape}")
+    d = hs_append_desc(types[kv.dtype], int(interleaved), kv.data_ptr(), kv.stride(0), _addr(norm_weight),
+                       inv_freq.data_ptr(), _addr(req_ids), positions.data_ptr(), _addr(q_rope), 0, 0, _addr(q), 0, 0, 0,
+                       norm_eps)
+    if q is not None:
+        d.q_rope_token_stride, d.q_rope_head_stride, d.q_heads = q_rope.stride(0), q_rope.stride(1), q_rope.shape[1]
+        d.q_token_stride, d.q_head_stride = q.stride(0), q.stride(1)
+    d._keep = (kv, inv_freq, positions, req_ids, norm_weight, q_rope, q)
+    return d
+
+
+def hs_append(pool: int, layer: int, ntok: int, desc: hs_append_desc, paged: hs_paged_rows | None = None,
+              to_history: bool = True, stream=None) -> None:
+    _check(load().hs_append(pool, layer, ntok, desc, paged, int(to_history), _stream(stream)), "hs_append")
+
+
+def hs_mla_prefix(pool: int, batch: int, q, prefix: hs_paged_rows, max_length: int, prefix_length, sm_scale: float,
+                  own_out, own_lse, out, out_type: int, lse, workspace, stream=None) -> None:
+    _check(load().hs_mla_prefix(pool, batch, _addr(q), prefix, max_length, _addr(prefix_length), sm_scale,
+                                _addr(own_out), _addr(own_lse), _addr(out), out_type, _addr(lse), _addr(workspace),
+                                0 if workspace is None else workspace.nbytes, _stream(stream)), "hs_mla_prefix")
+
+
+def hs_mla_prefix_workspace(pool: int, batch: int, max_length: int) -> int:
+    return int(load().hs_mla_prefix_workspace(pool, batch, max_length))
 
 
 def hs_get_error(pool: int, clear: bool = False) -> int:

@@ -12,7 +12,7 @@ import subprocess
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
-SOURCES = [os.path.join(HERE, "csrc", "hs_resolve.cu"), os.path.join(HERE, "csrc", "hs_attention.cu")]
+SOURCES = [os.path.join(HERE, "csrc", n) for n in ("hs_resolve.cu", "hs_attention.cu", "hs_append.cu", "hs_prefix.cu")]
 HEADERS = [os.path.join(ROOT, "include", "hs.h"), os.path.join(HERE, "csrc", "hs_block.cuh"),
            os.path.join(HERE, "csrc", "hs_pool.hpp")]
 BUILD_DIR = os.path.join(HERE, "_build")

@@ -29,5 +29,7 @@ struct hs_pool {
   int max_active[HS_MAX_CLUSTER + 1];  // clusters of each size resident at once
 };
 
+bool hs_paged_ok(const hs_paged_rows* p);  // whether a block table's sizes and alignments are usable
+bool hs_on_device(const hs_pool* p);      // whether the pool's device is the current one
 
 #endif  // HS_POOL_HPP_

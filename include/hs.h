@@ -271,6 +271,120 @@ int hs_mla_decode(hs_pool *pool, int32_t layer, int32_t batch, const void *q, co
 int hs_mla_decode_history(hs_pool *pool, int32_t layer, int32_t batch, const void *q, const int32_t *topk_idx,
                           int32_t k, float sm_scale, float *out, float *lse, hs_stream_t stream);
 
+/* Value types of the operators below. */
+#define HS_TYPE_BF16 0
+#define HS_TYPE_F16 1
+#define HS_TYPE_F32 2
+
+/*
+ * Rows of the ordinary paged HBM pool (the tier that hs_resolve_tiered serves in place), as a block table sees them.
+ *   rows: device memory of `count` rows of the pool's row_bytes, 16-byte aligned; count <= 2^31 - 64 (their
+ *     bytes may pass 32 bits).
+ *   pages: int32 page numbers (device or mapped host memory): token t of list l is row
+ *     pages[l * page_stride + t / page_rows] * page_rows + t % page_rows. A negative entry means that the pool does not
+ *     hold that page's tokens; so does one whose page does not lie wholly within `count`.
+ *   page_stride: entries of one list (>= 1): a token at or past page_stride * page_rows has no row.
+ *   page_rows: rows of a page, a power of two from 1 (a list of single rows, such as resident_row) to 65536.
+ */
+typedef struct {
+  void *rows;
+  int64_t count;
+  const int32_t *pages;
+  int64_t page_stride;
+  int32_t page_rows;
+} hs_paged_rows;
+
+/*
+ * What one append takes. Token i (0 <= i < ntok) belongs to request req_ids[i] (i itself when req_ids is NULL) at
+ * position positions[i]. Arrays are device memory; req_ids and positions may be mapped host memory.
+ *   type: HS_TYPE_* of kv and q_rope.
+ *   interleaved: which values form the 32 pairs that turn: 0: (j, j + 32); 1: (2j, 2j + 1).
+ *   kv: [ntok][576], the latent's 512 values and the rotary key's 64 before rotation; kv_stride: elements between
+ *     tokens, >= 576. kv 16-byte aligned, kv_stride * sizeof(type) a multiple of 16.
+ *   norm_weight: fp32 [512], 16-byte aligned, or NULL for no norm; norm_eps: >= 0. With it the latent becomes
+ *     z * norm_weight / sqrt(mean(z^2) + norm_eps).
+ *   inv_freq: fp32 [32], finite: pair j turns by positions[i] * inv_freq[j]. The product is taken modulo a full turn in
+ *     64-bit fixed point, so far positions lose nothing to a 32-bit angle.
+ *   q_rope: the queries' 64 rotary values, [ntok][q_heads][64], or NULL (then q_heads is 0). Strides in elements between
+ *     tokens and heads (>= 64), in bytes multiples of 16; 16-byte aligned.
+ *   q: bf16, receives the turned values at q[i*q_token_stride + h*q_head_stride + 512 .. 575] (the layout that
+ *     hs_mla_decode and hs_mla_prefix read, when the strides are q_heads * 576 and 576); same rules. q_rope may be
+ *     exactly the bf16 values at that place (turned in place), else the two must not overlap.
+ */
+typedef struct {
+  int32_t type;
+  int32_t interleaved;
+  const void *kv;
+  int64_t kv_stride;
+  const float *norm_weight;
+  const float *inv_freq;
+  const int32_t *req_ids;
+  const int32_t *positions;
+  const void *q_rope;
+  int64_t q_rope_token_stride;
+  int64_t q_rope_head_stride;
+  void *q;
+  int64_t q_token_stride;
+  int64_t q_head_stride;
+  int32_t q_heads;
+  float norm_eps;
+} hs_append_desc;
+
+/*
+ * Append (or rewrite) the KV rows of ntok tokens of `layer`, with the norm of the latent and the rotation of the key on
+ * the way, and turn the same tokens' queries. The row format goes by the pool's row_bytes:
+ *   1152: 576 bf16 (latent, rotary key);
+ *   656: 512 e4m3 latents, 4 fp32 scales, one for each 128 latents (their largest magnitude / 448, at
+ *     least 2^-126; 1 where all are 0),
+ *     64 bf16 of the rotary key; a latent is its e4m3 value times its scale.
+ *   Any other row_bytes: HS_ERR_UNSUPPORTED.
+ * Every tier that holds the token gets the row: the pool's row source when `to_history` is non-zero (the host pool,
+ * which must be writable, or the no-IO copy of a pool that has one), the paged rows when `paged` is given (list
+ * req_ids[i]), and always the hot slot that the token occupies, if it occupies one, so that a resolve after a rewrite
+ * (a rolled-back speculation, say) never serves the old row. Norm and rotation are computed in 32 bits; each value is
+ * rounded once.
+ * A token with a negative position is padding: it touches nothing. One whose position is >= ctx or whose request is not
+ * in 0 .. max_batch-1 is skipped whole, and the error word gets HS_DEVERR_RANGE. (request, position) pairs are distinct
+ * within a call (not checked: rows of a repeated pair may mix). ntok == 0 is a no-op; with req_ids NULL ntok <=
+ * max_batch. At least one of `paged`, to_history and q_rope is given. Enqueued on `stream` (of the pool's device, which
+ * must be the current one: HS_ERR_INVALID_ARG); capturable. Order it before the resolve, prefetch, gather or attention
+ * that reads the rows. Basis: the full history in host memory that the paper's cache sits on (Abstract) and the ordinary
+ * KV blocks of the "Hybrid HiSparse" card (Timeline) have to be written by somebody; the pages name no writer.
+ */
+int hs_append(hs_pool *pool, int32_t layer, int32_t ntok, const hs_append_desc *desc, const hs_paged_rows *paged,
+              int32_t to_history, hs_stream_t stream);
+
+/*
+ * Attention of a whole batch over one prefix that all of its requests share (a system prompt, a document), read from the
+ * ordinary paged HBM rows and computed once for all: the dense counterpart of hs_mla_decode, same rows (1152 bytes, else
+ * HS_ERR_UNSUPPORTED) and heads. With T the tokens t < length whose page the pool holds, for b < batch and h < 128:
+ *     s[t] = sm_scale * dot(q[b][h][0:576], row_t),  out[b][h][0:512] = sum_T softmax(s)[t] * row_t[0:512],
+ *     lse[b][h] = ln sum_T exp(s[t]).
+ * Rows outside T are never looked at, whatever they hold. With no token in T an output is zero and its lse -inf.
+ *   q: device bf16 [batch][128][576], 16-byte aligned. batch >= 0 is not bound by max_batch: several query tokens of one
+ *     request are several rows of the batch.
+ *   prefix: the paged rows; its list 0 is the prefix (page_stride entries of it at most are read).
+ *   max_length: tokens, >= 0, <= page_stride * page_rows. prefix_length: NULL, or device int32 [1], the length to use
+ *     (clamped to 0 .. max_length), read when the kernel runs: a captured graph can be replayed over a prefix that grew.
+ *   own_out, own_lse: NULL, or the same requests' attention over rows of their own, as hs_mla_decode wrote it (fp32
+ *     [batch][128][512], 16-byte aligned, and [batch][128]): out and lse are then those of both sets of rows together.
+ *   out: [batch][128][512] of out_type (HS_TYPE_BF16 or HS_TYPE_F32), 16-byte aligned; lse: fp32 [batch][128]. They
+ *     overlap no input, but with out_type HS_TYPE_F32 they may be own_out and own_lse themselves.
+ *   workspace: device memory of hs_mla_prefix_workspace bytes, 256-byte aligned (NULL where that is 0); its contents are
+ *     scratch. Calls that may run at the same time (two streams, two graphs) need workspaces of their own.
+ * The weights are rounded to bf16 before the value product; scores, sums and outputs accumulate in 32 bits, and lse sums
+ * the unrounded weights. Results are deterministic for given batch, max_length and device. Enqueued on `stream` (of the
+ * pool's device, which must be the current one); capturable; batch == 0 is a no-op. Basis: the "Hybrid HiSparse" card
+ * (Timeline) serves resident rows from the ordinary KV blocks; requests that share blocks are its plainest case.
+ */
+int hs_mla_prefix(hs_pool *pool, int32_t batch, const void *q, const hs_paged_rows *prefix, int32_t max_length,
+                  const int32_t *prefix_length, float sm_scale, const float *own_out, const float *own_lse, void *out,
+                  int32_t out_type, float *lse, void *workspace, size_t workspace_bytes, hs_stream_t stream);
+
+/* Bytes of workspace that hs_mla_prefix needs for a batch and max_length on the pool's device (0: none, or bad
+ * arguments). */
+size_t hs_mla_prefix_workspace(hs_pool *pool, int32_t batch, int32_t max_length);
+
 /*
  * Test hook of the attention consumer (not for production use; process-wide settings, not thread-safe). It lets a
  * test exercise failure detection without faulting the GPU: every wait inside the kernel is bounded, and on running
