@@ -31,5 +31,7 @@ struct hs_pool {
 
 bool hs_paged_ok(const hs_paged_rows* p);  // whether a block table's sizes and alignments are usable
 bool hs_on_device(const hs_pool* p);      // whether the pool's device is the current one
+// The settings of hs_debug_attention: polling rounds of the attention kernels' waits, and the stall hook.
+void hs_attention_waits(uint32_t* limit, int32_t* stall);
 
 #endif  // HS_POOL_HPP_

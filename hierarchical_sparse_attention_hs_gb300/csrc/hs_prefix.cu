@@ -1,36 +1,91 @@
-// Attention of a batch over a prefix that all of its requests share, sm_103a.
+// Attention of a batch over a prefix that all of its requests share, sm_103a (tcgen05 tensor cores, TMA, TMEM).
 //
 // For request b and head h, over the tokens t < length whose page the pool holds:
 //     s[t] = sm_scale * q[b][h] . row_t,   out = sum softmax(s)[t] row_t[0:512],   lse = ln sum e^s[t],
-// joined with what the request's own rows gave. The tokens are cut into splits; a split leaves its unnormalised output O,
-// its running maximum m (in log2 units) and its normaliser l, and a second kernel joins them:
+// joined with what the request's own rows gave. The tokens are cut into splits where there are fewer requests than the
+// device takes at once; a split leaves its unnormalised output O, its running maximum m (in log2 units) and its
+// normaliser l, and a second kernel joins them:
 //     M = max m_s,   total = sum 2^(m_s - M) l_s,   out = sum 2^(m_s - M) O_s / total,   lse = ln 2 (M + log2 total),
 // where the own rows count as one more split with m = own_lse / ln 2, l = 1, O = own_out.
+//
+// What bounds it. A row is 1152 bytes and serves 2 * 128 * (576 + 512) operations for each request, 242 per byte: with
+// one request the tensor cores and HBM are in balance, with more the tensor cores decide, as long as the rows come from
+// L2. Requests of one split run side by side and walk the same rows, so HBM is read about once for all.
+//
+// A pair of CTAs (a cluster of two) takes one request's 128 heads, 64 for each CTA, over one split, 128 keys a tile. The
+// 512 output columns of 128 heads in fp32 would fill a CTA's tensor memory; with 64 heads a CTA they take half (the pair's
+// MMAs, cta_group::2 with M = 128, put a head's even and odd column halves on lanes r and r + 64), which leaves room for
+// the scores. For S = Q K^T each CTA holds its 64 heads of Q and 64 of the tile's keys; for O += P V its 64 heads of P and
+// all 128 keys of 256 value columns. The MMA reads each CTA's operand half and shares it, so no operand is loaded twice
+// within a CTA, but the value half of a CTA's own keys lies in shared memory twice (K and V are addressed by one
+// descriptor for both CTAs, and their halves cut the rows differently).
+//
+// Warp roles per CTA: 0-3 softmax (thread t: TMEM lane t, head t % 64, keys 64 (t / 64) .. +63 of the tile), 4 the issuer
+// (the pair's first CTA issues for both), 5 loads Q and K, 6 loads V. K is one buffer of nine 64-column blocks, V one of
+// four 32-key chunks; each block or chunk is handed back as soon as the MMAs that read it have finished, so the next tile
+// streams in behind the current one. Per tile j the issuer runs S(j + 1) before O += P(j) V(j), so the softmax of a tile
+// overlaps the value product of the one before and the scores of the one after.
+//
+// Loads are TMA boxes of 64 columns x min(page_rows, 32) rows, 128-byte swizzle. A box whose page the pool does not hold,
+// or that lies behind the prefix, starts behind the last row of the tensor map: it reads nothing and fills with zeros. In
+// the one page that the prefix ends inside, single-row boxes do the same row by row. So rows outside the prefix are never
+// read, and a masked key's value row is zero, whatever memory holds; its score is masked to -inf by the softmax.
+//
+// Waits are bounded as in hs_attention.cu: on running out a role sets the abort flag, which ends every role, and the
+// HS_DEVERR_TIMEOUT bit.
 
+#include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <atomic>
 #include <cstdint>
 #include <cstring>
 
 #include "../../include/hs.h"
 #include "hs_pool.hpp"
+#include "hs_tcgen05.cuh"
 
 namespace {
 
+using namespace hs;
+
 constexpr int HEADS = 128, DQK = 576, DV = 512, ROW_BYTES = DQK * 2;
-constexpr int NK = 32;        // keys of a block
-constexpr int HG = 16;        // heads of a CTA
-constexpr int THREADS = 256;
-constexpr int SMEM = HG * DQK * 4 + NK * ROW_BYTES + HG * NK * 4;
+constexpr int NK = 128;            // keys of a tile
+constexpr int QH = HEADS / 2;      // heads of a CTA
+constexpr int KH = NK / 2;         // keys of a CTA's K half, and of a softmax thread
+constexpr int DVH = DV / 2;        // value columns of a CTA
+constexpr int BOX = 32;            // rows of the largest box
+constexpr int KBLK = DQK / 64;     // 64-column blocks of a row
+constexpr int VCHUNK = NK / BOX;   // 32-key chunks of V
+constexpr int BLK_BYTES = 64 * 128;      // 64 rows x 64 columns
+constexpr int SEG_BYTES = BOX * 128;     // 32 rows x 64 columns
+constexpr int VCHUNK_BYTES = (DVH / 64) * SEG_BYTES;
+constexpr int OFF_Q = 0;
+constexpr int OFF_K = OFF_Q + KBLK * BLK_BYTES;
+constexpr int OFF_V = OFF_K + KBLK * BLK_BYTES;
+constexpr int OFF_P = OFF_V + VCHUNK * VCHUNK_BYTES;
+constexpr int OFF_BAR = OFF_P + 2 * BLK_BYTES;
+// mbarriers: qfull kfull[9] kempty[9] vfull[4] vempty[4] sfull[2] sfree[2] pfull pdone odone stall mx[2]
+constexpr int B_QFULL = 0, B_KFULL = 1, B_KEMPTY = B_KFULL + KBLK, B_VFULL = B_KEMPTY + KBLK,
+              B_VEMPTY = B_VFULL + VCHUNK, B_SFULL = B_VEMPTY + VCHUNK, B_SFREE = B_SFULL + 2, B_PFULL = B_SFREE + 2,
+              B_PDONE = B_PFULL + 1, B_ODONE = B_PDONE + 1, B_STALL = B_ODONE + 1, B_MX = B_STALL + 1, NBAR = B_MX + 2;
+constexpr int OFF_MISC = OFF_BAR + NBAR * 8;            // tensor-memory address, abort flag
+constexpr int OFF_RED = (OFF_MISC + 8 + 15) & ~15;      // [2 parities][128 threads] floats
+constexpr int SMEM_BYTES = OFF_RED + 2 * 128 * 4;
+static_assert(SMEM_BYTES <= 232448, "shared memory per block");
+constexpr int SOFTMAX_WARPS = 4, MMA_WARP = 4, K_WARP = 5, V_WARP = 6, THREADS = 7 * 32;
+constexpr uint32_t TMEM_COLS = 512, TMEM_O = 0, TMEM_S = 256;  // O: 2 x 128 columns; S: two buffers of 64
+constexpr int TS = 36;             // row stride, in floats, of a softmax warp's output tile
+static_assert(SOFTMAX_WARPS * 32 * TS * 4 <= OFF_V - OFF_K, "output tiles fit the K buffer");
 
 struct PrefixArgs {
-  const __nv_bfloat16* q;
-  const uint8_t* rows;
   const int32_t* pages;
   int32_t page_shift, max_length;
-  int64_t page_limit;
+  int32_t page_limit;     // pages 0 .. page_limit - 1 lie within the rows
+  int32_t box_shift;      // log2 of the rows of a box
+  int32_t none;           // a row coordinate behind the last row
   const int32_t* length;  // or nullptr: max_length
   float scale_log2;
   int32_t batch, nsplit;
@@ -41,87 +96,384 @@ struct PrefixArgs {
   void* out;
   int32_t out_f32;
   float* lse;
+  int32_t* err;
+  uint32_t wait_limit;
+  int32_t stall;
 };
-
-__device__ __forceinline__ int32_t ld_fresh(const int32_t* p) {
-  int32_t v;
-  asm("ld.global.cv.s32 %0, [%1];" : "=r"(v) : "l"(p));
-  return v;
-}
 
 __device__ __forceinline__ int length_of(const PrefixArgs& a) {
   return a.length ? min(max(ld_fresh(a.length), 0), a.max_length) : a.max_length;
 }
+// Row of token `tok`, or -1.
+__device__ __forceinline__ int row_of(const PrefixArgs& a, int tok, int len) {
+  if (tok >= len) return -1;
+  const int page = a.pages[tok >> a.page_shift];
+  return page >= 0 && page < a.page_limit ? (page << a.page_shift) + (tok & ((1 << a.page_shift) - 1)) : -1;
+}
 
-// One CTA: 16 heads of one request over one split, 32 keys at a time.
-__global__ void __launch_bounds__(THREADS) hs_prefix_kernel(const PrefixArgs a) {
+// Shared-memory matrix descriptor, 128-byte swizzle. K-major: 8-row groups 1024 bytes apart (lbo unused). MN-major: `lbo`
+// between 64-element runs along M or N, 1024 bytes between 8-deep groups along K.
+__device__ __forceinline__ uint64_t sdesc128(uint32_t saddr, uint32_t lbo) {
+  return (uint64_t)((saddr >> 4) & 0x3FFFu) | ((uint64_t)((lbo >> 4) & 0x3FFFu) << 16) | ((uint64_t)(1024 >> 4) << 32) |
+         ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
+}
+__device__ __forceinline__ void mma2(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}\n" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(acc)
+      : "memory");
+}
+// arrive on the barrier at this offset in both CTAs once every MMA issued so far has finished
+__device__ __forceinline__ void commit2(uint64_t* b) {
+  asm volatile(
+      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(su32(b)),
+      "h"((uint16_t)3)
+      : "memory");
+}
+// A box at (column, row) into this CTA's shared memory; its bytes count on a barrier of the pair's first CTA.
+__device__ __forceinline__ void tma_box(uint32_t dst, const CUtensorMap* map, int col, int row, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4}], "
+      "[%2];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(col), "r"(row)
+      : "memory");
+}
+
+// The boxes of 64 columns x 32 rows (token tok0 on) at `dst`, lane u taking box u of the segment: `ncol` column blocks
+// from column block c0, `pitch` bytes apart. `row`: the lane's box's row (from seg_row).
+// A box that the prefix ends inside is loaded row by row.
+struct Seg {
+  int row;   // row of the lane's box, or -1: zeros
+  int full;  // rows of it within the prefix
+};
+__device__ __forceinline__ Seg seg_row(const PrefixArgs& a, int tok0, int len, int lane) {
+  const int rows = 1 << a.box_shift, tok = tok0 + (lane << a.box_shift);
+  Seg s;
+  s.row = (lane << a.box_shift) < BOX ? row_of(a, tok, len) : -1;
+  s.full = min(rows, len - tok);
+  return s;
+}
+__device__ __forceinline__ void load_seg(const PrefixArgs& a, const CUtensorMap* map, const CUtensorMap* map1, Seg s,
+                                         uint32_t dst, int col, uint32_t bar, int lane) {
+  const int rows = 1 << a.box_shift;
+  if ((lane << a.box_shift) >= BOX) return;
+  dst += (uint32_t)(lane << a.box_shift) * 128u;
+  if (s.row < 0 || s.full == rows) {
+    tma_box(dst, map, col, s.row < 0 ? a.none : s.row, bar);
+  } else {
+    for (int r = 0; r < rows; ++r) tma_box(dst + r * 128u, map1, col, r < s.full ? s.row + r : a.none, bar);
+  }
+}
+
+// One softmax warp's part of an output: its 32 heads' 256 columns from tensor memory times w0 (zeros without O), plus w1
+// times the own rows' output where w1 != 0. 32-column slices go through a shared tile (rows 144 bytes apart: conflict-free
+// 16-byte accesses both ways) so that global accesses are whole row segments. `base`: element offset of the warp's first
+// head, first column in out (and own_out).
+__device__ __forceinline__ void store_out(uint32_t tcol, bool have_o, float w0, float w1, float* tile, const float* own,
+                                          void* out, bool f32, size_t base, int lane) {
+  const int c4 = lane & 7;
+  const bool join = __any_sync(0xffffffffu, w1 != 0.f);
+  for (int c = 0; c < DVH; c += 32) {
+    uint32_t o[32];
+    if (have_o) {
+      tmem_ld32(tcol + c, o);
+      tmem_wait_ld();
+    } else {
+#pragma unroll
+      for (int i = 0; i < 32; ++i) o[i] = 0;
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      *reinterpret_cast<float4*>(tile + lane * TS + 4 * i) =
+          make_float4(__uint_as_float(o[4 * i]) * w0, __uint_as_float(o[4 * i + 1]) * w0,
+                      __uint_as_float(o[4 * i + 2]) * w0, __uint_as_float(o[4 * i + 3]) * w0);
+    __syncwarp();
+#pragma unroll
+    for (int r = 0; r < 8; ++r) {
+      const int h = 4 * r + (lane >> 3);
+      float4 v = *reinterpret_cast<const float4*>(tile + h * TS + 4 * c4);
+      const size_t at = base + (size_t)h * DV + c + 4 * c4;
+      if (join) {
+        const float w = __shfl_sync(0xffffffffu, w1, h);
+        if (w != 0.f) {
+          const float4 p = *reinterpret_cast<const float4*>(own + at);
+          v = make_float4(fmaf(w, p.x, v.x), fmaf(w, p.y, v.y), fmaf(w, p.z, v.z), fmaf(w, p.w, v.w));
+        }
+      }
+      if (f32) {
+        *reinterpret_cast<float4*>(static_cast<float*>(out) + at) = v;
+      } else {
+        const __nv_bfloat162 lo = __floats2bfloat162_rn(v.x, v.y), hi = __floats2bfloat162_rn(v.z, v.w);
+        *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(out) + at) =
+            make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
+      }
+    }
+    __syncwarp();
+  }
+}
+
+__global__ void __launch_bounds__(THREADS, 1)
+    hs_prefix_kernel(const PrefixArgs a, const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap map,
+                     const __grid_constant__ CUtensorMap map1) {
+  extern __shared__ __align__(1024) uint8_t smem[];
+  uint64_t* const bar = reinterpret_cast<uint64_t*>(smem + OFF_BAR);
+  volatile int* const abort_flag = reinterpret_cast<volatile int*>(smem + OFF_MISC + 4);
+  float* const red = reinterpret_cast<float*>(smem + OFF_RED);
+  const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
+  const uint32_t rank = cluster_rank();
+  const int unit = (int)(blockIdx.x >> 1), split = unit / a.batch, b = unit - split * a.batch;
+  const unsigned lim = a.wait_limit;
+
+  if (t == 0) {
+    for (int i = 0; i < NBAR; ++i) bar_init(bar + i, 1);
+    // one arrival for each softmax warp of the pair
+    for (int i = 0; i < 2; ++i) bar_init(bar + B_SFREE + i, 2 * SOFTMAX_WARPS);
+    bar_init(bar + B_PFULL, 2 * SOFTMAX_WARPS);
+    for (int i = 0; i < 2; ++i) bar_init(bar + B_MX + i, 2);  // the two warps that hold the same heads
+    *abort_flag = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == MMA_WARP)
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(su32(smem + OFF_MISC)),
+                 "r"(TMEM_COLS)
+                 : "memory");
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();  // both CTAs' barriers are ready
+  tc_fence_after();
+  const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(smem + OFF_MISC);
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  extern __shared__ __align__(16) uint8_t smem[];
-  float* qs = reinterpret_cast<float*>(smem);
-  __nv_bfloat16* ks = reinterpret_cast<__nv_bfloat16*>(smem + HG * DQK * 4);
-  float* ps = reinterpret_cast<float*>(smem + HG * DQK * 4 + NK * ROW_BYTES);
-  const int t = threadIdx.x, b = blockIdx.x, h0 = blockIdx.y * HG, split = blockIdx.z;
+
   const int len = length_of(a);
-  const int nblk = (len + NK - 1) / NK, per = (nblk + a.nsplit - 1) / a.nsplit;
-  const int j0 = split * per, j1 = min(nblk, j0 + per);
-  const __nv_bfloat16* q = a.q + ((size_t)b * HEADS + h0) * DQK;
-  for (int i = t; i < HG * DQK; i += THREADS) qs[i] = __bfloat162float(q[i]);
-  float acc[HG][2], m[HG], l[HG];
+  const int ntiles = (len + NK - 1) / NK, per = (ntiles + a.nsplit - 1) / a.nsplit;
+  const int j0 = min(ntiles, split * per), nt = min(ntiles, j0 + per) - j0;
+  const uint32_t lead = peer_addr(bar, 0);  // the first CTA's barriers
+  // test hook: every role that would start a copy or an MMA first waits on a barrier that nothing completes yet
+  bool ok = true;
+
+  if (warp == MMA_WARP) {
+    if (rank == 0 && lane == 0) {
+      constexpr uint32_t ID_S = idesc_bf16(HEADS, NK, 0, 0), ID_O = idesc_bf16(HEADS, 256, 0, 1);
+      const uint64_t dq = sdesc128(su32(smem + OFF_Q), 0), dk = sdesc128(su32(smem + OFF_K), 0),
+                     dp = sdesc128(su32(smem + OFF_P), 0), dv = sdesc128(su32(smem + OFF_V), SEG_BYTES);
+      ok = !a.stall || bar_wait(bar + B_STALL, 0, abort_flag, lim);
+      if (ok && nt > 0) ok = bar_wait(bar + B_QFULL, 0, abort_flag, lim);
+      for (int j = 0; j <= nt && ok && nt > 0; ++j) {
+        if (j < nt) {
+          const uint32_t d = tmem + TMEM_S + (uint32_t)(j & 1) * KH;
+          if (j >= 2) ok = bar_wait_cluster(bar + B_SFREE + (j & 1), (unsigned)((j >> 1) - 1) & 1u, abort_flag, lim);
+          tc_fence_after();
+          for (int c = 0; c < KBLK && ok; ++c) {
+            ok = bar_wait_cluster(bar + B_KFULL + c, (unsigned)j & 1u, abort_flag, lim);
+            if (!ok) break;
+            const uint64_t oa = dq + (uint64_t)(c * (BLK_BYTES >> 4)), ob = dk + (uint64_t)(c * (BLK_BYTES >> 4));
+            mma2(d, oa, ob, ID_S, c != 0 ? 1u : 0u);
+            mma2(d, oa + 2, ob + 2, ID_S, 1u);
+            mma2(d, oa + 4, ob + 4, ID_S, 1u);
+            mma2(d, oa + 6, ob + 6, ID_S, 1u);
+            commit2(bar + B_KEMPTY + c);
+          }
+          if (!ok) break;
+          commit2(bar + B_SFULL + (j & 1));
+        }
+        if (j >= 1) {
+          const int jp = j - 1;
+          ok = bar_wait_cluster(bar + B_PFULL, (unsigned)jp & 1u, abort_flag, lim);
+          tc_fence_after();
+          for (int c = 0; c < VCHUNK && ok; ++c) {
+            ok = bar_wait_cluster(bar + B_VFULL + c, (unsigned)jp & 1u, abort_flag, lim);
+            if (!ok) break;
 #pragma unroll
-  for (int h = 0; h < HG; ++h) acc[h][0] = acc[h][1] = l[h] = 0.f, m[h] = -INFINITY;
-  for (int j = j0; j < j1; ++j) {
-    __syncthreads();
-    for (int c = t; c < NK * (ROW_BYTES / 16); c += THREADS) {
-      const int r = c / (ROW_BYTES / 16), tok = j * NK + r;
-      uint4 v = make_uint4(0, 0, 0, 0);
-      if (tok < len) {
-        const int64_t page = ld_fresh(a.pages + (tok >> a.page_shift));
-        if (page >= 0 && page < a.page_limit)
-          v = *reinterpret_cast<const uint4*>(
-              a.rows + ((page << a.page_shift) + (tok & ((1 << a.page_shift) - 1))) * (int64_t)ROW_BYTES +
-              (c % (ROW_BYTES / 16)) * 16);
+            for (int k = 0; k < 2; ++k) {
+              // 16 keys: P's block c / 2, 32 bytes a step; V's chunk c, 16 rows a step; two halves of the CTA's columns
+              const uint64_t oa = dp + (uint64_t)((c >> 1) * (BLK_BYTES >> 4) + ((c & 1) * 2 + k) * 2);
+              const uint64_t ob = dv + (uint64_t)(c * (VCHUNK_BYTES >> 4) + k * (16 * 128 >> 4));
+              const uint32_t acc = jp > 0 || c > 0 || k > 0 ? 1u : 0u;
+              mma2(tmem + TMEM_O, oa, ob, ID_O, acc);
+              mma2(tmem + TMEM_O + 128, oa, ob + (uint64_t)(2 * SEG_BYTES >> 4), ID_O, acc);
+            }
+            commit2(bar + B_VEMPTY + c);
+          }
+          if (!ok) break;
+          commit2(bar + B_PDONE);
+        }
       }
-      reinterpret_cast<uint4*>(ks)[c] = v;
+      commit2(bar + B_ODONE);  // every MMA has finished
     }
-    __syncthreads();
-    for (int c = t; c < HG * NK; c += THREADS) {
-      const int h = c / NK, r = c % NK, tok = j * NK + r;
-      float s = 0.f;
-      for (int d = 0; d < DQK; ++d) s = fmaf(qs[h * DQK + d], __bfloat162float(ks[r * DQK + d]), s);
-      bool on = tok < len;
-      if (on) {
-        const int64_t page = ld_fresh(a.pages + (tok >> a.page_shift));
-        on = page >= 0 && page < a.page_limit;
+    __syncwarp();
+  } else if (warp == K_WARP) {
+    ok = !a.stall || __all_sync(0xffffffffu, bar_wait(bar + B_STALL, 0, abort_flag, lim));
+    if (ok && nt > 0 && lane == 0) {
+      if (rank == 0) bar_arrive_expect(bar + B_QFULL, 2 * KBLK * BLK_BYTES);
+      for (int c = 0; c < KBLK; ++c)
+        tma_box(su32(smem + OFF_Q + c * BLK_BYTES), &qmap, 64 * c, b * HEADS + (int)rank * QH, lead + B_QFULL * 8);
+    }
+    Seg next[2];
+    for (int i = 0; i < 2; ++i) next[i] = seg_row(a, j0 * NK + (int)rank * KH + i * BOX, nt > 0 ? len : 0, lane);
+    for (int j = 0; j < nt && ok; ++j) {
+      const Seg cur[2] = {next[0], next[1]};
+      for (int c = 0; c < KBLK; ++c) {
+        if (j > 0) ok = __all_sync(0xffffffffu, bar_wait(bar + B_KEMPTY + c, (unsigned)(j - 1) & 1u, abort_flag, lim));
+        if (!ok) break;
+        if (rank == 0 && lane == 0) bar_arrive_expect(bar + B_KFULL + c, 2 * BLK_BYTES);
+        for (int i = 0; i < 2; ++i)
+          load_seg(a, &map, &map1, cur[i], su32(smem + OFF_K + c * BLK_BYTES + i * SEG_BYTES), 64 * c,
+                   lead + (B_KFULL + c) * 8, lane);
+        if (c == 0 && j + 1 < nt)  // the next tile's rows, looked up a tile ahead
+          for (int i = 0; i < 2; ++i) next[i] = seg_row(a, (j0 + j + 1) * NK + (int)rank * KH + i * BOX, len, lane);
       }
-      ps[c] = on ? s * a.scale_log2 : -INFINITY;
     }
-    __syncthreads();
+  } else if (warp == V_WARP) {
+    ok = !a.stall || __all_sync(0xffffffffu, bar_wait(bar + B_STALL, 0, abort_flag, lim));
+    Seg next[VCHUNK];
+    for (int i = 0; i < VCHUNK; ++i) next[i] = seg_row(a, j0 * NK + i * BOX, nt > 0 ? len : 0, lane);
+    for (int j = 0; j < nt && ok; ++j) {
 #pragma unroll
-    for (int h = 0; h < HG; ++h) {
-      float mb = m[h];
-      for (int r = 0; r < NK; ++r) mb = fmaxf(mb, ps[h * NK + r]);
-      const float ref = mb == -INFINITY ? 0.f : mb;  // no finite score yet: nothing is subtracted, a NaN still shows
-      const float f = exp2f(m[h] - ref);
-      m[h] = mb;
-      l[h] *= f;
-      acc[h][0] *= f;
-      acc[h][1] *= f;
-      for (int r = 0; r < NK; ++r) {
-        const float p = exp2f(ps[h * NK + r] - ref);
-        const float pr = __bfloat162float(__float2bfloat16_rn(p));
-        l[h] += p;
-        acc[h][0] = fmaf(pr, __bfloat162float(ks[r * DQK + t]), acc[h][0]);
-        acc[h][1] = fmaf(pr, __bfloat162float(ks[r * DQK + t + THREADS]), acc[h][1]);
+      for (int c = 0; c < VCHUNK; ++c) {
+        if (j > 0) ok = ok && __all_sync(0xffffffffu, bar_wait(bar + B_VEMPTY + c, (unsigned)(j - 1) & 1u, abort_flag, lim));
+        if (!ok) break;
+        if (rank == 0 && lane == 0) bar_arrive_expect(bar + B_VFULL + c, 2 * VCHUNK_BYTES);
+        for (int i = 0; i < DVH / 64; ++i)
+          load_seg(a, &map, &map1, next[c], su32(smem + OFF_V + c * VCHUNK_BYTES + i * SEG_BYTES),
+                   (int)rank * DVH + 64 * i, lead + (B_VFULL + c) * 8, lane);
+        if (j + 1 < nt) next[c] = seg_row(a, (j0 + j + 1) * NK + c * BOX, len, lane);
+      }
+    }
+  } else {
+    // ---- softmax: thread t holds TMEM lane t, head r of this CTA, and the keys of its half of every tile
+    const int r = t & (QH - 1), hf = t >> 6;
+    const uint32_t trow = tmem + ((uint32_t)(warp * 32) << 16);
+    float m_run = -INFINITY, l_run = 0.f;
+    uint64_t mask_next = 0;
+    // value `v` of the other thread of the same head; n counts the exchanges
+    auto other = [&](float v, int n) {
+      float* const share = red + (n & 1) * 128;
+      share[t] = v;
+      __syncwarp();
+      if (lane == 0) bar_arrive(bar + B_MX + (warp & 1));
+      ok = __all_sync(0xffffffffu, bar_wait(bar + B_MX + (warp & 1), (unsigned)n & 1u, abort_flag, lim)) && ok;
+      return share[t ^ QH];
+    };
+    auto key_mask = [&](int j) {
+      const int tok = (j0 + j) * NK + hf * KH + lane;
+      const unsigned lo = __ballot_sync(0xffffffffu, row_of(a, tok, len) >= 0);
+      const unsigned hi = __ballot_sync(0xffffffffu, row_of(a, tok + 32, len) >= 0);
+      return (uint64_t)hi << 32 | lo;
+    };
+    if (nt > 0) mask_next = key_mask(0);
+    for (int j = 0; j < nt; ++j) {
+      const uint64_t mask = mask_next;
+      ok = __all_sync(0xffffffffu, bar_wait(bar + B_SFULL + (j & 1), (unsigned)(j >> 1) & 1u, abort_flag, lim));
+      if (!ok) break;
+      tc_fence_after();
+      uint32_t sv[2][32];
+      tmem_ld32(trow + TMEM_S + (uint32_t)(j & 1) * KH, sv[0]);
+      tmem_ld32(trow + TMEM_S + (uint32_t)(j & 1) * KH + 32, sv[1]);
+      if (j + 1 < nt) mask_next = key_mask(j + 1);
+      tmem_wait_ld();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) bar_arrive_peer(lead + (B_SFREE + (j & 1)) * 8);
+      float x[KH];
+      float mb = -INFINITY;
+#pragma unroll
+      for (int i = 0; i < KH; ++i) {
+        const float v = __uint_as_float(sv[i >> 5][i & 31]) * a.scale_log2;
+        x[i] = mask >> i & 1 ? v : -INFINITY;
+        mb = fmaxf(mb, x[i]);
+      }
+      // the two threads of a head agree on the tile's maximum
+      mb = fmaxf(mb, other(mb, j));
+      if (!ok) break;
+      float m_new = m_run;
+      if (mb > -INFINITY && (m_run == -INFINITY || mb > m_run + 8.f)) m_new = mb;
+      const bool resc = m_new != m_run && m_run != -INFINITY;
+      const bool any = __any_sync(0xffffffffu, resc);
+      // P's buffer is free, and O holds tiles 0 .. j-1, once the value product of tile j-1 has finished
+      float p[KH];
+      const float ref = m_new == -INFINITY ? 0.f : m_new;  // no finite score yet: nothing to subtract, a NaN still shows
+      float sum = 0.f;
+#pragma unroll
+      for (int i = 0; i < KH; ++i) {
+        p[i] = ex2_approx(x[i] - ref);
+        sum += p[i];
+      }
+      if (j >= 1) {
+        ok = __all_sync(0xffffffffu, bar_wait(bar + B_PDONE, (unsigned)(j - 1) & 1u, abort_flag, lim));
+        if (!ok) break;
+      }
+      if (any) {
+        tc_fence_after();
+        const float f = resc ? ex2_approx(m_run - m_new) : 1.f;
+        for (int c = 0; c < DVH; c += 16) {
+          float o[16];
+          tmem_ld16(trow + TMEM_O + c, o);
+#pragma unroll
+          for (int i = 0; i < 16; ++i) o[i] *= f;
+          tmem_st16(trow + TMEM_O + c, o);
+        }
+        tmem_wait_st();
+        l_run *= f;
+      }
+      m_run = m_new;
+      l_run += sum;
+      uint8_t* const prow = smem + OFF_P + hf * BLK_BYTES + r * 128;
+#pragma unroll
+      for (int c = 0; c < KH / 8; ++c) {
+        uint32_t w[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const __nv_bfloat162 v = __floats2bfloat162_rn(p[8 * c + 2 * i], p[8 * c + 2 * i + 1]);
+          w[i] = *reinterpret_cast<const uint32_t*>(&v);
+        }
+        *reinterpret_cast<uint4*>(prow + ((c ^ (r & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
+      }
+      fence_proxy_async();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) bar_arrive_peer(lead + B_PFULL * 8);
+    }
+    if (ok) ok = __all_sync(0xffffffffu, bar_wait(bar + B_ODONE, 0, abort_flag, lim));
+    if (ok) l_run += other(l_run, nt);
+    if (ok) {
+      tc_fence_after();
+      float* const tile = reinterpret_cast<float*>(smem + OFF_K) + warp * 32 * TS;
+      const int h0 = (int)rank * QH + (warp & 1) * 32;  // the warp's first head
+      const size_t bh = (size_t)b * HEADS + h0 + lane;
+      if (a.nsplit > 1) {
+        const size_t sh = (size_t)split * a.batch * HEADS;
+        if (nt > 0) store_out(trow + TMEM_O, true, 1.f, 0.f, tile, nullptr, a.part_o, true,
+                              (sh + (size_t)b * HEADS + h0) * DV + hf * DVH, lane);
+        if (hf == 0) a.part_ml[sh + bh] = make_float2(m_run, l_run);
+      } else {
+        const float own = a.own_lse ? a.own_lse[bh] * 1.4426950408889634f : -INFINITY;
+        const float mx = fmaxf(l_run != 0.f ? m_run : -INFINITY, own);
+        const float ref = mx == -INFINITY ? 0.f : mx;
+        const float w = l_run != 0.f ? exp2f(m_run == -INFINITY ? 0.f : m_run - ref) : 0.f;
+        const float wo = own != -INFINITY ? exp2f(own - ref) : 0.f;
+        const float total = fmaf(w, l_run, wo);
+        const float inv = total != 0.f ? 1.f / total : 0.f;
+        other(0.f, nt + 1);  // both threads of a head have read own_lse, which may be lse itself
+        // (without own rows the weight is 0 itself, not 0 times a reciprocal that may be NaN: own_out may be null)
+        store_out(trow + TMEM_O, nt > 0, w * inv, wo != 0.f ? wo * inv : 0.f, tile, a.own_out, a.out, a.out_f32 != 0,
+                  ((size_t)b * HEADS + h0) * DV + hf * DVH, lane);
+        if (hf == 0) a.lse[bh] = total != 0.f ? (ref + log2f(total)) * 0.6931471805599453f : -INFINITY;
       }
     }
   }
-  const size_t rh = ((size_t)split * a.batch + b) * HEADS + h0;
-#pragma unroll
-  for (int h = 0; h < HG; ++h) {
-    a.part_o[(rh + h) * DV + t] = acc[h][0];
-    a.part_o[(rh + h) * DV + t + THREADS] = acc[h][1];
-    if (t == 0) a.part_ml[rh + h] = make_float2(m[h], l[h]);
+
+  if (*abort_flag) {
+    // a wait ran out: let the copies in flight land before the shared memory goes, and report
+    for (int i = 0; i < 50; ++i) __nanosleep(1000);
+    if (t == 0) atomicOr(a.err, HS_DEVERR_TIMEOUT);
   }
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();
+  tc_fence_after();
+  if (warp == MMA_WARP)
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(TMEM_COLS) : "memory");
 }
 
 // One CTA joins one head of one request: thread t holds outputs 4t .. 4t + 3.
@@ -136,6 +488,7 @@ __global__ void __launch_bounds__(DV / 4) hs_prefix_join_kernel(const PrefixArgs
     const float2 ml = a.part_ml[(size_t)s * heads + bh];
     if (ml.y != 0.f) mx = fmaxf(mx, ml.x);
   }
+  const float ref = mx == -INFINITY ? 0.f : mx;
   float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
   float total = 0.f;
   auto add = [&](float w, const float* p) {
@@ -146,13 +499,13 @@ __global__ void __launch_bounds__(DV / 4) hs_prefix_join_kernel(const PrefixArgs
     o.w = fmaf(w, v.w, o.w);
   };
   if (own != -INFINITY) {
-    total = exp2f(own - mx);
+    total = exp2f(own - ref);
     add(total, a.own_out + bh * DV);
   }
   for (int s = 0; s < a.nsplit; ++s) {
     const float2 ml = a.part_ml[(size_t)s * heads + bh];
     if (ml.y == 0.f) continue;  // a split with no row
-    const float w = exp2f(ml.x - mx);
+    const float w = exp2f(ml.x == -INFINITY ? 0.f : ml.x - ref);
     total = fmaf(w, ml.y, total);
     add(w, a.part_o + ((size_t)s * heads + bh) * DV);
   }
@@ -166,19 +519,88 @@ __global__ void __launch_bounds__(DV / 4) hs_prefix_join_kernel(const PrefixArgs
         make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
   }
   __syncthreads();  // own_lse may be lse itself
-  if (t == 0) a.lse[bh] = total != 0.f ? (mx + log2f(total)) * 0.6931471805599453f : -INFINITY;
+  if (t == 0) a.lse[bh] = total != 0.f ? (ref + log2f(total)) * 0.6931471805599453f : -INFINITY;
 }
 
-int splits_of(const hs_pool* p, int32_t batch, int32_t max_length) {
-  const int blocks = (max_length + NK - 1) / NK;
-  return std::max(1, std::min({blocks, 2 * p->num_sms / std::max(1, batch * (HEADS / HG)), 64}));
+// How many pairs the current device holds at once, cached per device.
+int pairs_resident() {
+  static std::atomic<int> cache[64];
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) {
+    cudaGetLastError();
+    return 0;
+  }
+  int n = cache[dev].load(std::memory_order_relaxed);
+  if (n) return n;
+  if (cudaFuncSetAttribute(hs_prefix_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_BYTES) != cudaSuccess) {
+    cudaGetLastError();
+    return 0;
+  }
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(2, 1, 1);
+  cfg.blockDim = dim3(THREADS, 1, 1);
+  cfg.dynamicSmemBytes = SMEM_BYTES;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim.x = 2;
+  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  if (cudaOccupancyMaxActiveClusters(&n, hs_prefix_kernel, &cfg) != cudaSuccess) {
+    cudaGetLastError();
+    return 0;
+  }
+  cache[dev].store(n, std::memory_order_relaxed);
+  return n;
+}
+
+// The number of splits with the shortest expected time, in tiles: waves of units, each a run of tiles and a fixed cost of
+// about four of them (prologue, Q, epilogue), and for more than one split the join.
+int splits_of(int pairs, int32_t batch, int32_t max_length) {
+  const int tiles = (max_length + NK - 1) / NK;
+  int best = 1;
+  double least = 1e30;
+  for (int n = 1; n <= std::max(1, std::min(tiles, std::max(1, 4 * pairs / batch))); ++n) {
+    const int64_t units = (int64_t)batch * n;
+    const double cost = (double)((units + pairs - 1) / pairs) * ((tiles + n - 1) / n + 4) + (n > 1 ? 3 + 0.08 * units : 0);
+    if (cost < least) least = cost, best = n;
+  }
+  return best;
+}
+
+using EncodeFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
+                              const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                              CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+EncodeFn encoder() {
+  static std::atomic<EncodeFn> fn{nullptr};
+  EncodeFn f = fn.load(std::memory_order_acquire);
+  if (f) return f;
+  void* p = nullptr;
+  cudaDriverEntryPointQueryResult found;
+  if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &found) != cudaSuccess ||
+      found != cudaDriverEntryPointSuccess) {
+    cudaGetLastError();
+    return nullptr;
+  }
+  f = reinterpret_cast<EncodeFn>(p);
+  fn.store(f, std::memory_order_release);
+  return f;
+}
+// Rows of 576 bf16 values, boxes of 64 columns x `box` rows, 128-byte swizzle, zeros outside.
+bool make_map(EncodeFn f, CUtensorMap* m, const void* rows, uint64_t count, uint32_t box) {
+  const cuuint64_t dims[2] = {DQK, count}, strides[1] = {ROW_BYTES};
+  const cuuint32_t boxes[2] = {64, box}, steps[2] = {1, 1};
+  return f(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(rows), dims, strides, boxes, steps,
+           CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+           CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 }  // namespace
 
 extern "C" size_t hs_mla_prefix_workspace(hs_pool* pool, int32_t batch, int32_t max_length) {
-  if (!pool || batch <= 0 || max_length < 0) return 0;
-  return (size_t)splits_of(pool, batch, max_length) * (size_t)batch * HEADS * (DV * sizeof(float) + sizeof(float2));
+  if (!pool || batch <= 0 || max_length < 0 || max_length > 1 << 30 || batch > (1 << 24) / HEADS || !hs_on_device(pool)) return 0;
+  const int pairs = pairs_resident(), n = pairs > 0 ? splits_of(pairs, batch, max_length) : 1;
+  return n > 1 ? (size_t)n * (size_t)batch * HEADS * (DV * sizeof(float) + sizeof(float2)) : 0;
 }
 
 extern "C" int hs_mla_prefix(hs_pool* pool, int32_t batch, const void* q, const hs_paged_rows* prefix,
@@ -186,53 +608,69 @@ extern "C" int hs_mla_prefix(hs_pool* pool, int32_t batch, const void* q, const 
                              const float* own_lse, void* out, int32_t out_type, float* lse, void* workspace,
                              size_t workspace_bytes, hs_stream_t stream) {
   const auto aligned = [](const void* p, uintptr_t n) { return p && (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; };
-  if (!pool || !prefix || batch < 0 || batch > (1 << 24) / HEADS || max_length < 0 || !hs_paged_ok(prefix) ||
+  if (!pool || !prefix || batch < 0 || batch > (1 << 24) / HEADS || max_length < 0 || max_length > 1 << 30 || !hs_paged_ok(prefix) ||
       max_length > prefix->page_stride * prefix->page_rows || (out_type != HS_TYPE_BF16 && out_type != HS_TYPE_F32) ||
       (own_out != nullptr) != (own_lse != nullptr))
     return HS_ERR_INVALID_ARG;
   if (pool->d.row_bytes != ROW_BYTES) return HS_ERR_UNSUPPORTED;
   if (batch == 0) return HS_OK;
-  const size_t need = hs_mla_prefix_workspace(pool, batch, max_length);
   if (!aligned(q, 16) || !aligned(out, 16) || !aligned(lse, 4) || (own_out && (!aligned(own_out, 16) || !aligned(own_lse, 4))) ||
-      (prefix_length && !aligned(prefix_length, 4)) || (need && (!aligned(workspace, 256) || workspace_bytes < need)) ||
-      !hs_on_device(pool))
+      (prefix_length && !aligned(prefix_length, 4)) || !hs_on_device(pool))
     return HS_ERR_INVALID_ARG;
+  const int pairs = pairs_resident();
+  const EncodeFn encode = encoder();
+  if (pairs < 1 || !encode) return HS_ERR_UNSUPPORTED;
+  const int nsplit = splits_of(pairs, batch, max_length);
+  const size_t need = nsplit > 1 ? (size_t)nsplit * (size_t)batch * HEADS * (DV * sizeof(float) + sizeof(float2)) : 0;
+  if (need && (!aligned(workspace, 256) || workspace_bytes < need)) return HS_ERR_INVALID_ARG;
+
   PrefixArgs a;
   std::memset(&a, 0, sizeof(a));
-  a.q = static_cast<const __nv_bfloat16*>(q);
-  a.rows = static_cast<const uint8_t*>(prefix->rows);
   a.pages = prefix->pages;
   while ((1 << a.page_shift) < prefix->page_rows) ++a.page_shift;
+  a.box_shift = std::min(a.page_shift, 5);
   a.max_length = max_length;
-  a.page_limit = prefix->count / prefix->page_rows;
+  a.page_limit = (int32_t)(prefix->count / prefix->page_rows);
+  a.none = (int32_t)prefix->count;
   a.length = prefix_length;
   a.scale_log2 = sm_scale * 1.4426950408889634f;
   a.batch = batch;
-  a.nsplit = splits_of(pool, batch, max_length);
+  a.nsplit = nsplit;
   a.part_o = static_cast<float*>(workspace);
-  a.part_ml = reinterpret_cast<float2*>(a.part_o + (size_t)a.nsplit * batch * HEADS * DV);
+  a.part_ml = nsplit > 1 ? reinterpret_cast<float2*>(a.part_o + (size_t)nsplit * batch * HEADS * DV) : nullptr;
   a.own_out = own_out;
   a.own_lse = own_lse;
   a.out = out;
   a.out_f32 = out_type == HS_TYPE_F32;
   a.lse = lse;
-  if (cudaFuncSetAttribute(hs_prefix_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM) != cudaSuccess) {
-    cudaGetLastError();
-    return HS_ERR_UNSUPPORTED;
-  }
+  a.err = pool->err;
+  hs_attention_waits(&a.wait_limit, &a.stall);
+  CUtensorMap qmap, map, map1;
+  // an empty pool of rows still needs a map: one row, which page_limit = 0 keeps from being read
+  const uint64_t count = std::max<int64_t>(prefix->count, 1);
+  a.none = (int32_t)count;
+  if (!make_map(encode, &qmap, q, (uint64_t)batch * HEADS, QH) ||
+      !make_map(encode, &map, prefix->rows, count, 1u << a.box_shift) || !make_map(encode, &map1, prefix->rows, count, 1))
+    return HS_ERR_INVALID_ARG;
+
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)batch, HEADS / HG, (unsigned)a.nsplit);
+  cfg.gridDim = dim3((unsigned)(2 * batch * nsplit), 1, 1);
   cfg.blockDim = dim3(THREADS, 1, 1);
-  cfg.dynamicSmemBytes = SMEM;
+  cfg.dynamicSmemBytes = SMEM_BYTES;
   cfg.stream = reinterpret_cast<cudaStream_t>(stream);
-  cudaLaunchAttribute attr;
-  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr.val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
-  if (cudaLaunchKernelEx(&cfg, hs_prefix_kernel, a) != cudaSuccess) return HS_ERR_CUDA;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = 2;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  if (cudaLaunchKernelEx(&cfg, hs_prefix_kernel, a, qmap, map, map1) != cudaSuccess) return HS_ERR_CUDA;
+  if (nsplit == 1) return HS_OK;
   cfg.gridDim = dim3((unsigned)batch * HEADS, 1, 1);
   cfg.blockDim = dim3(DV / 4, 1, 1);
   cfg.dynamicSmemBytes = 0;
+  cfg.numAttrs = 1;
   return cudaLaunchKernelEx(&cfg, hs_prefix_join_kernel, a) == cudaSuccess ? HS_OK : HS_ERR_CUDA;
 }

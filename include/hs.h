@@ -280,7 +280,7 @@ int hs_mla_decode_history(hs_pool *pool, int32_t layer, int32_t batch, const voi
  * Rows of the ordinary paged HBM pool (the tier that hs_resolve_tiered serves in place), as a block table sees them.
  *   rows: device memory of `count` rows of the pool's row_bytes, 16-byte aligned; count <= 2^31 - 64 (their
  *     bytes may pass 32 bits).
- *   pages: int32 page numbers (device or mapped host memory): token t of list l is row
+ *   pages: int32 page numbers in device memory: token t of list l is row
  *     pages[l * page_stride + t / page_rows] * page_rows + t % page_rows. A negative entry means that the pool does not
  *     hold that page's tokens; so does one whose page does not lie wholly within `count`.
  *   page_stride: entries of one list (>= 1): a token at or past page_stride * page_rows has no row.
@@ -364,7 +364,7 @@ int hs_append(hs_pool *pool, int32_t layer, int32_t ntok, const hs_append_desc *
  *   q: device bf16 [batch][128][576], 16-byte aligned. batch >= 0 is not bound by max_batch: several query tokens of one
  *     request are several rows of the batch.
  *   prefix: the paged rows; its list 0 is the prefix (page_stride entries of it at most are read).
- *   max_length: tokens, >= 0, <= page_stride * page_rows. prefix_length: NULL, or device int32 [1], the length to use
+ *   max_length: tokens, 0 .. 2^30 and <= page_stride * page_rows. prefix_length: NULL, or device int32 [1], the length to use
  *     (clamped to 0 .. max_length), read when the kernel runs: a captured graph can be replayed over a prefix that grew.
  *   own_out, own_lse: NULL, or the same requests' attention over rows of their own, as hs_mla_decode wrote it (fp32
  *     [batch][128][512], 16-byte aligned, and [batch][128]): out and lse are then those of both sets of rows together.
@@ -390,12 +390,12 @@ size_t hs_mla_prefix_workspace(hs_pool *pool, int32_t batch, int32_t max_length)
  * test exercise failure detection without faulting the GPU: every wait inside the kernel is bounded, and on running
  * out it stops every role, frees its tensor memory, returns and sets HS_DEVERR_TIMEOUT.
  *   wait_limit: polling rounds after which a wait of the kernel's roles gives up (0 restores the default, 2^20).
- *   stall != 0: the tensor-core issuer of every CTA first waits on a barrier that nothing completes, so that wait
- *     runs out before any tensor-core work or row copy of the kernel is issued, and the abort path runs with
- *     nothing in flight. 0 restores normal operation.
+ *   stall != 0: the tensor-core issuer of every CTA (and the loaders of hs_mla_prefix) first waits on a barrier that
+ *     nothing completes, so that wait runs out before any tensor-core work or row copy of the kernel is issued, and
+ *     the abort path runs with nothing in flight. 0 restores normal operation.
  *   split_max_batch: if non-NULL, receives the largest batch for which hs_mla_decode splits a request's keys over
  *     two CTA pairs on the current device (larger batches run one pair per request).
- * Applies to the hs_mla_decode / hs_mla_decode_history calls made after it.
+ * Applies to the hs_mla_decode / hs_mla_decode_history / hs_mla_prefix calls made after it.
  */
 int hs_debug_attention(uint32_t wait_limit, int32_t stall, int32_t *split_max_batch);
 

@@ -355,3 +355,22 @@ def test_append_resolve_decode_and_prefix_together():
         assert ((out[b].cpu().double() - want).abs() <= 2.1 * 2.0 ** -8 * mean + 2.0 ** -8 * want.abs()).all()
         assert (lse[b].cpu().double() - torch.logsumexp(s, -1)).abs().max() <= 2.0 ** -7
     buf.close()
+
+
+@pytest.mark.parametrize("batch,length", [(2, 3000), (160, 130)])
+def test_a_wait_that_runs_out_is_reported(batch, length):
+    """With the stall hook nothing is copied or multiplied; every role's wait runs out, the kernel returns, the error word
+    says so, and the next call on the same pool is right (split and unsplit)."""
+    buf = hs.PoolBuffers(1, 2, 64, 16, 16, 1152)
+    p = buf.create()
+    c = Case(batch, length, 64, seed=1)
+    try:
+        hs.hs_debug_attention(64, True)
+        c.run(p)
+        torch.cuda.synchronize()
+    finally:
+        hs.hs_debug_attention()
+    assert hs.hs_get_error(p, clear=True) == hs.HS_DEVERR_TIMEOUT
+    c.check(*c.run(p))
+    assert hs.hs_get_error(p) == 0
+    buf.close()
