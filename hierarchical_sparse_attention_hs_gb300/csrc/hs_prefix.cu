@@ -12,24 +12,28 @@
 // one request the tensor cores and HBM are in balance, with more the tensor cores decide, as long as the rows come from
 // L2. Requests of one split run side by side and walk the same rows, so HBM is read about once for all.
 //
-// A pair of CTAs (a cluster of two) takes one request's 128 heads, 64 for each CTA, over one split, 128 keys a tile. The
+// A pair of CTAs (a cluster of two) takes one request's 128 heads, 64 for each CTA, over one split, 256 keys a tile. The
 // 512 output columns of 128 heads in fp32 would fill a CTA's tensor memory; with 64 heads a CTA they take half (the pair's
 // MMAs, cta_group::2 with M = 128, put a head's even and odd column halves on lanes r and r + 64), which leaves room for
-// the scores. For S = Q K^T each CTA holds its 64 heads of Q and 64 of the tile's keys; for O += P V its 64 heads of P and
-// all 128 keys of 256 value columns. The MMA reads each CTA's operand half and shares it, so no operand is loaded twice
-// within a CTA, but the value half of a CTA's own keys lies in shared memory twice (K and V are addressed by one
-// descriptor for both CTAs, and their halves cut the rows differently).
+// two buffers of scores. For S = Q K^T each CTA holds its 64 heads of Q and 128 of the tile's keys; for O += P V its 64
+// heads of P and all 256 keys of 256 value columns. The MMA reads each CTA's operand half and shares it; the value half of
+// a CTA's own keys is loaded twice (K and V are addressed by one descriptor for both CTAs, and their halves cut the rows
+// differently). Every MMA has N = 256: one of M = 128 takes 64 cycles there, the full rate, and 47.6 with N = 128 or 64
+// (measured), so a tile of 128 keys would run its scores at two thirds of the rate.
 //
-// Warp roles per CTA: 0-3 softmax (thread t: TMEM lane t, head t % 64, keys 64 (t / 64) .. +63 of the tile), 4 the issuer
-// (the pair's first CTA issues for both), 5 loads Q and K, 6 loads V. K is one buffer of nine 64-column blocks, V one of
-// four 32-key chunks; each block or chunk is handed back as soon as the MMAs that read it have finished, so the next tile
-// streams in behind the current one. Per tile j the issuer runs S(j + 1) before O += P(j) V(j), so the softmax of a tile
-// overlaps the value product of the one before and the scores of the one after.
+// Warp roles per CTA: 0-7 softmax (warp w: TMEM lanes 32 (w % 4) .. +31, that is head lane % 64 and key half lane / 64,
+// and keys 64 (w / 4) .. +63 of that half), 8 the issuer (the pair's first CTA issues for both), 9-15 the loaders. K and V
+// each pass through a ring of 16 KB stages, four for K and three for V, with a loader for each slot (one thread's wait,
+// expectation and copies of a stage take about 310 cycles one after the other, more than the stage's MMAs): a K stage is 64 columns of the CTA's 128
+// keys, a V stage 128 of its value columns of 64 keys; each feeds four MMAs, 256 cycles. Per tile j the issuer runs
+// S(j + 1) before O += P(j) V(j), so the softmax of a tile overlaps the value product of the one before and the scores of
+// the one after.
 //
-// Loads are TMA boxes of 64 columns x min(page_rows, 32) rows, 128-byte swizzle. A box whose page the pool does not hold,
-// or that lies behind the prefix, starts behind the last row of the tensor map: it reads nothing and fills with zeros. In
-// the one page that the prefix ends inside, single-row boxes do the same row by row. So rows outside the prefix are never
-// read, and a masked key's value row is zero, whatever memory holds; its score is masked to -inf by the softmax.
+// Loads are TMA boxes of 64 columns x min(page_rows, 64) rows, 128-byte swizzle. A box
+// whose page the pool does not hold, or that lies behind the prefix, starts behind the last row of the tensor map: it
+// reads nothing and fills with zeros. In the one page that the prefix ends inside, single-row boxes do the same row by
+// row. So rows outside the prefix are never read, and a masked key's value row is zero, whatever memory holds; its score
+// is masked to -inf by the softmax.
 //
 // Waits are bounded as in hs_attention.cu: on running out a role sets the abort flag, which ends every role, and the
 // HS_DEVERR_TIMEOUT bit.
@@ -52,33 +56,33 @@ namespace {
 using namespace hs;
 
 constexpr int HEADS = 128, DQK = 576, DV = 512, ROW_BYTES = DQK * 2;
-constexpr int NK = 128;            // keys of a tile
+constexpr int NK = 256;            // keys of a tile
 constexpr int QH = HEADS / 2;      // heads of a CTA
-constexpr int KH = NK / 2;         // keys of a CTA's K half, and of a softmax thread
+constexpr int KH = NK / 2;         // keys of a CTA's K half
 constexpr int DVH = DV / 2;        // value columns of a CTA
-constexpr int BOX = 32;            // rows of the largest box
-constexpr int KBLK = DQK / 64;     // 64-column blocks of a row
-constexpr int VCHUNK = NK / BOX;   // 32-key chunks of V
+constexpr int SEG = 64;            // keys of a segment: the rows of the largest box, and a softmax thread's keys
+constexpr int NSEG = NK / SEG;
+constexpr int KBLK = DQK / 64;     // 64-column blocks of a row: K stages of a tile
+constexpr int VST = NSEG * 2;      // V stages of a tile
 constexpr int BLK_BYTES = 64 * 128;      // 64 rows x 64 columns
-constexpr int SEG_BYTES = BOX * 128;     // 32 rows x 64 columns
-constexpr int VCHUNK_BYTES = (DVH / 64) * SEG_BYTES;
+constexpr int STAGE_BYTES = 2 * BLK_BYTES;
+constexpr int KST = 4, VRING = 3, NSTAGE = KST + VRING;  // stages of K's ring, of V's, and of both
 constexpr int OFF_Q = 0;
-constexpr int OFF_K = OFF_Q + KBLK * BLK_BYTES;
-constexpr int OFF_V = OFF_K + KBLK * BLK_BYTES;
-constexpr int OFF_P = OFF_V + VCHUNK * VCHUNK_BYTES;
-constexpr int OFF_BAR = OFF_P + 2 * BLK_BYTES;
-// mbarriers: qfull kfull[9] kempty[9] vfull[4] vempty[4] sfull[2] sfree[2] pfull pdone odone stall mx[2]
-constexpr int B_QFULL = 0, B_KFULL = 1, B_KEMPTY = B_KFULL + KBLK, B_VFULL = B_KEMPTY + KBLK,
-              B_VEMPTY = B_VFULL + VCHUNK, B_SFULL = B_VEMPTY + VCHUNK, B_SFREE = B_SFULL + 2, B_PFULL = B_SFREE + 2,
-              B_PDONE = B_PFULL + 1, B_ODONE = B_PDONE + 1, B_STALL = B_ODONE + 1, B_MX = B_STALL + 1, NBAR = B_MX + 2;
+constexpr int OFF_RING = OFF_Q + KBLK * BLK_BYTES;
+constexpr int OFF_P = OFF_RING + NSTAGE * STAGE_BYTES;
+constexpr int OFF_BAR = OFF_P + NSEG * BLK_BYTES;
+// mbarriers: qfull full[7] empty[7] sfull[2] sfree[2] pfull pdone odone stall mx[2]
+constexpr int B_QFULL = 0, B_FULL = 1, B_EMPTY = B_FULL + NSTAGE, B_SFULL = B_EMPTY + NSTAGE, B_SFREE = B_SFULL + 2,
+              B_PFULL = B_SFREE + 2, B_PDONE = B_PFULL + 1, B_ODONE = B_PDONE + 1, B_STALL = B_ODONE + 1,
+              B_MX = B_STALL + 1, NBAR = B_MX + 2;
 constexpr int OFF_MISC = OFF_BAR + NBAR * 8;            // tensor-memory address, abort flag
-constexpr int OFF_RED = (OFF_MISC + 8 + 15) & ~15;      // [2 parities][128 threads] floats
-constexpr int SMEM_BYTES = OFF_RED + 2 * 128 * 4;
+constexpr int OFF_RED = (OFF_MISC + 8 + 15) & ~15;      // [2 parities][NSEG][QH] floats
+constexpr int SMEM_BYTES = OFF_RED + 2 * NSEG * QH * 4;
 static_assert(SMEM_BYTES <= 232448, "shared memory per block");
-constexpr int SOFTMAX_WARPS = 4, MMA_WARP = 4, K_WARP = 5, V_WARP = 6, THREADS = 7 * 32;
-constexpr uint32_t TMEM_COLS = 512, TMEM_O = 0, TMEM_S = 256;  // O: 2 x 128 columns; S: two buffers of 64
+constexpr int SOFTMAX_WARPS = 8, MMA_WARP = 8, LOAD_WARP0 = 9, THREADS = (LOAD_WARP0 + NSTAGE) * 32;
+constexpr uint32_t TMEM_COLS = 512, TMEM_O = 0, TMEM_S = 256;  // O: 2 x 128 columns; S: two buffers of 128
 constexpr int TS = 36;             // row stride, in floats, of a softmax warp's output tile
-static_assert(SOFTMAX_WARPS * 32 * TS * 4 <= OFF_V - OFF_K, "output tiles fit the K buffer");
+static_assert(SOFTMAX_WARPS * 32 * TS * 4 <= NSTAGE * STAGE_BYTES, "output tiles fit the ring");
 
 struct PrefixArgs {
   const int32_t* pages;
@@ -131,50 +135,77 @@ __device__ __forceinline__ void commit2(uint64_t* b) {
       "h"((uint16_t)3)
       : "memory");
 }
-// A box at (column, row) into this CTA's shared memory; its bytes count on a barrier of the pair's first CTA.
-__device__ __forceinline__ void tma_box(uint32_t dst, const CUtensorMap* map, int col, int row, uint32_t bar) {
+// Arrive on a barrier of the pair's first CTA. What it orders are this thread's tensor-memory reads and shared-memory
+// writes before the MMAs that the issuer starts after its wait, which the tcgen05 and proxy fences before it cover; a
+// release of cluster scope on top would cost about 870 cycles an arrival (measured).
+__device__ __forceinline__ void arrive_lead(uint32_t addr) {
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
+}
+// One lane of a converged warp, the same at every call.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}\n" : "=r"(p));
+  return p != 0;
+}
+// A box at column block `blk` and row `row` into this CTA's shared memory; its bytes count on a barrier of the pair's
+// first CTA.
+__device__ __forceinline__ void tma_box(uint32_t dst, const CUtensorMap* map, int blk, int row, uint32_t bar) {
   asm volatile(
-      "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4}], "
-      "[%2];" ::"r"(dst),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(col), "r"(row)
+      "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, "
+      "%5}], [%2];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(0), "r"(row), "r"(blk)
       : "memory");
 }
 
-// The boxes of 64 columns x 32 rows (token tok0 on) at `dst`, lane u taking box u of the segment: `ncol` column blocks
-// from column block c0, `pitch` bytes apart. `row`: the lane's box's row (from seg_row).
-// A box that the prefix ends inside is loaded row by row.
+// A segment of 64 tokens: lane u holds the page of box u, and of box u + 32 where boxes are single rows. Only the page is
+// fetched, a tile before it is used; the arithmetic on it waits until then.
 struct Seg {
-  int row;   // row of the lane's box, or -1: zeros
-  int full;  // rows of it within the prefix
+  int page[2];
 };
-__device__ __forceinline__ Seg seg_row(const PrefixArgs& a, int tok0, int len, int lane) {
-  const int rows = 1 << a.box_shift, tok = tok0 + (lane << a.box_shift);
+__device__ __forceinline__ Seg seg_pages(const PrefixArgs& a, int tok0, int len, int lane) {
   Seg s;
-  s.row = (lane << a.box_shift) < BOX ? row_of(a, tok, len) : -1;
-  s.full = min(rows, len - tok);
+  s.page[0] = a.pages[min(tok0 + (lane << a.box_shift), len - 1) >> a.page_shift];
+  s.page[1] = a.box_shift ? 0 : a.pages[min(tok0 + 32 + lane, len - 1) >> a.page_shift];
   return s;
 }
-__device__ __forceinline__ void load_seg(const PrefixArgs& a, const CUtensorMap* map, const CUtensorMap* map1, Seg s,
-                                         uint32_t dst, int col, uint32_t bar, int lane) {
+// The lane's boxes of the segment: NBLK column blocks from `blk` on to `dst`, where a column block's 64 rows lie together.
+// `map` has boxes of one column block, `wide` of NBLK. A box that the prefix ends inside is loaded row by row.
+template <int NBLK>
+__device__ __forceinline__ void load_seg(const PrefixArgs& a, const CUtensorMap* map, const CUtensorMap* wide,
+                                         const CUtensorMap* map1, const Seg& s, int tok0, int len, uint32_t dst, int blk,
+                                         uint32_t bar, int lane) {
   const int rows = 1 << a.box_shift;
-  if ((lane << a.box_shift) >= BOX) return;
-  dst += (uint32_t)(lane << a.box_shift) * 128u;
-  if (s.row < 0 || s.full == rows) {
-    tma_box(dst, map, col, s.row < 0 ? a.none : s.row, bar);
-  } else {
-    for (int r = 0; r < rows; ++r) tma_box(dst + r * 128u, map1, col, r < s.full ? s.row + r : a.none, bar);
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int off = (lane + 32 * i) << a.box_shift, tok = tok0 + off;
+    if (off >= SEG) break;
+    const bool on = tok < len && s.page[i] >= 0 && s.page[i] < a.page_limit;
+    const int row = on ? (s.page[i] << a.page_shift) + (tok & ((1 << a.page_shift) - 1)) : a.none;
+    const int have = min(rows, len - tok);
+    if (!on || have == rows) {
+      if (rows == SEG) {  // the blocks' rows lie together: one box
+        tma_box(dst, wide, blk, row, bar);
+      } else {
+#pragma unroll
+        for (int n = 0; n < NBLK; ++n) tma_box(dst + (uint32_t)(n * BLK_BYTES + off * 128), map, blk + n, row, bar);
+      }
+    } else {
+      for (int n = 0; n < NBLK; ++n)
+        for (int r = 0; r < rows; ++r)
+          tma_box(dst + (uint32_t)(n * BLK_BYTES + (off + r) * 128), map1, blk + n, r < have ? row + r : a.none, bar);
+    }
   }
 }
 
-// One softmax warp's part of an output: its 32 heads' 256 columns from tensor memory times w0 (zeros without O), plus w1
+// One softmax warp's part of an output: its 32 heads' columns c_lo .. c_lo + 127 from tensor memory times w0 (zeros without O), plus w1
 // times the own rows' output where w1 != 0. 32-column slices go through a shared tile (rows 144 bytes apart: conflict-free
 // 16-byte accesses both ways) so that global accesses are whole row segments. `base`: element offset of the warp's first
 // head, first column in out (and own_out).
 __device__ __forceinline__ void store_out(uint32_t tcol, bool have_o, float w0, float w1, float* tile, const float* own,
-                                          void* out, bool f32, size_t base, int lane) {
+                                          void* out, bool f32, size_t base, int lane, int c_lo) {
   const int c4 = lane & 7;
   const bool join = __any_sync(0xffffffffu, w1 != 0.f);
-  for (int c = 0; c < DVH; c += 32) {
+  for (int c = c_lo; c < c_lo + DVH / 2; c += 32) {
     uint32_t o[32];
     if (have_o) {
       tmem_ld32(tcol + c, o);
@@ -215,12 +246,13 @@ __device__ __forceinline__ void store_out(uint32_t tcol, bool have_o, float w0, 
 
 __global__ void __launch_bounds__(THREADS, 1)
     hs_prefix_kernel(const PrefixArgs a, const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap map,
-                     const __grid_constant__ CUtensorMap map1) {
+                     const __grid_constant__ CUtensorMap map2, const __grid_constant__ CUtensorMap map1) {
   extern __shared__ __align__(1024) uint8_t smem[];
   uint64_t* const bar = reinterpret_cast<uint64_t*>(smem + OFF_BAR);
   volatile int* const abort_flag = reinterpret_cast<volatile int*>(smem + OFF_MISC + 4);
   float* const red = reinterpret_cast<float*>(smem + OFF_RED);
-  const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
+  const int t = threadIdx.x, lane = t & 31;
+  const int warp = __shfl_sync(0xffffffffu, t >> 5, 0);  // the same in all lanes, and known to be
   const uint32_t rank = cluster_rank();
   const int unit = (int)(blockIdx.x >> 1), split = unit / a.batch, b = unit - split * a.batch;
   const unsigned lim = a.wait_limit;
@@ -230,7 +262,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     // one arrival for each softmax warp of the pair
     for (int i = 0; i < 2; ++i) bar_init(bar + B_SFREE + i, 2 * SOFTMAX_WARPS);
     bar_init(bar + B_PFULL, 2 * SOFTMAX_WARPS);
-    for (int i = 0; i < 2; ++i) bar_init(bar + B_MX + i, 2);  // the two warps that hold the same heads
+    for (int i = 0; i < 2; ++i) bar_init(bar + B_MX + i, NSEG);  // the warps that hold the same heads
     *abort_flag = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
@@ -242,171 +274,187 @@ __global__ void __launch_bounds__(THREADS, 1)
   __syncthreads();
   cluster_sync();  // both CTAs' barriers are ready
   tc_fence_after();
-  const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(smem + OFF_MISC);
+  const uint32_t tmem = __shfl_sync(0xffffffffu, *reinterpret_cast<volatile uint32_t*>(smem + OFF_MISC), 0);
   asm volatile("griddepcontrol.wait;" ::: "memory");
 
   const int len = length_of(a);
   const int ntiles = (len + NK - 1) / NK, per = (ntiles + a.nsplit - 1) / a.nsplit;
   const int j0 = min(ntiles, split * per), nt = min(ntiles, j0 + per) - j0;
   const uint32_t lead = peer_addr(bar, 0);  // the first CTA's barriers
-  // test hook: every role that would start a copy or an MMA first waits on a barrier that nothing completes yet
+  // test hook: the roles that would start a copy or an MMA first wait on a barrier that nothing completes
   bool ok = true;
 
   if (warp == MMA_WARP) {
-    if (rank == 0 && lane == 0) {
+    // The whole warp walks the loop, so that the descriptors stay in uniform registers; one lane issues.
+    if (rank == 0) {
       constexpr uint32_t ID_S = idesc_bf16(HEADS, NK, 0, 0), ID_O = idesc_bf16(HEADS, 256, 0, 1);
-      const uint64_t dq = sdesc128(su32(smem + OFF_Q), 0), dk = sdesc128(su32(smem + OFF_K), 0),
-                     dp = sdesc128(su32(smem + OFF_P), 0), dv = sdesc128(su32(smem + OFF_V), SEG_BYTES);
-      ok = !a.stall || bar_wait(bar + B_STALL, 0, abort_flag, lim);
-      if (ok && nt > 0) ok = bar_wait(bar + B_QFULL, 0, abort_flag, lim);
+      const bool leader = elect_one();
+      const uint64_t dq = sdesc128(su32(smem + OFF_Q), 0), dp = sdesc128(su32(smem + OFF_P), 0),
+                     dk = sdesc128(su32(smem + OFF_RING), 0), dv = sdesc128(su32(smem + OFF_RING), BLK_BYTES);
+      int kst = 0, vst = 0;
+      unsigned kph = 0, vph = 0;
+      auto wait = [&](int i, unsigned parity) { return __all_sync(0xffffffffu, bar_wait(bar + i, parity, abort_flag, lim)); };
+      // four MMAs on the next stage: A's step of 32 bytes, B's of `step` (in units of 16), then the stage is free
+      auto four = [&](int st, uint32_t d, uint64_t oa, uint64_t ob, int step, uint32_t id, uint32_t acc) {
+        if (leader) {
+          mma2(d, oa, ob, id, acc);
+          mma2(d, oa + 2, ob + step, id, 1u);
+          mma2(d, oa + 4, ob + 2 * step, id, 1u);
+          mma2(d, oa + 6, ob + 3 * step, id, 1u);
+          commit2(bar + B_EMPTY + st);
+        }
+        __syncwarp();
+      };
+      ok = !a.stall || wait(B_STALL, 0);
+      if (ok && nt > 0) ok = wait(B_QFULL, 0);
       for (int j = 0; j <= nt && ok && nt > 0; ++j) {
         if (j < nt) {
-          const uint32_t d = tmem + TMEM_S + (uint32_t)(j & 1) * KH;
-          if (j >= 2) ok = bar_wait_cluster(bar + B_SFREE + (j & 1), (unsigned)((j >> 1) - 1) & 1u, abort_flag, lim);
+          if (j >= 2) ok = wait(B_SFREE + (j & 1), (unsigned)((j >> 1) - 1) & 1u);
           tc_fence_after();
           for (int c = 0; c < KBLK && ok; ++c) {
-            ok = bar_wait_cluster(bar + B_KFULL + c, (unsigned)j & 1u, abort_flag, lim);
-            if (!ok) break;
-            const uint64_t oa = dq + (uint64_t)(c * (BLK_BYTES >> 4)), ob = dk + (uint64_t)(c * (BLK_BYTES >> 4));
-            mma2(d, oa, ob, ID_S, c != 0 ? 1u : 0u);
-            mma2(d, oa + 2, ob + 2, ID_S, 1u);
-            mma2(d, oa + 4, ob + 4, ID_S, 1u);
-            mma2(d, oa + 6, ob + 6, ID_S, 1u);
-            commit2(bar + B_KEMPTY + c);
+            ok = wait(B_FULL + kst, kph);
+            if (ok) four(kst, tmem + TMEM_S + (uint32_t)(j & 1) * KH, dq + (uint64_t)(c * (BLK_BYTES >> 4)),
+                         dk + (uint64_t)(kst * (STAGE_BYTES >> 4)), 2, ID_S, c != 0 ? 1u : 0u);
+            if (++kst == KST) kst = 0, kph ^= 1u;
           }
           if (!ok) break;
-          commit2(bar + B_SFULL + (j & 1));
+          if (leader) commit2(bar + B_SFULL + (j & 1));
         }
         if (j >= 1) {
-          const int jp = j - 1;
-          ok = bar_wait_cluster(bar + B_PFULL, (unsigned)jp & 1u, abort_flag, lim);
+          ok = wait(B_PFULL, (unsigned)(j - 1) & 1u);
           tc_fence_after();
-          for (int c = 0; c < VCHUNK && ok; ++c) {
-            ok = bar_wait_cluster(bar + B_VFULL + c, (unsigned)jp & 1u, abort_flag, lim);
-            if (!ok) break;
-#pragma unroll
-            for (int k = 0; k < 2; ++k) {
-              // 16 keys: P's block c / 2, 32 bytes a step; V's chunk c, 16 rows a step; two halves of the CTA's columns
-              const uint64_t oa = dp + (uint64_t)((c >> 1) * (BLK_BYTES >> 4) + ((c & 1) * 2 + k) * 2);
-              const uint64_t ob = dv + (uint64_t)(c * (VCHUNK_BYTES >> 4) + k * (16 * 128 >> 4));
-              const uint32_t acc = jp > 0 || c > 0 || k > 0 ? 1u : 0u;
-              mma2(tmem + TMEM_O, oa, ob, ID_O, acc);
-              mma2(tmem + TMEM_O + 128, oa, ob + (uint64_t)(2 * SEG_BYTES >> 4), ID_O, acc);
-            }
-            commit2(bar + B_VEMPTY + c);
+          for (int c = 0; c < VST && ok; ++c) {
+            // 64 keys: block c / 2 of P; 128 of the CTA's value columns, 16 rows a step
+            ok = wait(B_FULL + KST + vst, vph);
+            if (ok) four(KST + vst, tmem + TMEM_O + (uint32_t)(c & 1) * 128, dp + (uint64_t)((c >> 1) * (BLK_BYTES >> 4)),
+                         dv + (uint64_t)((KST + vst) * (STAGE_BYTES >> 4)), 128, ID_O, j > 1 || c > 1 ? 1u : 0u);
+            if (++vst == VRING) vst = 0, vph ^= 1u;
           }
           if (!ok) break;
-          commit2(bar + B_PDONE);
+          if (leader) commit2(bar + B_PDONE);
         }
       }
-      commit2(bar + B_ODONE);  // every MMA has finished
+      __syncwarp();
+      if (leader) commit2(bar + B_ODONE);  // every MMA has finished
     }
     __syncwarp();
-  } else if (warp == K_WARP) {
-    ok = !a.stall || __all_sync(0xffffffffu, bar_wait(bar + B_STALL, 0, abort_flag, lim));
-    if (ok && nt > 0 && lane == 0) {
+  } else if (warp >= LOAD_WARP0) {
+    // ---- the loader of ring slot s: every KST-th K stage or every VRING-th V stage. Each lane that has boxes walks them by
+    //      itself; lane 0 of the first CTA expects both CTAs' bytes. (A stage is full only with every lane's boxes, so no
+    //      lane falls a whole round behind another.)
+    ok = !a.stall || bar_wait(bar + B_STALL, 0, abort_flag, lim);
+    const int s = warp - LOAD_WARP0;
+    const bool is_k = s < KST;
+    if (s == 0 && ok && nt > 0 && lane == 0) {
       if (rank == 0) bar_arrive_expect(bar + B_QFULL, 2 * KBLK * BLK_BYTES);
-      for (int c = 0; c < KBLK; ++c)
-        tma_box(su32(smem + OFF_Q + c * BLK_BYTES), &qmap, 64 * c, b * HEADS + (int)rank * QH, lead + B_QFULL * 8);
+      for (int c = 0; c < KBLK; c += 3)
+        tma_box(su32(smem + OFF_Q + c * BLK_BYTES), &qmap, c, b * HEADS + (int)rank * QH, lead + B_QFULL * 8);
     }
-    Seg next[2];
-    for (int i = 0; i < 2; ++i) next[i] = seg_row(a, j0 * NK + (int)rank * KH + i * BOX, nt > 0 ? len : 0, lane);
-    for (int j = 0; j < nt && ok; ++j) {
-      const Seg cur[2] = {next[0], next[1]};
-      for (int c = 0; c < KBLK; ++c) {
-        if (j > 0) ok = __all_sync(0xffffffffu, bar_wait(bar + B_KEMPTY + c, (unsigned)(j - 1) & 1u, abort_flag, lim));
+    if (nt > 0 && (lane << a.box_shift) < SEG) {
+      const uint32_t dst = su32(smem + OFF_RING + s * STAGE_BYTES), fb = lead + (B_FULL + s) * 8;
+      int c = is_k ? s : s - KST, tok = j0 * NK;  // the stage within its tile, the tile's first token
+      const int end = (j0 + nt) * NK;
+      // a stage's first token: the CTA's half of the keys, or the segment that the V stage belongs to
+      auto first = [&]() { return tok + (is_k ? (int)rank * KH : (c >> 1) * SEG); };
+      Seg p0 = seg_pages(a, first(), len, lane), p1 = seg_pages(a, first() + SEG, len, lane);
+      unsigned ph = 1;  // a barrier that has not completed a phase passes for the parity before its first
+      while (tok < end && ok) {
+        ok = bar_wait(bar + B_EMPTY + s, ph, abort_flag, lim);  // the MMAs that read the slot have finished
         if (!ok) break;
-        if (rank == 0 && lane == 0) bar_arrive_expect(bar + B_KFULL + c, 2 * BLK_BYTES);
-        for (int i = 0; i < 2; ++i)
-          load_seg(a, &map, &map1, cur[i], su32(smem + OFF_K + c * BLK_BYTES + i * SEG_BYTES), 64 * c,
-                   lead + (B_KFULL + c) * 8, lane);
-        if (c == 0 && j + 1 < nt)  // the next tile's rows, looked up a tile ahead
-          for (int i = 0; i < 2; ++i) next[i] = seg_row(a, (j0 + j + 1) * NK + (int)rank * KH + i * BOX, len, lane);
+        ph ^= 1u;
+        if (rank == 0 && lane == 0) bar_arrive_expect(bar + B_FULL + s, 2 * STAGE_BYTES);
+        if (is_k) {
+          load_seg<1>(a, &map, &map, &map1, p0, first(), len, dst, c, fb, lane);
+          load_seg<1>(a, &map, &map, &map1, p1, first() + SEG, len, dst + BLK_BYTES, c, fb, lane);
+          c += KST;
+          if (c >= KBLK) c -= KBLK, tok += NK;
+        } else {
+          load_seg<2>(a, &map, &map2, &map1, p0, first(), len, dst, (int)rank * (DVH / 64) + (c & 1) * 2, fb, lane);
+          c += VRING;
+          if (c >= VST) c -= VST, tok += NK;
+        }
+        p0 = seg_pages(a, first(), len, lane);
+        if (is_k) p1 = seg_pages(a, first() + SEG, len, lane);
       }
     }
-  } else if (warp == V_WARP) {
-    ok = !a.stall || __all_sync(0xffffffffu, bar_wait(bar + B_STALL, 0, abort_flag, lim));
-    Seg next[VCHUNK];
-    for (int i = 0; i < VCHUNK; ++i) next[i] = seg_row(a, j0 * NK + i * BOX, nt > 0 ? len : 0, lane);
-    for (int j = 0; j < nt && ok; ++j) {
-#pragma unroll
-      for (int c = 0; c < VCHUNK; ++c) {
-        if (j > 0) ok = ok && __all_sync(0xffffffffu, bar_wait(bar + B_VEMPTY + c, (unsigned)(j - 1) & 1u, abort_flag, lim));
-        if (!ok) break;
-        if (rank == 0 && lane == 0) bar_arrive_expect(bar + B_VFULL + c, 2 * VCHUNK_BYTES);
-        for (int i = 0; i < DVH / 64; ++i)
-          load_seg(a, &map, &map1, next[c], su32(smem + OFF_V + c * VCHUNK_BYTES + i * SEG_BYTES),
-                   (int)rank * DVH + 64 * i, lead + (B_VFULL + c) * 8, lane);
-        if (j + 1 < nt) next[c] = seg_row(a, (j0 + j + 1) * NK + c * BOX, len, lane);
-      }
-    }
+    __syncwarp();
   } else {
-    // ---- softmax: thread t holds TMEM lane t, head r of this CTA, and the keys of its half of every tile
-    const int r = t & (QH - 1), hf = t >> 6;
-    const uint32_t trow = tmem + ((uint32_t)(warp * 32) << 16);
+    // ---- softmax: a thread holds head r of this CTA and 64 keys of every tile, segment sg
+    const int q = warp & 3, sub = warp >> 2, r = (q & 1) * 32 + lane, hf = q >> 1, sg = hf * 2 + sub;
+    const uint32_t trow = tmem + ((uint32_t)(q * 32) << 16);
     float m_run = -INFINITY, l_run = 0.f;
-    uint64_t mask_next = 0;
-    // value `v` of the other thread of the same head; n counts the exchanges
-    auto other = [&](float v, int n) {
-      float* const share = red + (n & 1) * 128;
-      share[t] = v;
+    // hands `v` to the other three threads of the head; n counts the exchanges
+    auto exchange = [&](float v, int n) {
+      float* const share = red + (n & 1) * NSEG * QH;
+      share[sg * QH + r] = v;
       __syncwarp();
-      if (lane == 0) bar_arrive(bar + B_MX + (warp & 1));
-      ok = __all_sync(0xffffffffu, bar_wait(bar + B_MX + (warp & 1), (unsigned)n & 1u, abort_flag, lim)) && ok;
-      return share[t ^ QH];
+      if (lane == 0) bar_arrive(bar + B_MX + (q & 1));
+      ok = __all_sync(0xffffffffu, bar_wait(bar + B_MX + (q & 1), (unsigned)n & 1u, abort_flag, lim)) && ok;
+      return share + r;
     };
     auto key_mask = [&](int j) {
-      const int tok = (j0 + j) * NK + hf * KH + lane;
+      const int tok = (j0 + j) * NK + sg * SEG + lane;
       const unsigned lo = __ballot_sync(0xffffffffu, row_of(a, tok, len) >= 0);
       const unsigned hi = __ballot_sync(0xffffffffu, row_of(a, tok + 32, len) >= 0);
       return (uint64_t)hi << 32 | lo;
     };
-    if (nt > 0) mask_next = key_mask(0);
+    uint64_t mask_next = nt > 0 ? key_mask(0) : 0;
     for (int j = 0; j < nt; ++j) {
       const uint64_t mask = mask_next;
       ok = __all_sync(0xffffffffu, bar_wait(bar + B_SFULL + (j & 1), (unsigned)(j >> 1) & 1u, abort_flag, lim));
       if (!ok) break;
       tc_fence_after();
       uint32_t sv[2][32];
-      tmem_ld32(trow + TMEM_S + (uint32_t)(j & 1) * KH, sv[0]);
-      tmem_ld32(trow + TMEM_S + (uint32_t)(j & 1) * KH + 32, sv[1]);
+      const uint32_t scol = trow + TMEM_S + (uint32_t)((j & 1) * KH + sub * SEG);
+      tmem_ld32(scol, sv[0]);
+      tmem_ld32(scol + 32, sv[1]);
       if (j + 1 < nt) mask_next = key_mask(j + 1);
       tmem_wait_ld();
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) bar_arrive_peer(lead + (B_SFREE + (j & 1)) * 8);
-      float x[KH];
-      float mb = -INFINITY;
+      if (lane == 0) arrive_lead(lead + (B_SFREE + (j & 1)) * 8);
+      float x[SEG];
+      float mb = -INFINITY, scale = a.scale_log2;
 #pragma unroll
-      for (int i = 0; i < KH; ++i) {
-        const float v = __uint_as_float(sv[i >> 5][i & 31]) * a.scale_log2;
-        x[i] = mask >> i & 1 ? v : -INFINITY;
-        mb = fmaxf(mb, x[i]);
+      for (int i = 0; i < SEG; ++i) x[i] = __uint_as_float(sv[i >> 5][i & 31]);
+      if (!(scale > 0.f)) {  // the maximum is taken before the scale, which then has to be positive
+#pragma unroll
+        for (int i = 0; i < SEG; ++i) x[i] *= scale;
+        scale = 1.f;
       }
-      // the two threads of a head agree on the tile's maximum
-      mb = fmaxf(mb, other(mb, j));
+      if (~mask) {  // some key has no row: the same in all lanes
+#pragma unroll
+        for (int i = 0; i < SEG; ++i) x[i] = mask >> i & 1 ? x[i] : -INFINITY;
+      }
+#pragma unroll
+      for (int i = 0; i < SEG; ++i) mb = fmaxf(mb, x[i]);
+      // the four threads of a head agree on the tile's maximum
+      const float* const share = exchange(mb, j);
       if (!ok) break;
+      mb = scale * fmaxf(fmaxf(share[0], share[QH]), fmaxf(share[2 * QH], share[3 * QH]));
       float m_new = m_run;
       if (mb > -INFINITY && (m_run == -INFINITY || mb > m_run + 8.f)) m_new = mb;
       const bool resc = m_new != m_run && m_run != -INFINITY;
-      const bool any = __any_sync(0xffffffffu, resc);
-      // P's buffer is free, and O holds tiles 0 .. j-1, once the value product of tile j-1 has finished
-      float p[KH];
       const float ref = m_new == -INFINITY ? 0.f : m_new;  // no finite score yet: nothing to subtract, a NaN still shows
-      float sum = 0.f;
+      float sum[4] = {0.f, 0.f, 0.f, 0.f};
+      uint32_t p[SEG / 2];
 #pragma unroll
-      for (int i = 0; i < KH; ++i) {
-        p[i] = ex2_approx(x[i] - ref);
-        sum += p[i];
+      for (int i = 0; i < SEG / 2; ++i) {
+        const float p0 = ex2_approx(fmaf(x[2 * i], scale, -ref)), p1 = ex2_approx(fmaf(x[2 * i + 1], scale, -ref));
+        sum[i & 3] += p0 + p1;
+        const __nv_bfloat162 v = __floats2bfloat162_rn(p0, p1);
+        p[i] = *reinterpret_cast<const uint32_t*>(&v);
       }
+      // P's buffer is free, and O holds tiles 0 .. j-1, once the value product of tile j-1 has finished
       if (j >= 1) {
         ok = __all_sync(0xffffffffu, bar_wait(bar + B_PDONE, (unsigned)(j - 1) & 1u, abort_flag, lim));
         if (!ok) break;
       }
-      if (any) {
+      if (__any_sync(0xffffffffu, resc)) {
+        // each of the two threads with the same lane takes half of its columns
         tc_fence_after();
         const float f = resc ? ex2_approx(m_run - m_new) : 1.f;
-        for (int c = 0; c < DVH; c += 16) {
+        for (int c = sub * (DVH / 2); c < (sub + 1) * (DVH / 2); c += 16) {
           float o[16];
           tmem_ld16(trow + TMEM_O + c, o);
 #pragma unroll
@@ -417,35 +465,31 @@ __global__ void __launch_bounds__(THREADS, 1)
         l_run *= f;
       }
       m_run = m_new;
-      l_run += sum;
-      uint8_t* const prow = smem + OFF_P + hf * BLK_BYTES + r * 128;
+      l_run += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+      uint8_t* const prow = smem + OFF_P + sg * BLK_BYTES + r * 128;
 #pragma unroll
-      for (int c = 0; c < KH / 8; ++c) {
-        uint32_t w[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const __nv_bfloat162 v = __floats2bfloat162_rn(p[8 * c + 2 * i], p[8 * c + 2 * i + 1]);
-          w[i] = *reinterpret_cast<const uint32_t*>(&v);
-        }
-        *reinterpret_cast<uint4*>(prow + ((c ^ (r & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
-      }
+      for (int c = 0; c < SEG / 8; ++c)
+        *reinterpret_cast<uint4*>(prow + ((c ^ (r & 7)) << 4)) = make_uint4(p[4 * c], p[4 * c + 1], p[4 * c + 2], p[4 * c + 3]);
       fence_proxy_async();
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) bar_arrive_peer(lead + B_PFULL * 8);
+      if (lane == 0) arrive_lead(lead + B_PFULL * 8);
     }
     if (ok) ok = __all_sync(0xffffffffu, bar_wait(bar + B_ODONE, 0, abort_flag, lim));
-    if (ok) l_run += other(l_run, nt);
+    if (ok) {
+      const float* const share = exchange(l_run, nt);
+      l_run = (share[0] + share[QH]) + (share[2 * QH] + share[3 * QH]);
+    }
     if (ok) {
       tc_fence_after();
-      float* const tile = reinterpret_cast<float*>(smem + OFF_K) + warp * 32 * TS;
-      const int h0 = (int)rank * QH + (warp & 1) * 32;  // the warp's first head
+      float* const tile = reinterpret_cast<float*>(smem + OFF_RING) + warp * 32 * TS;
+      const int h0 = (int)rank * QH + (q & 1) * 32;  // the warp's first head
       const size_t bh = (size_t)b * HEADS + h0 + lane;
       if (a.nsplit > 1) {
         const size_t sh = (size_t)split * a.batch * HEADS;
         if (nt > 0) store_out(trow + TMEM_O, true, 1.f, 0.f, tile, nullptr, a.part_o, true,
-                              (sh + (size_t)b * HEADS + h0) * DV + hf * DVH, lane);
-        if (hf == 0) a.part_ml[sh + bh] = make_float2(m_run, l_run);
+                              (sh + (size_t)b * HEADS + h0) * DV + hf * DVH, lane, sub * (DVH / 2));
+        if (sg == 0) a.part_ml[sh + bh] = make_float2(m_run, l_run);
       } else {
         const float own = a.own_lse ? a.own_lse[bh] * 1.4426950408889634f : -INFINITY;
         const float mx = fmaxf(l_run != 0.f ? m_run : -INFINITY, own);
@@ -454,11 +498,11 @@ __global__ void __launch_bounds__(THREADS, 1)
         const float wo = own != -INFINITY ? exp2f(own - ref) : 0.f;
         const float total = fmaf(w, l_run, wo);
         const float inv = total != 0.f ? 1.f / total : 0.f;
-        other(0.f, nt + 1);  // both threads of a head have read own_lse, which may be lse itself
+        exchange(0.f, nt + 1);  // all threads of a head have read own_lse, which may be lse itself
         // (without own rows the weight is 0 itself, not 0 times a reciprocal that may be NaN: own_out may be null)
         store_out(trow + TMEM_O, nt > 0, w * inv, wo != 0.f ? wo * inv : 0.f, tile, a.own_out, a.out, a.out_f32 != 0,
-                  ((size_t)b * HEADS + h0) * DV + hf * DVH, lane);
-        if (hf == 0) a.lse[bh] = total != 0.f ? (ref + log2f(total)) * 0.6931471805599453f : -INFINITY;
+                  ((size_t)b * HEADS + h0) * DV + hf * DVH, lane, sub * (DVH / 2));
+        if (sg == 0) a.lse[bh] = total != 0.f ? (ref + log2f(total)) * 0.6931471805599453f : -INFINITY;
       }
     }
   }
@@ -586,11 +630,12 @@ EncodeFn encoder() {
   fn.store(f, std::memory_order_release);
   return f;
 }
-// Rows of 576 bf16 values, boxes of 64 columns x `box` rows, 128-byte swizzle, zeros outside.
-bool make_map(EncodeFn f, CUtensorMap* m, const void* rows, uint64_t count, uint32_t box) {
-  const cuuint64_t dims[2] = {DQK, count}, strides[1] = {ROW_BYTES};
-  const cuuint32_t boxes[2] = {64, box}, steps[2] = {1, 1};
-  return f(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(rows), dims, strides, boxes, steps,
+// Rows of 576 bf16 values as (column, row, 64-column block): boxes of 64 columns x `box` rows x `blocks` blocks, which lie
+// block by block in shared memory, 128-byte swizzle, zeros outside.
+bool make_map(EncodeFn f, CUtensorMap* m, const void* rows, uint64_t count, uint32_t box, uint32_t blocks) {
+  const cuuint64_t dims[3] = {64, count, KBLK}, strides[2] = {ROW_BYTES, 128};
+  const cuuint32_t boxes[3] = {64, box, blocks}, steps[3] = {1, 1, 1};
+  return f(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(rows), dims, strides, boxes, steps,
            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
@@ -628,7 +673,7 @@ extern "C" int hs_mla_prefix(hs_pool* pool, int32_t batch, const void* q, const 
   std::memset(&a, 0, sizeof(a));
   a.pages = prefix->pages;
   while ((1 << a.page_shift) < prefix->page_rows) ++a.page_shift;
-  a.box_shift = std::min(a.page_shift, 5);
+  a.box_shift = std::min(a.page_shift, 6);
   a.max_length = max_length;
   a.page_limit = (int32_t)(prefix->count / prefix->page_rows);
   a.none = (int32_t)prefix->count;
@@ -645,12 +690,13 @@ extern "C" int hs_mla_prefix(hs_pool* pool, int32_t batch, const void* q, const 
   a.lse = lse;
   a.err = pool->err;
   hs_attention_waits(&a.wait_limit, &a.stall);
-  CUtensorMap qmap, map, map1;
+  CUtensorMap qmap, map, map2, map1;
   // an empty pool of rows still needs a map: one row, which page_limit = 0 keeps from being read
   const uint64_t count = std::max<int64_t>(prefix->count, 1);
   a.none = (int32_t)count;
-  if (!make_map(encode, &qmap, q, (uint64_t)batch * HEADS, QH) ||
-      !make_map(encode, &map, prefix->rows, count, 1u << a.box_shift) || !make_map(encode, &map1, prefix->rows, count, 1))
+  if (!make_map(encode, &qmap, q, (uint64_t)batch * HEADS, QH, 3) ||
+      !make_map(encode, &map, prefix->rows, count, 1u << a.box_shift, 1) ||
+      !make_map(encode, &map2, prefix->rows, count, 1u << a.box_shift, 2) || !make_map(encode, &map1, prefix->rows, count, 1, 1))
     return HS_ERR_INVALID_ARG;
 
   cudaLaunchConfig_t cfg = {};
@@ -666,7 +712,7 @@ extern "C" int hs_mla_prefix(hs_pool* pool, int32_t batch, const void* q, const 
   attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  if (cudaLaunchKernelEx(&cfg, hs_prefix_kernel, a, qmap, map, map1) != cudaSuccess) return HS_ERR_CUDA;
+  if (cudaLaunchKernelEx(&cfg, hs_prefix_kernel, a, qmap, map, map2, map1) != cudaSuccess) return HS_ERR_CUDA;
   if (nsplit == 1) return HS_OK;
   cfg.gridDim = dim3((unsigned)batch * HEADS, 1, 1);
   cfg.blockDim = dim3(DV / 4, 1, 1);
