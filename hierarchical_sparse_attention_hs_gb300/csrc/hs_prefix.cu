@@ -23,9 +23,10 @@
 //
 // Warp roles per CTA: 0-7 softmax (warp w: TMEM lanes 32 (w % 4) .. +31, that is head lane % 64 and key half lane / 64,
 // and keys 64 (w / 4) .. +63 of that half), 8 the issuer (the pair's first CTA issues for both), 9-15 the loaders. K and V
-// each pass through a ring of 16 KB stages, four for K and three for V, with a loader for each slot (one thread's wait,
-// expectation and copies of a stage take about 310 cycles one after the other, more than the stage's MMAs): a K stage is 64 columns of the CTA's 128
-// keys, a V stage 128 of its value columns of 64 keys; each feeds four MMAs, 256 cycles. Per tile j the issuer runs
+// pass through one ring of 16 KB stages in the order in which the MMAs read them, with a loader for each slot (one
+// thread's wait, expectation and copies of a stage take about 310 cycles one after the other, more than the stage's MMAs):
+// a K stage is 64 columns of the CTA's 128 keys, a V stage 128 of its value columns of 64 keys; each feeds four MMAs, 256
+// cycles. Per tile j the issuer runs
 // S(j + 1) before O += P(j) V(j), so the softmax of a tile overlaps the value product of the one before and the scores of
 // the one after.
 //
@@ -66,7 +67,7 @@ constexpr int KBLK = DQK / 64;     // 64-column blocks of a row: K stages of a t
 constexpr int VST = NSEG * 2;      // V stages of a tile
 constexpr int BLK_BYTES = 64 * 128;      // 64 rows x 64 columns
 constexpr int STAGE_BYTES = 2 * BLK_BYTES;
-constexpr int KST = 4, VRING = 3, NSTAGE = KST + VRING;  // stages of K's ring, of V's, and of both
+constexpr int NSTAGE = 7;          // stages of the ring
 constexpr int OFF_Q = 0;
 constexpr int OFF_RING = OFF_Q + KBLK * BLK_BYTES;
 constexpr int OFF_P = OFF_RING + NSTAGE * STAGE_BYTES;
@@ -78,6 +79,7 @@ constexpr int B_QFULL = 0, B_FULL = 1, B_EMPTY = B_FULL + NSTAGE, B_SFULL = B_EM
 constexpr int OFF_MISC = OFF_BAR + NBAR * 8;            // tensor-memory address, abort flag
 constexpr int OFF_RED = (OFF_MISC + 8 + 15) & ~15;      // [2 parities][NSEG][QH] floats
 constexpr int SMEM_BYTES = OFF_RED + 2 * NSEG * QH * 4;
+static_assert(NSTAGE <= KBLK, "the ring starts within the first K");
 static_assert(SMEM_BYTES <= 232448, "shared memory per block");
 constexpr int SOFTMAX_WARPS = 8, MMA_WARP = 8, LOAD_WARP0 = 9, THREADS = (LOAD_WARP0 + NSTAGE) * 32;
 constexpr uint32_t TMEM_COLS = 512, TMEM_O = 0, TMEM_S = 256;  // O: 2 x 128 columns; S: two buffers of 128
@@ -291,11 +293,11 @@ __global__ void __launch_bounds__(THREADS, 1)
       const bool leader = elect_one();
       const uint64_t dq = sdesc128(su32(smem + OFF_Q), 0), dp = sdesc128(su32(smem + OFF_P), 0),
                      dk = sdesc128(su32(smem + OFF_RING), 0), dv = sdesc128(su32(smem + OFF_RING), BLK_BYTES);
-      int kst = 0, vst = 0;
-      unsigned kph = 0, vph = 0;
+      int st = 0;
+      unsigned ph = 0;
       auto wait = [&](int i, unsigned parity) { return __all_sync(0xffffffffu, bar_wait(bar + i, parity, abort_flag, lim)); };
       // four MMAs on the next stage: A's step of 32 bytes, B's of `step` (in units of 16), then the stage is free
-      auto four = [&](int st, uint32_t d, uint64_t oa, uint64_t ob, int step, uint32_t id, uint32_t acc) {
+      auto four = [&](uint32_t d, uint64_t oa, uint64_t ob, int step, uint32_t id, uint32_t acc) {
         if (leader) {
           mma2(d, oa, ob, id, acc);
           mma2(d, oa + 2, ob + step, id, 1u);
@@ -304,6 +306,7 @@ __global__ void __launch_bounds__(THREADS, 1)
           commit2(bar + B_EMPTY + st);
         }
         __syncwarp();
+        if (++st == NSTAGE) st = 0, ph ^= 1u;
       };
       ok = !a.stall || wait(B_STALL, 0);
       if (ok && nt > 0) ok = wait(B_QFULL, 0);
@@ -312,10 +315,9 @@ __global__ void __launch_bounds__(THREADS, 1)
           if (j >= 2) ok = wait(B_SFREE + (j & 1), (unsigned)((j >> 1) - 1) & 1u);
           tc_fence_after();
           for (int c = 0; c < KBLK && ok; ++c) {
-            ok = wait(B_FULL + kst, kph);
-            if (ok) four(kst, tmem + TMEM_S + (uint32_t)(j & 1) * KH, dq + (uint64_t)(c * (BLK_BYTES >> 4)),
-                         dk + (uint64_t)(kst * (STAGE_BYTES >> 4)), 2, ID_S, c != 0 ? 1u : 0u);
-            if (++kst == KST) kst = 0, kph ^= 1u;
+            ok = wait(B_FULL + st, ph);
+            if (ok) four(tmem + TMEM_S + (uint32_t)(j & 1) * KH, dq + (uint64_t)(c * (BLK_BYTES >> 4)),
+                         dk + (uint64_t)(st * (STAGE_BYTES >> 4)), 2, ID_S, c != 0 ? 1u : 0u);
           }
           if (!ok) break;
           if (leader) commit2(bar + B_SFULL + (j & 1));
@@ -325,10 +327,9 @@ __global__ void __launch_bounds__(THREADS, 1)
           tc_fence_after();
           for (int c = 0; c < VST && ok; ++c) {
             // 64 keys: block c / 2 of P; 128 of the CTA's value columns, 16 rows a step
-            ok = wait(B_FULL + KST + vst, vph);
-            if (ok) four(KST + vst, tmem + TMEM_O + (uint32_t)(c & 1) * 128, dp + (uint64_t)((c >> 1) * (BLK_BYTES >> 4)),
-                         dv + (uint64_t)((KST + vst) * (STAGE_BYTES >> 4)), 128, ID_O, j > 1 || c > 1 ? 1u : 0u);
-            if (++vst == VRING) vst = 0, vph ^= 1u;
+            ok = wait(B_FULL + st, ph);
+            if (ok) four(tmem + TMEM_O + (uint32_t)(c & 1) * 128, dp + (uint64_t)((c >> 1) * (BLK_BYTES >> 4)),
+                         dv + (uint64_t)(st * (STAGE_BYTES >> 4)), 128, ID_O, j > 1 || c > 1 ? 1u : 0u);
           }
           if (!ok) break;
           if (leader) commit2(bar + B_PDONE);
@@ -339,12 +340,11 @@ __global__ void __launch_bounds__(THREADS, 1)
     }
     __syncwarp();
   } else if (warp >= LOAD_WARP0) {
-    // ---- the loader of ring slot s: every KST-th K stage or every VRING-th V stage. Each lane that has boxes walks them by
-    //      itself; lane 0 of the first CTA expects both CTAs' bytes. (A stage is full only with every lane's boxes, so no
-    //      lane falls a whole round behind another.)
+    // ---- the loader of ring slot s: every NSTAGE-th stage of K(0) K(1) V(0) K(2) V(1) ... K(nt-1) V(nt-2) V(nt-1), the
+    //      order in which the issuer takes them. Each lane that has boxes walks them by itself; lane 0 of the first CTA
+    //      expects both CTAs' bytes. (A stage is full only with every lane's boxes, so no lane falls a round behind.)
     ok = !a.stall || bar_wait(bar + B_STALL, 0, abort_flag, lim);
     const int s = warp - LOAD_WARP0;
-    const bool is_k = s < KST;
     if (s == 0 && ok && nt > 0 && lane == 0) {
       if (rank == 0) bar_arrive_expect(bar + B_QFULL, 2 * KBLK * BLK_BYTES);
       for (int c = 0; c < KBLK; c += 3)
@@ -352,29 +352,38 @@ __global__ void __launch_bounds__(THREADS, 1)
     }
     if (nt > 0 && (lane << a.box_shift) < SEG) {
       const uint32_t dst = su32(smem + OFF_RING + s * STAGE_BYTES), fb = lead + (B_FULL + s) * 8;
-      int c = is_k ? s : s - KST, tok = j0 * NK;  // the stage within its tile, the tile's first token
-      const int end = (j0 + nt) * NK;
+      bool is_k = true;
+      int j = 0, c = s;  // the stage's tile and its place in it
       // a stage's first token: the CTA's half of the keys, or the segment that the V stage belongs to
-      auto first = [&]() { return tok + (is_k ? (int)rank * KH : (c >> 1) * SEG); };
+      auto first = [&]() { return (j0 + j) * NK + (is_k ? (int)rank * KH : (c >> 1) * SEG); };
       Seg p0 = seg_pages(a, first(), len, lane), p1 = seg_pages(a, first() + SEG, len, lane);
       unsigned ph = 1;  // a barrier that has not completed a phase passes for the parity before its first
-      while (tok < end && ok) {
-        ok = bar_wait(bar + B_EMPTY + s, ph, abort_flag, lim);  // the MMAs that read the slot have finished
+      while (j < nt) {
+        ok = ok && bar_wait(bar + B_EMPTY + s, ph, abort_flag, lim);  // the MMAs that read the slot have finished
         if (!ok) break;
         ph ^= 1u;
         if (rank == 0 && lane == 0) bar_arrive_expect(bar + B_FULL + s, 2 * STAGE_BYTES);
         if (is_k) {
           load_seg<1>(a, &map, &map, &map1, p0, first(), len, dst, c, fb, lane);
           load_seg<1>(a, &map, &map, &map1, p1, first() + SEG, len, dst + BLK_BYTES, c, fb, lane);
-          c += KST;
-          if (c >= KBLK) c -= KBLK, tok += NK;
         } else {
           load_seg<2>(a, &map, &map2, &map1, p0, first(), len, dst, (int)rank * (DVH / 64) + (c & 1) * 2, fb, lane);
-          c += VRING;
-          if (c >= VST) c -= VST, tok += NK;
         }
-        p0 = seg_pages(a, first(), len, lane);
-        if (is_k) p1 = seg_pages(a, first() + SEG, len, lane);
+        c += NSTAGE;
+        while (j < nt && c >= (is_k ? KBLK : VST)) {
+          c -= is_k ? KBLK : VST;
+          if (is_k) {
+            if (j == 0 && nt > 1) j = 1;
+            else is_k = false, j = max(j - 1, 0);
+          } else {
+            if (j + 2 < nt) is_k = true, j += 2;
+            else ++j;
+          }
+        }
+        if (j < nt) {
+          p0 = seg_pages(a, first(), len, lane);
+          if (is_k) p1 = seg_pages(a, first() + SEG, len, lane);
+        }
       }
     }
     __syncwarp();
