@@ -86,6 +86,8 @@ constexpr uint32_t TMEM_COLS = 512, TMEM_O = 0, TMEM_S = 256;  // O: 2 x 128 col
 constexpr int TS = 36;             // row stride, in floats, of a softmax warp's output tile
 static_assert(SOFTMAX_WARPS * 32 * TS * 4 <= NSTAGE * STAGE_BYTES, "output tiles fit the ring");
 
+constexpr int JG = 4;              // thread groups of the joining kernel
+
 struct PrefixArgs {
   const int32_t* pages;
   int32_t page_shift, max_length;
@@ -278,6 +280,7 @@ __global__ void __launch_bounds__(THREADS, 1)
   tc_fence_after();
   const uint32_t tmem = __shfl_sync(0xffffffffu, *reinterpret_cast<volatile uint32_t*>(smem + OFF_MISC), 0);
   asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;");  // the joining kernel's blocks may settle in; they wait for the end
 
   const int len = length_of(a);
   const int ntiles = (len + NK - 1) / NK, per = (ntiles + a.nsplit - 1) / a.nsplit;
@@ -529,40 +532,74 @@ __global__ void __launch_bounds__(THREADS, 1)
     asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(TMEM_COLS) : "memory");
 }
 
-// One CTA joins one head of one request: thread t holds outputs 4t .. 4t + 3.
-__global__ void __launch_bounds__(DV / 4) hs_prefix_join_kernel(const PrefixArgs a) {
+// One CTA joins one head of one request: thread t of a group holds outputs 4t .. 4t + 3 of every JG-th split, four loads in
+// flight; the groups' sums meet in shared memory. (One group with a load at a time took 40 us for 74 splits: a chain of
+// latencies.)
+__global__ void __launch_bounds__(JG * DV / 4) hs_prefix_join_kernel(const PrefixArgs a) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;");
-  const int t = threadIdx.x;
+  extern __shared__ float weight[];  // [nsplit], 0 for a split with no row
+  __shared__ float4 part[JG - 1][DV / 4];
+  __shared__ float red[2][JG * DV / 4 / 32];
+  const int t = threadIdx.x & (DV / 4 - 1), g = threadIdx.x / (DV / 4), n = a.nsplit;
   const size_t bh = blockIdx.x, heads = (size_t)a.batch * HEADS;
   const float own = a.own_lse ? a.own_lse[bh] * 1.4426950408889634f : -INFINITY;
+  // the largest maximum, then every split's weight and their total; a split beyond the first 512 has another turn
+  auto over_block = [&](float v, bool sum, int k) {
+    for (int o = 16; o; o >>= 1) {
+      const float w = __shfl_xor_sync(0xffffffffu, v, o);
+      v = sum ? v + w : fmaxf(v, w);
+    }
+    if ((threadIdx.x & 31) == 0) red[k][threadIdx.x >> 5] = v;
+    __syncthreads();
+    v = red[k][0];
+    for (int i = 1; i < JG * DV / 4 / 32; ++i) v = sum ? v + red[k][i] : fmaxf(v, red[k][i]);
+    return v;
+  };
   float mx = own;
-  for (int s = 0; s < a.nsplit; ++s) {
+  for (int s = threadIdx.x; s < n; s += JG * DV / 4) {
     const float2 ml = a.part_ml[(size_t)s * heads + bh];
     if (ml.y != 0.f) mx = fmaxf(mx, ml.x);
   }
+  mx = over_block(mx, false, 0);
   const float ref = mx == -INFINITY ? 0.f : mx;
+  const float wo = own != -INFINITY ? exp2f(own - ref) : 0.f;
+  float total = threadIdx.x == 0 ? wo : 0.f;
+  for (int s = threadIdx.x; s < n; s += JG * DV / 4) {
+    const float2 ml = a.part_ml[(size_t)s * heads + bh];
+    const float w = ml.y != 0.f ? exp2f(ml.x == -INFINITY ? 0.f : ml.x - ref) : 0.f;
+    weight[s] = w;
+    if (ml.y != 0.f) total = fmaf(w, ml.y, total);
+  }
+  total = over_block(total, true, 1);  // (its barrier also publishes the weights)
+  const float inv = total != 0.f ? 1.f / total : 0.f;
   float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-  float total = 0.f;
-  auto add = [&](float w, const float* p) {
-    const float4 v = *reinterpret_cast<const float4*>(p + 4 * t);
+  auto add = [&](float w, float4 v) {
     o.x = fmaf(w, v.x, o.x);
     o.y = fmaf(w, v.y, o.y);
     o.z = fmaf(w, v.z, o.z);
     o.w = fmaf(w, v.w, o.w);
   };
-  if (own != -INFINITY) {
-    total = exp2f(own - ref);
-    add(total, a.own_out + bh * DV);
+  for (int s0 = g; s0 < n; s0 += 4 * JG) {
+    float w[4];
+    float4 v[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const int s = s0 + u * JG;
+      w[u] = s < n ? weight[s] : 0.f;
+      // a split with no row wrote no output
+      if (w[u] != 0.f) v[u] = __ldcs(reinterpret_cast<const float4*>(a.part_o + ((size_t)s * heads + bh) * DV) + t);
+    }
+#pragma unroll
+    for (int u = 0; u < 4; ++u)
+      if (w[u] != 0.f) add(w[u], v[u]);
   }
-  for (int s = 0; s < a.nsplit; ++s) {
-    const float2 ml = a.part_ml[(size_t)s * heads + bh];
-    if (ml.y == 0.f) continue;  // a split with no row
-    const float w = exp2f(ml.x == -INFINITY ? 0.f : ml.x - ref);
-    total = fmaf(w, ml.y, total);
-    add(w, a.part_o + ((size_t)s * heads + bh) * DV);
-  }
-  const float inv = total != 0.f ? 1.f / total : 0.f;
+  if (g == 0 && wo != 0.f) add(wo, *(reinterpret_cast<const float4*>(a.own_out + bh * DV) + t));
+  if (g > 0) part[g - 1][t] = o;
+  __syncthreads();
+  if (g > 0) return;
+#pragma unroll
+  for (int i = 0; i < JG - 1; ++i) add(1.f, part[i][t]);
   o = make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
   if (a.out_f32) {
     reinterpret_cast<float4*>(static_cast<float*>(a.out) + bh * DV)[t] = o;
@@ -571,7 +608,7 @@ __global__ void __launch_bounds__(DV / 4) hs_prefix_join_kernel(const PrefixArgs
     reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.out) + bh * DV)[t] =
         make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
   }
-  __syncthreads();  // own_lse may be lse itself
+  // (every thread has read own_lse, which may be lse itself, before the barriers above)
   if (t == 0) a.lse[bh] = total != 0.f ? (ref + log2f(total)) * 0.6931471805599453f : -INFINITY;
 }
 
@@ -608,14 +645,14 @@ int pairs_resident() {
 }
 
 // The number of splits with the shortest expected time, in tiles: waves of units, each a run of tiles and a fixed cost of
-// about four of them (prologue, Q, epilogue), and for more than one split the join.
+// about three of them (prologue, Q, epilogue), and for more than one split the join.
 int splits_of(int pairs, int32_t batch, int32_t max_length) {
   const int tiles = (max_length + NK - 1) / NK;
   int best = 1;
   double least = 1e30;
   for (int n = 1; n <= std::max(1, std::min(tiles, std::max(1, 4 * pairs / batch))); ++n) {
     const int64_t units = (int64_t)batch * n;
-    const double cost = (double)((units + pairs - 1) / pairs) * ((tiles + n - 1) / n + 4) + (n > 1 ? 3 + 0.08 * units : 0);
+    const double cost = (double)((units + pairs - 1) / pairs) * ((tiles + n - 1) / n + 3) + (n > 1 ? 1.5 + 0.025 * units : 0);
     if (cost < least) least = cost, best = n;
   }
   return best;
@@ -724,8 +761,8 @@ extern "C" int hs_mla_prefix(hs_pool* pool, int32_t batch, const void* q, const 
   if (cudaLaunchKernelEx(&cfg, hs_prefix_kernel, a, qmap, map, map2, map1) != cudaSuccess) return HS_ERR_CUDA;
   if (nsplit == 1) return HS_OK;
   cfg.gridDim = dim3((unsigned)batch * HEADS, 1, 1);
-  cfg.blockDim = dim3(DV / 4, 1, 1);
-  cfg.dynamicSmemBytes = 0;
+  cfg.blockDim = dim3(JG * DV / 4, 1, 1);
+  cfg.dynamicSmemBytes = (size_t)nsplit * sizeof(float);
   cfg.numAttrs = 1;
   return cudaLaunchKernelEx(&cfg, hs_prefix_join_kernel, a) == cudaSuccess ? HS_OK : HS_ERR_CUDA;
 }
