@@ -86,7 +86,7 @@ constexpr uint32_t TMEM_COLS = 512, TMEM_O = 0, TMEM_S = 256;  // O: 2 x 128 col
 constexpr int TS = 36;             // row stride, in floats, of a softmax warp's output tile
 static_assert(SOFTMAX_WARPS * 32 * TS * 4 <= NSTAGE * STAGE_BYTES, "output tiles fit the ring");
 
-constexpr int JG = 4;              // thread groups of the joining kernel
+constexpr int MAX_SPLIT = 128;     // splits of a request
 
 struct PrefixArgs {
   const int32_t* pages;
@@ -532,46 +532,40 @@ __global__ void __launch_bounds__(THREADS, 1)
     asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(TMEM_COLS) : "memory");
 }
 
-// One CTA joins one head of one request: thread t of a group holds outputs 4t .. 4t + 3 of every JG-th split, four loads in
-// flight; the groups' sums meet in shared memory. (One group with a load at a time took 40 us for 74 splits: a chain of
-// latencies.)
-__global__ void __launch_bounds__(JG * DV / 4) hs_prefix_join_kernel(const PrefixArgs a) {
+// One CTA joins one head of one request: thread t of a group of 128 holds outputs 4t .. 4t + 3 of every G-th split, four
+// loads in flight; the groups' sums meet in shared memory. Every warp works the splits' weights out for itself (lane u:
+// splits u, u + 32, ...), so that nothing else waits for the block. Up to 16 splits one group does; more of them are
+// divided over four (a single group walking 74 splits took 40 us for one request: a chain of latencies).
+template <int G>
+__global__ void __launch_bounds__(G * DV / 4) hs_prefix_join_kernel(const PrefixArgs a) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;");
-  extern __shared__ float weight[];  // [nsplit], 0 for a split with no row
-  __shared__ float4 part[JG - 1][DV / 4];
-  __shared__ float red[2][JG * DV / 4 / 32];
-  const int t = threadIdx.x & (DV / 4 - 1), g = threadIdx.x / (DV / 4), n = a.nsplit;
+  __shared__ float4 part[G > 1 ? G - 1 : 1][DV / 4];
+  constexpr int PER = G > 1 ? MAX_SPLIT / 32 : 1;  // splits of a lane
+  const int t = threadIdx.x & (DV / 4 - 1), g = threadIdx.x / (DV / 4), lane = threadIdx.x & 31, n = a.nsplit;
   const size_t bh = blockIdx.x, heads = (size_t)a.batch * HEADS;
   const float own = a.own_lse ? a.own_lse[bh] * 1.4426950408889634f : -INFINITY;
-  // the largest maximum, then every split's weight and their total; a split beyond the first 512 has another turn
-  auto over_block = [&](float v, bool sum, int k) {
-    for (int o = 16; o; o >>= 1) {
-      const float w = __shfl_xor_sync(0xffffffffu, v, o);
-      v = sum ? v + w : fmaxf(v, w);
-    }
-    if ((threadIdx.x & 31) == 0) red[k][threadIdx.x >> 5] = v;
-    __syncthreads();
-    v = red[k][0];
-    for (int i = 1; i < JG * DV / 4 / 32; ++i) v = sum ? v + red[k][i] : fmaxf(v, red[k][i]);
-    return v;
-  };
+  float2 ml[PER];
+#pragma unroll
+  for (int i = 0; i < PER; ++i)
+    ml[i] = lane + 32 * i < n ? a.part_ml[(size_t)(lane + 32 * i) * heads + bh] : make_float2(0.f, 0.f);
   float mx = own;
-  for (int s = threadIdx.x; s < n; s += JG * DV / 4) {
-    const float2 ml = a.part_ml[(size_t)s * heads + bh];
-    if (ml.y != 0.f) mx = fmaxf(mx, ml.x);
-  }
-  mx = over_block(mx, false, 0);
+#pragma unroll
+  for (int i = 0; i < PER; ++i)
+    if (ml[i].y != 0.f) mx = fmaxf(mx, ml[i].x);
+#pragma unroll
+  for (int o = 16; o; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
   const float ref = mx == -INFINITY ? 0.f : mx;
-  const float wo = own != -INFINITY ? exp2f(own - ref) : 0.f;
-  float total = threadIdx.x == 0 ? wo : 0.f;
-  for (int s = threadIdx.x; s < n; s += JG * DV / 4) {
-    const float2 ml = a.part_ml[(size_t)s * heads + bh];
-    const float w = ml.y != 0.f ? exp2f(ml.x == -INFINITY ? 0.f : ml.x - ref) : 0.f;
-    weight[s] = w;
-    if (ml.y != 0.f) total = fmaf(w, ml.y, total);
+  float weight[PER], total = 0.f;
+#pragma unroll
+  for (int i = 0; i < PER; ++i) {  // a split with no row: no weight, and no output to read
+    weight[i] = ml[i].y != 0.f ? exp2f(ml[i].x == -INFINITY ? 0.f : ml[i].x - ref) : 0.f;
+    total += ml[i].y != 0.f ? weight[i] * ml[i].y : 0.f;
   }
-  total = over_block(total, true, 1);  // (its barrier also publishes the weights)
+#pragma unroll
+  for (int o = 16; o; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
+  const float wo = own != -INFINITY ? exp2f(own - ref) : 0.f;
+  total += wo;
   const float inv = total != 0.f ? 1.f / total : 0.f;
   float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
   auto add = [&](float w, float4 v) {
@@ -580,26 +574,29 @@ __global__ void __launch_bounds__(JG * DV / 4) hs_prefix_join_kernel(const Prefi
     o.z = fmaf(w, v.z, o.z);
     o.w = fmaf(w, v.w, o.w);
   };
-  for (int s0 = g; s0 < n; s0 += 4 * JG) {
-    float w[4];
-    float4 v[4];
 #pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      const int s = s0 + u * JG;
-      w[u] = s < n ? weight[s] : 0.f;
-      // a split with no row wrote no output
-      if (w[u] != 0.f) v[u] = __ldcs(reinterpret_cast<const float4*>(a.part_o + ((size_t)s * heads + bh) * DV) + t);
+  for (int i = 0; i < PER; ++i) {
+    for (int s0 = 32 * i + g; s0 < min(n, 32 * i + 32); s0 += 4 * G) {
+      float w[4];
+      float4 v[4];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const int s = s0 + u * G;
+        w[u] = __shfl_sync(0xffffffffu, weight[i], s & 31);
+        if (s >= 32 * i + 32) w[u] = 0.f;
+        if (w[u] != 0.f) v[u] = __ldcs(reinterpret_cast<const float4*>(a.part_o + ((size_t)s * heads + bh) * DV) + t);
+      }
+#pragma unroll
+      for (int u = 0; u < 4; ++u)
+        if (w[u] != 0.f) add(w[u], v[u]);
     }
-#pragma unroll
-    for (int u = 0; u < 4; ++u)
-      if (w[u] != 0.f) add(w[u], v[u]);
   }
   if (g == 0 && wo != 0.f) add(wo, *(reinterpret_cast<const float4*>(a.own_out + bh * DV) + t));
-  if (g > 0) part[g - 1][t] = o;
-  __syncthreads();
+  if (G > 1 && g > 0) part[g - 1][t] = o;
+  __syncthreads();  // (and every thread has read own_lse, which may be lse itself)
   if (g > 0) return;
 #pragma unroll
-  for (int i = 0; i < JG - 1; ++i) add(1.f, part[i][t]);
+  for (int i = 0; i < G - 1; ++i) add(1.f, part[i][t]);
   o = make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
   if (a.out_f32) {
     reinterpret_cast<float4*>(static_cast<float*>(a.out) + bh * DV)[t] = o;
@@ -608,7 +605,6 @@ __global__ void __launch_bounds__(JG * DV / 4) hs_prefix_join_kernel(const Prefi
     reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.out) + bh * DV)[t] =
         make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
   }
-  // (every thread has read own_lse, which may be lse itself, before the barriers above)
   if (t == 0) a.lse[bh] = total != 0.f ? (ref + log2f(total)) * 0.6931471805599453f : -INFINITY;
 }
 
@@ -650,7 +646,7 @@ int splits_of(int pairs, int32_t batch, int32_t max_length) {
   const int tiles = (max_length + NK - 1) / NK;
   int best = 1;
   double least = 1e30;
-  for (int n = 1; n <= std::max(1, std::min(tiles, std::max(1, 4 * pairs / batch))); ++n) {
+  for (int n = 1; n <= std::max(1, std::min({tiles, MAX_SPLIT, std::max(1, 4 * pairs / batch)})); ++n) {
     const int64_t units = (int64_t)batch * n;
     const double cost = (double)((units + pairs - 1) / pairs) * ((tiles + n - 1) / n + 3) + (n > 1 ? 1.5 + 0.025 * units : 0);
     if (cost < least) least = cost, best = n;
@@ -761,8 +757,11 @@ extern "C" int hs_mla_prefix(hs_pool* pool, int32_t batch, const void* q, const 
   if (cudaLaunchKernelEx(&cfg, hs_prefix_kernel, a, qmap, map, map2, map1) != cudaSuccess) return HS_ERR_CUDA;
   if (nsplit == 1) return HS_OK;
   cfg.gridDim = dim3((unsigned)batch * HEADS, 1, 1);
-  cfg.blockDim = dim3(JG * DV / 4, 1, 1);
-  cfg.dynamicSmemBytes = (size_t)nsplit * sizeof(float);
+  cfg.dynamicSmemBytes = 0;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, hs_prefix_join_kernel, a) == cudaSuccess ? HS_OK : HS_ERR_CUDA;
+  const int groups = nsplit <= 16 ? 1 : 4;
+  cfg.blockDim = dim3((unsigned)groups * DV / 4, 1, 1);
+  const cudaError_t e = groups == 1 ? cudaLaunchKernelEx(&cfg, hs_prefix_join_kernel<1>, a)
+                                    : cudaLaunchKernelEx(&cfg, hs_prefix_join_kernel<4>, a);
+  return e == cudaSuccess ? HS_OK : HS_ERR_CUDA;
 }

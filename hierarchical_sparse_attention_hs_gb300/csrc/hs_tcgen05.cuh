@@ -8,8 +8,17 @@
 
 namespace hs {
 
-constexpr unsigned WAIT_LIMIT = 1u << 20;  // try_wait rounds (each may suspend briefly) before a wait gives up
+// A wait gives up after this many try_wait rounds, or once it has lasted WAIT_NS: a round may suspend its thread for as
+// long as the system likes (2^20 rounds that failed took more than 90 s), and the form of try_wait that takes a time limit
+// of its own made the attention over a shared prefix 6 % slower, whatever the limit.
+constexpr unsigned WAIT_LIMIT = 1u << 20;
+constexpr uint64_t WAIT_NS = 2000000000ull;
 
+__device__ __forceinline__ uint64_t now_ns() {
+  uint64_t t;
+  asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
+  return t;
+}
 __device__ __forceinline__ uint32_t su32(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
 
 __device__ __forceinline__ int32_t ld_fresh(const int32_t* p) {
@@ -46,11 +55,13 @@ __device__ __forceinline__ bool bar_poll(uint64_t* b, unsigned parity) {
       : "memory");
   return ok != 0;
 }
-// Wait for the phase of the given parity; false once the abort flag is set or after `limit` rounds (which sets
-// it).
+// Wait for the phase of the given parity; false once the abort flag is set, or after `limit` rounds or WAIT_NS (which
+// set it).
 __device__ __forceinline__ bool bar_wait(uint64_t* b, unsigned parity, volatile int* abort_flag,
                                          unsigned limit = WAIT_LIMIT) {
-  for (unsigned it = 0; it < limit; ++it) {
+  if (bar_test(b, parity)) return true;
+  const uint64_t t0 = now_ns();
+  for (unsigned it = 1; it < limit && now_ns() - t0 < WAIT_NS; ++it) {
     if (bar_test(b, parity)) return true;
     if (*abort_flag) return false;
   }
@@ -80,7 +91,8 @@ __device__ __forceinline__ void bar_arrive_peer(uint32_t addr) {
 // a wait whose arrivals come from the peer (cluster-scope acquire makes its stores visible)
 __device__ __forceinline__ bool bar_wait_cluster(uint64_t* b, unsigned parity, volatile int* abort_flag,
                                                  unsigned limit) {
-  for (unsigned it = 0; it < limit; ++it) {
+  const uint64_t t0 = now_ns();
+  for (unsigned it = 0; it < limit && now_ns() - t0 < WAIT_NS; ++it) {
     uint32_t ok;
     asm volatile(
         "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
