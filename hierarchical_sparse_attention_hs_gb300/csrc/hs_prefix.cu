@@ -72,19 +72,18 @@ constexpr int OFF_Q = 0;
 constexpr int OFF_RING = OFF_Q + KBLK * BLK_BYTES;
 constexpr int OFF_P = OFF_RING + NSTAGE * STAGE_BYTES;
 constexpr int OFF_BAR = OFF_P + NSEG * BLK_BYTES;
-// mbarriers: qfull full[7] empty[7] sfull[2] sfree[2] pfull pdone odone stall mx[2]
-constexpr int B_QFULL = 0, B_FULL = 1, B_EMPTY = B_FULL + NSTAGE, B_SFULL = B_EMPTY + NSTAGE, B_SFREE = B_SFULL + 2,
-              B_PFULL = B_SFREE + 2, B_PDONE = B_PFULL + 1, B_ODONE = B_PDONE + 1, B_STALL = B_ODONE + 1,
-              B_MX = B_STALL + 1, NBAR = B_MX + 2;
+// mbarriers: qfull full[7] empty[7] sfull[2] sfree[2] pfull pdone drain stall mx[2]
+constexpr int B_QFULL = 0, B_FULL = 1, B_EMPTY = B_FULL + NSTAGE, B_SFULL = B_EMPTY + NSTAGE,
+              B_SFREE = B_SFULL + 2, B_PFULL = B_SFREE + 2, B_PDONE = B_PFULL + 1, B_DRAIN = B_PDONE + 1,
+              B_STALL = B_DRAIN + 1, B_MX = B_STALL + 1, NBAR = B_MX + 2;
 constexpr int OFF_MISC = OFF_BAR + NBAR * 8;            // tensor-memory address, abort flag
 constexpr int OFF_RED = (OFF_MISC + 8 + 15) & ~15;      // [2 parities][NSEG][QH] floats
 constexpr int SMEM_BYTES = OFF_RED + 2 * NSEG * QH * 4;
 static_assert(NSTAGE <= KBLK, "the ring starts within the first K");
 static_assert(SMEM_BYTES <= 232448, "shared memory per block");
 constexpr int SOFTMAX_WARPS = 8, MMA_WARP = 8, LOAD_WARP0 = 9, THREADS = (LOAD_WARP0 + NSTAGE) * 32;
+static_assert(THREADS <= 512, "128 registers a thread");
 constexpr uint32_t TMEM_COLS = 512, TMEM_O = 0, TMEM_S = 256;  // O: 2 x 128 columns; S: two buffers of 128
-constexpr int TS = 36;             // row stride, in floats, of a softmax warp's output tile
-static_assert(SOFTMAX_WARPS * 32 * TS * 4 <= NSTAGE * STAGE_BYTES, "output tiles fit the ring");
 
 constexpr int MAX_SPLIT = 128;     // splits of a request
 
@@ -96,9 +95,12 @@ struct PrefixArgs {
   int32_t none;           // a row coordinate behind the last row
   const int32_t* length;  // or nullptr: max_length
   float scale_log2;
-  int32_t batch, nsplit;
-  float* part_o;          // [nsplit][batch][HEADS][DV]
-  float2* part_ml;        // [nsplit][batch][HEADS]: (m, l)
+  int32_t batch;
+  int32_t whole;          // requests 0 .. whole - 1 are one unit each; the others are cut into nsplit units
+  int32_t nsplit;
+  int32_t units;
+  float* part_o;          // [nsplit][batch - whole][HEADS][DV]
+  float2* part_ml;        // [nsplit][batch - whole][HEADS]: (m, l)
   const float* own_out;
   const float* own_lse;
   void* out;
@@ -112,6 +114,41 @@ struct PrefixArgs {
 __device__ __forceinline__ int length_of(const PrefixArgs& a) {
   return a.length ? min(max(ld_fresh(a.length), 0), a.max_length) : a.max_length;
 }
+// The prefix's tiles: all of them, and how they are dealt out over the splits: `per` each, one more for the first `more`.
+struct Tiles {
+  int n, per, more;
+};
+// A pair's walk over its units (every pairs-th) and their tiles: the same sequence in every role. (Nothing is divided here:
+// with divisions in its walks the kernel took a quarter longer, though they would run once a unit.)
+struct Walk {
+  int u, b, split;  // unit, its request, its split (-1: the request is whole)
+  int j0, nt, j;    // the unit's first tile, its tiles, and the tile within it
+  __device__ __forceinline__ void set(const PrefixArgs& a, int unit, const Tiles& t) {
+    u = b = unit;
+    split = -1;
+    j = j0 = 0;
+    nt = t.n;
+    if (u >= a.whole && u < a.units) {
+      for (split = 0; b >= a.batch; ++split) b -= a.batch - a.whole;
+      nt = t.per + (split < t.more ? 1 : 0);
+      j0 = split * t.per + min(split, t.more);
+    }
+  }
+  // the first unit from u on that has tiles; false behind the last
+  __device__ __forceinline__ bool settle(const PrefixArgs& a, const Tiles& t) {
+    while (u < a.units && nt == 0) set(a, u + (int)(gridDim.x >> 1), t);
+    return u < a.units;
+  }
+  __device__ __forceinline__ bool start(const PrefixArgs& a, const Tiles& t) {
+    set(a, (int)(blockIdx.x >> 1), t);
+    return settle(a, t);
+  }
+  __device__ __forceinline__ bool next(const PrefixArgs& a, const Tiles& t) {
+    if (++j < nt) return true;
+    set(a, u + (int)(gridDim.x >> 1), t);
+    return settle(a, t);
+  }
+};
 // Row of token `tok`, or -1.
 __device__ __forceinline__ int row_of(const PrefixArgs& a, int tok, int len) {
   if (tok >= len) return -1;
@@ -201,14 +238,15 @@ __device__ __forceinline__ void load_seg(const PrefixArgs& a, const CUtensorMap*
   }
 }
 
-// One softmax warp's part of an output: its 32 heads' columns c_lo .. c_lo + 127 from tensor memory times w0 (zeros without O), plus w1
-// times the own rows' output where w1 != 0. 32-column slices go through a shared tile (rows 144 bytes apart: conflict-free
-// 16-byte accesses both ways) so that global accesses are whole row segments. `base`: element offset of the warp's first
-// head, first column in out (and own_out).
+// One softmax warp's part of an output: its 32 heads' columns c_lo .. c_lo + 127 from tensor memory times w0 (zeros
+// without O), plus w1 times the own rows' output where w1 != 0. 32-column slices go through a shared tile of 32 rows of 128
+// bytes (16-byte chunk k of row r at k ^ (r % 8): no conflicts either way) so that global accesses are whole row segments.
+// `base`: element offset of the warp's first head, first column in out (and own).
 __device__ __forceinline__ void store_out(uint32_t tcol, bool have_o, float w0, float w1, float* tile, const float* own,
                                           void* out, bool f32, size_t base, int lane, int c_lo) {
   const int c4 = lane & 7;
   const bool join = __any_sync(0xffffffffu, w1 != 0.f);
+#pragma unroll 1
   for (int c = c_lo; c < c_lo + DVH / 2; c += 32) {
     uint32_t o[32];
     if (have_o) {
@@ -218,24 +256,26 @@ __device__ __forceinline__ void store_out(uint32_t tcol, bool have_o, float w0, 
 #pragma unroll
       for (int i = 0; i < 32; ++i) o[i] = 0;
     }
+    float4 p[8];
+    if (join) {
+#pragma unroll
+      for (int r = 0; r < 8; ++r)
+        if (__shfl_sync(0xffffffffu, w1, 4 * r + (lane >> 3)) != 0.f)
+          p[r] = *reinterpret_cast<const float4*>(own + base + (size_t)(4 * r + (lane >> 3)) * DV + c + 4 * c4);
+    }
 #pragma unroll
     for (int i = 0; i < 8; ++i)
-      *reinterpret_cast<float4*>(tile + lane * TS + 4 * i) =
+      *reinterpret_cast<float4*>(tile + lane * 32 + ((i ^ (lane & 7)) << 2)) =
           make_float4(__uint_as_float(o[4 * i]) * w0, __uint_as_float(o[4 * i + 1]) * w0,
                       __uint_as_float(o[4 * i + 2]) * w0, __uint_as_float(o[4 * i + 3]) * w0);
     __syncwarp();
 #pragma unroll
     for (int r = 0; r < 8; ++r) {
       const int h = 4 * r + (lane >> 3);
-      float4 v = *reinterpret_cast<const float4*>(tile + h * TS + 4 * c4);
+      float4 v = *reinterpret_cast<const float4*>(tile + h * 32 + ((c4 ^ (h & 7)) << 2));
       const size_t at = base + (size_t)h * DV + c + 4 * c4;
-      if (join) {
-        const float w = __shfl_sync(0xffffffffu, w1, h);
-        if (w != 0.f) {
-          const float4 p = *reinterpret_cast<const float4*>(own + at);
-          v = make_float4(fmaf(w, p.x, v.x), fmaf(w, p.y, v.y), fmaf(w, p.z, v.z), fmaf(w, p.w, v.w));
-        }
-      }
+      const float w = join ? __shfl_sync(0xffffffffu, w1, h) : 0.f;
+      if (w != 0.f) v = make_float4(fmaf(w, p[r].x, v.x), fmaf(w, p[r].y, v.y), fmaf(w, p[r].z, v.z), fmaf(w, p[r].w, v.w));
       if (f32) {
         *reinterpret_cast<float4*>(static_cast<float*>(out) + at) = v;
       } else {
@@ -258,7 +298,6 @@ __global__ void __launch_bounds__(THREADS, 1)
   const int t = threadIdx.x, lane = t & 31;
   const int warp = __shfl_sync(0xffffffffu, t >> 5, 0);  // the same in all lanes, and known to be
   const uint32_t rank = cluster_rank();
-  const int unit = (int)(blockIdx.x >> 1), split = unit / a.batch, b = unit - split * a.batch;
   const unsigned lim = a.wait_limit;
 
   if (t == 0) {
@@ -283,14 +322,18 @@ __global__ void __launch_bounds__(THREADS, 1)
   asm volatile("griddepcontrol.launch_dependents;");  // the joining kernel's blocks may settle in; they wait for the end
 
   const int len = length_of(a);
-  const int ntiles = (len + NK - 1) / NK, per = (ntiles + a.nsplit - 1) / a.nsplit;
-  const int j0 = min(ntiles, split * per), nt = min(ntiles, j0 + per) - j0;
+  Tiles tiles;
+  tiles.n = (len + NK - 1) / NK;
+  tiles.per = tiles.n / a.nsplit;
+  tiles.more = tiles.n - tiles.per * a.nsplit;
   const uint32_t lead = peer_addr(bar, 0);  // the first CTA's barriers
   // test hook: the roles that would start a copy or an MMA first wait on a barrier that nothing completes
   bool ok = true;
+  Walk w;
 
   if (warp == MMA_WARP) {
-    // The whole warp walks the loop, so that the descriptors stay in uniform registers; one lane issues.
+    // ---- the issuer, of the pair's first CTA. The whole warp walks the loop, so that the descriptors stay in uniform
+    //      registers; one lane issues. Tile g of the pair's walk: scores of tile g, then the value product of tile g - 1.
     if (rank == 0) {
       constexpr uint32_t ID_S = idesc_bf16(HEADS, NK, 0, 0), ID_O = idesc_bf16(HEADS, 256, 0, 1);
       const bool leader = elect_one();
@@ -312,59 +355,81 @@ __global__ void __launch_bounds__(THREADS, 1)
         if (++st == NSTAGE) st = 0, ph ^= 1u;
       };
       ok = !a.stall || wait(B_STALL, 0);
-      if (ok && nt > 0) ok = wait(B_QFULL, 0);
-      for (int j = 0; j <= nt && ok && nt > 0; ++j) {
-        if (j < nt) {
-          if (j >= 2) ok = wait(B_SFREE + (j & 1), (unsigned)((j >> 1) - 1) & 1u);
+      bool more = w.start(a, tiles), pending = false, pending_first = false;
+      int g = 0, nq = 0;  // tiles whose scores have been issued, and units
+      while ((more || pending) && ok) {
+        const bool first = w.j == 0;
+        if (more) {
+          if (first) ok = wait(B_QFULL, (unsigned)nq++ & 1u);
+          if (g >= 2) ok = ok && wait(B_SFREE + (g & 1), (unsigned)((g >> 1) - 1) & 1u);
           tc_fence_after();
           for (int c = 0; c < KBLK && ok; ++c) {
             ok = wait(B_FULL + st, ph);
-            if (ok) four(tmem + TMEM_S + (uint32_t)(j & 1) * KH, dq + (uint64_t)(c * (BLK_BYTES >> 4)),
+            if (ok) four(tmem + TMEM_S + (uint32_t)(g & 1) * KH, dq + (uint64_t)(c * (BLK_BYTES >> 4)),
                          dk + (uint64_t)(st * (STAGE_BYTES >> 4)), 2, ID_S, c != 0 ? 1u : 0u);
           }
           if (!ok) break;
-          if (leader) commit2(bar + B_SFULL + (j & 1));
+          if (leader) commit2(bar + B_SFULL + (g & 1));
         }
-        if (j >= 1) {
-          ok = wait(B_PFULL, (unsigned)(j - 1) & 1u);
+        if (pending) {
+          // P of a unit's first tile comes after the softmax warps have stored the unit before, so O is free too
+          ok = wait(B_PFULL, (unsigned)(g - 1) & 1u);
           tc_fence_after();
           for (int c = 0; c < VST && ok; ++c) {
             // 64 keys: block c / 2 of P; 128 of the CTA's value columns, 16 rows a step
             ok = wait(B_FULL + st, ph);
             if (ok) four(tmem + TMEM_O + (uint32_t)(c & 1) * 128, dp + (uint64_t)((c >> 1) * (BLK_BYTES >> 4)),
-                         dv + (uint64_t)(st * (STAGE_BYTES >> 4)), 128, ID_O, j > 1 || c > 1 ? 1u : 0u);
+                         dv + (uint64_t)(st * (STAGE_BYTES >> 4)), 128, ID_O, !pending_first || c > 1 ? 1u : 0u);
           }
           if (!ok) break;
           if (leader) commit2(bar + B_PDONE);
         }
+        pending = more;
+        if (more) {
+          pending_first = first;
+          ++g;
+          more = w.next(a, tiles);
+        }
       }
       __syncwarp();
-      if (leader) commit2(bar + B_ODONE);  // every MMA has finished
+      if (leader) commit2(bar + B_DRAIN);
     }
     __syncwarp();
   } else if (warp >= LOAD_WARP0) {
-    // ---- the loader of ring slot s: every NSTAGE-th stage of K(0) K(1) V(0) K(2) V(1) ... K(nt-1) V(nt-2) V(nt-1), the
-    //      order in which the issuer takes them. Each lane that has boxes walks them by itself; lane 0 of the first CTA
-    //      expects both CTAs' bytes. (A stage is full only with every lane's boxes, so no lane falls a round behind.)
+    // ---- the loader of ring slot s: every NSTAGE-th stage of K(0) K(1) V(0) K(2) V(1) ... over the tiles of the pair's
+    //      walk, the order in which the issuer takes them. Each lane that has boxes walks them by itself; lane 0 of the
+    //      first CTA expects both CTAs' bytes. (A stage is full only with every lane's boxes, so no lane falls a round
+    //      behind.)
     ok = !a.stall || bar_wait(bar + B_STALL, 0, abort_flag, lim);
     const int s = warp - LOAD_WARP0;
-    if (s == 0 && ok && nt > 0 && lane == 0) {
-      if (rank == 0) bar_arrive_expect(bar + B_QFULL, 2 * KBLK * BLK_BYTES);
-      for (int c = 0; c < KBLK; c += 3)
-        tma_box(su32(smem + OFF_Q + c * BLK_BYTES), &qmap, c, b * HEADS + (int)rank * QH, lead + B_QFULL * 8);
-    }
-    if (nt > 0 && (lane << a.box_shift) < SEG) {
+    if ((lane << a.box_shift) < SEG && ok) {
       const uint32_t dst = su32(smem + OFF_RING + s * STAGE_BYTES), fb = lead + (B_FULL + s) * 8;
-      bool is_k = true;
-      int j = 0, c = s;  // the stage's tile and its place in it
+      Walk v;  // w: the tile whose K is next, v: whose V is
+      bool kmore = w.start(a, tiles), vmore = v.start(a, tiles), is_k = true, head = true;
+      int c = s;  // the stage's place in its tile's K or V
+      // Q of the unit of `x`, and its own rows' output on its way into L2
+      auto load_q = [&](const Walk& x) {
+        if (lane != 0) return;
+        const int row = x.b * HEADS + (int)rank * QH;
+        if (rank == 0) bar_arrive_expect(bar + B_QFULL, 2 * KBLK * BLK_BYTES);
+        for (int i = 0; i < KBLK; i += 3) tma_box(su32(smem + OFF_Q + i * BLK_BYTES), &qmap, i, row, lead + B_QFULL * 8);
+        if (x.split < 0 && a.own_out)
+          asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(a.own_out + (size_t)row * DV), "r"(QH * DV * 4)
+                       : "memory");
+      };
+      bool q_next = s == 0 && kmore;  // Q is this loader's to load, once its slot is free
       // a stage's first token: the CTA's half of the keys, or the segment that the V stage belongs to
-      auto first = [&]() { return (j0 + j) * NK + (is_k ? (int)rank * KH : (c >> 1) * SEG); };
-      Seg p0 = seg_pages(a, first(), len, lane), p1 = seg_pages(a, first() + SEG, len, lane);
+      auto first = [&]() { return is_k ? (w.j0 + w.j) * NK + (int)rank * KH : (v.j0 + v.j) * NK + (c >> 1) * SEG; };
+      Seg p0 = {}, p1 = {};
+      if (kmore) p0 = seg_pages(a, first(), len, lane), p1 = seg_pages(a, first() + SEG, len, lane);
       unsigned ph = 1;  // a barrier that has not completed a phase passes for the parity before its first
-      while (j < nt) {
-        ok = ok && bar_wait(bar + B_EMPTY + s, ph, abort_flag, lim);  // the MMAs that read the slot have finished
+      while (vmore) {
+        ok = bar_wait(bar + B_EMPTY + s, ph, abort_flag, lim);  // the MMAs that read the slot have finished
         if (!ok) break;
         ph ^= 1u;
+        if (q_next) load_q(w);
+        // the slot of a unit's last K stage is free when the unit's last scores have been taken, and so is Q
+        q_next = is_k && c == KBLK - 1 && w.j + 1 == w.nt;
         if (rank == 0 && lane == 0) bar_arrive_expect(bar + B_FULL + s, 2 * STAGE_BYTES);
         if (is_k) {
           load_seg<1>(a, &map, &map, &map1, p0, first(), len, dst, c, fb, lane);
@@ -373,17 +438,20 @@ __global__ void __launch_bounds__(THREADS, 1)
           load_seg<2>(a, &map, &map2, &map1, p0, first(), len, dst, (int)rank * (DVH / 64) + (c & 1) * 2, fb, lane);
         }
         c += NSTAGE;
-        while (j < nt && c >= (is_k ? KBLK : VST)) {
-          c -= is_k ? KBLK : VST;
+        while (vmore && c >= (is_k ? KBLK : VST)) {
           if (is_k) {
-            if (j == 0 && nt > 1) j = 1;
-            else is_k = false, j = max(j - 1, 0);
+            c -= KBLK;
+            kmore = w.next(a, tiles);
+            q_next = q_next && kmore;
+            is_k = head && kmore;
+            head = false;
           } else {
-            if (j + 2 < nt) is_k = true, j += 2;
-            else ++j;
+            c -= VST;
+            vmore = v.next(a, tiles);
+            is_k = kmore;
           }
         }
-        if (j < nt) {
+        if (vmore) {
           p0 = seg_pages(a, first(), len, lane);
           if (is_k) p1 = seg_pages(a, first() + SEG, len, lane);
         }
@@ -394,137 +462,172 @@ __global__ void __launch_bounds__(THREADS, 1)
     // ---- softmax: a thread holds head r of this CTA and 64 keys of every tile, segment sg
     const int q = warp & 3, sub = warp >> 2, r = (q & 1) * 32 + lane, hf = q >> 1, sg = hf * 2 + sub;
     const uint32_t trow = tmem + ((uint32_t)(q * 32) << 16);
+    uint8_t* const prows = smem + OFF_P + sg * BLK_BYTES + (q & 1) * 32 * 128;  // the warp's 32 rows of P
     float m_run = -INFINITY, l_run = 0.f;
-    // hands `v` to the other three threads of the head; n counts the exchanges
-    auto exchange = [&](float v, int n) {
-      float* const share = red + (n & 1) * NSEG * QH;
+    int nx = 0;  // exchanges
+    // hands `v` to the other three threads of the head
+    auto exchange = [&](float v) {
+      float* const share = red + (nx & 1) * NSEG * QH;
       share[sg * QH + r] = v;
       __syncwarp();
       if (lane == 0) bar_arrive(bar + B_MX + (q & 1));
-      ok = __all_sync(0xffffffffu, bar_wait(bar + B_MX + (q & 1), (unsigned)n & 1u, abort_flag, lim)) && ok;
+      ok = __all_sync(0xffffffffu, bar_wait(bar + B_MX + (q & 1), (unsigned)nx & 1u, abort_flag, lim)) && ok;
+      ++nx;
       return share + r;
     };
-    auto key_mask = [&](int j) {
-      const int tok = (j0 + j) * NK + sg * SEG + lane;
+    auto key_mask = [&](int tile) {
+      const int tok = tile * NK + sg * SEG + lane;
       const unsigned lo = __ballot_sync(0xffffffffu, row_of(a, tok, len) >= 0);
       const unsigned hi = __ballot_sync(0xffffffffu, row_of(a, tok + 32, len) >= 0);
       return (uint64_t)hi << 32 | lo;
     };
-    uint64_t mask_next = nt > 0 ? key_mask(0) : 0;
-    for (int j = 0; j < nt; ++j) {
-      const uint64_t mask = mask_next;
-      ok = __all_sync(0xffffffffu, bar_wait(bar + B_SFULL + (j & 1), (unsigned)(j >> 1) & 1u, abort_flag, lim));
-      if (!ok) break;
-      tc_fence_after();
-      uint32_t sv[2][32];
-      const uint32_t scol = trow + TMEM_S + (uint32_t)((j & 1) * KH + sub * SEG);
-      tmem_ld32(scol, sv[0]);
-      tmem_ld32(scol + 32, sv[1]);
-      if (j + 1 < nt) mask_next = key_mask(j + 1);
-      tmem_wait_ld();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) arrive_lead(lead + (B_SFREE + (j & 1)) * 8);
-      float x[SEG];
-      float mb = -INFINITY, scale = a.scale_log2;
-#pragma unroll
-      for (int i = 0; i < SEG; ++i) x[i] = __uint_as_float(sv[i >> 5][i & 31]);
-      if (!(scale > 0.f)) {  // the maximum is taken before the scale, which then has to be positive
-#pragma unroll
-        for (int i = 0; i < SEG; ++i) x[i] *= scale;
-        scale = 1.f;
-      }
-      if (~mask) {  // some key has no row: the same in all lanes
-#pragma unroll
-        for (int i = 0; i < SEG; ++i) x[i] = mask >> i & 1 ? x[i] : -INFINITY;
-      }
-#pragma unroll
-      for (int i = 0; i < SEG; ++i) mb = fmaxf(mb, x[i]);
-      // the four threads of a head agree on the tile's maximum
-      const float* const share = exchange(mb, j);
-      if (!ok) break;
-      mb = scale * fmaxf(fmaxf(share[0], share[QH]), fmaxf(share[2 * QH], share[3 * QH]));
-      float m_new = m_run;
-      if (mb > -INFINITY && (m_run == -INFINITY || mb > m_run + 8.f)) m_new = mb;
-      const bool resc = m_new != m_run && m_run != -INFINITY;
-      const float ref = m_new == -INFINITY ? 0.f : m_new;  // no finite score yet: nothing to subtract, a NaN still shows
-      float sum[4] = {0.f, 0.f, 0.f, 0.f};
-      uint32_t p[SEG / 2];
-#pragma unroll
-      for (int i = 0; i < SEG / 2; ++i) {
-        const float p0 = ex2_approx(fmaf(x[2 * i], scale, -ref)), p1 = ex2_approx(fmaf(x[2 * i + 1], scale, -ref));
-        sum[i & 3] += p0 + p1;
-        const __nv_bfloat162 v = __floats2bfloat162_rn(p0, p1);
-        p[i] = *reinterpret_cast<const uint32_t*>(&v);
-      }
-      // P's buffer is free, and O holds tiles 0 .. j-1, once the value product of tile j-1 has finished
-      if (j >= 1) {
-        ok = __all_sync(0xffffffffu, bar_wait(bar + B_PDONE, (unsigned)(j - 1) & 1u, abort_flag, lim));
-        if (!ok) break;
-      }
-      if (__any_sync(0xffffffffu, resc)) {
-        // each of the two threads with the same lane takes half of its columns
-        tc_fence_after();
-        const float f = resc ? ex2_approx(m_run - m_new) : 1.f;
-        for (int c = sub * (DVH / 2); c < (sub + 1) * (DVH / 2); c += 16) {
-          float o[16];
-          tmem_ld16(trow + TMEM_O + c, o);
-#pragma unroll
-          for (int i = 0; i < 16; ++i) o[i] *= f;
-          tmem_st16(trow + TMEM_O + c, o);
-        }
-        tmem_wait_st();
-        l_run *= f;
-      }
-      m_run = m_new;
-      l_run += (sum[0] + sum[1]) + (sum[2] + sum[3]);
-      uint8_t* const prow = smem + OFF_P + sg * BLK_BYTES + r * 128;
-#pragma unroll
-      for (int c = 0; c < SEG / 8; ++c)
-        *reinterpret_cast<uint4*>(prow + ((c ^ (r & 7)) << 4)) = make_uint4(p[4 * c], p[4 * c + 1], p[4 * c + 2], p[4 * c + 3]);
-      fence_proxy_async();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) arrive_lead(lead + B_PFULL * 8);
-    }
-    if (ok) ok = __all_sync(0xffffffffu, bar_wait(bar + B_ODONE, 0, abort_flag, lim));
-    if (ok) {
-      const float* const share = exchange(l_run, nt);
-      l_run = (share[0] + share[QH]) + (share[2 * QH] + share[3 * QH]);
-    }
-    if (ok) {
-      tc_fence_after();
-      float* const tile = reinterpret_cast<float*>(smem + OFF_RING) + warp * 32 * TS;
+    // a unit's output: its part, or joined with the own rows. The warp's rows of P stage the stores.
+    auto finish = [&](int b, int split, bool have_o) {
+      float* const tile = reinterpret_cast<float*>(prows);
       const int h0 = (int)rank * QH + (q & 1) * 32;  // the warp's first head
-      const size_t bh = (size_t)b * HEADS + h0 + lane;
-      if (a.nsplit > 1) {
-        const size_t sh = (size_t)split * a.batch * HEADS;
-        if (nt > 0) store_out(trow + TMEM_O, true, 1.f, 0.f, tile, nullptr, a.part_o, true,
-                              (sh + (size_t)b * HEADS + h0) * DV + hf * DVH, lane, sub * (DVH / 2));
-        if (sg == 0) a.part_ml[sh + bh] = make_float2(m_run, l_run);
-      } else {
-        const float own = a.own_lse ? a.own_lse[bh] * 1.4426950408889634f : -INFINITY;
-        const float mx = fmaxf(l_run != 0.f ? m_run : -INFINITY, own);
-        const float ref = mx == -INFINITY ? 0.f : mx;
-        const float w = l_run != 0.f ? exp2f(m_run == -INFINITY ? 0.f : m_run - ref) : 0.f;
-        const float wo = own != -INFINITY ? exp2f(own - ref) : 0.f;
-        const float total = fmaf(w, l_run, wo);
-        const float inv = total != 0.f ? 1.f / total : 0.f;
-        exchange(0.f, nt + 1);  // all threads of a head have read own_lse, which may be lse itself
-        // (without own rows the weight is 0 itself, not 0 times a reciprocal that may be NaN: own_out may be null)
-        store_out(trow + TMEM_O, nt > 0, w * inv, wo != 0.f ? wo * inv : 0.f, tile, a.own_out, a.out, a.out_f32 != 0,
-                  ((size_t)b * HEADS + h0) * DV + hf * DVH, lane, sub * (DVH / 2));
-        if (sg == 0) a.lse[bh] = total != 0.f ? (ref + log2f(total)) * 0.6931471805599453f : -INFINITY;
+      if (split >= 0) {
+        const size_t row = ((size_t)split * (a.batch - a.whole) + b - a.whole) * HEADS + h0;
+        if (have_o) store_out(trow + TMEM_O, true, 1.f, 0.f, tile, nullptr, a.part_o, true, row * DV + hf * DVH, lane, sub * (DVH / 2));
+        if (sg == 0) a.part_ml[row + lane] = make_float2(m_run, l_run);
+        return;
       }
+      const size_t row = (size_t)b * HEADS + h0;
+      const float own = a.own_lse ? a.own_lse[row + lane] * 1.4426950408889634f : -INFINITY;
+      const float mx = fmaxf(l_run != 0.f ? m_run : -INFINITY, own);
+      const float ref = mx == -INFINITY ? 0.f : mx;
+      const float f = l_run != 0.f ? exp2f(m_run == -INFINITY ? 0.f : m_run - ref) : 0.f;
+      const float fo = own != -INFINITY ? exp2f(own - ref) : 0.f;
+      const float total = fmaf(f, l_run, fo);
+      const float inv = total != 0.f ? 1.f / total : 0.f;
+      exchange(0.f);  // all threads of a head have read own_lse, which may be lse itself
+      // (without own rows the weight is 0 itself, not 0 times a reciprocal that may be NaN: own_out may be null)
+      store_out(trow + TMEM_O, have_o, f * inv, fo != 0.f ? fo * inv : 0.f, tile, a.own_out, a.out, a.out_f32 != 0,
+                row * DV + hf * DVH, lane, sub * (DVH / 2));
+      if (sg == 0) a.lse[row + lane] = total != 0.f ? (ref + log2f(total)) * 0.6931471805599453f : -INFINITY;
+    };
+    const float scale = a.scale_log2 > 0.f ? a.scale_log2 : 1.f;  // the maximum is taken before the scale: see below
+    int g = 0;  // tiles of the pair's walk
+    w.set(a, (int)(blockIdx.x >> 1), tiles);
+    uint64_t mask_next = w.u < a.units && w.nt > 0 ? key_mask(w.j0) : 0;
+    while (w.u < a.units && ok) {
+      m_run = -INFINITY, l_run = 0.f;
+      for (int j = 0; j < w.nt; ++j, ++g) {
+        const uint64_t mask = mask_next;
+        ok = __all_sync(0xffffffffu, bar_wait(bar + B_SFULL + (g & 1), (unsigned)(g >> 1) & 1u, abort_flag, lim));
+        if (!ok) break;
+        tc_fence_after();
+        // The scores are read twice, 32 at a time: for the maximum, and once the four threads of a head agree on it. (Holding
+        // all 64 across the exchange takes more registers than 16 warps leave.)
+        const uint32_t scol = trow + TMEM_S + (uint32_t)((g & 1) * KH + sub * SEG);
+        uint32_t sv[32];
+        float mb = -INFINITY;
+        // 32 of the thread's scores before the scale, -inf without a row. (A scale that is not positive is applied here,
+        // and is 1 later.) Both conditions are the same in all lanes.
+        auto load32 = [&](int h) {
+          tmem_ld32(scol + 32 * h, sv);
+          tmem_wait_ld();
+          if (!(a.scale_log2 > 0.f)) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) sv[i] = __float_as_uint(__uint_as_float(sv[i]) * a.scale_log2);
+          }
+          const uint32_t m32 = (uint32_t)(mask >> (32 * h));
+          if (~m32) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) sv[i] = m32 >> i & 1 ? sv[i] : 0xff800000u;
+          }
+        };
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          load32(h);
+#pragma unroll
+          for (int i = 0; i < 32; ++i) mb = fmaxf(mb, __uint_as_float(sv[i]));
+        }
+        if (j + 1 < w.nt) mask_next = key_mask(w.j0 + j + 1);
+        const float* share = exchange(mb);
+        if (!ok) break;
+        mb = scale * fmaxf(fmaxf(share[0], share[QH]), fmaxf(share[2 * QH], share[3 * QH]));
+        float m_new = m_run;
+        if (mb > -INFINITY && (m_run == -INFINITY || mb > m_run + 8.f)) m_new = mb;
+        const bool resc = m_new != m_run && m_run != -INFINITY;
+        const float ref = m_new == -INFINITY ? 0.f : m_new;  // no finite score yet: nothing to subtract, a NaN still shows
+        float sum[2] = {0.f, 0.f};
+        uint32_t p[SEG / 2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          load32(h);
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            const float p0 = ex2_approx(fmaf(__uint_as_float(sv[2 * i]), scale, -ref)),
+                        p1 = ex2_approx(fmaf(__uint_as_float(sv[2 * i + 1]), scale, -ref));
+            sum[i & 1] += p0 + p1;
+            const __nv_bfloat162 v = __floats2bfloat162_rn(p0, p1);
+            p[16 * h + i] = *reinterpret_cast<const uint32_t*>(&v);
+          }
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) arrive_lead(lead + (B_SFREE + (g & 1)) * 8);
+        // P's buffer is free, and O holds the tiles before, once the value product of the tile before has finished
+        if (g >= 1) {
+          ok = __all_sync(0xffffffffu, bar_wait(bar + B_PDONE, (unsigned)(g - 1) & 1u, abort_flag, lim));
+          if (!ok) break;
+        }
+        if (__any_sync(0xffffffffu, resc)) {
+          // each of the two threads with the same lane takes half of its columns
+          tc_fence_after();
+          const float f = resc ? ex2_approx(m_run - m_new) : 1.f;
+#pragma unroll 1
+          for (int c = sub * (DVH / 2); c < (sub + 1) * (DVH / 2); c += 16) {
+            float o[16];
+            tmem_ld16(trow + TMEM_O + c, o);
+#pragma unroll
+            for (int i = 0; i < 16; ++i) o[i] *= f;
+            tmem_st16(trow + TMEM_O + c, o);
+          }
+          tmem_wait_st();
+          l_run *= f;
+        }
+        m_run = m_new;
+        l_run += sum[0] + sum[1];
+#pragma unroll
+        for (int c = 0; c < SEG / 8; ++c)
+          *reinterpret_cast<uint4*>(prows + lane * 128 + ((c ^ (lane & 7)) << 4)) =
+              make_uint4(p[4 * c], p[4 * c + 1], p[4 * c + 2], p[4 * c + 3]);
+        fence_proxy_async();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) arrive_lead(lead + B_PFULL * 8);
+      }
+      if (!ok) break;
+      const Walk x = w;
+      w.set(a, x.u + (int)(gridDim.x >> 1), tiles);
+      mask_next = w.u < a.units && w.nt > 0 ? key_mask(w.j0) : 0;
+      if (x.nt > 0) {
+        ok = __all_sync(0xffffffffu, bar_wait(bar + B_PDONE, (unsigned)(g - 1) & 1u, abort_flag, lim));
+        if (!ok) break;
+        const float* const share = exchange(l_run);
+        if (!ok) break;
+        l_run = (share[0] + share[QH]) + (share[2 * QH] + share[3 * QH]);
+        tc_fence_after();
+      }
+      finish(x.b, x.split, x.nt > 0);
+      tc_fence_before();
     }
   }
 
-  if (*abort_flag) {
-    // a wait ran out: let the copies in flight land before the shared memory goes, and report
-    for (int i = 0; i < 50; ++i) __nanosleep(1000);
-    if (t == 0) atomicOr(a.err, HS_DEVERR_TIMEOUT);
-  }
   tc_fence_before();
+  __syncthreads();
+  if (warp == MMA_WARP) {  // every MMA has finished before the tensor memory is freed, after an abort too
+    bool drained = bar_test(bar + B_DRAIN, 0);
+    for (const uint64_t t0 = now_ns(); !drained && now_ns() - t0 < WAIT_NS;) drained = bar_test(bar + B_DRAIN, 0);
+    if (!drained) *abort_flag = 1;
+    __syncwarp();
+    if (*abort_flag) {
+      // a wait ran out: let the copies in flight land before the shared memory goes, and report
+      for (int i = 0; i < 50; ++i) __nanosleep(1000);
+      if (lane == 0) atomicOr(a.err, HS_DEVERR_TIMEOUT);
+    }
+  }
   __syncthreads();
   cluster_sync();
   tc_fence_after();
@@ -543,12 +646,12 @@ __global__ void __launch_bounds__(G * DV / 4) hs_prefix_join_kernel(const Prefix
   __shared__ float4 part[G > 1 ? G - 1 : 1][DV / 4];
   constexpr int PER = G > 1 ? MAX_SPLIT / 32 : 1;  // splits of a lane
   const int t = threadIdx.x & (DV / 4 - 1), g = threadIdx.x / (DV / 4), lane = threadIdx.x & 31, n = a.nsplit;
-  const size_t bh = blockIdx.x, heads = (size_t)a.batch * HEADS;
+  const size_t part_row = blockIdx.x, heads = (size_t)(a.batch - a.whole) * HEADS, bh = (size_t)a.whole * HEADS + part_row;
   const float own = a.own_lse ? a.own_lse[bh] * 1.4426950408889634f : -INFINITY;
   float2 ml[PER];
 #pragma unroll
   for (int i = 0; i < PER; ++i)
-    ml[i] = lane + 32 * i < n ? a.part_ml[(size_t)(lane + 32 * i) * heads + bh] : make_float2(0.f, 0.f);
+    ml[i] = lane + 32 * i < n ? a.part_ml[(size_t)(lane + 32 * i) * heads + part_row] : make_float2(0.f, 0.f);
   float mx = own;
 #pragma unroll
   for (int i = 0; i < PER; ++i)
@@ -584,7 +687,7 @@ __global__ void __launch_bounds__(G * DV / 4) hs_prefix_join_kernel(const Prefix
         const int s = s0 + u * G;
         w[u] = __shfl_sync(0xffffffffu, weight[i], s & 31);
         if (s >= 32 * i + 32) w[u] = 0.f;
-        if (w[u] != 0.f) v[u] = __ldcs(reinterpret_cast<const float4*>(a.part_o + ((size_t)s * heads + bh) * DV) + t);
+        if (w[u] != 0.f) v[u] = __ldcs(reinterpret_cast<const float4*>(a.part_o + ((size_t)s * heads + part_row) * DV) + t);
       }
 #pragma unroll
       for (int u = 0; u < 4; ++u)
@@ -640,16 +743,29 @@ int pairs_resident() {
   return n;
 }
 
-// The number of splits with the shortest expected time, in tiles: waves of units, each a run of tiles and a fixed cost of
-// about three of them (prologue, Q, epilogue), and for more than one split the join.
-int splits_of(int pairs, int32_t batch, int32_t max_length) {
-  const int tiles = (max_length + NK - 1) / NK;
-  int best = 1;
-  double least = 1e30;
-  for (int n = 1; n <= std::max(1, std::min({tiles, MAX_SPLIT, std::max(1, 4 * pairs / batch)})); ++n) {
-    const int64_t units = (int64_t)batch * n;
-    const double cost = (double)((units + pairs - 1) / pairs) * ((tiles + n - 1) / n + 3) + (n > 1 ? 1.5 + 0.025 * units : 0);
-    if (cost < least) least = cost, best = n;
+// How a batch is cut into units: requests 0 .. whole - 1 are one unit each, the others `nsplit` units.
+struct Cut {
+  int whole, nsplit;
+  size_t workspace(int batch) const {
+    return nsplit > 1 ? (size_t)nsplit * (size_t)(batch - whole) * HEADS * (DV * sizeof(float) + sizeof(float2)) : 0;
+  }
+};
+// The cut with the shortest expected time, in tiles (1.2 to 2.6 us): a pair's units one after the other, each its tiles and
+// about one more (the softmax of its last tile and its store), three for the start and the end of the kernel, and the join
+// of splits. Either all requests are cut, or as many as fill the pairs whole times over stay whole and the rest is cut.
+Cut cut_of(int pairs, int32_t batch, int32_t max_length) {
+  const int tiles = (max_length + NK - 1) / NK, full = batch / pairs * pairs;
+  Cut best = {batch, 1};
+  double least = (double)((batch + pairs - 1) / pairs) * (tiles + 1);
+  for (int whole = 0;; whole = full) {
+    const int rest = batch - whole;
+    for (int n = 2; rest > 0 && n <= std::min({tiles, MAX_SPLIT, 4 * pairs / rest}); ++n) {
+      const int64_t units = (int64_t)rest * n;
+      const double cost = (double)(whole / pairs) * (tiles + 1) +
+                          (double)((units + pairs - 1) / pairs) * ((tiles + n - 1) / n + 1) + 1.5 + 0.025 * units;
+      if (cost < least) least = cost, best = {whole, n};
+    }
+    if (whole == full) break;
   }
   return best;
 }
@@ -686,8 +802,8 @@ bool make_map(EncodeFn f, CUtensorMap* m, const void* rows, uint64_t count, uint
 
 extern "C" size_t hs_mla_prefix_workspace(hs_pool* pool, int32_t batch, int32_t max_length) {
   if (!pool || batch <= 0 || max_length < 0 || max_length > 1 << 30 || batch > (1 << 24) / HEADS || !hs_on_device(pool)) return 0;
-  const int pairs = pairs_resident(), n = pairs > 0 ? splits_of(pairs, batch, max_length) : 1;
-  return n > 1 ? (size_t)n * (size_t)batch * HEADS * (DV * sizeof(float) + sizeof(float2)) : 0;
+  const int pairs = pairs_resident();
+  return pairs > 0 ? cut_of(pairs, batch, max_length).workspace(batch) : 0;
 }
 
 extern "C" int hs_mla_prefix(hs_pool* pool, int32_t batch, const void* q, const hs_paged_rows* prefix,
@@ -707,8 +823,8 @@ extern "C" int hs_mla_prefix(hs_pool* pool, int32_t batch, const void* q, const 
   const int pairs = pairs_resident();
   const EncodeFn encode = encoder();
   if (pairs < 1 || !encode) return HS_ERR_UNSUPPORTED;
-  const int nsplit = splits_of(pairs, batch, max_length);
-  const size_t need = nsplit > 1 ? (size_t)nsplit * (size_t)batch * HEADS * (DV * sizeof(float) + sizeof(float2)) : 0;
+  const Cut cut = cut_of(pairs, batch, max_length);
+  const size_t need = cut.workspace(batch);
   if (need && (!aligned(workspace, 256) || workspace_bytes < need)) return HS_ERR_INVALID_ARG;
 
   PrefixArgs a;
@@ -722,9 +838,12 @@ extern "C" int hs_mla_prefix(hs_pool* pool, int32_t batch, const void* q, const 
   a.length = prefix_length;
   a.scale_log2 = sm_scale * 1.4426950408889634f;
   a.batch = batch;
-  a.nsplit = nsplit;
+  const int rest = batch - cut.whole;
+  a.whole = cut.whole;
+  a.nsplit = cut.nsplit;
+  a.units = cut.whole + rest * cut.nsplit;
   a.part_o = static_cast<float*>(workspace);
-  a.part_ml = nsplit > 1 ? reinterpret_cast<float2*>(a.part_o + (size_t)nsplit * batch * HEADS * DV) : nullptr;
+  a.part_ml = rest ? reinterpret_cast<float2*>(a.part_o + (size_t)cut.nsplit * rest * HEADS * DV) : nullptr;
   a.own_out = own_out;
   a.own_lse = own_lse;
   a.out = out;
@@ -742,7 +861,7 @@ extern "C" int hs_mla_prefix(hs_pool* pool, int32_t batch, const void* q, const 
     return HS_ERR_INVALID_ARG;
 
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(2 * batch * nsplit), 1, 1);
+  cfg.gridDim = dim3((unsigned)(2 * std::min(a.units, pairs)), 1, 1);
   cfg.blockDim = dim3(THREADS, 1, 1);
   cfg.dynamicSmemBytes = SMEM_BYTES;
   cfg.stream = reinterpret_cast<cudaStream_t>(stream);
@@ -755,11 +874,11 @@ extern "C" int hs_mla_prefix(hs_pool* pool, int32_t batch, const void* q, const 
   cfg.attrs = attr;
   cfg.numAttrs = 2;
   if (cudaLaunchKernelEx(&cfg, hs_prefix_kernel, a, qmap, map, map2, map1) != cudaSuccess) return HS_ERR_CUDA;
-  if (nsplit == 1) return HS_OK;
-  cfg.gridDim = dim3((unsigned)batch * HEADS, 1, 1);
+  if (!rest) return HS_OK;
+  cfg.gridDim = dim3((unsigned)rest * HEADS, 1, 1);
   cfg.dynamicSmemBytes = 0;
   cfg.numAttrs = 1;
-  const int groups = nsplit <= 16 ? 1 : 4;
+  const int groups = cut.nsplit <= 16 ? 1 : 4;
   cfg.blockDim = dim3((unsigned)groups * DV / 4, 1, 1);
   const cudaError_t e = groups == 1 ? cudaLaunchKernelEx(&cfg, hs_prefix_join_kernel<1>, a)
                                     : cudaLaunchKernelEx(&cfg, hs_prefix_join_kernel<4>, a);
