@@ -198,42 +198,48 @@ __device__ __forceinline__ void tma_box(uint32_t dst, const CUtensorMap* map, in
       : "memory");
 }
 
-// A segment of 64 tokens: lane u holds the page of box u, and of box u + 32 where boxes are single rows. Only the page is
-// fetched, a tile before it is used; the arithmetic on it waits until then.
-struct Seg {
-  int page[2];
+// The lane's boxes of a segment of 64 tokens: box u for lane u, and box u + 32 where boxes are single rows. Pages are
+// fetched well before they are used, rows worked out from them before the wait for a stage.
+struct Boxes {
+  int page[2], row[2], have[2];  // have: rows of the box within the prefix, all of them where it loads as one
 };
-__device__ __forceinline__ Seg seg_pages(const PrefixArgs& a, int tok0, int len, int lane) {
-  Seg s;
+__device__ __forceinline__ void fetch_pages(const PrefixArgs& a, Boxes& s, int tok0, int len, int lane) {
   s.page[0] = a.pages[min(tok0 + (lane << a.box_shift), len - 1) >> a.page_shift];
   s.page[1] = a.box_shift ? 0 : a.pages[min(tok0 + 32 + lane, len - 1) >> a.page_shift];
-  return s;
 }
-// The lane's boxes of the segment: NBLK column blocks from `blk` on to `dst`, where a column block's 64 rows lie together.
-// `map` has boxes of one column block, `wide` of NBLK. A box that the prefix ends inside is loaded row by row.
-template <int NBLK>
-__device__ __forceinline__ void load_seg(const PrefixArgs& a, const CUtensorMap* map, const CUtensorMap* wide,
-                                         const CUtensorMap* map1, const Seg& s, int tok0, int len, uint32_t dst, int blk,
-                                         uint32_t bar, int lane) {
-  const int rows = 1 << a.box_shift;
+__device__ __forceinline__ void find_rows(const PrefixArgs& a, Boxes& s, int tok0, int len, int lane) {
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
-    const int off = (lane + 32 * i) << a.box_shift, tok = tok0 + off;
-    if (off >= SEG) break;
+    const int tok = tok0 + ((lane + 32 * i) << a.box_shift), rows = 1 << a.box_shift;
     const bool on = tok < len && s.page[i] >= 0 && s.page[i] < a.page_limit;
-    const int row = on ? (s.page[i] << a.page_shift) + (tok & ((1 << a.page_shift) - 1)) : a.none;
-    const int have = min(rows, len - tok);
-    if (!on || have == rows) {
-      if (rows == SEG) {  // the blocks' rows lie together: one box
-        tma_box(dst, wide, blk, row, bar);
-      } else {
+    s.row[i] = on ? (s.page[i] << a.page_shift) + (tok & ((1 << a.page_shift) - 1)) : a.none;
+    s.have[i] = on ? min(rows, len - tok) : rows;
+  }
+}
+// Loads them: NBLK column blocks from `blk` on to `dst`, where a column block's 64 rows lie together. `map` has boxes of one
+// column block, `wide` of NBLK. A box that the prefix ends inside is loaded row by row.
+template <int NBLK>
+__device__ __forceinline__ void load_boxes(const PrefixArgs& a, const CUtensorMap* map, const CUtensorMap* wide,
+                                           const CUtensorMap* map1, const Boxes& s, uint32_t dst, int blk, uint32_t bar,
+                                           int lane) {
+  const int rows = 1 << a.box_shift;
+  if (s.have[0] == SEG) {  // the segment is one box, with its blocks' rows together
+    tma_box(dst, wide, blk, s.row[0], bar);
+    return;
+  }
 #pragma unroll
-        for (int n = 0; n < NBLK; ++n) tma_box(dst + (uint32_t)(n * BLK_BYTES + off * 128), map, blk + n, row, bar);
+  for (int i = 0; i < 2; ++i) {
+    const int off = (lane + 32 * i) << a.box_shift;
+    if (off >= SEG) break;
+#pragma unroll 1
+    for (int n = 0; n < NBLK; ++n) {
+      const uint32_t d = dst + (uint32_t)(n * BLK_BYTES + off * 128);
+      if (s.have[i] == rows) {
+        tma_box(d, map, blk + n, s.row[i], bar);
+      } else {
+#pragma unroll 1
+        for (int r = 0; r < rows; ++r) tma_box(d + r * 128u, map1, blk + n, r < s.have[i] ? s.row[i] + r : a.none, bar);
       }
-    } else {
-      for (int n = 0; n < NBLK; ++n)
-        for (int r = 0; r < rows; ++r)
-          tma_box(dst + (uint32_t)(n * BLK_BYTES + (off + r) * 128), map1, blk + n, r < have ? row + r : a.none, bar);
     }
   }
 }
@@ -420,23 +426,26 @@ __global__ void __launch_bounds__(THREADS, 1)
       bool q_next = s == 0 && kmore;  // Q is this loader's to load, once its slot is free
       // a stage's first token: the CTA's half of the keys, or the segment that the V stage belongs to
       auto first = [&]() { return is_k ? (w.j0 + w.j) * NK + (int)rank * KH : (v.j0 + v.j) * NK + (c >> 1) * SEG; };
-      Seg p0 = {}, p1 = {};
-      if (kmore) p0 = seg_pages(a, first(), len, lane), p1 = seg_pages(a, first() + SEG, len, lane);
+      Boxes p0 = {}, p1 = {};
+      if (kmore) fetch_pages(a, p0, first(), len, lane), fetch_pages(a, p1, first() + SEG, len, lane);
       unsigned ph = 1;  // a barrier that has not completed a phase passes for the parity before its first
       while (vmore) {
+        find_rows(a, p0, first(), len, lane);
+        if (is_k) find_rows(a, p1, first() + SEG, len, lane);
+        const int blk = is_k ? c : (int)rank * (DVH / 64) + (c & 1) * 2;
         ok = bar_wait(bar + B_EMPTY + s, ph, abort_flag, lim);  // the MMAs that read the slot have finished
         if (!ok) break;
         ph ^= 1u;
+        if (rank == 0 && lane == 0) bar_arrive_expect(bar + B_FULL + s, 2 * STAGE_BYTES);
+        if (is_k) {
+          load_boxes<1>(a, &map, &map, &map1, p0, dst, blk, fb, lane);
+          load_boxes<1>(a, &map, &map, &map1, p1, dst + BLK_BYTES, blk, fb, lane);
+        } else {
+          load_boxes<2>(a, &map, &map2, &map1, p0, dst, blk, fb, lane);
+        }
         if (q_next) load_q(w);
         // the slot of a unit's last K stage is free when the unit's last scores have been taken, and so is Q
         q_next = is_k && c == KBLK - 1 && w.j + 1 == w.nt;
-        if (rank == 0 && lane == 0) bar_arrive_expect(bar + B_FULL + s, 2 * STAGE_BYTES);
-        if (is_k) {
-          load_seg<1>(a, &map, &map, &map1, p0, first(), len, dst, c, fb, lane);
-          load_seg<1>(a, &map, &map, &map1, p1, first() + SEG, len, dst + BLK_BYTES, c, fb, lane);
-        } else {
-          load_seg<2>(a, &map, &map2, &map1, p0, first(), len, dst, (int)rank * (DVH / 64) + (c & 1) * 2, fb, lane);
-        }
         c += NSTAGE;
         while (vmore && c >= (is_k ? KBLK : VST)) {
           if (is_k) {
@@ -452,8 +461,8 @@ __global__ void __launch_bounds__(THREADS, 1)
           }
         }
         if (vmore) {
-          p0 = seg_pages(a, first(), len, lane);
-          if (is_k) p1 = seg_pages(a, first() + SEG, len, lane);
+          fetch_pages(a, p0, first(), len, lane);
+          if (is_k) fetch_pages(a, p1, first() + SEG, len, lane);
         }
       }
     }
