@@ -91,7 +91,7 @@ struct PrefixArgs {
   const int32_t* pages;
   int32_t page_shift, max_length;
   int32_t page_limit;     // pages 0 .. page_limit - 1 lie within the rows
-  int32_t box_shift;      // log2 of the rows of a box
+  int32_t box_shift;      // log2 of the rows of a box (4 to 64)
   int32_t none;           // a row coordinate behind the last row
   const int32_t* length;  // or nullptr: max_length
   float scale_log2;
@@ -198,48 +198,69 @@ __device__ __forceinline__ void tma_box(uint32_t dst, const CUtensorMap* map, in
       : "memory");
 }
 
-// The lane's boxes of a segment of 64 tokens: box u for lane u, and box u + 32 where boxes are single rows. Pages are
-// fetched well before they are used, rows worked out from them before the wait for a stage.
-struct Boxes {
-  int page[2], row[2], have[2];  // have: rows of the box within the prefix, all of them where it loads as one
-};
-__device__ __forceinline__ void fetch_pages(const PrefixArgs& a, Boxes& s, int tok0, int len, int lane) {
-  s.page[0] = a.pages[min(tok0 + (lane << a.box_shift), len - 1) >> a.page_shift];
-  s.page[1] = a.box_shift ? 0 : a.pages[min(tok0 + 32 + lane, len - 1) >> a.page_shift];
+// Four rows of one column block, from column `col` on, to four consecutive 128-byte rows. (All four exist: see find_rows.)
+__device__ __forceinline__ void tma_gather4(uint32_t dst, const CUtensorMap* map, int col, const int (&row)[4], uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes [%0], [%1, "
+      "{%3, %4, %5, %6, %7}], [%2];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(col), "r"(row[0]), "r"(row[1]), "r"(row[2]), "r"(row[3])
+      : "memory");
 }
-__device__ __forceinline__ void find_rows(const PrefixArgs& a, Boxes& s, int tok0, int len, int lane) {
+// The lane's box of a segment of 64 tokens: box u for lane u, of min(page_rows, 64) rows, but of four where pages have
+// fewer. Pages are fetched well before they are used, rows worked out from them before the wait for a stage.
+struct Box {
+  int page[4], row[4];  // [0] alone where the box's rows lie together
+  int have;             // rows of the box within the prefix, all of them where it loads as one
+};
+__device__ __forceinline__ void fetch_pages(const PrefixArgs& a, Box& s, int tok0, int len, int lane) {
+  const int tok = tok0 + (lane << a.box_shift);
+  s.page[0] = a.pages[min(tok, len - 1) >> a.page_shift];
+  if (a.page_shift < 2) {
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const int tok = tok0 + ((lane + 32 * i) << a.box_shift), rows = 1 << a.box_shift;
-    const bool on = tok < len && s.page[i] >= 0 && s.page[i] < a.page_limit;
-    s.row[i] = on ? (s.page[i] << a.page_shift) + (tok & ((1 << a.page_shift) - 1)) : a.none;
-    s.have[i] = on ? min(rows, len - tok) : rows;
+    for (int i = 1; i < 4; ++i) s.page[i] = a.pages[min(tok + i, len - 1) >> a.page_shift];
   }
 }
-// Loads them: NBLK column blocks from `blk` on to `dst`, where a column block's 64 rows lie together. `map` has boxes of one
+__device__ __forceinline__ void find_rows(const PrefixArgs& a, Box& s, int tok0, int len, int lane) {
+  const int tok = tok0 + (lane << a.box_shift), rows = 1 << a.box_shift;
+  auto row = [&](int i) {
+    const bool on = tok + i < len && s.page[i] >= 0 && s.page[i] < a.page_limit;
+    return on ? (s.page[i] << a.page_shift) + ((tok + i) & ((1 << a.page_shift) - 1)) : a.none;
+  };
+  s.row[0] = row(0);
+  s.have = s.row[0] != a.none ? min(rows, len - tok) : rows;
+  if (a.page_shift < 2) {
+#pragma unroll
+    for (int i = 1; i < 4; ++i) s.row[i] = row(i);
+    // four rows that the pool holds are gathered by one copy; with some missing they are loaded one by one
+    s.have = s.row[0] != a.none && s.row[1] != a.none && s.row[2] != a.none && s.row[3] != a.none ? 4 : 0;
+  }
+}
+// Loads it: NBLK column blocks from `blk` on to `dst`, where a column block's 64 rows lie together. `map` has boxes of one
 // column block, `wide` of NBLK. A box that the prefix ends inside is loaded row by row.
 template <int NBLK>
-__device__ __forceinline__ void load_boxes(const PrefixArgs& a, const CUtensorMap* map, const CUtensorMap* wide,
-                                           const CUtensorMap* map1, const Boxes& s, uint32_t dst, int blk, uint32_t bar,
-                                           int lane) {
-  const int rows = 1 << a.box_shift;
-  if (s.have[0] == SEG) {  // the segment is one box, with its blocks' rows together
+__device__ __forceinline__ void load_box(const PrefixArgs& a, const CUtensorMap* map, const CUtensorMap* wide,
+                                         const CUtensorMap* map1, const CUtensorMap* gather, const Box& s, uint32_t dst,
+                                         int blk, uint32_t bar, int lane) {
+  if (s.have == SEG) {  // the segment is one box, with its blocks' rows together
     tma_box(dst, wide, blk, s.row[0], bar);
     return;
   }
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const int off = (lane + 32 * i) << a.box_shift;
-    if (off >= SEG) break;
+  const int rows = 1 << a.box_shift;
 #pragma unroll 1
-    for (int n = 0; n < NBLK; ++n) {
-      const uint32_t d = dst + (uint32_t)(n * BLK_BYTES + off * 128);
-      if (s.have[i] == rows) {
-        tma_box(d, map, blk + n, s.row[i], bar);
+  for (int n = 0; n < NBLK; ++n) {
+    const uint32_t d = dst + (uint32_t)(n * BLK_BYTES + ((lane << a.box_shift) * 128));
+    if (a.page_shift < 2) {
+      if (s.have) {
+        tma_gather4(d, gather, (blk + n) * 64, s.row, bar);
       } else {
-#pragma unroll 1
-        for (int r = 0; r < rows; ++r) tma_box(d + r * 128u, map1, blk + n, r < s.have[i] ? s.row[i] + r : a.none, bar);
+#pragma unroll
+        for (int r = 0; r < 4; ++r) tma_box(d + r * 128u, map1, blk + n, s.row[r], bar);
       }
+    } else if (s.have == rows) {
+      tma_box(d, map, blk + n, s.row[0], bar);
+    } else {
+#pragma unroll 1
+      for (int r = 0; r < rows; ++r) tma_box(d + r * 128u, map1, blk + n, r < s.have ? s.row[0] + r : a.none, bar);
     }
   }
 }
@@ -296,7 +317,8 @@ __device__ __forceinline__ void store_out(uint32_t tcol, bool have_o, float w0, 
 
 __global__ void __launch_bounds__(THREADS, 1)
     hs_prefix_kernel(const PrefixArgs a, const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap map,
-                     const __grid_constant__ CUtensorMap map2, const __grid_constant__ CUtensorMap map1) {
+                     const __grid_constant__ CUtensorMap map2, const __grid_constant__ CUtensorMap map1,
+                     const __grid_constant__ CUtensorMap gather) {
   extern __shared__ __align__(1024) uint8_t smem[];
   uint64_t* const bar = reinterpret_cast<uint64_t*>(smem + OFF_BAR);
   volatile int* const abort_flag = reinterpret_cast<volatile int*>(smem + OFF_MISC + 4);
@@ -426,7 +448,7 @@ __global__ void __launch_bounds__(THREADS, 1)
       bool q_next = s == 0 && kmore;  // Q is this loader's to load, once its slot is free
       // a stage's first token: the CTA's half of the keys, or the segment that the V stage belongs to
       auto first = [&]() { return is_k ? (w.j0 + w.j) * NK + (int)rank * KH : (v.j0 + v.j) * NK + (c >> 1) * SEG; };
-      Boxes p0 = {}, p1 = {};
+      Box p0 = {}, p1 = {};
       if (kmore) fetch_pages(a, p0, first(), len, lane), fetch_pages(a, p1, first() + SEG, len, lane);
       unsigned ph = 1;  // a barrier that has not completed a phase passes for the parity before its first
       while (vmore) {
@@ -438,10 +460,10 @@ __global__ void __launch_bounds__(THREADS, 1)
         ph ^= 1u;
         if (rank == 0 && lane == 0) bar_arrive_expect(bar + B_FULL + s, 2 * STAGE_BYTES);
         if (is_k) {
-          load_boxes<1>(a, &map, &map, &map1, p0, dst, blk, fb, lane);
-          load_boxes<1>(a, &map, &map, &map1, p1, dst + BLK_BYTES, blk, fb, lane);
+          load_box<1>(a, &map, &map, &map1, &gather, p0, dst, blk, fb, lane);
+          load_box<1>(a, &map, &map, &map1, &gather, p1, dst + BLK_BYTES, blk, fb, lane);
         } else {
-          load_boxes<2>(a, &map, &map2, &map1, p0, dst, blk, fb, lane);
+          load_box<2>(a, &map, &map2, &map1, &gather, p0, dst, blk, fb, lane);
         }
         if (q_next) load_q(w);
         // the slot of a unit's last K stage is free when the unit's last scores have been taken, and so is Q
@@ -807,6 +829,15 @@ bool make_map(EncodeFn f, CUtensorMap* m, const void* rows, uint64_t count, uint
            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// The same rows as (column, row), for gathering: a box is 64 columns of one row.
+bool make_gather_map(EncodeFn f, CUtensorMap* m, const void* rows, uint64_t count) {
+  const cuuint64_t dims[2] = {DQK, count}, strides[1] = {ROW_BYTES};
+  const cuuint32_t boxes[2] = {64, 1}, steps[2] = {1, 1};
+  return f(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(rows), dims, strides, boxes, steps,
+           CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+           CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 }  // namespace
 
 extern "C" size_t hs_mla_prefix_workspace(hs_pool* pool, int32_t batch, int32_t max_length) {
@@ -840,7 +871,7 @@ extern "C" int hs_mla_prefix(hs_pool* pool, int32_t batch, const void* q, const 
   std::memset(&a, 0, sizeof(a));
   a.pages = prefix->pages;
   while ((1 << a.page_shift) < prefix->page_rows) ++a.page_shift;
-  a.box_shift = std::min(a.page_shift, 6);
+  a.box_shift = std::max(2, std::min(a.page_shift, 6));
   a.max_length = max_length;
   a.page_limit = (int32_t)(prefix->count / prefix->page_rows);
   a.none = (int32_t)prefix->count;
@@ -860,13 +891,14 @@ extern "C" int hs_mla_prefix(hs_pool* pool, int32_t batch, const void* q, const 
   a.lse = lse;
   a.err = pool->err;
   hs_attention_waits(&a.wait_limit, &a.stall);
-  CUtensorMap qmap, map, map2, map1;
+  CUtensorMap qmap, map, map2, map1, gather;
   // an empty pool of rows still needs a map: one row, which page_limit = 0 keeps from being read
   const uint64_t count = std::max<int64_t>(prefix->count, 1);
   a.none = (int32_t)count;
   if (!make_map(encode, &qmap, q, (uint64_t)batch * HEADS, QH, 3) ||
       !make_map(encode, &map, prefix->rows, count, 1u << a.box_shift, 1) ||
-      !make_map(encode, &map2, prefix->rows, count, 1u << a.box_shift, 2) || !make_map(encode, &map1, prefix->rows, count, 1, 1))
+      !make_map(encode, &map2, prefix->rows, count, 1u << a.box_shift, 2) || !make_map(encode, &map1, prefix->rows, count, 1, 1) ||
+      !make_gather_map(encode, &gather, prefix->rows, count))
     return HS_ERR_INVALID_ARG;
 
   cudaLaunchConfig_t cfg = {};
@@ -882,7 +914,7 @@ extern "C" int hs_mla_prefix(hs_pool* pool, int32_t batch, const void* q, const 
   attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  if (cudaLaunchKernelEx(&cfg, hs_prefix_kernel, a, qmap, map, map2, map1) != cudaSuccess) return HS_ERR_CUDA;
+  if (cudaLaunchKernelEx(&cfg, hs_prefix_kernel, a, qmap, map, map2, map1, gather) != cudaSuccess) return HS_ERR_CUDA;
   if (!rest) return HS_OK;
   cfg.gridDim = dim3((unsigned)rest * HEADS, 1, 1);
   cfg.dynamicSmemBytes = 0;
