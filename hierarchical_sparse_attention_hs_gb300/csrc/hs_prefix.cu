@@ -236,10 +236,11 @@ __device__ __forceinline__ void find_rows(const PrefixArgs& a, Box& s, int tok0,
   }
 }
 // Loads it: NBLK column blocks from `blk` on to `dst`, where a column block's 64 rows lie together. `map` has boxes of one
-// column block, `wide` of NBLK. A box that the prefix ends inside is loaded row by row.
+// column block, `wide` of NBLK, map1 of one row, `small` of four rows (or, for pages of fewer, gathers four). A box that the
+// prefix ends inside is loaded in fours, and row by row where it ends.
 template <int NBLK>
 __device__ __forceinline__ void load_box(const PrefixArgs& a, const CUtensorMap* map, const CUtensorMap* wide,
-                                         const CUtensorMap* map1, const CUtensorMap* gather, const Box& s, uint32_t dst,
+                                         const CUtensorMap* map1, const CUtensorMap* small, const Box& s, uint32_t dst,
                                          int blk, uint32_t bar, int lane) {
   if (s.have == SEG) {  // the segment is one box, with its blocks' rows together
     tma_box(dst, wide, blk, s.row[0], bar);
@@ -251,7 +252,7 @@ __device__ __forceinline__ void load_box(const PrefixArgs& a, const CUtensorMap*
     const uint32_t d = dst + (uint32_t)(n * BLK_BYTES + ((lane << a.box_shift) * 128));
     if (a.page_shift < 2) {
       if (s.have) {
-        tma_gather4(d, gather, (blk + n) * 64, s.row, bar);
+        tma_gather4(d, small, (blk + n) * 64, s.row, bar);
       } else {
 #pragma unroll
         for (int r = 0; r < 4; ++r) tma_box(d + r * 128u, map1, blk + n, s.row[r], bar);
@@ -260,7 +261,13 @@ __device__ __forceinline__ void load_box(const PrefixArgs& a, const CUtensorMap*
       tma_box(d, map, blk + n, s.row[0], bar);
     } else {
 #pragma unroll 1
-      for (int r = 0; r < rows; ++r) tma_box(d + r * 128u, map1, blk + n, r < s.have ? s.row[0] + r : a.none, bar);
+      for (int r = 0; r < rows; r += 4) {
+        if (r + 4 <= s.have || r >= s.have) {
+          tma_box(d + r * 128u, small, blk + n, r < s.have ? s.row[0] + r : a.none, bar);
+        } else {
+          for (int i = r; i < r + 4; ++i) tma_box(d + i * 128u, map1, blk + n, i < s.have ? s.row[0] + i : a.none, bar);
+        }
+      }
     }
   }
 }
@@ -318,7 +325,7 @@ __device__ __forceinline__ void store_out(uint32_t tcol, bool have_o, float w0, 
 __global__ void __launch_bounds__(THREADS, 1)
     hs_prefix_kernel(const PrefixArgs a, const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap map,
                      const __grid_constant__ CUtensorMap map2, const __grid_constant__ CUtensorMap map1,
-                     const __grid_constant__ CUtensorMap gather) {
+                     const __grid_constant__ CUtensorMap small) {
   extern __shared__ __align__(1024) uint8_t smem[];
   uint64_t* const bar = reinterpret_cast<uint64_t*>(smem + OFF_BAR);
   volatile int* const abort_flag = reinterpret_cast<volatile int*>(smem + OFF_MISC + 4);
@@ -328,6 +335,10 @@ __global__ void __launch_bounds__(THREADS, 1)
   const uint32_t rank = cluster_rank();
   const unsigned lim = a.wait_limit;
 
+  if (t == 32) {  // the copies' descriptors on their way while the barriers are set up
+    for (const CUtensorMap* m : {&qmap, &map, &map2, &small})
+      asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(m)) : "memory");
+  }
   if (t == 0) {
     for (int i = 0; i < NBAR; ++i) bar_init(bar + i, 1);
     // one arrival for each softmax warp of the pair
@@ -445,10 +456,11 @@ __global__ void __launch_bounds__(THREADS, 1)
           asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(a.own_out + (size_t)row * DV), "r"(QH * DV * 4)
                        : "memory");
       };
-      bool q_next = s == 0 && kmore;  // Q is this loader's to load, once its slot is free
+      bool q_next = false;  // the next unit's Q is this loader's to load, once its slot is free
       // a stage's first token: the CTA's half of the keys, or the segment that the V stage belongs to
       auto first = [&]() { return is_k ? (w.j0 + w.j) * NK + (int)rank * KH : (v.j0 + v.j) * NK + (c >> 1) * SEG; };
       Box p0 = {}, p1 = {};
+      if (kmore && s == 0) load_q(w);
       if (kmore) fetch_pages(a, p0, first(), len, lane), fetch_pages(a, p1, first() + SEG, len, lane);
       unsigned ph = 1;  // a barrier that has not completed a phase passes for the parity before its first
       while (vmore) {
@@ -460,10 +472,10 @@ __global__ void __launch_bounds__(THREADS, 1)
         ph ^= 1u;
         if (rank == 0 && lane == 0) bar_arrive_expect(bar + B_FULL + s, 2 * STAGE_BYTES);
         if (is_k) {
-          load_box<1>(a, &map, &map, &map1, &gather, p0, dst, blk, fb, lane);
-          load_box<1>(a, &map, &map, &map1, &gather, p1, dst + BLK_BYTES, blk, fb, lane);
+          load_box<1>(a, &map, &map, &map1, &small, p0, dst, blk, fb, lane);
+          load_box<1>(a, &map, &map, &map1, &small, p1, dst + BLK_BYTES, blk, fb, lane);
         } else {
-          load_box<2>(a, &map, &map2, &map1, &gather, p0, dst, blk, fb, lane);
+          load_box<2>(a, &map, &map2, &map1, &small, p0, dst, blk, fb, lane);
         }
         if (q_next) load_q(w);
         // the slot of a unit's last K stage is free when the unit's last scores have been taken, and so is Q
@@ -891,14 +903,15 @@ extern "C" int hs_mla_prefix(hs_pool* pool, int32_t batch, const void* q, const 
   a.lse = lse;
   a.err = pool->err;
   hs_attention_waits(&a.wait_limit, &a.stall);
-  CUtensorMap qmap, map, map2, map1, gather;
+  CUtensorMap qmap, map, map2, map1, small;
   // an empty pool of rows still needs a map: one row, which page_limit = 0 keeps from being read
   const uint64_t count = std::max<int64_t>(prefix->count, 1);
   a.none = (int32_t)count;
   if (!make_map(encode, &qmap, q, (uint64_t)batch * HEADS, QH, 3) ||
       !make_map(encode, &map, prefix->rows, count, 1u << a.box_shift, 1) ||
       !make_map(encode, &map2, prefix->rows, count, 1u << a.box_shift, 2) || !make_map(encode, &map1, prefix->rows, count, 1, 1) ||
-      !make_gather_map(encode, &gather, prefix->rows, count))
+      !(a.page_shift < 2 ? make_gather_map(encode, &small, prefix->rows, count)
+                         : make_map(encode, &small, prefix->rows, count, 4, 1)))
     return HS_ERR_INVALID_ARG;
 
   cudaLaunchConfig_t cfg = {};
@@ -914,7 +927,7 @@ extern "C" int hs_mla_prefix(hs_pool* pool, int32_t batch, const void* q, const 
   attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  if (cudaLaunchKernelEx(&cfg, hs_prefix_kernel, a, qmap, map, map2, map1, gather) != cudaSuccess) return HS_ERR_CUDA;
+  if (cudaLaunchKernelEx(&cfg, hs_prefix_kernel, a, qmap, map, map2, map1, small) != cudaSuccess) return HS_ERR_CUDA;
   if (!rest) return HS_OK;
   cfg.gridDim = dim3((unsigned)rest * HEADS, 1, 1);
   cfg.dynamicSmemBytes = 0;
