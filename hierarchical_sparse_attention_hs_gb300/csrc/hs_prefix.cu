@@ -272,31 +272,83 @@ __device__ __forceinline__ void load_box(const PrefixArgs& a, const CUtensorMap*
   }
 }
 
-// One softmax warp's part of an output: its 32 heads' columns c_lo .. c_lo + 127 from tensor memory times w0 (zeros
-// without O), plus w1 times the own rows' output where w1 != 0. 32-column slices go through a shared tile of 32 rows of 128
-// bytes (16-byte chunk k of row r at k ^ (r % 8): no conflicts either way) so that global accesses are whole row segments.
-// `base`: element offset of the warp's first head, first column in out (and own).
-__device__ __forceinline__ void store_out(uint32_t tcol, bool have_o, float w0, float w1, float* tile, const float* own,
-                                          void* out, bool f32, size_t base, int lane, int c_lo) {
+// One softmax warp's part of an output without own rows: its 32 heads' columns c_lo .. c_lo + 127 from tensor memory times
+// w0 (zeros without O), 128 bytes of every row at a time, staged in `tile` (32 rows of 128 bytes, 16-byte chunk k of row r at
+// k ^ (r % 8): no conflicts, and the 128-byte swizzle of `map`) and stored by TMA from (column, row) on. The tile may be
+// written again, and the kernel end, once the last copy has read it: the function waits for that. (Through registers
+// instead, tile to coalesced stores, a unit's 64 KB took 2.7 us a CTA.)
+__device__ __forceinline__ void store_tma(uint32_t tcol, bool have_o, float w0, uint8_t* tile, const CUtensorMap* map,
+                                          bool f32, int col, int row, int lane, int c_lo) {
+  const int step = f32 ? 32 : 64;
+#pragma unroll 1
+  for (int c = c_lo; c < c_lo + DVH / 2; c += step) {
+    if (c > c_lo) {
+      if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+      __syncwarp();
+    }
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      uint32_t o[32];
+      if (f32 && h == 1) break;
+      if (have_o) {
+        tmem_ld32(tcol + c + 32 * h, o);
+        tmem_wait_ld();
+      } else {
+#pragma unroll
+        for (int i = 0; i < 32; ++i) o[i] = 0;
+      }
+      uint32_t w[32];
+      if (f32) {
+#pragma unroll
+        for (int i = 0; i < 32; ++i) w[i] = __float_as_uint(__uint_as_float(o[i]) * w0);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          const __nv_bfloat162 v = __floats2bfloat162_rn(__uint_as_float(o[2 * i]) * w0, __uint_as_float(o[2 * i + 1]) * w0);
+          w[i] = *reinterpret_cast<const uint32_t*>(&v);
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        if (!f32 && i >= 4) break;
+        const int k = f32 ? i : 4 * h + i;
+        *reinterpret_cast<uint4*>(tile + lane * 128 + ((k ^ (lane & 7)) << 4)) =
+            make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+      }
+    }
+    fence_proxy_async();
+    __syncwarp();
+    if (lane == 0)
+      asm volatile(
+          "cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%2, %3}], [%1];\n\t"
+          "cp.async.bulk.commit_group;" ::"l"(reinterpret_cast<uint64_t>(map)),
+          "r"(su32(tile)), "r"(col + c), "r"(row)
+          : "memory");
+  }
+  if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+  __syncwarp();
+}
+
+// The same joined with the own rows: plus w1 times their output where w1 != 0. 32-column slices go through the tile so that
+// global accesses are whole row segments. `base`: element offset of the warp's first head, first column in out and own.
+__device__ __forceinline__ void store_join(uint32_t tcol, bool have_o, float w0, float w1, float* tile, const float* own,
+                                           void* out, bool f32, size_t base, int lane, int c_lo) {
   const int c4 = lane & 7;
-  const bool join = __any_sync(0xffffffffu, w1 != 0.f);
 #pragma unroll 1
   for (int c = c_lo; c < c_lo + DVH / 2; c += 32) {
     uint32_t o[32];
+    float4 p[8];
     if (have_o) {
       tmem_ld32(tcol + c, o);
-      tmem_wait_ld();
     } else {
 #pragma unroll
       for (int i = 0; i < 32; ++i) o[i] = 0;
     }
-    float4 p[8];
-    if (join) {
 #pragma unroll
-      for (int r = 0; r < 8; ++r)
-        if (__shfl_sync(0xffffffffu, w1, 4 * r + (lane >> 3)) != 0.f)
-          p[r] = *reinterpret_cast<const float4*>(own + base + (size_t)(4 * r + (lane >> 3)) * DV + c + 4 * c4);
-    }
+    for (int r = 0; r < 8; ++r)
+      if (__shfl_sync(0xffffffffu, w1, 4 * r + (lane >> 3)) != 0.f)
+        p[r] = *reinterpret_cast<const float4*>(own + base + (size_t)(4 * r + (lane >> 3)) * DV + c + 4 * c4);
+    if (have_o) tmem_wait_ld();
 #pragma unroll
     for (int i = 0; i < 8; ++i)
       *reinterpret_cast<float4*>(tile + lane * 32 + ((i ^ (lane & 7)) << 2)) =
@@ -308,7 +360,7 @@ __device__ __forceinline__ void store_out(uint32_t tcol, bool have_o, float w0, 
       const int h = 4 * r + (lane >> 3);
       float4 v = *reinterpret_cast<const float4*>(tile + h * 32 + ((c4 ^ (h & 7)) << 2));
       const size_t at = base + (size_t)h * DV + c + 4 * c4;
-      const float w = join ? __shfl_sync(0xffffffffu, w1, h) : 0.f;
+      const float w = __shfl_sync(0xffffffffu, w1, h);
       if (w != 0.f) v = make_float4(fmaf(w, p[r].x, v.x), fmaf(w, p[r].y, v.y), fmaf(w, p[r].z, v.z), fmaf(w, p[r].w, v.w));
       if (f32) {
         *reinterpret_cast<float4*>(static_cast<float*>(out) + at) = v;
@@ -325,7 +377,8 @@ __device__ __forceinline__ void store_out(uint32_t tcol, bool have_o, float w0, 
 __global__ void __launch_bounds__(THREADS, 1)
     hs_prefix_kernel(const PrefixArgs a, const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap map,
                      const __grid_constant__ CUtensorMap map2, const __grid_constant__ CUtensorMap map1,
-                     const __grid_constant__ CUtensorMap small) {
+                     const __grid_constant__ CUtensorMap small, const __grid_constant__ CUtensorMap omap,
+                     const __grid_constant__ CUtensorMap pmap) {
   extern __shared__ __align__(1024) uint8_t smem[];
   uint64_t* const bar = reinterpret_cast<uint64_t*>(smem + OFF_BAR);
   volatile int* const abort_flag = reinterpret_cast<volatile int*>(smem + OFF_MISC + 4);
@@ -336,7 +389,7 @@ __global__ void __launch_bounds__(THREADS, 1)
   const unsigned lim = a.wait_limit;
 
   if (t == 32) {  // the copies' descriptors on their way while the barriers are set up
-    for (const CUtensorMap* m : {&qmap, &map, &map2, &small})
+    for (const CUtensorMap* m : {&qmap, &map, &map2, &small, &omap})
       asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(m)) : "memory");
   }
   if (t == 0) {
@@ -524,29 +577,34 @@ __global__ void __launch_bounds__(THREADS, 1)
       const unsigned hi = __ballot_sync(0xffffffffu, row_of(a, tok + 32, len) >= 0);
       return (uint64_t)hi << 32 | lo;
     };
-    // a unit's output: its part, or joined with the own rows. The warp's rows of P stage the stores.
+    // a unit's output: its part, or the final one, joined with the own rows. The warp's rows of P stage the stores.
     auto finish = [&](int b, int split, bool have_o) {
-      float* const tile = reinterpret_cast<float*>(prows);
       const int h0 = (int)rank * QH + (q & 1) * 32;  // the warp's first head
-      if (split >= 0) {
-        const size_t row = ((size_t)split * (a.batch - a.whole) + b - a.whole) * HEADS + h0;
-        if (have_o) store_out(trow + TMEM_O, true, 1.f, 0.f, tile, nullptr, a.part_o, true, row * DV + hf * DVH, lane, sub * (DVH / 2));
+      const bool part = split >= 0;
+      const int64_t row = part ? ((int64_t)split * (a.batch - a.whole) + b - a.whole) * HEADS + h0 : (int64_t)b * HEADS + h0;
+      float f = 1.f, fo = 0.f;
+      if (part) {
         if (sg == 0) a.part_ml[row + lane] = make_float2(m_run, l_run);
-        return;
+        if (!have_o) return;
+      } else {
+        const float own = a.own_lse ? a.own_lse[row + lane] * 1.4426950408889634f : -INFINITY;
+        const float mx = fmaxf(l_run != 0.f ? m_run : -INFINITY, own);
+        const float ref = mx == -INFINITY ? 0.f : mx;
+        f = l_run != 0.f ? exp2f(m_run == -INFINITY ? 0.f : m_run - ref) : 0.f;
+        fo = own != -INFINITY ? exp2f(own - ref) : 0.f;
+        const float total = fmaf(f, l_run, fo);
+        const float inv = total != 0.f ? 1.f / total : 0.f;
+        f *= inv;
+        fo = fo != 0.f ? fo * inv : 0.f;  // (0 itself without own rows, not 0 times a reciprocal that may be NaN)
+        if (a.own_lse) exchange(0.f);     // all threads of a head have read own_lse, which may be lse itself
+        if (sg == 0) a.lse[row + lane] = total != 0.f ? (ref + log2f(total)) * 0.6931471805599453f : -INFINITY;
       }
-      const size_t row = (size_t)b * HEADS + h0;
-      const float own = a.own_lse ? a.own_lse[row + lane] * 1.4426950408889634f : -INFINITY;
-      const float mx = fmaxf(l_run != 0.f ? m_run : -INFINITY, own);
-      const float ref = mx == -INFINITY ? 0.f : mx;
-      const float f = l_run != 0.f ? exp2f(m_run == -INFINITY ? 0.f : m_run - ref) : 0.f;
-      const float fo = own != -INFINITY ? exp2f(own - ref) : 0.f;
-      const float total = fmaf(f, l_run, fo);
-      const float inv = total != 0.f ? 1.f / total : 0.f;
-      exchange(0.f);  // all threads of a head have read own_lse, which may be lse itself
-      // (without own rows the weight is 0 itself, not 0 times a reciprocal that may be NaN: own_out may be null)
-      store_out(trow + TMEM_O, have_o, f * inv, fo != 0.f ? fo * inv : 0.f, tile, a.own_out, a.out, a.out_f32 != 0,
-                row * DV + hf * DVH, lane, sub * (DVH / 2));
-      if (sg == 0) a.lse[row + lane] = total != 0.f ? (ref + log2f(total)) * 0.6931471805599453f : -INFINITY;
+      if (__any_sync(0xffffffffu, fo != 0.f))
+        store_join(trow + TMEM_O, have_o, f, fo, reinterpret_cast<float*>(prows), a.own_out, a.out, a.out_f32 != 0,
+                   (size_t)row * DV + hf * DVH, lane, sub * (DVH / 2));
+      else
+        store_tma(trow + TMEM_O, have_o, f, prows, part ? &pmap : &omap, part || a.out_f32 != 0, hf * DVH, (int)row, lane,
+                  sub * (DVH / 2));
     };
     const float scale = a.scale_log2 > 0.f ? a.scale_log2 : 1.f;  // the maximum is taken before the scale: see below
     int g = 0;  // tiles of the pair's walk
@@ -850,6 +908,15 @@ bool make_gather_map(EncodeFn f, CUtensorMap* m, const void* rows, uint64_t coun
            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// Outputs as (column, row): boxes of 128 bytes x 32 rows, 128-byte swizzle.
+bool make_out_map(EncodeFn f, CUtensorMap* m, void* out, uint64_t rows, bool f32) {
+  const cuuint64_t dims[2] = {DV, rows}, strides[1] = {(cuuint64_t)DV * (f32 ? 4 : 2)};
+  const cuuint32_t boxes[2] = {f32 ? 32u : 64u, 32}, steps[2] = {1, 1};
+  return f(m, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, out, dims, strides, boxes, steps,
+           CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_NONE,
+           CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 }  // namespace
 
 extern "C" size_t hs_mla_prefix_workspace(hs_pool* pool, int32_t batch, int32_t max_length) {
@@ -903,7 +970,7 @@ extern "C" int hs_mla_prefix(hs_pool* pool, int32_t batch, const void* q, const 
   a.lse = lse;
   a.err = pool->err;
   hs_attention_waits(&a.wait_limit, &a.stall);
-  CUtensorMap qmap, map, map2, map1, small;
+  CUtensorMap qmap, map, map2, map1, small, omap, pmap;
   // an empty pool of rows still needs a map: one row, which page_limit = 0 keeps from being read
   const uint64_t count = std::max<int64_t>(prefix->count, 1);
   a.none = (int32_t)count;
@@ -911,7 +978,9 @@ extern "C" int hs_mla_prefix(hs_pool* pool, int32_t batch, const void* q, const 
       !make_map(encode, &map, prefix->rows, count, 1u << a.box_shift, 1) ||
       !make_map(encode, &map2, prefix->rows, count, 1u << a.box_shift, 2) || !make_map(encode, &map1, prefix->rows, count, 1, 1) ||
       !(a.page_shift < 2 ? make_gather_map(encode, &small, prefix->rows, count)
-                         : make_map(encode, &small, prefix->rows, count, 4, 1)))
+                         : make_map(encode, &small, prefix->rows, count, 4, 1)) ||
+      !make_out_map(encode, &omap, out, (uint64_t)batch * HEADS, a.out_f32 != 0) ||
+      !make_out_map(encode, &pmap, rest ? workspace : out, (uint64_t)(rest ? rest * cut.nsplit : batch) * HEADS, rest || a.out_f32))
     return HS_ERR_INVALID_ARG;
 
   cudaLaunchConfig_t cfg = {};
@@ -927,7 +996,7 @@ extern "C" int hs_mla_prefix(hs_pool* pool, int32_t batch, const void* q, const 
   attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  if (cudaLaunchKernelEx(&cfg, hs_prefix_kernel, a, qmap, map, map2, map1, small) != cudaSuccess) return HS_ERR_CUDA;
+  if (cudaLaunchKernelEx(&cfg, hs_prefix_kernel, a, qmap, map, map2, map1, small, omap, pmap) != cudaSuccess) return HS_ERR_CUDA;
   if (!rest) return HS_OK;
   cfg.gridDim = dim3((unsigned)rest * HEADS, 1, 1);
   cfg.dynamicSmemBytes = 0;
