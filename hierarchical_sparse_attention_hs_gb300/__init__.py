@@ -145,7 +145,8 @@ def _stream(s) -> int | None:
     if s is None:
         import torch
 
-        return torch.cuda.current_stream().cuda_stream
+        # the handle alone: making a Stream object of it takes longer than a small kernel
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     if isinstance(s, int):
         return s
     return s.cuda_stream

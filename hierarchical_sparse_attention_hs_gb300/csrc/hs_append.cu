@@ -11,10 +11,10 @@
 // The fraction's signed upper 32 bits, exact to 2^-32 turns, go to sincospif. (Double arithmetic per token would cost
 // more than the memory traffic: this device has few FP64 units.)
 //
-// Work. One warp per row and one warp per 16 heads of a token's queries, both looping with the grid's stride. A lane
+// Work. One warp per row and one warp per 16 heads of a token's queries, each with several once there are many. A lane
 // holds 16 latents (two 16-byte chunks for 16-bit inputs) and one pair of the key, so a row is loaded and stored in
-// whole 128-byte segments and the norm's sum and the scales' maxima are warp shuffles. All loads of a row are issued
-// before its first use. Nothing passes through shared memory.
+// whole 128-byte segments and the norm's sum and the scales' maxima are warp shuffles. Nothing passes
+// through shared memory.
 
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -36,6 +36,7 @@ constexpr int ROW_FP8 = LATENT + 4 * 4 + ROPE * 2;  // 656
 constexpr int FP8_ROPE = LATENT + 4 * 4;         // byte offset of the rotary key in an fp8 row
 constexpr int Q_HEADS = 16;                      // heads of one warp's work item: four 16-byte loads a lane in flight
 constexpr int THREADS = 128, WARPS = THREADS / 32;
+constexpr int ROW_BLOCKS = 12, Q_BLOCKS = 16;      // blocks an SM of either kind, at most
 
 struct AppendArgs {
   const void* kv;
@@ -60,6 +61,7 @@ struct AppendArgs {
   const int32_t* pages;
   int64_t page_stride, page_limit;  // pages 0 .. page_limit - 1 lie within the rows
   int32_t page_shift;
+  int32_t per_warp;       // tokens of a warp's rows
   int32_t row_blocks;     // blocks 0 .. row_blocks - 1 write rows, the others turn queries
   int32_t* err;
 };
@@ -139,110 +141,137 @@ __device__ __forceinline__ bool token_of(const AppendArgs& a, int i, int* req, i
   return *pos < a.ctx && *req >= 0 && *req < a.max_batch;
 }
 
+// A warp's `per` consecutive tokens. Where they go is looked up 32 tokens at a time, one lane each (position, request, then
+// slot and page: a chain of loads that every row would otherwise wait for), and a row's values are loaded while the one
+// before is worked on.
 template <class T, bool FP8, bool INTER>
 __device__ __forceinline__ void append_rows(const AppendArgs& a, int lane, int warp) {
   constexpr int RB = FP8 ? ROW_FP8 : ROW_BF16;
+  constexpr uint32_t ALL = 0xffffffffu;
   const unsigned long long rate = turn_rate(a.inv_freq, lane);
-  for (int i = warp; i < a.ntok; i += a.row_blocks * WARPS) {
-    const T* x = static_cast<const T*>(a.kv) + (int64_t)i * a.kv_stride;
-    Raw8<T> raw[2];
-    raw[0].load(x + 8 * lane);
-    raw[1].load(x + LATENT / 2 + 8 * lane);
-    const float k0 = to_f32(x[LATENT + (INTER ? 2 * lane : lane)]);
-    const float k1 = to_f32(x[LATENT + (INTER ? 2 * lane + 1 : lane + PAIRS)]);
-    int req, pos;
-    if (!token_of(a, i, &req, &pos)) {
-      if (lane == 0 && pos >= 0) atomicOr(a.err, HS_DEVERR_RANGE);
-      continue;
+  float wt[2][8] = {};  // the lane's weights of the norm
+  if (a.norm_weight) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      Raw8<float> w;
+      w.load(a.norm_weight + h * (LATENT / 2) + 8 * lane);
+      w.get(wt[h]);
     }
-    const int64_t rq = req;
-    // where the row goes: the hot slot that maps the token, the paged rows, the history
-    uint8_t* dst[3] = {nullptr, nullptr, a.history ? a.history + rq * a.req_stride + (int64_t)pos * RB : nullptr};
-    const int slot = __ldcg(a.tok2slot + rq * a.ctx + pos);
-    if (slot >= 0 && slot < a.slots) dst[0] = a.hot + (rq * a.slots + slot) * (int64_t)RB;
-    if (a.paged) {
-      const int64_t pi = pos >> a.page_shift;
-      const int64_t page = pi < a.page_stride ? ld_fresh(a.pages + rq * a.page_stride + pi) : -1;
-      if (page >= 0 && page < a.page_limit)
-        dst[1] = a.paged + ((page << a.page_shift) + (pos & ((1 << a.page_shift) - 1))) * (int64_t)RB;
-    }
-    float z[2][8];
-    raw[0].get(z[0]);
-    raw[1].get(z[1]);
-    if (a.norm_weight) {
-      float ss = 0.f;
-#pragma unroll
-      for (int h = 0; h < 2; ++h)
-#pragma unroll
-        for (int e = 0; e < 8; ++e) ss = fmaf(z[h][e], z[h][e], ss);
-#pragma unroll
-      for (int o = 16; o; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-      const float r = rsqrtf(ss * (1.f / LATENT) + a.eps);
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        Raw8<float> w;
-        w.load(a.norm_weight + h * (LATENT / 2) + 8 * lane);
-        float wv[8];
-        w.get(wv);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) z[h][e] *= r * wv[e];
-      }
-    }
-    // the rotary key: lane j turns pair j; lane l then writes the values 2l and 2l + 1
-    float c, s;
-    angle_of(rate, pos, &c, &s);
-    const float t0 = k0 * c - k1 * s, t1 = k0 * s + k1 * c;
-    uint32_t kw;
-    if (INTER) {
-      kw = pack_bf16(t0, t1);
-    } else {
-      const int src = (2 * lane) & 31;
-      const float lo0 = __shfl_sync(0xffffffffu, t0, src), lo1 = __shfl_sync(0xffffffffu, t0, src + 1);
-      const float hi0 = __shfl_sync(0xffffffffu, t1, src), hi1 = __shfl_sync(0xffffffffu, t1, src + 1);
-      kw = lane < 16 ? pack_bf16(lo0, lo1) : pack_bf16(hi0, hi1);
-    }
-    if (FP8) {
-      // lanes 0-15 hold groups 0 and 2 of 128 latents, lanes 16-31 groups 1 and 3
-      uint2 w[2];
-      float scale[2];
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        float m = 0.f;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) m = fmaxf(m, fabsf(z[h][e]));
-#pragma unroll
-        for (int o = 8; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-        scale[h] = m > 0.f ? fmaxf(m / 448.f, 1.17549435e-38f) : 1.f;  // at least 2^-126: its reciprocal is finite
-        const float inv = 1.f / scale[h];
-        w[h] = make_uint2(pack_e4m3(z[h][0] * inv, z[h][1] * inv, z[h][2] * inv, z[h][3] * inv),
-                          pack_e4m3(z[h][4] * inv, z[h][5] * inv, z[h][6] * inv, z[h][7] * inv));
-      }
-#pragma unroll
-      for (int d = 0; d < 3; ++d) {
-        uint8_t* o = dst[d];
-        if (!o) continue;
-        *reinterpret_cast<uint2*>(o + 8 * lane) = w[0];
-        *reinterpret_cast<uint2*>(o + LATENT / 2 + 8 * lane) = w[1];
-        if ((lane & 15) == 0) {
-          float* sc = reinterpret_cast<float*>(o + LATENT) + (lane >> 4);
-          sc[0] = scale[0];
-          sc[2] = scale[1];
+  }
+  const int64_t begin = (int64_t)warp * a.per_warp;
+  const int end = (int)min((int64_t)a.ntok, begin + a.per_warp);
+  const T* const kv = static_cast<const T*>(a.kv);
+  Raw8<T> ahead[2];
+  T pair[2];
+  auto load = [&](int i) {
+    const T* x = kv + (int64_t)i * a.kv_stride;
+    ahead[0].load(x + 8 * lane);
+    ahead[1].load(x + LATENT / 2 + 8 * lane);
+    pair[0] = x[LATENT + (INTER ? 2 * lane : lane)];
+    pair[1] = x[LATENT + (INTER ? 2 * lane + 1 : lane + PAIRS)];
+  };
+  if (begin < end) load((int)begin);
+  for (int i0 = (int)min(begin, (int64_t)a.ntok); i0 < end; i0 += 32) {
+    int my_req = -1, my_pos = -1, my_slot = -1, my_row = -1;
+    if (i0 + lane < end) {
+      if (token_of(a, i0 + lane, &my_req, &my_pos)) {
+        my_slot = __ldcg(a.tok2slot + (int64_t)my_req * a.ctx + my_pos);
+        if (a.paged) {
+          const int64_t pi = my_pos >> a.page_shift;
+          const int page = pi < a.page_stride ? a.pages[my_req * a.page_stride + pi] : -1;
+          if (page >= 0 && page < a.page_limit) my_row = (page << a.page_shift) + (my_pos & ((1 << a.page_shift) - 1));
         }
-        *reinterpret_cast<uint32_t*>(o + FP8_ROPE + 4 * lane) = kw;
+      } else {
+        if (my_pos >= 0) atomicOr(a.err, HS_DEVERR_RANGE);
+        my_pos = -1;
       }
-    } else {
-      uint4 w[2];
+    }
+    const int m = min(32, end - i0);
+    for (int k = 0; k < m; ++k) {
+      const Raw8<T> raw[2] = {ahead[0], ahead[1]};
+      const float k0 = to_f32(pair[0]), k1 = to_f32(pair[1]);
+      if (i0 + k + 1 < end) load(i0 + k + 1);
+      const int pos = __shfl_sync(ALL, my_pos, k);
+      const int64_t req = __shfl_sync(ALL, my_req, k);
+      const int slot = __shfl_sync(ALL, my_slot, k), row = __shfl_sync(ALL, my_row, k);
+      if (pos < 0) continue;
+      // where the row goes: the hot slot that maps the token, the paged rows, the history
+      uint8_t* dst[3] = {slot >= 0 && slot < a.slots ? a.hot + (req * a.slots + slot) * RB : nullptr,
+                         row >= 0 ? a.paged + (int64_t)row * RB : nullptr,
+                         a.history ? a.history + req * a.req_stride + (int64_t)pos * RB : nullptr};
+      float z[2][8];
+      raw[0].get(z[0]);
+      raw[1].get(z[1]);
+      if (a.norm_weight) {
+        float ss = 0.f;
 #pragma unroll
-      for (int h = 0; h < 2; ++h)
-        w[h] = make_uint4(pack_bf16(z[h][0], z[h][1]), pack_bf16(z[h][2], z[h][3]), pack_bf16(z[h][4], z[h][5]),
-                          pack_bf16(z[h][6], z[h][7]));
+        for (int h = 0; h < 2; ++h)
 #pragma unroll
-      for (int d = 0; d < 3; ++d) {
-        uint8_t* o = dst[d];
-        if (!o) continue;
-        *reinterpret_cast<uint4*>(o + 16 * lane) = w[0];
-        *reinterpret_cast<uint4*>(o + LATENT + 16 * lane) = w[1];
-        *reinterpret_cast<uint32_t*>(o + 2 * LATENT + 4 * lane) = kw;
+          for (int e = 0; e < 8; ++e) ss = fmaf(z[h][e], z[h][e], ss);
+#pragma unroll
+        for (int o = 16; o; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+        const float r = rsqrtf(ss * (1.f / LATENT) + a.eps);
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+          for (int e = 0; e < 8; ++e) z[h][e] *= r * wt[h][e];
+      }
+      // the rotary key: lane j turns pair j; lane l then writes the values 2l and 2l + 1
+      float c, s;
+      angle_of(rate, pos, &c, &s);
+      const float t0 = k0 * c - k1 * s, t1 = k0 * s + k1 * c;
+      uint32_t kw;
+      if (INTER) {
+        kw = pack_bf16(t0, t1);
+      } else {
+        const int src = (2 * lane) & 31;
+        const float lo0 = __shfl_sync(0xffffffffu, t0, src), lo1 = __shfl_sync(0xffffffffu, t0, src + 1);
+        const float hi0 = __shfl_sync(0xffffffffu, t1, src), hi1 = __shfl_sync(0xffffffffu, t1, src + 1);
+        kw = lane < 16 ? pack_bf16(lo0, lo1) : pack_bf16(hi0, hi1);
+      }
+      if (FP8) {
+        // lanes 0-15 hold groups 0 and 2 of 128 latents, lanes 16-31 groups 1 and 3
+        uint2 w[2];
+        float scale[2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          float m = 0.f;
+#pragma unroll
+          for (int e = 0; e < 8; ++e) m = fmaxf(m, fabsf(z[h][e]));
+#pragma unroll
+          for (int o = 8; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+          scale[h] = m > 0.f ? fmaxf(m / 448.f, 1.17549435e-38f) : 1.f;  // at least 2^-126: its reciprocal is finite
+          const float inv = 1.f / scale[h];
+          w[h] = make_uint2(pack_e4m3(z[h][0] * inv, z[h][1] * inv, z[h][2] * inv, z[h][3] * inv),
+                            pack_e4m3(z[h][4] * inv, z[h][5] * inv, z[h][6] * inv, z[h][7] * inv));
+        }
+#pragma unroll
+        for (int d = 0; d < 3; ++d) {
+          uint8_t* o = dst[d];
+          if (!o) continue;
+          *reinterpret_cast<uint2*>(o + 8 * lane) = w[0];
+          *reinterpret_cast<uint2*>(o + LATENT / 2 + 8 * lane) = w[1];
+          if ((lane & 15) == 0) {
+            float* sc = reinterpret_cast<float*>(o + LATENT) + (lane >> 4);
+            sc[0] = scale[0];
+            sc[2] = scale[1];
+          }
+          *reinterpret_cast<uint32_t*>(o + FP8_ROPE + 4 * lane) = kw;
+        }
+      } else {
+        uint4 w[2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+          w[h] = make_uint4(pack_bf16(z[h][0], z[h][1]), pack_bf16(z[h][2], z[h][3]), pack_bf16(z[h][4], z[h][5]),
+                            pack_bf16(z[h][6], z[h][7]));
+#pragma unroll
+        for (int d = 0; d < 3; ++d) {
+          uint8_t* o = dst[d];
+          if (!o) continue;
+          *reinterpret_cast<uint4*>(o + 16 * lane) = w[0];
+          *reinterpret_cast<uint4*>(o + LATENT + 16 * lane) = w[1];
+          *reinterpret_cast<uint32_t*>(o + 2 * LATENT + 4 * lane) = kw;
+        }
       }
     }
   }
@@ -256,13 +285,13 @@ __device__ __forceinline__ void turn_queries(const AppendArgs& a, int lane, int 
   const int64_t items = (int64_t)a.ntok * a.head_items;
   for (int64_t it = warp; it < items; it += warps) {
     const int i = (int)(it / a.head_items), h0 = (int)(it - (int64_t)i * a.head_items) * Q_HEADS + sub;
-    int req, pos;
-    if (!token_of(a, i, &req, &pos)) continue;  // the row's warp reports it
     const T* src = static_cast<const T*>(a.q_rope) + (int64_t)i * a.qr_token + 8 * c8;
     Raw8<T> raw[Q_HEADS / 4];
 #pragma unroll
     for (int u = 0; u < Q_HEADS / 4; ++u)
       if (h0 + 4 * u < a.heads) raw[u].load(src + (int64_t)(h0 + 4 * u) * a.qr_head);
+    int req, pos;
+    if (!token_of(a, i, &req, &pos)) continue;  // the row's warp reports it
     float cl, sl;
     angle_of(rate, pos, &cl, &sl);
     // interleaved: this lane's four pairs are 4 c8 ..; half-split: its eight values belong to pairs 8 (c8 % 4) ..
@@ -407,12 +436,14 @@ extern "C" int hs_append(hs_pool* pool, int32_t layer, int32_t ntok, const hs_ap
   }
   a.err = pool->err;
 
-  // A few blocks' worth of warps per SM, each looping over several rows once there are more, so that the turn rates
-  // (64-bit arithmetic) are worked out once per warp and not per row.
-  const int64_t most = (int64_t)pool->num_sms * 16;
+  // As many warps as the device holds, each with its share of the tokens (and of the queries' items): the turn rates (64-bit
+  // arithmetic) are worked out once per warp, not per row.
+  const int64_t most = (int64_t)pool->num_sms * ROW_BLOCKS;
   const int64_t items = (int64_t)ntok * a.head_items;
-  a.row_blocks = (int32_t)std::min<int64_t>(((int64_t)ntok + WARPS - 1) / WARPS, most);
-  const int64_t q_blocks = std::min<int64_t>((items + WARPS - 1) / WARPS, most);
+  a.per_warp = (int32_t)((ntok + most * WARPS - 1) / (most * WARPS));
+  const int64_t row_warps = ((int64_t)ntok + a.per_warp - 1) / a.per_warp;
+  a.row_blocks = (int32_t)((row_warps + WARPS - 1) / WARPS);
+  const int64_t q_blocks = std::min<int64_t>((items + WARPS - 1) / WARPS, (int64_t)pool->num_sms * Q_BLOCKS);
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(a.row_blocks + q_blocks), 1, 1);
   cfg.blockDim = dim3(THREADS, 1, 1);
