@@ -231,8 +231,13 @@ __device__ __forceinline__ void find_rows(const PrefixArgs& a, Box& s, int tok0,
   if (a.page_shift < 2) {
 #pragma unroll
     for (int i = 1; i < 4; ++i) s.row[i] = row(i);
-    // four rows that the pool holds are gathered by one copy; with some missing they are loaded one by one
-    s.have = s.row[0] != a.none && s.row[1] != a.none && s.row[2] != a.none && s.row[3] != a.none ? 4 : 0;
+    // Four rows are gathered by one copy if the pool holds any of them. A missing one takes the place of one that is there:
+    // its weight is 0, and where the row's values are not finite the outputs are not a number either way (such a value
+    // makes the row's own score infinite or not a number). Without any they are filled with zeros one by one.
+    const int some = min(min(s.row[0], s.row[1]), min(s.row[2], s.row[3]));
+    s.have = some != a.none ? 4 : 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) s.row[i] = s.row[i] != a.none ? s.row[i] : some;
   }
 }
 // Loads it: NBLK column blocks from `blk` on to `dst`, where a column block's 64 rows lie together. `map` has boxes of one
@@ -334,43 +339,54 @@ __device__ __forceinline__ void store_tma(uint32_t tcol, bool have_o, float w0, 
 __device__ __forceinline__ void store_join(uint32_t tcol, bool have_o, float w0, float w1, float* tile, const float* own,
                                            void* out, bool f32, size_t base, int lane, int c_lo) {
   const int c4 = lane & 7;
+  uint32_t joined = 0;  // which of the lane's eight rows of a slice have own rows
+#pragma unroll
+  for (int r = 0; r < 8; ++r) joined |= (__shfl_sync(0xffffffffu, w1, 4 * r + (lane >> 3)) != 0.f ? 1u : 0u) << r;
+  float4 p[8];  // the own rows' slice, loaded a slice ahead
+  auto load_own = [&](int c) {
+#pragma unroll
+    for (int r = 0; r < 8; ++r)
+      if (joined >> r & 1) p[r] = *reinterpret_cast<const float4*>(own + base + (size_t)(4 * r + (lane >> 3)) * DV + c + 4 * c4);
+  };
+  load_own(c_lo);
 #pragma unroll 1
   for (int c = c_lo; c < c_lo + DVH / 2; c += 32) {
     uint32_t o[32];
-    float4 p[8];
     if (have_o) {
       tmem_ld32(tcol + c, o);
+      tmem_wait_ld();
     } else {
 #pragma unroll
       for (int i = 0; i < 32; ++i) o[i] = 0;
     }
-#pragma unroll
-    for (int r = 0; r < 8; ++r)
-      if (__shfl_sync(0xffffffffu, w1, 4 * r + (lane >> 3)) != 0.f)
-        p[r] = *reinterpret_cast<const float4*>(own + base + (size_t)(4 * r + (lane >> 3)) * DV + c + 4 * c4);
-    if (have_o) tmem_wait_ld();
 #pragma unroll
     for (int i = 0; i < 8; ++i)
       *reinterpret_cast<float4*>(tile + lane * 32 + ((i ^ (lane & 7)) << 2)) =
           make_float4(__uint_as_float(o[4 * i]) * w0, __uint_as_float(o[4 * i + 1]) * w0,
                       __uint_as_float(o[4 * i + 2]) * w0, __uint_as_float(o[4 * i + 3]) * w0);
     __syncwarp();
+    float4 v[8];
 #pragma unroll
     for (int r = 0; r < 8; ++r) {
       const int h = 4 * r + (lane >> 3);
-      float4 v = *reinterpret_cast<const float4*>(tile + h * 32 + ((c4 ^ (h & 7)) << 2));
-      const size_t at = base + (size_t)h * DV + c + 4 * c4;
+      v[r] = *reinterpret_cast<const float4*>(tile + h * 32 + ((c4 ^ (h & 7)) << 2));
       const float w = __shfl_sync(0xffffffffu, w1, h);
-      if (w != 0.f) v = make_float4(fmaf(w, p[r].x, v.x), fmaf(w, p[r].y, v.y), fmaf(w, p[r].z, v.z), fmaf(w, p[r].w, v.w));
+      if (joined >> r & 1)
+        v[r] = make_float4(fmaf(w, p[r].x, v[r].x), fmaf(w, p[r].y, v[r].y), fmaf(w, p[r].z, v[r].z), fmaf(w, p[r].w, v[r].w));
+    }
+    __syncwarp();
+    if (c + 32 < c_lo + DVH / 2) load_own(c + 32);
+#pragma unroll
+    for (int r = 0; r < 8; ++r) {
+      const size_t at = base + (size_t)(4 * r + (lane >> 3)) * DV + c + 4 * c4;
       if (f32) {
-        *reinterpret_cast<float4*>(static_cast<float*>(out) + at) = v;
+        *reinterpret_cast<float4*>(static_cast<float*>(out) + at) = v[r];
       } else {
-        const __nv_bfloat162 lo = __floats2bfloat162_rn(v.x, v.y), hi = __floats2bfloat162_rn(v.z, v.w);
+        const __nv_bfloat162 lo = __floats2bfloat162_rn(v[r].x, v[r].y), hi = __floats2bfloat162_rn(v[r].z, v[r].w);
         *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(out) + at) =
             make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
       }
     }
-    __syncwarp();
   }
 }
 

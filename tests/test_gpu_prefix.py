@@ -211,6 +211,28 @@ def test_not_a_number_shows(pool):
     assert torch.isfinite(out[0]).all() and torch.isfinite(out[1, :7]).all() and torch.isfinite(out[1, 8:]).all()
 
 
+@pytest.mark.parametrize("page", [1, 2, 16])
+def test_infinite_values_stay_where_they_are(pool, page):
+    """An infinite latent of a row that is attended to: its score is infinite, so a head's outputs are all not a number
+    (+inf) or only the column of the value is (-inf: weight 0 times infinity), as the formula has it. Rows next to pages that
+    the pool does not hold change nothing."""
+    c = Case(2, 300, page, seed=12, holes=0.4, garbage=False)
+    c.q[1, :, 5] = 0.25  # the second request's scores of that row: the value's sign
+    c.q[0, :, 5] = -0.25
+    c.rows[c.at[17], 5] = math.inf
+    out, lse = c.run(pool)
+    torch.cuda.synchronize()
+    assert torch.isnan(out[1]).all() and torch.isnan(lse[1]).all()
+    assert torch.isnan(out[0, :, 5]).all() and torch.isfinite(lse[0]).all()
+    got, c.rows[c.at[17]] = out[0].double(), 0
+    rest = torch.cat([c.at[:17], c.at[18:]]).cuda()
+    k = c.rows[rest].double()
+    s = c.scale * c.q[0].double() @ k.t()
+    want = torch.softmax(s, -1) @ k[:, :DV]
+    keep = torch.arange(DV, device="cuda") != 5
+    assert ((got - want).abs()[:, keep] <= 2.1 * 2.0 ** -8 * (torch.softmax(s, -1) @ k[:, :DV].abs())[:, keep]).all()
+
+
 def test_repeated_pages_and_results(pool):
     """A page may appear twice (its rows then count twice), and the same call gives the same bits."""
     c = Case(9, 900, 16, seed=8)
