@@ -279,22 +279,23 @@ __device__ __forceinline__ void load_box(const PrefixArgs& a, const CUtensorMap*
 
 // One softmax warp's part of an output without own rows: its 32 heads' columns c_lo .. c_lo + 127 from tensor memory times
 // w0 (zeros without O), 128 bytes of every row at a time, staged in `tile` (32 rows of 128 bytes, 16-byte chunk k of row r at
-// k ^ (r % 8): no conflicts, and the 128-byte swizzle of `map`) and stored by TMA from (column, row) on. The tile may be
-// written again, and the kernel end, once the last copy has read it: the function waits for that. (Through registers
-// instead, tile to coalesced stores, a unit's 64 KB took 2.7 us a CTA.)
+// k ^ (r % 8): no conflicts, and the 128-byte swizzle of `map`) and stored by TMA from (column, row) on. The last copy is
+// left in flight: wait_tile_read before the tile is written again and before the kernel ends. (Through registers instead,
+// tile to coalesced stores, a unit's 64 KB took 2.7 us a CTA.)
+__device__ __forceinline__ void wait_tile_read(int lane) {
+  if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+  __syncwarp();
+}
 __device__ __forceinline__ void store_tma(uint32_t tcol, bool have_o, float w0, uint8_t* tile, const CUtensorMap* map,
                                           bool f32, int col, int row, int lane, int c_lo) {
   const int step = f32 ? 32 : 64;
 #pragma unroll 1
   for (int c = c_lo; c < c_lo + DVH / 2; c += step) {
-    if (c > c_lo) {
-      if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
-      __syncwarp();
-    }
+    uint32_t w[32];  // the row's 128 bytes
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      uint32_t o[32];
       if (f32 && h == 1) break;
+      uint32_t o[32];
       if (have_o) {
         tmem_ld32(tcol + c + 32 * h, o);
         tmem_wait_ld();
@@ -302,7 +303,6 @@ __device__ __forceinline__ void store_tma(uint32_t tcol, bool have_o, float w0, 
 #pragma unroll
         for (int i = 0; i < 32; ++i) o[i] = 0;
       }
-      uint32_t w[32];
       if (f32) {
 #pragma unroll
         for (int i = 0; i < 32; ++i) w[i] = __float_as_uint(__uint_as_float(o[i]) * w0);
@@ -310,17 +310,15 @@ __device__ __forceinline__ void store_tma(uint32_t tcol, bool have_o, float w0, 
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
           const __nv_bfloat162 v = __floats2bfloat162_rn(__uint_as_float(o[2 * i]) * w0, __uint_as_float(o[2 * i + 1]) * w0);
-          w[i] = *reinterpret_cast<const uint32_t*>(&v);
+          w[16 * h + i] = *reinterpret_cast<const uint32_t*>(&v);
         }
       }
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        if (!f32 && i >= 4) break;
-        const int k = f32 ? i : 4 * h + i;
-        *reinterpret_cast<uint4*>(tile + lane * 128 + ((k ^ (lane & 7)) << 4)) =
-            make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
-      }
     }
+    wait_tile_read(lane);
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      *reinterpret_cast<uint4*>(tile + lane * 128 + ((i ^ (lane & 7)) << 4)) =
+          make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
     fence_proxy_async();
     __syncwarp();
     if (lane == 0)
@@ -330,8 +328,6 @@ __device__ __forceinline__ void store_tma(uint32_t tcol, bool have_o, float w0, 
           "r"(su32(tile)), "r"(col + c), "r"(row)
           : "memory");
   }
-  if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
-  __syncwarp();
 }
 
 // The same joined with the own rows: plus w1 times their output where w1 != 0. 32-column slices go through the tile so that
@@ -349,6 +345,7 @@ __device__ __forceinline__ void store_join(uint32_t tcol, bool have_o, float w0,
       if (joined >> r & 1) p[r] = *reinterpret_cast<const float4*>(own + base + (size_t)(4 * r + (lane >> 3)) * DV + c + 4 * c4);
   };
   load_own(c_lo);
+  wait_tile_read(lane);
 #pragma unroll 1
   for (int c = c_lo; c < c_lo + DVH / 2; c += 32) {
     uint32_t o[32];
@@ -706,6 +703,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         }
         m_run = m_new;
         l_run += sum[0] + sum[1];
+        if (j == 0) wait_tile_read(lane);  // the stores of the unit before are staged in the warp's rows of P
 #pragma unroll
         for (int c = 0; c < SEG / 8; ++c)
           *reinterpret_cast<uint4*>(prows + lane * 128 + ((c ^ (lane & 7)) << 4)) =
@@ -716,10 +714,11 @@ __global__ void __launch_bounds__(THREADS, 1)
         if (lane == 0) arrive_lead(lead + B_PFULL * 8);
       }
       if (!ok) break;
-      const Walk x = w;
-      w.set(a, x.u + (int)(gridDim.x >> 1), tiles);
+      const int b = w.b, split = w.split;
+      const bool have_o = w.nt > 0;
+      w.set(a, w.u + (int)(gridDim.x >> 1), tiles);
       mask_next = w.u < a.units && w.nt > 0 ? key_mask(w.j0) : 0;
-      if (x.nt > 0) {
+      if (have_o) {
         ok = __all_sync(0xffffffffu, bar_wait(bar + B_PDONE, (unsigned)(g - 1) & 1u, abort_flag, lim));
         if (!ok) break;
         const float* const share = exchange(l_run);
@@ -727,9 +726,10 @@ __global__ void __launch_bounds__(THREADS, 1)
         l_run = (share[0] + share[QH]) + (share[2 * QH] + share[3 * QH]);
         tc_fence_after();
       }
-      finish(x.b, x.split, x.nt > 0);
+      finish(b, split, have_o);
       tc_fence_before();
     }
+    wait_tile_read(lane);
   }
 
   tc_fence_before();
@@ -744,8 +744,8 @@ __global__ void __launch_bounds__(THREADS, 1)
       for (int i = 0; i < 50; ++i) __nanosleep(1000);
       if (lane == 0) atomicOr(a.err, HS_DEVERR_TIMEOUT);
     }
+    __syncwarp();
   }
-  __syncthreads();
   cluster_sync();
   tc_fence_after();
   if (warp == MMA_WARP)
