@@ -35,6 +35,7 @@ constexpr int ROW_BF16 = WIDTH * 2;              // 1152
 constexpr int ROW_FP8 = LATENT + 4 * 4 + ROPE * 2;  // 656
 constexpr int FP8_ROPE = LATENT + 4 * 4;         // byte offset of the rotary key in an fp8 row
 constexpr int Q_HEADS = 16;                      // heads of one warp's work item: four 16-byte loads a lane in flight
+constexpr int MAX_TOKENS = 1 << 30;              // and items of 16 heads of a token's queries
 constexpr int THREADS = 128, WARPS = THREADS / 32;
 constexpr int ROW_BLOCKS = 12, Q_BLOCKS = 16;      // blocks an SM of either kind, at most
 
@@ -282,9 +283,9 @@ template <class T, bool INTER>
 __device__ __forceinline__ void turn_queries(const AppendArgs& a, int lane, int warp, int warps) {
   const unsigned long long rate = turn_rate(a.inv_freq, lane);
   const int c8 = lane & 7, sub = lane >> 3;
-  const int64_t items = (int64_t)a.ntok * a.head_items;
-  for (int64_t it = warp; it < items; it += warps) {
-    const int i = (int)(it / a.head_items), h0 = (int)(it - (int64_t)i * a.head_items) * Q_HEADS + sub;
+  const unsigned items = (unsigned)a.ntok * (unsigned)a.head_items;  // the host has seen to it that this is below 2^31
+  for (unsigned it = (unsigned)warp; it < items; it += (unsigned)warps) {
+    const int i = (int)(it / (unsigned)a.head_items), h0 = (int)(it - (unsigned)i * (unsigned)a.head_items) * Q_HEADS + sub;
     const T* src = static_cast<const T*>(a.q_rope) + (int64_t)i * a.qr_token + 8 * c8;
     Raw8<T> raw[Q_HEADS / 4];
 #pragma unroll
@@ -399,6 +400,7 @@ extern "C" int hs_append(hs_pool* pool, int32_t layer, int32_t ntok, const hs_ap
                    !stride_ok(d.q_rope_head_stride, ROPE, size, d.q_heads) ||
                    !stride_ok(d.q_token_stride, WIDTH, 2, ntok) || !stride_ok(d.q_head_stride, WIDTH, 2, d.q_heads)))
     return HS_ERR_INVALID_ARG;
+  if (ntok > MAX_TOKENS || (int64_t)ntok * ((d.q_heads + Q_HEADS - 1) / Q_HEADS) > MAX_TOKENS) return HS_ERR_INVALID_ARG;
   if (!hs_on_device(pool)) return HS_ERR_INVALID_ARG;
 
   AppendArgs a;

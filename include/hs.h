@@ -341,12 +341,13 @@ typedef struct {
  * Every tier that holds the token gets the row: the pool's row source when `to_history` is non-zero (the host pool,
  * which must be writable, or the no-IO copy of a pool that has one), the paged rows when `paged` is given (list
  * req_ids[i]), and always the hot slot that the token occupies, if it occupies one, so that a resolve after a rewrite
- * (a rolled-back speculation, say) never serves the old row. Norm and rotation are computed in 32 bits; each value is
+ * (a rolled-back speculation, say) never serves the old row. (Of a no-IO pool the host copy is not written; of a pool
+ * whose layers read overlapping host rows, the row that they share.) Norm and rotation are computed in 32 bits; each value is
  * rounded once.
  * A token with a negative position is padding: it touches nothing. One whose position is >= ctx or whose request is not
  * in 0 .. max_batch-1 is skipped whole, and the error word gets HS_DEVERR_RANGE. (request, position) pairs are distinct
- * within a call (not checked: rows of a repeated pair may mix). ntok == 0 is a no-op; with req_ids NULL ntok <=
- * max_batch. At least one of `paged`, to_history and q_rope is given. Enqueued on `stream` (of the pool's device, which
+ * within a call (not checked: rows of a repeated pair may mix). ntok == 0 is a no-op; ntok <= 2^30, and
+ * so is ntok * ceil(q_heads / 16); with req_ids NULL ntok <= max_batch. At least one of `paged`, to_history and q_rope is given. Enqueued on `stream` (of the pool's device, which
  * must be the current one: HS_ERR_INVALID_ARG); capturable. Order it before the resolve, prefetch, gather or attention
  * that reads the rows. Basis: the full history in host memory that the paper's cache sits on (Abstract) and the ordinary
  * KV blocks of the "Hybrid HiSparse" card (Timeline) have to be written by somebody; the pages name no writer.

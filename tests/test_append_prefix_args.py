@@ -72,6 +72,8 @@ def test_append_refuses_calls():
     append(INVALID, layer=-1)
     append(INVALID, layer=2)
     append(INVALID, ntok=-1)
+    append(INVALID, ntok=(1 << 30) + 1)
+    append(INVALID, ntok=1 << 28, q_heads=81)
     append(INVALID, ntok=5, req_ids=None)  # token i is request i: at most max_batch
     append(UNSUPPORTED, pool=fake_pool(row_bytes=1024))
     append(INVALID, to_history=False, q_rope=None, q=None, q_heads=0)  # nothing to do

@@ -232,6 +232,21 @@ def test_far_positions():
     s.check_all(history=False)
 
 
+def test_rows_past_four_gigabytes():
+    """Row offsets of the paged pool pass 32 bits."""
+    s = Setup(40, requests=2, ctx=128, page=64)
+    count = (5 << 30) // 1152 // 64 * 64
+    s.rows = torch.empty((count, 1152), dtype=torch.uint8, device="cuda")
+    s.pages = (count // 64 - 1 - torch.arange(4).int() * 3).view(2, 2).contiguous()
+    s.rows[-700:] = 9
+    s.run()
+    i = s.at()
+    assert int(i.min()) * 1152 > 1 << 32
+    s.check_rows(s.rows[torch.from_numpy(i).cuda()].cpu().numpy())
+    rest = np.setdiff1d(np.arange(count - 700, count), i)
+    assert (s.rows[torch.from_numpy(rest).cuda()] == 9).all()
+
+
 def test_values_at_the_edges():
     s = Setup(6, 656, torch.float32, norm=False)
     s.kv[0] = 0

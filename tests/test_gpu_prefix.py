@@ -202,6 +202,64 @@ def test_peaked_scores(pool):
     c.check(*c.run(pool))
 
 
+@pytest.mark.parametrize("scale", [-0.05, 0.0, 1e-6])
+def test_scales(pool, scale):
+    """A negative scale turns the order of the scores round; with none every row weighs the same."""
+    for holes in (0.0, 0.4):
+        c = Case(2, 700, 16, seed=3, holes=holes)
+        c.scale = abs(scale)
+        if scale < 0:
+            c.q = -c.q
+        want = c.run(pool)
+        c.check(*want)
+        if scale < 0:
+            c.q, c.scale = -c.q, scale
+            got = c.run(pool)
+            torch.cuda.synchronize()
+            assert torch.allclose(got[0].float(), want[0].float(), rtol=2 ** -6, atol=2 ** -8)
+            assert torch.allclose(got[1], want[1], rtol=1e-5, atol=1e-5)
+
+
+def test_queries_and_units_of_many_shapes(pool):
+    """Whole requests and splits in one launch (a batch past a multiple of the pairs), single tiles, and a prefix shorter
+    than the splits that the longest one was cut into."""
+    for batch, room, used in ((90, 1500, 1500), (230, 600, 600), (100, 3000, 200), (100, 3000, 0), (3, 30000, 700), (1, 300, 256)):
+        c = Case(batch, used, 64, seed=batch, room=room).own(shift=3.0)
+        c.check(*c.run(pool, length_d=torch.tensor([used], dtype=torch.int32, device="cuda")))
+
+
+def test_first_call_under_capture():
+    """Nothing has been called before in the process: the first call of each operator is captured, and replayed."""
+    import subprocess
+    import sys
+
+    code = """
+import sys, torch
+sys.path[:0] = [%r, %r]
+import hierarchical_sparse_attention_hs_gb300 as hs
+from test_gpu_prefix import Case
+buf = hs.PoolBuffers(1, 4, 64, 16, 16, 1152)
+pool = buf.create()
+c = Case(3, 500, 16, seed=1)
+out, lse = torch.zeros(3, 128, 512, dtype=torch.bfloat16, device='cuda'), torch.zeros(3, 128, device='cuda')
+work = torch.zeros(64 << 20, dtype=torch.uint8, device='cuda')
+kv = torch.randn(4, 576).to(torch.bfloat16).cuda()
+d = hs.append_desc(kv, torch.zeros(32).cuda(), torch.arange(4, dtype=torch.int32).cuda())
+torch.cuda.synchronize()
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    hs.hs_append(pool, 0, 4, d)
+    hs.hs_mla_prefix(pool, 3, c.q, hs.paged_rows(c.rows, c.pages, 16), 500, None, c.scale, None, None, out, 0, lse, work)
+g.replay()
+c.check(out, lse)
+got = torch.from_numpy(buf.host.numpy().reshape(4, 64, 1152)).view(torch.bfloat16)
+assert all(torch.equal(got[i, i], kv[i].cpu()) for i in range(4))
+print('captured')
+""" % (str(__import__("pathlib").Path(__file__).resolve().parents[1]), str(__import__("pathlib").Path(__file__).resolve().parent))
+    r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and "captured" in r.stdout, r.stderr[-2000:]
+
+
 def test_not_a_number_shows(pool):
     c = Case(2, 200, 16, seed=2)
     c.q[1, 7, 3] = math.nan
