@@ -13,8 +13,8 @@
 //
 // Work. One warp per row and one warp per 16 heads of a token's queries, each with several once there are many. A lane
 // holds 16 latents (two 16-byte chunks for 16-bit inputs) and one pair of the key, so a row is loaded and stored in
-// whole 128-byte segments and the norm's sum and the scales' maxima are warp shuffles. Nothing passes
-// through shared memory.
+// whole 128-byte segments and the norm's sum and the scales' maxima are warp shuffles. Only the norm's weights
+// pass through shared memory.
 
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -146,19 +146,10 @@ __device__ __forceinline__ bool token_of(const AppendArgs& a, int i, int* req, i
 // slot and page: a chain of loads that every row would otherwise wait for), and a row's values are loaded while the one
 // before is worked on.
 template <class T, bool FP8, bool INTER>
-__device__ __forceinline__ void append_rows(const AppendArgs& a, int lane, int warp) {
+__device__ __forceinline__ void append_rows(const AppendArgs& a, float* weight, int lane, int warp) {
   constexpr int RB = FP8 ? ROW_FP8 : ROW_BF16;
   constexpr uint32_t ALL = 0xffffffffu;
   const unsigned long long rate = turn_rate(a.inv_freq, lane);
-  float wt[2][8] = {};  // the lane's weights of the norm
-  if (a.norm_weight) {
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      Raw8<float> w;
-      w.load(a.norm_weight + h * (LATENT / 2) + 8 * lane);
-      w.get(wt[h]);
-    }
-  }
   const int64_t begin = (int64_t)warp * a.per_warp;
   const int end = (int)min((int64_t)a.ntok, begin + a.per_warp);
   const T* const kv = static_cast<const T*>(a.kv);
@@ -172,6 +163,10 @@ __device__ __forceinline__ void append_rows(const AppendArgs& a, int lane, int w
     pair[1] = x[LATENT + (INTER ? 2 * lane + 1 : lane + PAIRS)];
   };
   if (begin < end) load((int)begin);
+  if (a.norm_weight) {  // shared by the block's warps: 16 registers a lane less, or 2 KB less to load for each row
+    reinterpret_cast<float4*>(weight)[threadIdx.x] = reinterpret_cast<const float4*>(a.norm_weight)[threadIdx.x];
+    __syncthreads();
+  }
   for (int i0 = (int)min(begin, (int64_t)a.ntok); i0 < end; i0 += 32) {
     int my_req = -1, my_pos = -1, my_slot = -1, my_row = -1;
     if (i0 + lane < end) {
@@ -215,7 +210,13 @@ __device__ __forceinline__ void append_rows(const AppendArgs& a, int lane, int w
 #pragma unroll
         for (int h = 0; h < 2; ++h)
 #pragma unroll
-          for (int e = 0; e < 8; ++e) z[h][e] *= r * wt[h][e];
+          for (int e = 0; e < 8; e += 4) {
+            const float4 w = *reinterpret_cast<const float4*>(weight + h * (LATENT / 2) + 8 * lane + e);
+            z[h][e] *= r * w.x;
+            z[h][e + 1] *= r * w.y;
+            z[h][e + 2] *= r * w.z;
+            z[h][e + 3] *= r * w.w;
+          }
       }
       // the rotary key: lane j turns pair j; lane l then writes the values 2l and 2l + 1
       float c, s;
@@ -342,8 +343,10 @@ __global__ void __launch_bounds__(THREADS) hs_append_kernel(const AppendArgs a) 
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;");
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+  __shared__ __align__(16) float weight[LATENT];
+  static_assert(THREADS * 4 == LATENT, "one 16-byte load a thread");
   if ((int)blockIdx.x < a.row_blocks)
-    append_rows<T, FP8, INTER>(a, lane, (int)blockIdx.x * WARPS + w);
+    append_rows<T, FP8, INTER>(a, weight, lane, (int)blockIdx.x * WARPS + w);
   else
     turn_queries<T, INTER>(a, lane, ((int)blockIdx.x - a.row_blocks) * WARPS + w,
                            ((int)gridDim.x - a.row_blocks) * WARPS);
