@@ -64,7 +64,6 @@ constexpr int DVH = DV / 2;        // value columns of a CTA
 constexpr int SEG = 64;            // keys of a segment: the rows of the largest box, and a softmax thread's keys
 constexpr int NSEG = NK / SEG;
 constexpr int KBLK = DQK / 64;     // 64-column blocks of a row: K stages of a tile
-constexpr int VST = NSEG * 2;      // V stages of a tile
 constexpr int BLK_BYTES = 64 * 128;      // 64 rows x 64 columns
 constexpr int STAGE_BYTES = 2 * BLK_BYTES;
 constexpr int NSTAGE = 7;          // stages of the ring
@@ -114,9 +113,12 @@ struct PrefixArgs {
 __device__ __forceinline__ int length_of(const PrefixArgs& a) {
   return a.length ? min(max(ld_fresh(a.length), 0), a.max_length) : a.max_length;
 }
-// The prefix's tiles: all of them, and how they are dealt out over the splits: `per` each, one more for the first `more`.
+// The prefix's tiles: all of them, and how they are dealt out over the splits: `per` each, one more for the first `more`. Of
+// the last tile only the first `last_segs` segments begin within the prefix: the others are neither loaded (their scores
+// are masked, whatever the buffer holds) nor multiplied with V.
 struct Tiles {
-  int n, per, more;
+  int n, per, more, last_segs;
+  __device__ __forceinline__ int segs(int tile) const { return tile == n - 1 ? last_segs : NSEG; }
 };
 // A pair's walk over its units (every pairs-th) and their tiles: the same sequence in every role. (Nothing is divided here:
 // with divisions in its walks the kernel took a quarter longer, though they would run once a unit.)
@@ -233,7 +235,7 @@ __device__ __forceinline__ void find_rows(const PrefixArgs& a, Box& s, int tok0,
     for (int i = 1; i < 4; ++i) s.row[i] = row(i);
     // Four rows are gathered by one copy if the pool holds any of them. A missing one takes the place of one that is there:
     // its weight is 0, and where the row's values are not finite the outputs are not a number either way (such a value
-    // makes the row's own score infinite or not a number). Without any they are filled with zeros one by one.
+    // makes the row's own score infinite or not a number). Without any the box is one of zeros.
     const int some = min(min(s.row[0], s.row[1]), min(s.row[2], s.row[3]));
     s.have = some != a.none ? 4 : 0;
 #pragma unroll
@@ -256,12 +258,10 @@ __device__ __forceinline__ void load_box(const PrefixArgs& a, const CUtensorMap*
   for (int n = 0; n < NBLK; ++n) {
     const uint32_t d = dst + (uint32_t)(n * BLK_BYTES + ((lane << a.box_shift) * 128));
     if (a.page_shift < 2) {
-      if (s.have) {
+      if (s.have)
         tma_gather4(d, small, (blk + n) * 64, s.row, bar);
-      } else {
-#pragma unroll
-        for (int r = 0; r < 4; ++r) tma_box(d + r * 128u, map1, blk + n, s.row[r], bar);
-      }
+      else
+        tma_box(d, map, blk + n, a.none, bar);
     } else if (s.have == rows) {
       tma_box(d, map, blk + n, s.row[0], bar);
     } else {
@@ -431,6 +431,7 @@ __global__ void __launch_bounds__(THREADS, 1)
   tiles.n = (len + NK - 1) / NK;
   tiles.per = tiles.n / a.nsplit;
   tiles.more = tiles.n - tiles.per * a.nsplit;
+  tiles.last_segs = (len - (tiles.n - 1) * NK + SEG - 1) / SEG;
   const uint32_t lead = peer_addr(bar, 0);  // the first CTA's barriers
   // test hook: the roles that would start a copy or an MMA first wait on a barrier that nothing completes
   bool ok = true;
@@ -461,7 +462,7 @@ __global__ void __launch_bounds__(THREADS, 1)
       };
       ok = !a.stall || wait(B_STALL, 0);
       bool more = w.start(a, tiles), pending = false, pending_first = false;
-      int g = 0, nq = 0;  // tiles whose scores have been issued, and units
+      int g = 0, nq = 0, pending_v = 0;  // tiles whose scores have been issued, units, V stages of the pending product
       while ((more || pending) && ok) {
         const bool first = w.j == 0;
         if (more) {
@@ -480,7 +481,7 @@ __global__ void __launch_bounds__(THREADS, 1)
           // P of a unit's first tile comes after the softmax warps have stored the unit before, so O is free too
           ok = wait(B_PFULL, (unsigned)(g - 1) & 1u);
           tc_fence_after();
-          for (int c = 0; c < VST && ok; ++c) {
+          for (int c = 0; c < pending_v && ok; ++c) {
             // 64 keys: block c / 2 of P; 128 of the CTA's value columns, 16 rows a step
             ok = wait(B_FULL + st, ph);
             if (ok) four(tmem + TMEM_O + (uint32_t)(c & 1) * 128, dp + (uint64_t)((c >> 1) * (BLK_BYTES >> 4)),
@@ -492,6 +493,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         pending = more;
         if (more) {
           pending_first = first;
+          pending_v = 2 * tiles.segs(w.j0 + w.j);
           ++g;
           more = w.next(a, tiles);
         }
@@ -533,13 +535,16 @@ __global__ void __launch_bounds__(THREADS, 1)
         find_rows(a, p0, first(), len, lane);
         if (is_k) find_rows(a, p1, first() + SEG, len, lane);
         const int blk = is_k ? c : (int)rank * (DVH / 64) + (c & 1) * 2;
+        // K: 64 columns of every segment within the prefix, each in one of the CTAs
+        const uint32_t bytes = is_k ? (uint32_t)tiles.segs(w.j0 + w.j) * BLK_BYTES : 2 * STAGE_BYTES;
+        const int here = is_k ? (len - first() + SEG - 1) >> 6 : 0;  // of them in this one (at most two are loaded)
         ok = bar_wait(bar + B_EMPTY + s, ph, abort_flag, lim);  // the MMAs that read the slot have finished
         if (!ok) break;
         ph ^= 1u;
-        if (rank == 0 && lane == 0) bar_arrive_expect(bar + B_FULL + s, 2 * STAGE_BYTES);
+        if (rank == 0 && lane == 0) bar_arrive_expect(bar + B_FULL + s, bytes);
         if (is_k) {
-          load_box<1>(a, &map, &map, &map1, &small, p0, dst, blk, fb, lane);
-          load_box<1>(a, &map, &map, &map1, &small, p1, dst + BLK_BYTES, blk, fb, lane);
+          if (here > 0) load_box<1>(a, &map, &map, &map1, &small, p0, dst, blk, fb, lane);
+          if (here > 1) load_box<1>(a, &map, &map, &map1, &small, p1, dst + BLK_BYTES, blk, fb, lane);
         } else {
           load_box<2>(a, &map, &map2, &map1, &small, p0, dst, blk, fb, lane);
         }
@@ -547,7 +552,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         // the slot of a unit's last K stage is free when the unit's last scores have been taken, and so is Q
         q_next = is_k && c == KBLK - 1 && w.j + 1 == w.nt;
         c += NSTAGE;
-        while (vmore && c >= (is_k ? KBLK : VST)) {
+        for (int end; vmore && c >= (end = is_k ? KBLK : 2 * tiles.segs(v.j0 + v.j));) {
           if (is_k) {
             c -= KBLK;
             kmore = w.next(a, tiles);
@@ -555,7 +560,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             is_k = head && kmore;
             head = false;
           } else {
-            c -= VST;
+            c -= end;
             vmore = v.next(a, tiles);
             is_k = kmore;
           }
@@ -622,11 +627,10 @@ __global__ void __launch_bounds__(THREADS, 1)
     const float scale = a.scale_log2 > 0.f ? a.scale_log2 : 1.f;  // the maximum is taken before the scale: see below
     int g = 0;  // tiles of the pair's walk
     w.set(a, (int)(blockIdx.x >> 1), tiles);
-    uint64_t mask_next = w.u < a.units && w.nt > 0 ? key_mask(w.j0) : 0;
     while (w.u < a.units && ok) {
       m_run = -INFINITY, l_run = 0.f;
       for (int j = 0; j < w.nt; ++j, ++g) {
-        const uint64_t mask = mask_next;
+        const uint64_t mask = key_mask(w.j0 + j);
         ok = __all_sync(0xffffffffu, bar_wait(bar + B_SFULL + (g & 1), (unsigned)(g >> 1) & 1u, abort_flag, lim));
         if (!ok) break;
         tc_fence_after();
@@ -656,7 +660,6 @@ __global__ void __launch_bounds__(THREADS, 1)
 #pragma unroll
           for (int i = 0; i < 32; ++i) mb = fmaxf(mb, __uint_as_float(sv[i]));
         }
-        if (j + 1 < w.nt) mask_next = key_mask(w.j0 + j + 1);
         const float* share = exchange(mb);
         if (!ok) break;
         mb = scale * fmaxf(fmaxf(share[0], share[QH]), fmaxf(share[2 * QH], share[3 * QH]));
@@ -717,7 +720,6 @@ __global__ void __launch_bounds__(THREADS, 1)
       const int b = w.b, split = w.split;
       const bool have_o = w.nt > 0;
       w.set(a, w.u + (int)(gridDim.x >> 1), tiles);
-      mask_next = w.u < a.units && w.nt > 0 ? key_mask(w.j0) : 0;
       if (have_o) {
         ok = __all_sync(0xffffffffu, bar_wait(bar + B_PDONE, (unsigned)(g - 1) & 1u, abort_flag, lim));
         if (!ok) break;
