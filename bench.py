@@ -206,7 +206,7 @@ def kernel_sources_sha16() -> str:
 
 def attention_sources_sha16() -> str:
     """Hash of the files the attention kernel is compiled from, which its committed ncu capture must match."""
-    return _sources_sha16(("hs_attention.cu", "hs_pool.hpp"))
+    return _sources_sha16(("hs_attention.cu", "hs_pool.hpp", "hs_internal.hpp", "hs_tcgen05.cuh"))
 
 
 def _load_capture(name: str, sha_key: str, sha: str):

@@ -26,7 +26,7 @@
 #include <cstring>
 
 #include "../../include/hs.h"
-#include "hs_pool.hpp"
+#include "hs_internal.hpp"
 
 namespace {
 

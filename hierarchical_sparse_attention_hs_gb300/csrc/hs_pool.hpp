@@ -29,9 +29,5 @@ struct hs_pool {
   int max_active[HS_MAX_CLUSTER + 1];  // clusters of each size resident at once
 };
 
-bool hs_paged_ok(const hs_paged_rows* p);  // whether a block table's sizes and alignments are usable
-bool hs_on_device(const hs_pool* p);      // whether the pool's device is the current one
-// The settings of hs_debug_attention: polling rounds of the attention kernels' waits, and the stall hook.
-void hs_attention_waits(uint32_t* limit, int32_t* stall);
 
 #endif  // HS_POOL_HPP_

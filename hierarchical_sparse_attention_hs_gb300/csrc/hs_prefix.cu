@@ -49,7 +49,7 @@
 #include <cstring>
 
 #include "../../include/hs.h"
-#include "hs_pool.hpp"
+#include "hs_internal.hpp"
 #include "hs_tcgen05.cuh"
 
 namespace {
