@@ -17,9 +17,9 @@
 // pass through shared memory.
 //
 // Measured on one GB300 (reads and writes over the time): 1 to 32 tokens with 128 heads 2.1-2.2 us, a launch's own cost;
-// 256 2.8 us; 2,047 with 128 heads 18.6 us from fp32 (5.8 TB/s) and 13.5 from bf16; 131,071 without queries 54 us into bf16
-// rows (5.6 TB/s) and 50 into fp8 rows (4.8: issue-bound, 0.73 instructions a cycle and scheduler); 4,096 into host memory
-// 17.5 us for fp8 rows and 26 for bf16, the link's 154 and 181 GB/s of writes.
+// 256 2.8 us; 2,047 with 128 heads 18.5 us from fp32 (5.8 TB/s) and 13.5 from bf16; 131,071 without queries 55 us into bf16
+// rows (5.5 TB/s) and 50 into fp8 rows (4.8: issue-bound, 0.73 instructions a cycle and scheduler); 4,096 into host memory
+// 17.5 us for fp8 rows and 26 for bf16, 153 and 180 GB/s of writes over the link.
 
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -42,7 +42,8 @@ constexpr int FP8_ROPE = LATENT + 4 * 4;         // byte offset of the rotary ke
 constexpr int Q_HEADS = 16;                      // heads of one warp's work item: four 16-byte loads a lane in flight
 constexpr int MAX_TOKENS = 1 << 30;              // and items of 16 heads of a token's queries
 constexpr int THREADS = 128, WARPS = THREADS / 32;
-// Blocks an SM of either kind, at most. 131,071 rows with 8, 12, 16 blocks: fp8 58, 50, 52 us; bf16 61, 54, 50.
+// Blocks an SM of either kind, at most. 131,071 rows with 8, 12, 16 blocks: from bf16 into fp8 rows
+// 59.5, 49.7, 52.6 us, into bf16 rows 49.8, 54.5, 49.7; from fp32 79.6, 69.7, 70.6.
 constexpr int ROW_BLOCKS = 12, Q_BLOCKS = 16;
 
 struct AppendArgs {

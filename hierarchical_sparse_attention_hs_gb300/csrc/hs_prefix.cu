@@ -41,11 +41,12 @@
 // prefix are never read, and a masked key's value row is zero, whatever memory holds; its score is masked to -inf by the
 // softmax. Segments of 64 tokens behind the prefix's end are left out altogether.
 //
-// Measured on one GB300: 76 requests over 8,192 tokens 97 us, 1,790 TFLOP/s, 0.94 of the measured bf16 product; 32 over
-// 65,537 356 us, 1,640; 100 over 2,047 50 us; 1 over 131,072 49 us. With loads taken out the first runs at 2,060 TFLOP/s (84
-// us): what it waits for is L2, which gives an SM 71 bytes a cycle when both SMs of a TPC read different data (116 when
-// they read the same), against the 64 that the full rate takes. Nine ring stages instead of seven (four blocks of Q in
-// tensor memory, one score buffer) changed nothing.
+// Measured on one GB300, medians of replayed graphs: 76 requests over 8,192 tokens 101 us, 1,720 TFLOP/s, 0.90 of the
+// measured bf16 product (98 to 103 us on other occasions); 32 over 65,537 362 us, 1,610; 100 over 2,047 51 us; 1 over
+// 131,072 49 us. Of the first the tensor pipe is active for 70 % of the cycles (under the profiler). L2 gives an SM 71
+// bytes a cycle when both SMs of a TPC read different data (116 when they read the same), against the 64 that the full
+// rate takes. Nine ring stages instead of seven, with four blocks of Q in tensor memory and one score buffer: 105 us against
+// 99 for the first, not kept.
 //
 // Waits are bounded: on running out a role sets the abort flag, which ends every role, and the HS_DEVERR_TIMEOUT bit.
 
