@@ -41,9 +41,9 @@
 // prefix are never read, and a masked key's value row is zero, whatever memory holds; its score is masked to -inf by the
 // softmax. Segments of 64 tokens behind the prefix's end are left out altogether.
 //
-// Measured on one GB300, medians of replayed graphs: 76 requests over 8,192 tokens 101 us, 1,720 TFLOP/s, 0.90 of the
-// measured bf16 product (98 to 103 us on other occasions); 32 over 65,537 362 us, 1,610; 100 over 2,047 51 us; 1 over
-// 131,072 49 us. Of the first the tensor pipe is active for 70 % of the cycles (under the profiler). L2 gives an SM 71
+// Measured on one GB300, medians of replayed graphs: 76 requests over 8,192 tokens 100 to 101 us, 1,717 to 1,734
+// TFLOP/s, 0.90 of the measured bf16 product; 32 over 65,537 360 to 363 us, 1,610; 100 over 2,047 51 us; 1 over
+// 131,072 49 us. Of the first the tensor pipe is active for 71 % of the cycles (under the profiler). L2 gives an SM 71
 // bytes a cycle when both SMs of a TPC read different data (116 when they read the same), against the 64 that the full
 // rate takes. Nine ring stages instead of seven, with four blocks of Q in tensor memory and one score buffer: 105 us against
 // 99 for the first, not kept.

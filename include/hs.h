@@ -347,10 +347,11 @@ typedef struct {
  * A token with a negative position is padding: it touches nothing. One whose position is >= ctx or whose request is not
  * in 0 .. max_batch-1 is skipped whole, and the error word gets HS_DEVERR_RANGE. (request, position) pairs are distinct
  * within a call (not checked: rows of a repeated pair may mix). ntok == 0 is a no-op; ntok <= 2^30, and
- * so is ntok * ceil(q_heads / 16); with req_ids NULL ntok <= max_batch. At least one of `paged`, to_history and q_rope is given. Enqueued on `stream` (of the pool's device, which
- * must be the current one: HS_ERR_INVALID_ARG); capturable. Order it before the resolve, prefetch, gather or attention
- * that reads the rows. Basis: the full history in host memory that the paper's cache sits on (Abstract) and the ordinary
- * KV blocks of the "Hybrid HiSparse" card (Timeline) have to be written by somebody; the pages name no writer.
+ * so is ntok * ceil(q_heads / 16); with req_ids NULL ntok <= max_batch. At least one of `paged`, to_history and q_rope
+ * is given. Enqueued on `stream` (of the pool's device, which must be the current one: HS_ERR_INVALID_ARG);
+ * capturable. Order it before the resolve, prefetch, gather or attention that reads the rows. Basis: the full history
+ * in host memory that the paper's cache sits on (Abstract) and the ordinary KV blocks of the "Hybrid HiSparse" card
+ * (Timeline) have to be written by somebody; the pages name no writer.
  */
 int hs_append(hs_pool *pool, int32_t layer, int32_t ntok, const hs_append_desc *desc, const hs_paged_rows *paged,
               int32_t to_history, hs_stream_t stream);
@@ -390,7 +391,8 @@ size_t hs_mla_prefix_workspace(hs_pool *pool, int32_t batch, int32_t max_length)
  * Test hook of the attention consumer (not for production use; process-wide settings, not thread-safe). It lets a
  * test exercise failure detection without faulting the GPU: every wait inside the kernel is bounded, and on running
  * out it stops every role, frees its tensor memory, returns and sets HS_DEVERR_TIMEOUT.
- *   wait_limit: polling rounds after which a wait of the kernel's roles gives up (0 restores the default, 2^20).
+ *   wait_limit: polling rounds after which a wait of the kernel's roles gives up (0 restores the default, 2^20); it also
+ *     gives up after two seconds.
  *   stall != 0: the tensor-core issuer of every CTA (and the loaders of hs_mla_prefix) first waits on a barrier that
  *     nothing completes, so that wait runs out before any tensor-core work or row copy of the kernel is issued, and
  *     the abort path runs with nothing in flight. 0 restores normal operation.
