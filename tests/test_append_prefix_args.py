@@ -122,6 +122,13 @@ def test_empty_calls_do_nothing():
     hs.hs_mla_prefix(ctypes.addressof(block), 0, None, pages(), 100, None, 0.1, None, None, None, 0, None, None, 0)
 
 
+@pytest.mark.parametrize("stride, rows", [(1 << 48, 1 << 16), (1 << 47, 1 << 16), ((1 << 63) - 1, 1), ((1 << 63) - 1, 64)])
+def test_prefix_takes_lists_of_any_stride(stride, rows):
+    """A list longer than 2^63 tokens is longer than max_length (an empty batch ends the call behind that check)."""
+    hs.hs_mla_prefix(ctypes.addressof(fake_pool()), 0, None, pages(page_stride=stride, page_rows=rows), 100, None, 0.1, None,
+                     None, None, 0, None, None, 0)
+
+
 def test_helpers_check_shapes_and_types():
     kv, f, p = torch.zeros(3, 576, dtype=torch.bfloat16), torch.zeros(32), torch.zeros(3, dtype=torch.int32)
     q, qr = torch.zeros(3, 8, 576, dtype=torch.bfloat16), torch.zeros(3, 8, 64, dtype=torch.bfloat16)
