@@ -960,7 +960,8 @@ extern "C" int hs_mla_prefix(hs_pool* pool, int32_t batch, const void* q, const 
                              size_t workspace_bytes, hs_stream_t stream) {
   const auto aligned = [](const void* p, uintptr_t n) { return p && (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; };
   if (!pool || !prefix || batch < 0 || batch > (1 << 24) / HEADS || max_length < 0 || max_length > 1 << 30 || !hs_paged_ok(prefix) ||
-      ((int64_t)max_length + prefix->page_rows - 1) / prefix->page_rows > prefix->page_stride || (out_type != HS_TYPE_BF16 && out_type != HS_TYPE_F32) ||
+      ((int64_t)max_length + prefix->page_rows - 1) / prefix->page_rows > prefix->page_stride ||
+      (out_type != HS_TYPE_BF16 && out_type != HS_TYPE_F32) ||
       (own_out != nullptr) != (own_lse != nullptr))
     return HS_ERR_INVALID_ARG;
   if (pool->d.row_bytes != ROW_BYTES) return HS_ERR_UNSUPPORTED;

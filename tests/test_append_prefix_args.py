@@ -125,7 +125,8 @@ def test_empty_calls_do_nothing():
 @pytest.mark.parametrize("stride, rows", [(1 << 48, 1 << 16), (1 << 47, 1 << 16), ((1 << 63) - 1, 1), ((1 << 63) - 1, 64)])
 def test_prefix_takes_lists_of_any_stride(stride, rows):
     """A list longer than 2^63 tokens is longer than max_length (an empty batch ends the call behind that check)."""
-    hs.hs_mla_prefix(ctypes.addressof(fake_pool()), 0, None, pages(page_stride=stride, page_rows=rows), 100, None, 0.1, None,
+    block = fake_pool()
+    hs.hs_mla_prefix(ctypes.addressof(block), 0, None, pages(page_stride=stride, page_rows=rows), 100, None, 0.1, None,
                      None, None, 0, None, None, 0)
 
 
