@@ -17,8 +17,8 @@
 // pass through shared memory.
 //
 // Measured on one GB300 (reads and writes over the time): 1 to 32 tokens with 128 heads 2.1-2.2 us, a launch's own cost;
-// 256 2.8 us; 2,047 with 128 heads 18.5 us from fp32 (5.8 TB/s) and 13.5 from bf16; 131,071 without queries 55 us into bf16
-// rows (5.5 TB/s) and 50 into fp8 rows (4.8: issue-bound, 0.73 instructions a cycle and scheduler); 4,096 into host memory
+// 256 2.8 us; 2,047 with 128 heads 18.5 us from fp32 (5.8 TB/s) and 13.5 from bf16; 131,071 without queries 50 us into bf16
+// rows (6.1 TB/s) and 50 into fp8 rows (4.8: issue-bound, 0.73 instructions a cycle and scheduler); 4,096 into host memory
 // 17.5 us for fp8 rows and 26 for bf16, 153 and 180 GB/s of writes over the link.
 
 #include <cuda_bf16.h>
@@ -42,9 +42,11 @@ constexpr int FP8_ROPE = LATENT + 4 * 4;         // byte offset of the rotary ke
 constexpr int Q_HEADS = 16;                      // heads of one warp's work item: four 16-byte loads a lane in flight
 constexpr int MAX_TOKENS = 1 << 30;              // and items of 16 heads of a token's queries
 constexpr int THREADS = 128, WARPS = THREADS / 32;
-// Blocks an SM of either kind, at most. 131,071 rows with 8, 12, 16 blocks: from bf16 into fp8 rows
-// 59.5, 49.7, 52.6 us, into bf16 rows 49.8, 54.5, 49.7; from fp32 79.6, 69.7, 70.6.
-constexpr int ROW_BLOCKS = 12, Q_BLOCKS = 16;
+// Blocks an SM of either kind, at most. 131,071 rows with 8, 12, 16 blocks an SM: from bf16 into fp8 rows 59.5, 49.7,
+// 52.6 us; from fp32 into bf16 rows 79.6, 69.7, 70.6; from bf16 into bf16 rows 49.7, 54.4, 49.8. The last at other sizes:
+// 5,000 rows 5.1, 4.7, 4.7 us; 8,191 5.3, 5.2, 6.1; 16,384 8.7, 10.1, 9.5; 65,536 26.5, 28.4, 26.9. So 16-bit values into
+// bf16 rows get 8, all others 12.
+constexpr int ROW_BLOCKS = 12, ROW_BLOCKS_PLAIN = 8, Q_BLOCKS = 16;
 
 struct AppendArgs {
   const void* kv;
@@ -450,7 +452,8 @@ extern "C" int hs_append(hs_pool* pool, int32_t layer, int32_t ntok, const hs_ap
 
   // As many warps as the device holds, each with its share of the tokens (and of the queries' items): the turn rates (64-bit
   // arithmetic) are worked out once per warp, not per row.
-  const int64_t most = (int64_t)pool->num_sms * ROW_BLOCKS;
+  const bool fp8 = pool->d.row_bytes == ROW_FP8, inter = d.interleaved != 0;
+  const int64_t most = (int64_t)pool->num_sms * (fp8 || size == 4 ? ROW_BLOCKS : ROW_BLOCKS_PLAIN);
   const int64_t items = (int64_t)ntok * a.head_items;
   a.per_warp = (int32_t)((ntok + most * WARPS - 1) / (most * WARPS));
   const int64_t row_warps = ((int64_t)ntok + a.per_warp - 1) / a.per_warp;
@@ -465,7 +468,6 @@ extern "C" int hs_append(hs_pool* pool, int32_t layer, int32_t ntok, const hs_ap
   attr.val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  const bool fp8 = pool->d.row_bytes == ROW_FP8, inter = d.interleaved != 0;
   const cudaError_t e = d.type == HS_TYPE_BF16  ? launch<__nv_bfloat16>(cfg, a, fp8, inter)
                         : d.type == HS_TYPE_F16 ? launch<__half>(cfg, a, fp8, inter)
                                                 : launch<float>(cfg, a, fp8, inter);
