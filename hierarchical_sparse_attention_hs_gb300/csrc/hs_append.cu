@@ -372,6 +372,7 @@ cudaError_t launch(const cudaLaunchConfig_t& cfg, const AppendArgs& a, bool fp8,
 }
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
+bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3) == 0; }
 // `n` strides of at least `least` elements of `size` bytes, multiples of 16 bytes, used by `count` items
 bool stride_ok(int64_t stride, int64_t least, int size, int64_t count) {
   return count <= 1 || (stride >= least && stride <= INT64_MAX / size / (count > 0 ? count : 1) && (stride * size) % 16 == 0);
@@ -380,7 +381,7 @@ bool stride_ok(int64_t stride, int64_t least, int size, int64_t count) {
 }  // namespace
 
 bool hs_paged_ok(const hs_paged_rows* p) {
-  return p->rows && p->pages && aligned16(p->rows) && (reinterpret_cast<uintptr_t>(p->pages) & 3) == 0 && p->count >= 0 &&
+  return p->rows && p->pages && aligned16(p->rows) && aligned4(p->pages) && p->count >= 0 &&
          p->count <= INT32_MAX - 63 && p->page_stride >= 1 && p->page_rows >= 1 && p->page_rows <= 65536 &&
          (p->page_rows & (p->page_rows - 1)) == 0;
 }
@@ -404,6 +405,7 @@ extern "C" int hs_append(hs_pool* pool, int32_t layer, int32_t ntok, const hs_ap
   if (ntok == 0) return HS_OK;
   const int size = d.type == HS_TYPE_F32 ? 4 : 2;
   if (!d.kv || !aligned16(d.kv) || !stride_ok(d.kv_stride, WIDTH, size, ntok) || !d.inv_freq || !d.positions ||
+      !aligned4(d.inv_freq) || !aligned4(d.positions) || !aligned4(d.req_ids) ||
       (d.norm_weight && (!aligned16(d.norm_weight) || !(d.norm_eps >= 0.f))) || (!d.req_ids && ntok > pool->d.max_batch))
     return HS_ERR_INVALID_ARG;
   if ((d.q_rope != nullptr) != (d.q != nullptr) || (d.q_rope != nullptr) != (d.q_heads > 0) || d.q_heads < 0)

@@ -296,7 +296,8 @@ typedef struct {
 
 /*
  * What one append takes. Token i (0 <= i < ntok) belongs to request req_ids[i] (i itself when req_ids is NULL) at
- * position positions[i]. Arrays are device memory; req_ids and positions may be mapped host memory.
+ * position positions[i]. Arrays are device memory; req_ids and positions may be mapped host memory. 32-bit arrays are
+ * 4-byte aligned.
  *   type: HS_TYPE_* of kv and q_rope.
  *   interleaved: which values form the 32 pairs that turn: 0: (j, j + 32); 1: (2j, 2j + 1).
  *   kv: [ntok][576], the latent's 512 values and the rotary key's 64 before rotation; kv_stride: elements between

@@ -1,0 +1,113 @@
+"""hs_append, hs_mla_prefix: a good call reaches its launches and a call that differs from it in one argument is refused.
+
+The calls run in a process of their own, in which a stand-in for the CUDA runtime (fake_cudart.c) is loaded first, so that
+the checks run to the end without a device and nothing is launched. Without it a good call is refused as well (its pool
+belongs to no device), and a refusal would prove nothing about the argument.
+"""
+import json
+import os
+import subprocess
+import sys
+
+import pytest
+
+from hierarchical_sparse_attention_hs_gb300 import build as hs_build
+
+HERE = os.path.dirname(os.path.abspath(__file__))
+
+PREAMBLE = """
+import ctypes, json, sys
+sys.path.insert(0, %r)
+import hierarchical_sparse_attention_hs_gb300 as hs
+
+A = 1 << 20  # an aligned address that is never dereferenced
+fake = ctypes.CDLL(%r)
+fake.fake_grid.restype = ctypes.POINTER(ctypes.c_uint)
+
+
+def pool(row_bytes=1152, max_batch=4, ctx=1000, layers=2):
+    block = ctypes.create_string_buffer(4096)
+    d = hs.hs_pool_desc(layers, max_batch, ctx, 64, 32, row_bytes, A, 0, 0, A, A, None)
+    ctypes.memmove(block, ctypes.byref(d), ctypes.sizeof(d))
+    # behind the descriptor and the layout: the device's number, and its SMs
+    at = ctypes.addressof(block) + ctypes.sizeof(hs.hs_pool_desc) + ctypes.sizeof(hs.hs_meta_layout)
+    ctypes.memmove(at, (ctypes.c_int32 * 2)(0, 152), 8)
+    return block
+
+
+def desc(**kw):
+    d = dict(type=hs.HS_TYPE_BF16, interleaved=1, kv=A, kv_stride=576, norm_weight=A, inv_freq=A, req_ids=A, positions=A,
+             q_rope=A, q_rope_token_stride=128 * 64, q_rope_head_stride=64, q=A, q_token_stride=128 * 576,
+             q_head_stride=576, q_heads=128, norm_eps=1e-6)
+    out = hs.hs_append_desc()
+    for k, v in {**d, **kw}.items():
+        setattr(out, k, v)
+    return out
+
+
+def pages(**kw):
+    out = hs.hs_paged_rows()
+    for k, v in {**dict(rows=A, count=100, pages=A, page_stride=10, page_rows=16), **kw}.items():
+        setattr(out, k, v)
+    return out
+
+
+def code(call):
+    before = fake.fake_launches()
+    try:
+        call()
+        rc = 0
+    except hs.HsError as e:
+        rc = e.code
+    made = fake.fake_launches() - before
+    assert (made > 0) == (rc == 0), (rc, made)
+    return rc
+
+
+def append(ntok=3, p=None, paged=None, to_history=True, layer=0, **kw):
+    block = p or pool()
+    return code(lambda: hs.hs_append(ctypes.addressof(block), layer, ntok, desc(**kw), paged, to_history, 0))
+
+
+def prefix(batch=2, q=A, paged=None, max_length=100, length=None, own_out=None, own_lse=None, out=A,
+           out_type=hs.HS_TYPE_BF16, lse=A, p=None, work=A, nbytes=1 << 40):
+    block = p or pool()
+    # straight at the library: the binding takes a workspace's size from its tensor
+    def call():
+        rc = hs.load().hs_mla_prefix(ctypes.addressof(block), batch, q, paged or pages(), max_length, length, 0.1, own_out,
+                                     own_lse, out, out_type, lse, work, nbytes, 0)
+        if rc:
+            raise hs.HsError(rc, "hs_mla_prefix")
+    return code(call)
+
+
+"""
+
+
+@pytest.fixture(scope="module")
+def under(tmp_path_factory):
+    """Runs Python code with the stand-in loaded; what it leaves in `got` comes back."""
+    hs_build.build()
+    so = str(tmp_path_factory.mktemp("fake") / "fake_cudart.so")
+    subprocess.check_call(["gcc", "-shared", "-fPIC", "-O1", "-o", so, os.path.join(HERE, "fake_cudart.c")])
+
+    def run(code):
+        text = PREAMBLE % (os.path.dirname(HERE), so) + code + "\nprint(json.dumps(got))\n"
+        r = subprocess.run([sys.executable, "-c", text], capture_output=True, text=True, timeout=300,
+                           env=dict(os.environ, LD_PRELOAD=so))
+        assert r.returncode == 0, r.stderr[-2000:]
+        return json.loads(r.stdout.splitlines()[-1])
+
+    return run
+
+
+def test_append_refuses_misaligned_arrays(under):
+    """inv_freq, positions and req_ids hold 4-byte values: an address that is not a multiple of 4 would fault."""
+    got = under("""
+got = {"good": append(), "no ids": append(req_ids=None)}
+for name in ("inv_freq", "positions", "req_ids"):
+    got[name] = [append(**{name: A + off}) for off in (1, 2, 3, 4)]
+""")
+    assert got["good"] == 0 and got["no ids"] == 0
+    for name in ("inv_freq", "positions", "req_ids"):
+        assert got[name] == [-1, -1, -1, 0], name
