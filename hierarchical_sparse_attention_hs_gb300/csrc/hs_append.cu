@@ -414,7 +414,8 @@ extern "C" int hs_append(hs_pool* pool, int32_t layer, int32_t ntok, const hs_ap
                    !stride_ok(d.q_rope_head_stride, ROPE, size, d.q_heads) ||
                    !stride_ok(d.q_token_stride, WIDTH, 2, ntok) || !stride_ok(d.q_head_stride, WIDTH, 2, d.q_heads)))
     return HS_ERR_INVALID_ARG;
-  if (ntok > MAX_TOKENS || (int64_t)ntok * ((d.q_heads + Q_HEADS - 1) / Q_HEADS) > MAX_TOKENS) return HS_ERR_INVALID_ARG;
+  const int64_t head_items = ((int64_t)d.q_heads + Q_HEADS - 1) / Q_HEADS;
+  if (ntok > MAX_TOKENS || ntok * head_items > MAX_TOKENS) return HS_ERR_INVALID_ARG;
   if (!hs_on_device(pool)) return HS_ERR_INVALID_ARG;
 
   AppendArgs a;
@@ -432,7 +433,7 @@ extern "C" int hs_append(hs_pool* pool, int32_t layer, int32_t ntok, const hs_ap
   a.q_token = d.q_token_stride;
   a.q_head = d.q_head_stride;
   a.heads = d.q_heads;
-  a.head_items = (d.q_heads + Q_HEADS - 1) / Q_HEADS;
+  a.head_items = (int32_t)head_items;
   a.eps = d.norm_eps;
   a.ntok = ntok;
   a.max_batch = pool->d.max_batch;

@@ -111,3 +111,17 @@ for name in ("inv_freq", "positions", "req_ids"):
     assert got["good"] == 0 and got["no ids"] == 0
     for name in ("inv_freq", "positions", "req_ids"):
         assert got[name] == [-1, -1, -1, 0], name
+
+
+def test_append_counts_heads_in_64_bits(under):
+    """The work items of a token's queries are ceil(q_heads / 16); the largest counts round up past 32 bits."""
+    got = under("""
+got = []
+for heads in (128, (1 << 31) - 16, (1 << 31) - 15, (1 << 31) - 1):
+    rc = append(ntok=1, q_heads=heads)
+    got.append([rc, list(fake.fake_grid(fake.fake_launches() - 1)[:3])])
+got.append([append(ntok=8, q_heads=(1 << 31) - 1), append(ntok=9, q_heads=(1 << 31) - 1)])
+""")
+    assert got[0] == [0, [1 + 2, 1, 1]]  # a block of rows; 8 items are the warps of 2 blocks
+    assert got[1] == got[2] == got[3] == [0, [1 + 152 * 16, 1, 1]]
+    assert got[4] == [0, -1]  # 8 * 2^27 items are the limit
