@@ -201,12 +201,12 @@ def _sources_sha16(names) -> str:
 def kernel_sources_sha16() -> str:
     """Hash of the files the resolve kernel is compiled from (its translation unit and the headers it includes),
     which a committed ncu capture of that kernel must match."""
-    return _sources_sha16(("hs_resolve.cu", "hs_block.cuh", "hs_pool.hpp"))
+    return _sources_sha16(("hs_resolve.cu", "hs_block.cuh", "hs_load.cuh", "hs_pool.hpp"))
 
 
 def attention_sources_sha16() -> str:
     """Hash of the files the attention kernel is compiled from, which its committed ncu capture must match."""
-    return _sources_sha16(("hs_attention.cu", "hs_pool.hpp", "hs_internal.hpp", "hs_tcgen05.cuh"))
+    return _sources_sha16(("hs_attention.cu", "hs_pool.hpp", "hs_internal.hpp", "hs_load.cuh", "hs_tcgen05.cuh"))
 
 
 def _load_capture(name: str, sha_key: str, sha: str):

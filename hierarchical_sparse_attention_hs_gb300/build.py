@@ -14,7 +14,8 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 SOURCES = [os.path.join(HERE, "csrc", n) for n in ("hs_resolve.cu", "hs_attention.cu", "hs_append.cu", "hs_prefix.cu")]
 HEADERS = [os.path.join(ROOT, "include", "hs.h")] + [
-    os.path.join(HERE, "csrc", n) for n in ("hs_block.cuh", "hs_pool.hpp", "hs_internal.hpp", "hs_tcgen05.cuh")]
+    os.path.join(HERE, "csrc", n) for n in ("hs_block.cuh", "hs_pool.hpp", "hs_internal.hpp", "hs_load.cuh",
+                                        "hs_tcgen05.cuh")]
 BUILD_DIR = os.path.join(HERE, "_build")
 LIB_PATH = os.path.join(BUILD_DIR, "libhs.so")
 ARCH_FLAGS = ["-gencode", "arch=compute_103a,code=sm_103a"]

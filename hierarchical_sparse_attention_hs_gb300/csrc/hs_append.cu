@@ -32,8 +32,11 @@
 
 #include "../../include/hs.h"
 #include "hs_internal.hpp"
+#include "hs_load.cuh"
 
 namespace {
+
+using hs::ld_fresh;
 
 constexpr int LATENT = 512, ROPE = 64, PAIRS = ROPE / 2, WIDTH = LATENT + ROPE;
 constexpr int ROW_BF16 = WIDTH * 2;              // 1152
@@ -75,12 +78,6 @@ struct AppendArgs {
   int32_t row_blocks;     // blocks 0 .. row_blocks - 1 write rows, the others turn queries
   int32_t* err;
 };
-
-__device__ __forceinline__ int32_t ld_fresh(const int32_t* p) {
-  int32_t v;
-  asm("ld.global.cv.s32 %0, [%1];" : "=r"(v) : "l"(p));
-  return v;
-}
 
 // Eight consecutive values as they lie in memory, then in 32 bits. (Plain loads: queries may be turned in place.)
 template <class T>

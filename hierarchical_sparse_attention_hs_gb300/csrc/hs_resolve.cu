@@ -52,12 +52,14 @@
 
 #include "../../include/hs.h"
 #include "hs_block.cuh"
+#include "hs_load.cuh"
 #include "hs_pool.hpp"
 
 namespace {
 
 using hs::bits_of;
 using hs::Group;
+using hs::ld_fresh;
 using hs::NT;
 using hs::NW;
 using hs::RED_INTS;
@@ -160,15 +162,6 @@ __device__ __forceinline__ uint4 load_row_chunk_device(const uint8_t* p) {
 template <bool FROM_HOST>
 __device__ __forceinline__ uint4 load_row_chunk(const uint8_t* p) {
   return FROM_HOST ? load_row_chunk_host(p) : load_row_chunk_device(p);
-}
-
-// Loads of the caller's index arrays (selections, resident maps, slot lists): `.cv` fetches afresh, so a stale
-// L2 copy of a host-memory line is never used and these arrays may live in device memory or in mapped
-// page-locked host memory, read over the host link without a separate copy.
-__device__ __forceinline__ int32_t ld_fresh(const int32_t* p) {
-  int32_t v;
-  asm("ld.global.cv.s32 %0, [%1];" : "=r"(v) : "l"(p));
-  return v;
 }
 
 // Asynchronous global-to-shared copies (completion waited for by the issuing thread, then a block barrier).

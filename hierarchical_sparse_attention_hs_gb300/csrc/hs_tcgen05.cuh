@@ -6,6 +6,8 @@
 
 #include <cstdint>
 
+#include "hs_load.cuh"
+
 namespace hs {
 
 // A wait gives up after this many try_wait rounds, or once it has lasted WAIT_NS: a round may suspend its thread for as
@@ -20,12 +22,6 @@ __device__ __forceinline__ uint64_t now_ns() {
   return t;
 }
 __device__ __forceinline__ uint32_t su32(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
-
-__device__ __forceinline__ int32_t ld_fresh(const int32_t* p) {
-  int32_t v;
-  asm("ld.global.cv.s32 %0, [%1];" : "=r"(v) : "l"(p));
-  return v;
-}
 
 // shared-memory writes of this thread become visible to the tensor cores' (async proxy) reads
 __device__ __forceinline__ void fence_proxy_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
