@@ -68,7 +68,7 @@ class hs_meta_layout(ctypes.Structure):
 
 class hs_paged_rows(ctypes.Structure):
     _fields_ = [("rows", ctypes.c_void_p), ("count", ctypes.c_int64), ("pages", ctypes.c_void_p),
-                ("page_stride", ctypes.c_int64), ("page_rows", ctypes.c_int32)]
+                ("page_stride", ctypes.c_int64), ("page_rows", ctypes.c_int32), ("lists", ctypes.c_int32)]
 
 
 class hs_append_desc(ctypes.Structure):
@@ -272,10 +272,13 @@ def hs_gather_history(pool: int, layer: int, batch: int, topk_idx, k: int, dst, 
 
 def paged_rows(rows, pages, page_rows: int) -> hs_paged_rows:
     """The struct of an ordinary paged pool: `rows` a tensor [count][...] of contiguous rows, `pages` int32 [lists][entries]
-    (or [entries], one list). It keeps both tensors alive; build it once and pass it to every call."""
+    (or [entries], one list, request 0's). It keeps both tensors alive; build it once and pass it to every call."""
     if not rows.is_contiguous() or not pages.is_contiguous():
         raise ValueError("paged_rows takes contiguous tensors")
-    p = hs_paged_rows(rows.data_ptr(), rows.shape[0], pages.data_ptr(), pages.shape[-1], page_rows)
+    if pages.dim() not in (1, 2) or pages.numel() == 0:
+        raise ValueError(f"pages is [lists][entries] or [entries], not {tuple(pages.shape)}")
+    lists = 1 if pages.dim() == 1 else pages.shape[0]
+    p = hs_paged_rows(rows.data_ptr(), rows.shape[0], pages.data_ptr(), pages.shape[-1], page_rows, lists)
     p._keep = (rows, pages)
     return p
 

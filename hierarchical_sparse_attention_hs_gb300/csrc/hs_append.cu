@@ -74,6 +74,7 @@ struct AppendArgs {
   const int32_t* pages;
   int64_t page_stride, page_limit;  // pages 0 .. page_limit - 1 lie within the rows
   int32_t page_shift;
+  int32_t lists;          // lists of pages, one a request
   int32_t per_warp;       // tokens of a warp's rows
   int32_t row_blocks;     // blocks 0 .. row_blocks - 1 write rows, the others turn queries
   int32_t* err;
@@ -178,7 +179,7 @@ __device__ __forceinline__ void append_rows(const AppendArgs& a, float* weight, 
     if (i0 + lane < end) {
       if (token_of(a, i0 + lane, &my_req, &my_pos)) {
         my_slot = __ldcg(a.tok2slot + (int64_t)my_req * a.ctx + my_pos);
-        if (a.paged) {
+        if (a.paged && my_req < a.lists) {
           const int64_t pi = my_pos >> a.page_shift;
           const int page = pi < a.page_stride ? a.pages[my_req * a.page_stride + pi] : -1;
           if (page >= 0 && page < a.page_limit) my_row = (page << a.page_shift) + (my_pos & ((1 << a.page_shift) - 1));
@@ -379,7 +380,7 @@ bool stride_ok(int64_t stride, int64_t least, int size, int64_t count) {
 
 bool hs_paged_ok(const hs_paged_rows* p) {
   return p->rows && p->pages && aligned16(p->rows) && aligned4(p->pages) && p->count >= 0 &&
-         p->count <= INT32_MAX - 63 && p->page_stride >= 1 && p->page_rows >= 1 && p->page_rows <= 65536 &&
+         p->count <= INT32_MAX - 63 && p->page_stride >= 1 && p->lists >= 0 && p->page_rows >= 1 && p->page_rows <= 65536 &&
          (p->page_rows & (p->page_rows - 1)) == 0;
 }
 
@@ -446,6 +447,7 @@ extern "C" int hs_append(hs_pool* pool, int32_t layer, int32_t ntok, const hs_ap
     a.pages = paged->pages;
     a.page_stride = paged->page_stride;
     a.page_limit = paged->count / paged->page_rows;
+    a.lists = paged->lists ? paged->lists : pool->d.max_batch;
     while ((1 << a.page_shift) < paged->page_rows) ++a.page_shift;
   }
   a.err = pool->err;

@@ -285,6 +285,8 @@ int hs_mla_decode_history(hs_pool *pool, int32_t layer, int32_t batch, const voi
  *     hold that page's tokens; so does one whose page does not lie wholly within `count`.
  *   page_stride: entries of one list (>= 1): a token at or past page_stride * page_rows has no row.
  *   page_rows: rows of a page, a power of two from 1 (a list of single rows, such as resident_row) to 65536.
+ *   lists: lists that `pages` holds: the tokens of a request at or past it have no row. 0: one for each of the pool's
+ *     max_batch requests.
  */
 typedef struct {
   void *rows;
@@ -292,6 +294,7 @@ typedef struct {
   const int32_t *pages;
   int64_t page_stride;
   int32_t page_rows;
+  int32_t lists;
 } hs_paged_rows;
 
 /*
@@ -349,7 +352,7 @@ typedef struct {
  * in 0 .. max_batch-1 is skipped whole, and the error word gets HS_DEVERR_RANGE. (request, position) pairs are distinct
  * within a call (not checked: rows of a repeated pair may mix). ntok == 0 is a no-op; ntok <= 2^30, and
  * so is ntok * ceil(q_heads / 16); with req_ids NULL ntok <= max_batch. At least one of `paged`, to_history and q_rope
- * is given. Enqueued on `stream` (of the pool's device, which must be the current one: HS_ERR_INVALID_ARG);
+ * is given. A token that `paged` has no row for is not written there. Enqueued on `stream` (of the pool's device, which must be the current one: HS_ERR_INVALID_ARG);
  * capturable. Order it before the resolve, prefetch, gather or attention that reads the rows. Basis: the full history
  * in host memory that the paper's cache sits on (Abstract) and the ordinary KV blocks of the "Hybrid HiSparse" card
  * (Timeline) have to be written by somebody; the pages name no writer.

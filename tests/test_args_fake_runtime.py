@@ -125,3 +125,11 @@ got.append([append(ntok=8, q_heads=(1 << 31) - 1), append(ntok=9, q_heads=(1 << 
     assert got[0] == [0, [1 + 2, 1, 1]]  # a block of rows; 8 items are the warps of 2 blocks
     assert got[1] == got[2] == got[3] == [0, [1 + 152 * 16, 1, 1]]
     assert got[4] == [0, -1]  # 8 * 2^27 items are the limit
+
+
+def test_lists_of_pages(under):
+    """A block table says how many lists it holds; fewer than none is refused, and none of them means one a request."""
+    got = under("""
+got = {str(n): [append(paged=pages(lists=n)), prefix(paged=pages(lists=n))] for n in (-1, -(1 << 31), 0, 1, 4, 9)}
+""")
+    assert got == {"-1": [-1, -1], str(-(1 << 31)): [-1, -1], "0": [0, 0], "1": [0, 0], "4": [0, 0], "9": [0, 0]}
