@@ -11,6 +11,7 @@ Hierarchical KV Cache Management" (Abstract); the policy and the memory layout a
 from __future__ import annotations
 
 import ctypes
+import math
 import os
 import threading
 
@@ -40,6 +41,8 @@ HS_DEVERR_STATE = 4
 HS_DEVERR_TIMEOUT = 8
 HS_TYPE_BF16, HS_TYPE_F16, HS_TYPE_F32 = 0, 1, 2
 MLA_HEADS, MLA_D_QK, MLA_D_V = 128, 576, 512  # shape of the sparse MLA decode consumer
+
+KV_ROW_BYTES = (MLA_D_QK * 2, MLA_D_V + 4 * 4 + (MLA_D_QK - MLA_D_V) * 2)  # the row formats of hs_append: bf16, fp8
 
 LIB_PATH = _build_mod.LIB_PATH
 _lib = None
@@ -271,10 +274,18 @@ def hs_gather_history(pool: int, layer: int, batch: int, topk_idx, k: int, dst, 
 
 
 def paged_rows(rows, pages, page_rows: int) -> hs_paged_rows:
-    """The struct of an ordinary paged pool: `rows` a tensor [count][...] of contiguous rows, `pages` int32 [lists][entries]
-    (or [entries], one list, request 0's). It keeps both tensors alive; build it once and pass it to every call."""
+    """The struct of an ordinary paged pool: `rows` a tensor [count][...] of contiguous rows, each 1152 or 656 bytes (the
+    pool's row_bytes), `pages` int32 [lists][entries] (or [entries], one list, request 0's). It keeps both tensors alive;
+    build it once and pass it to every call."""
+    import torch
+
     if not rows.is_contiguous() or not pages.is_contiguous():
         raise ValueError("paged_rows takes contiguous tensors")
+    row_bytes = rows.element_size() * math.prod(rows.shape[1:])
+    if row_bytes not in KV_ROW_BYTES:
+        raise ValueError(f"rows is [count][...] with rows of 1152 or 656 bytes: {tuple(rows.shape)} of {rows.dtype} has {row_bytes}")
+    if pages.dtype != torch.int32:
+        raise ValueError(f"pages is int32, not {pages.dtype}")
     if pages.dim() not in (1, 2) or pages.numel() == 0:
         raise ValueError(f"pages is [lists][entries] or [entries], not {tuple(pages.shape)}")
     lists = 1 if pages.dim() == 1 else pages.shape[0]

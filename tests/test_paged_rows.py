@@ -22,3 +22,21 @@ def test_lists_are_counted():
                 torch.zeros(0, dtype=torch.int32)):
         with pytest.raises(ValueError):
             hs.paged_rows(rows(), bad, 16)
+
+
+def test_pages_are_int32():
+    """torch's default integer type, taken for int32, would make every other page 0."""
+    for dtype in (torch.int64, torch.int16, torch.float32):
+        with pytest.raises(ValueError, match="int32"):
+            hs.paged_rows(rows(), torch.zeros(4, dtype=dtype), 16)
+
+
+def test_rows_are_counted_by_their_bytes():
+    pages = torch.zeros(4, dtype=torch.int32)
+    for good in (rows(), rows(64, 1152, torch.uint8), rows(64, 656, torch.uint8), rows(64, 288, torch.float32),
+                 torch.zeros(64, 9, 64, dtype=torch.bfloat16), rows(0)):
+        assert hs.paged_rows(good, pages, 16).count == good.shape[0]
+    for bad in (torch.zeros(4, 16, 576, dtype=torch.bfloat16), rows(64, 576, torch.float32), rows(64, 512), rows(64, 576, torch.uint8),
+                torch.zeros(64 * 576, dtype=torch.bfloat16)):
+        with pytest.raises(ValueError, match="1152 or 656"):
+            hs.paged_rows(bad, pages, 16)
