@@ -46,6 +46,7 @@ KV_ROW_BYTES = (MLA_D_QK * 2, MLA_D_V + 4 * 4 + (MLA_D_QK - MLA_D_V) * 2)  # the
 
 LIB_PATH = _build_mod.LIB_PATH
 _lib = None
+_pool_row_bytes = {}  # of each open pool, by its handle
 _lock = threading.Lock()
 
 
@@ -206,6 +207,7 @@ def hs_get_meta_layout(desc: hs_pool_desc) -> dict:
 def hs_pool_create(desc: hs_pool_desc, stream=None) -> int:
     h = ctypes.c_void_p()
     _check(load().hs_pool_create(ctypes.byref(desc), _stream(stream), ctypes.byref(h)), "hs_pool_create")
+    _pool_row_bytes[h.value] = desc.row_bytes
     return h.value
 
 
@@ -290,8 +292,14 @@ def paged_rows(rows, pages, page_rows: int) -> hs_paged_rows:
         raise ValueError(f"pages is [lists][entries] or [entries], not {tuple(pages.shape)}")
     lists = 1 if pages.dim() == 1 else pages.shape[0]
     p = hs_paged_rows(rows.data_ptr(), rows.shape[0], pages.data_ptr(), pages.shape[-1], page_rows, lists)
-    p._keep = (rows, pages)
+    p._keep, p._row_bytes = (rows, pages), row_bytes
     return p
+
+
+def _check_row_bytes(pool: int, paged) -> None:
+    have, want = getattr(paged, "_row_bytes", None), _pool_row_bytes.get(pool)
+    if have and want and have != want:
+        raise ValueError(f"the paged rows have {have} bytes, the pool's {want}")
 
 
 def append_desc(kv, inv_freq, positions, req_ids=None, norm_weight=None, norm_eps: float = 0.0,
@@ -331,11 +339,14 @@ def append_desc(kv, inv_freq, positions, req_ids=None, norm_weight=None, norm_ep
 
 def hs_append(pool: int, layer: int, ntok: int, desc: hs_append_desc, paged: hs_paged_rows | None = None,
               to_history: bool = True, stream=None) -> None:
+    if paged is not None:
+        _check_row_bytes(pool, paged)
     _check(load().hs_append(pool, layer, ntok, desc, paged, int(to_history), _stream(stream)), "hs_append")
 
 
 def hs_mla_prefix(pool: int, batch: int, q, prefix: hs_paged_rows, max_length: int, prefix_length, sm_scale: float,
                   own_out, own_lse, out, out_type: int, lse, workspace, stream=None) -> None:
+    _check_row_bytes(pool, prefix)
     _check(load().hs_mla_prefix(pool, batch, _addr(q), prefix, max_length, _addr(prefix_length), sm_scale,
                                 _addr(own_out), _addr(own_lse), _addr(out), out_type, _addr(lse), _addr(workspace),
                                 0 if workspace is None else workspace.nbytes, _stream(stream)), "hs_mla_prefix")
@@ -359,6 +370,7 @@ def hs_get_counters(pool: int, layer: int) -> list:
 
 def hs_pool_destroy(pool: int) -> None:
     _check(load().hs_pool_destroy(pool), "hs_pool_destroy")
+    _pool_row_bytes.pop(pool, None)
 
 
 def hs_host_alloc(nbytes: int) -> int:

@@ -40,3 +40,23 @@ def test_rows_are_counted_by_their_bytes():
                 torch.zeros(64 * 576, dtype=torch.bfloat16)):
         with pytest.raises(ValueError, match="1152 or 656"):
             hs.paged_rows(bad, pages, 16)
+
+
+def test_rows_have_the_pools_bytes(monkeypatch):
+    """Rows of one format beside a pool of the other are refused before the library is called."""
+    pages = torch.zeros(4, dtype=torch.int32)
+    bf16, fp8 = hs.paged_rows(rows(), pages, 16), hs.paged_rows(rows(64, 656, torch.uint8), pages, 16)
+    monkeypatch.setitem(hs._pool_row_bytes, 7, 1152)
+    monkeypatch.setitem(hs._pool_row_bytes, 8, 656)
+    monkeypatch.setattr(hs, "load", lambda: (_ for _ in ()).throw(KeyError("called")))
+    for pool, good, bad in ((7, bf16, fp8), (8, fp8, bf16)):
+        with pytest.raises(ValueError, match="bytes"):
+            hs.hs_append(pool, 0, 1, hs.hs_append_desc(), bad, False, 0)
+        with pytest.raises(ValueError, match="bytes"):
+            hs.hs_mla_prefix(pool, 1, 0, bad, 16, None, 1.0, None, None, 0, 0, 0, None, 0)
+        with pytest.raises(KeyError, match="called"):
+            hs.hs_append(pool, 0, 1, hs.hs_append_desc(), good, False, 0)
+    with pytest.raises(KeyError, match="called"):  # a struct that somebody else filled, a pool from elsewhere
+        hs.hs_append(7, 0, 1, hs.hs_append_desc(), hs.hs_paged_rows(), False, 0)
+    with pytest.raises(KeyError, match="called"):
+        hs.hs_append(9, 0, 1, hs.hs_append_desc(), fp8, False, 0)
