@@ -333,12 +333,14 @@ def append_desc(kv, inv_freq, positions, req_ids=None, norm_weight=None, norm_ep
     if q is not None:
         d.q_rope_token_stride, d.q_rope_head_stride, d.q_heads = q_rope.stride(0), q_rope.stride(1), q_rope.shape[1]
         d.q_token_stride, d.q_head_stride = q.stride(0), q.stride(1)
-    d._keep = (kv, inv_freq, positions, req_ids, norm_weight, q_rope, q)
+    d._keep, d._tokens = (kv, inv_freq, positions, req_ids, norm_weight, q_rope, q), n
     return d
 
 
 def hs_append(pool: int, layer: int, ntok: int, desc: hs_append_desc, paged: hs_paged_rows | None = None,
               to_history: bool = True, stream=None) -> None:
+    if ntok > getattr(desc, "_tokens", ntok):
+        raise ValueError(f"{ntok} tokens, but the descriptor's tensors hold {desc._tokens}")
     if paged is not None:
         _check_row_bytes(pool, paged)
     _check(load().hs_append(pool, layer, ntok, desc, paged, int(to_history), _stream(stream)), "hs_append")

@@ -298,7 +298,7 @@ typedef struct {
 } hs_paged_rows;
 
 /*
- * What one append takes. Token i (0 <= i < ntok) belongs to request req_ids[i] (i itself when req_ids is NULL) at
+ * What one append takes (of at least ntok tokens). Token i (0 <= i < ntok) belongs to request req_ids[i] (i itself when req_ids is NULL) at
  * position positions[i]. Arrays are device memory; req_ids and positions may be mapped host memory. 32-bit arrays are
  * 4-byte aligned.
  *   type: HS_TYPE_* of kv and q_rope.
