@@ -346,9 +346,34 @@ def hs_append(pool: int, layer: int, ntok: int, desc: hs_append_desc, paged: hs_
     _check(load().hs_append(pool, layer, ntok, desc, paged, int(to_history), _stream(stream)), "hs_append")
 
 
+_dtypes = None  # torch's bf16, fp32 and int32, once torch is loaded
+
+
+def _load_dtypes():
+    global _dtypes
+    import torch
+
+    _dtypes = torch.bfloat16, torch.float32, torch.int32
+    return _dtypes
+
+
+def _fits(t, dtype, nbytes: int) -> bool:
+    """Whether a tensor has this type and as many bytes, in order. (Of an address nothing is known; None is the library's.)"""
+    return t is None or type(t) is int or (t.dtype is dtype and t.nbytes >= nbytes and t.is_contiguous())
+
+
 def hs_mla_prefix(pool: int, batch: int, q, prefix: hs_paged_rows, max_length: int, prefix_length, sm_scale: float,
                   own_out, own_lse, out, out_type: int, lse, workspace, stream=None) -> None:
     _check_row_bytes(pool, prefix)
+    bf16, f32, i32 = _dtypes or _load_dtypes()
+    rows = batch * MLA_HEADS
+    out_dtype = f32 if out_type == HS_TYPE_F32 else bf16
+    if not (_fits(q, bf16, rows * MLA_D_QK * 2) and _fits(out, out_dtype, rows * MLA_D_V * out_dtype.itemsize) and
+            _fits(lse, f32, rows * 4) and
+            (own_out is None or _fits(own_out, f32, rows * MLA_D_V * 4) and _fits(own_lse, f32, rows * 4)) and
+            (prefix_length is None or _fits(prefix_length, i32, 4))):
+        raise ValueError(f"hs_mla_prefix of {batch} takes contiguous tensors: q bf16 [{batch}][128][576], out {out_dtype} "
+                         f"[{batch}][128][512], lse fp32 [{batch}][128], own_out and own_lse fp32 as out and lse, prefix_length int32")
     _check(load().hs_mla_prefix(pool, batch, _addr(q), prefix, max_length, _addr(prefix_length), sm_scale,
                                 _addr(own_out), _addr(own_lse), _addr(out), out_type, _addr(lse), _addr(workspace),
                                 0 if workspace is None else workspace.nbytes, _stream(stream)), "hs_mla_prefix")
