@@ -89,6 +89,8 @@ class hs_append_desc(ctypes.Structure):
 def load():
     """Open libhs.so (built by ``build.build()``); raises if it is missing -- there is no other path."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is not None:
             return _lib
