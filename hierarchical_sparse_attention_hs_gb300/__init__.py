@@ -25,7 +25,7 @@ __all__ = [
     "hs_resolve_shared", "hs_resolve_tiered", "hs_mla_decode", "hs_mla_decode_history", "HS_DEVERR_TIMEOUT",
     "MLA_HEADS", "MLA_D_QK", "MLA_D_V", "hs_probe_launch", "hs_debug_attention", "hs_step_begin_fused", "hs_probe_link_static", "HS_ERR_TOO_LARGE",
     "hs_resolve_ids", "hs_prefetch_ids", "hs_append", "hs_append_desc", "append_desc", "hs_paged_rows", "paged_rows",
-    "hs_mla_prefix", "hs_mla_prefix_workspace", "HS_TYPE_BF16", "HS_TYPE_F16", "HS_TYPE_F32",
+    "hs_mla_prefix", "hs_mla_prefix_workspace", "hs_mla_prefix_workspace_bound", "HS_TYPE_BF16", "HS_TYPE_F16", "HS_TYPE_F32",
 ]
 
 HS_OK = 0
@@ -130,6 +130,7 @@ def load():
             "hs_mla_prefix": (ctypes.c_int, [vp, i32, vp, P(hs_paged_rows), i32, vp, ctypes.c_float, vp, vp, vp, i32, vp,
                                              vp, sz, vp]),
             "hs_mla_prefix_workspace": (sz, [vp, i32, i32]),
+            "hs_mla_prefix_workspace_bound": (ctypes.c_int, [vp, i32, i32, P(sz)]),
         }
         for name, (res, args) in sig.items():
             fn = getattr(lib, name)
@@ -383,6 +384,12 @@ def hs_mla_prefix(pool: int, batch: int, q, prefix: hs_paged_rows, max_length: i
 
 def hs_mla_prefix_workspace(pool: int, batch: int, max_length: int) -> int:
     return int(load().hs_mla_prefix_workspace(pool, batch, max_length))
+
+
+def hs_mla_prefix_workspace_bound(pool: int, batch: int, max_length: int) -> int:
+    n = ctypes.c_size_t()
+    _check(load().hs_mla_prefix_workspace_bound(pool, batch, max_length, ctypes.byref(n)), "hs_mla_prefix_workspace_bound")
+    return int(n.value)
 
 
 def hs_get_error(pool: int, clear: bool = False) -> int:

@@ -875,9 +875,14 @@ int pairs_resident() {
 
 // How a batch is cut into units: requests 0 .. whole - 1 are one unit each, the others `nsplit` units.
 struct Cut {
+  static constexpr size_t SPLIT_BYTES = HEADS * (DV * sizeof(float) + sizeof(float2));  // of one split of one request
   int whole, nsplit;
-  size_t workspace(int batch) const {
-    return nsplit > 1 ? (size_t)nsplit * (size_t)(batch - whole) * HEADS * (DV * sizeof(float) + sizeof(float2)) : 0;
+  size_t workspace(int batch) const { return nsplit > 1 ? (size_t)nsplit * (size_t)(batch - whole) * SPLIT_BYTES : 0; }
+  // The most that any cut_of takes for up to this batch and length: a request has at most as many splits as tiles and
+  // MAX_SPLIT, and all splits together are at most 4 * pairs.
+  static size_t most(int pairs, int32_t batch, int32_t max_length) {
+    const int tiles = (max_length + NK - 1) / NK;
+    return tiles < 2 ? 0 : (size_t)std::min<int64_t>(4 * pairs, (int64_t)batch * std::min(tiles, MAX_SPLIT)) * SPLIT_BYTES;
   }
 };
 // The cut with the shortest expected time, in tiles (1.2 to 2.6 us): a pair's units one after the other, each its tiles and
@@ -952,6 +957,17 @@ extern "C" size_t hs_mla_prefix_workspace(hs_pool* pool, int32_t batch, int32_t 
   if (!pool || batch <= 0 || max_length < 0 || max_length > 1 << 30 || batch > (1 << 24) / HEADS || !hs_on_device(pool)) return 0;
   const int pairs = pairs_resident();
   return pairs > 0 ? cut_of(pairs, batch, max_length).workspace(batch) : 0;
+}
+
+extern "C" int hs_mla_prefix_workspace_bound(hs_pool* pool, int32_t batch, int32_t max_length, size_t* bytes) {
+  if (!bytes) return HS_ERR_INVALID_ARG;
+  *bytes = 0;
+  if (!pool || batch < 0 || batch > (1 << 24) / HEADS || max_length < 0 || max_length > 1 << 30 || !hs_on_device(pool))
+    return HS_ERR_INVALID_ARG;
+  const int pairs = pairs_resident();
+  if (pairs < 1) return HS_ERR_UNSUPPORTED;
+  *bytes = Cut::most(pairs, batch, max_length);
+  return HS_OK;
 }
 
 extern "C" int hs_mla_prefix(hs_pool* pool, int32_t batch, const void* q, const hs_paged_rows* prefix,

@@ -367,8 +367,8 @@ int hs_append(hs_pool *pool, int32_t layer, int32_t ntok, const hs_append_desc *
  *     s[t] = sm_scale * dot(q[b][h][0:576], row_t),  out[b][h][0:512] = sum_T softmax(s)[t] * row_t[0:512],
  *     lse[b][h] = ln sum_T exp(s[t]).
  * Rows outside T are never looked at, whatever they hold. With no token in T an output is zero and its lse -inf.
- *   q: device bf16 [batch][128][576], 16-byte aligned. batch >= 0 is not bound by max_batch: several query tokens of one
- *     request are several rows of the batch.
+ *   q: device bf16 [batch][128][576], 16-byte aligned. batch is 0 .. 131072 and not bound by max_batch: several query tokens
+ *     of one request are several rows of the batch.
  *   prefix: the paged rows; its list 0 is the prefix (page_stride entries of it at most are read).
  *   max_length: tokens, 0 .. 2^30 and <= page_stride * page_rows. prefix_length: NULL, or device int32 [1], the length to use
  *     (clamped to 0 .. max_length), read when the kernel runs: a captured graph can be replayed over a prefix that grew.
@@ -376,8 +376,8 @@ int hs_append(hs_pool *pool, int32_t layer, int32_t ntok, const hs_append_desc *
  *     [batch][128][512], 16-byte aligned, and [batch][128]): out and lse are then those of both sets of rows together.
  *   out: [batch][128][512] of out_type (HS_TYPE_BF16 or HS_TYPE_F32), 16-byte aligned; lse: fp32 [batch][128]. They
  *     overlap no input, but with out_type HS_TYPE_F32 they may be own_out and own_lse themselves.
- *   workspace: device memory of hs_mla_prefix_workspace bytes, 256-byte aligned (NULL where that is 0); its contents are
- *     scratch. Calls that may run at the same time (two streams, two graphs) need workspaces of their own.
+ *   workspace: device memory of hs_mla_prefix_workspace bytes or more for this batch and max_length (or of
+ *     hs_mla_prefix_workspace_bound for the largest), 256-byte aligned (NULL where that is 0); its contents are scratch. Calls that may run at the same time (two streams, two graphs) need workspaces of their own.
  * The weights are rounded to bf16 before the value product; scores, sums and outputs accumulate in 32 bits, and lse sums
  * the unrounded weights. Results are deterministic for given batch, max_length and device. Enqueued on `stream` (of the
  * pool's device, which must be the current one); capturable; batch == 0 is a no-op. Basis: the "Hybrid HiSparse" card
@@ -387,9 +387,14 @@ int hs_mla_prefix(hs_pool *pool, int32_t batch, const void *q, const hs_paged_ro
                   const int32_t *prefix_length, float sm_scale, const float *own_out, const float *own_lse, void *out,
                   int32_t out_type, float *lse, void *workspace, size_t workspace_bytes, hs_stream_t stream);
 
-/* Bytes of workspace that hs_mla_prefix needs for a batch and max_length on the pool's device (0: none, or bad
- * arguments). */
+/* Bytes of workspace that hs_mla_prefix needs for this batch and max_length on the pool's device, which must be the current
+ * one (0: none, or bad arguments, which the call itself then refuses). A smaller batch or length may need more: with 76 pairs
+ * of CTAs resident, 8,192 tokens take none for 76 requests, 31.6 MB for 40 and 8.4 MB for one. */
 size_t hs_mla_prefix_workspace(hs_pool *pool, int32_t batch, int32_t max_length);
+
+/* The same for a workspace that is made once: *bytes suffices for every call of at most `batch` requests and max_length
+ * tokens (80 MB at most with 76 pairs resident). HS_ERR_INVALID_ARG for bad arguments or a pool of another device. */
+int hs_mla_prefix_workspace_bound(hs_pool *pool, int32_t batch, int32_t max_length, size_t *bytes);
 
 /*
  * Test hook of the attention consumer (not for production use; process-wide settings, not thread-safe). It lets a

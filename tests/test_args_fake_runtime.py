@@ -133,3 +133,42 @@ def test_lists_of_pages(under):
 got = {str(n): [append(paged=pages(lists=n)), prefix(paged=pages(lists=n))] for n in (-1, -(1 << 31), 0, 1, 4, 9)}
 """)
     assert got == {"-1": [-1, -1], str(-(1 << 31)): [-1, -1], "0": [0, 0], "1": [0, 0], "4": [0, 0], "9": [0, 0]}
+
+
+def test_workspace_of_the_largest_call_serves_the_smaller_ones(under):
+    """The workspace of one call is no bound for calls of fewer requests or tokens; the bound is, and no call of a sweep
+    (76 pairs of CTAs) is refused with it."""
+    got = under("""
+block = pool()
+p = ctypes.addressof(block)
+need, bound = hs.hs_mla_prefix_workspace, hs.hs_mla_prefix_workspace_bound
+tokens = [0, 1, 256, 257, 511, 513, 2047, 4096, 8192, 9001, 30000, 131072, 1 << 20, 1 << 30]
+over, low, refused = [], 0, []
+for B in list(range(1, 80)) + [100, 152, 153, 229, 1000, 131072]:
+    for L in tokens:
+        top = bound(p, B, L)
+        low = max(low, top)
+        smaller = [(b, l) for b in {1, 2, 3, B // 3, B // 2, B - 1, B} if 0 < b <= B for l in tokens if l <= L]
+        over += [(B, L, b, l) for b, l in smaller if need(p, b, l) > top]
+for b in (1, 2, 7, 40, 75, 76, 77, 100, 150, 153):
+    for l in tokens:
+        n = bound(p, 153, 1 << 30)
+        if prefix(batch=b, max_length=l, paged=pages(page_stride=1 << 26), nbytes=n):
+            refused.append((b, l))
+        if need(p, b, l) and not prefix(batch=b, max_length=l, paged=pages(page_stride=1 << 26), nbytes=need(p, b, l) - 1):
+            refused.append((b, l, "not"))
+def rc(*a):
+    try:
+        return [0, bound(*a)]
+    except hs.HsError as e:
+        return [e.code, None]
+got = dict(over=over[:5], refused=refused[:5], most=low, listed=[need(p, 76, 8192), need(p, 40, 8192), need(p, 1, 8192)],
+           bad=[rc(0, 1, 1), rc(p, -1, 1), rc(p, 131073, 1), rc(p, 1, -1), rc(p, 1, (1 << 30) + 1)], none=[rc(p, 0, 100), rc(p, 5, 256)],
+           null=hs.load().hs_mla_prefix_workspace_bound(p, 1, 1, None),
+           batches=[prefix(batch=131072, max_length=1), prefix(batch=131073, max_length=1)])
+""")
+    assert got["over"] == [] and got["refused"] == []
+    assert got["most"] == 4 * 76 * 128 * (512 * 4 + 8)
+    assert got["listed"][0] < got["listed"][2] < got["listed"][1]
+    assert [x[0] for x in got["bad"]] == [-1] * 5 and got["none"] == [[0, 0], [0, 0]] and got["null"] == -1
+    assert got["batches"] == [0, -1]
