@@ -27,6 +27,7 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <atomic>
 #include <cstdint>
 #include <cstring>
 
@@ -45,11 +46,17 @@ constexpr int FP8_ROPE = LATENT + 4 * 4;         // byte offset of the rotary ke
 constexpr int Q_HEADS = 16;                      // heads of one warp's work item: four 16-byte loads a lane in flight
 constexpr int MAX_TOKENS = 1 << 30;              // and items of 16 heads of a token's queries
 constexpr int THREADS = 128, WARPS = THREADS / 32;
-// Blocks an SM of either kind, at most. 131,071 rows with 8, 12, 16 blocks an SM: from bf16 into fp8 rows 59.5, 49.7,
-// 52.6 us; from fp32 into bf16 rows 79.6, 69.7, 70.6; from bf16 into bf16 rows 49.7, 54.4, 49.8. The last at other sizes:
-// 5,000 rows 5.1, 4.7, 4.7 us; 8,191 5.3, 5.2, 6.1; 16,384 8.7, 10.1, 9.5; 65,536 26.5, 28.4, 26.9. So 16-bit values into
-// bf16 rows get 8, all others 12.
-constexpr int ROW_BLOCKS = 12, ROW_BLOCKS_PLAIN = 8, Q_BLOCKS = 16;
+// Blocks of a kernel that an SM holds at least. A launch of many tokens has as many blocks of rows as the device holds: all
+// warps get the same number of tokens, so time goes in whole waves, and in one wave a warp works its turn rates out once.
+// For 656-byte rows a bound of 7 (72 registers a thread) measured best; 131,071 / 16,384 / 8,191 rows in us: from 16 bits
+// 50.5 / 9.3 / 6.0 (a bound of 8 50.5 / 10.2 / 6.4, of 6 51.8 / 9.7 / 6.8, twelve blocks where seven fit 50.2 / 10.6 / 6.0), from fp32
+// 61.0 / 10.6 / 6.4 (of 6 63.2 / 11.1 / 7.3, of 5 64.5 / 11.3 / 6.7, twelve blocks 65.7 / 13.1 / 6.5). For 1152-byte rows the
+// compiler's own choice is kept, 8 blocks from 16 bits, 50.2 / 8.9 / 5.3 (a bound of 7 50.3 / 8.8 / 5.0, of 6 52.9 / 9.2 / 5.6; one of 8
+// took the queries of 256 and 2,047 tokens from 2.8 and 13.4 to 3.05 and 14.0), 6 from fp32, 70.3 / 11.4 / 6.4 (a bound of 7 73.4 / 10.9
+// / 5.6, of 5 70.9 / 11.7 / 5.8).
+template <bool FP8>
+constexpr int MIN_BLOCKS = FP8 ? 7 : 0;  // 0: none
+constexpr int Q_BLOCKS = 16;  // blocks of queries an SM, at most
 
 struct AppendArgs {
   const void* kv;
@@ -74,7 +81,7 @@ struct AppendArgs {
   const int32_t* pages;
   int64_t page_stride, page_limit;  // pages 0 .. page_limit - 1 lie within the rows
   int32_t page_shift;
-  int32_t lists;          // lists of pages, one a request
+  int32_t lists;          // lists of pages, one a request; 0 without paged rows
   int32_t per_warp;       // tokens of a warp's rows
   int32_t row_blocks;     // blocks 0 .. row_blocks - 1 write rows, the others turn queries
   int32_t* err;
@@ -179,7 +186,7 @@ __device__ __forceinline__ void append_rows(const AppendArgs& a, float* weight, 
     if (i0 + lane < end) {
       if (token_of(a, i0 + lane, &my_req, &my_pos)) {
         my_slot = __ldcg(a.tok2slot + (int64_t)my_req * a.ctx + my_pos);
-        if (a.paged && my_req < a.lists) {
+        if (my_req < a.lists) {
           const int64_t pi = my_pos >> a.page_shift;
           const int page = pi < a.page_stride ? a.pages[my_req * a.page_stride + pi] : -1;
           if (page >= 0 && page < a.page_limit) my_row = (page << a.page_shift) + (my_pos & ((1 << a.page_shift) - 1));
@@ -346,7 +353,7 @@ __device__ __forceinline__ void turn_queries(const AppendArgs& a, int lane, int 
 }
 
 template <class T, bool FP8, bool INTER>
-__global__ void __launch_bounds__(THREADS) hs_append_kernel(const AppendArgs a) {
+__global__ void __launch_bounds__(THREADS, MIN_BLOCKS<FP8>) hs_append_kernel(const AppendArgs a) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;");
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
@@ -359,14 +366,24 @@ __global__ void __launch_bounds__(THREADS) hs_append_kernel(const AppendArgs a) 
                            ((int)gridDim.x - a.row_blocks) * WARPS);
 }
 
-template <class T, bool FP8>
-cudaError_t launch(const cudaLaunchConfig_t& cfg, const AppendArgs& a, bool inter) {
-  return inter ? cudaLaunchKernelEx(&cfg, hs_append_kernel<T, FP8, true>, a)
-               : cudaLaunchKernelEx(&cfg, hs_append_kernel<T, FP8, false>, a);
-}
+using Kernel = void (*)(AppendArgs);
 template <class T>
-cudaError_t launch(const cudaLaunchConfig_t& cfg, const AppendArgs& a, bool fp8, bool inter) {
-  return fp8 ? launch<T, true>(cfg, a, inter) : launch<T, false>(cfg, a, inter);
+Kernel kernel_of(bool fp8, bool inter) {
+  if (fp8) return inter ? hs_append_kernel<T, true, true> : hs_append_kernel<T, true, false>;
+  return inter ? hs_append_kernel<T, false, true> : hs_append_kernel<T, false, false>;
+}
+// How many blocks of a kernel an SM of the device holds, cached per device and `form` (0 .. 11); 0 on an error.
+int blocks_held(Kernel kernel, int form, int device) {
+  static std::atomic<int> cache[64][12];
+  if (device < 0 || device >= 64) return 0;
+  int n = cache[device][form].load(std::memory_order_relaxed);
+  if (n) return n;
+  if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, reinterpret_cast<const void*>(kernel), THREADS, 0) != cudaSuccess) {
+    cudaGetLastError();
+    return 0;
+  }
+  cache[device][form].store(n, std::memory_order_relaxed);
+  return n;
 }
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
@@ -452,10 +469,15 @@ extern "C" int hs_append(hs_pool* pool, int32_t layer, int32_t ntok, const hs_ap
   }
   a.err = pool->err;
 
-  // As many warps as the device holds, each with its share of the tokens (and of the queries' items): the turn rates (64-bit
-  // arithmetic) are worked out once per warp, not per row.
+  // As many warps of rows as the device holds at once, each with its share of the tokens (and of the queries' items, whose
+  // warps come on top): the turn rates (64-bit arithmetic) are worked out once per warp, not per row.
   const bool fp8 = pool->d.row_bytes == ROW_FP8, inter = d.interleaved != 0;
-  const int64_t most = (int64_t)pool->num_sms * (fp8 || size == 4 ? ROW_BLOCKS : ROW_BLOCKS_PLAIN);
+  const Kernel kernel = d.type == HS_TYPE_BF16  ? kernel_of<__nv_bfloat16>(fp8, inter)
+                        : d.type == HS_TYPE_F16 ? kernel_of<__half>(fp8, inter)
+                                                : kernel_of<float>(fp8, inter);
+  const int held = blocks_held(kernel, d.type * 4 + fp8 * 2 + inter, pool->device);
+  if (held < 1) return HS_ERR_CUDA;
+  const int64_t most = (int64_t)pool->num_sms * held;
   const int64_t items = (int64_t)ntok * a.head_items;
   a.per_warp = (int32_t)((ntok + most * WARPS - 1) / (most * WARPS));
   const int64_t row_warps = ((int64_t)ntok + a.per_warp - 1) / a.per_warp;
@@ -470,8 +492,5 @@ extern "C" int hs_append(hs_pool* pool, int32_t layer, int32_t ntok, const hs_ap
   attr.val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  const cudaError_t e = d.type == HS_TYPE_BF16  ? launch<__nv_bfloat16>(cfg, a, fp8, inter)
-                        : d.type == HS_TYPE_F16 ? launch<__half>(cfg, a, fp8, inter)
-                                                : launch<float>(cfg, a, fp8, inter);
-  return e == cudaSuccess ? HS_OK : HS_ERR_CUDA;
+  return cudaLaunchKernelEx(&cfg, kernel, a) == cudaSuccess ? HS_OK : HS_ERR_CUDA;
 }

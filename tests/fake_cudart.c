@@ -24,6 +24,13 @@ int cudaOccupancyMaxActiveClusters(int *clusters, const void *f, const void *con
   *clusters = 76;
   return 0;
 }
+static int held = 8; /* blocks of any kernel that an SM holds */
+void fake_hold(int blocks) { held = blocks; }
+int cudaOccupancyMaxActiveBlocksPerMultiprocessor(int *blocks, const void *f, int threads, size_t smem) {
+  (void)f, (void)threads, (void)smem;
+  *blocks = held;
+  return held ? 0 : 2;
+}
 static int encode_tensor_map(void) { return 0; }
 int cudaGetDriverEntryPointByVersion(const char *symbol, void **f, unsigned version, unsigned long long flags, int *found) {
   (void)symbol, (void)version, (void)flags;

@@ -172,3 +172,26 @@ got = dict(over=over[:5], refused=refused[:5], most=low, listed=[need(p, 76, 819
     assert got["listed"][0] < got["listed"][2] < got["listed"][1]
     assert [x[0] for x in got["bad"]] == [-1] * 5 and got["none"] == [[0, 0], [0, 0]] and got["null"] == -1
     assert got["batches"] == [0, -1]
+
+
+def test_rows_of_many_tokens_are_one_wave(under):
+    """A launch of many tokens has as many blocks of rows as the device holds of its kernel, asked once for each kernel:
+    more would run as a second, partly filled wave."""
+    got = under("""
+got, held = [], 0
+for rb in (1152, 656):
+    for type in (hs.HS_TYPE_BF16, hs.HS_TYPE_F16, hs.HS_TYPE_F32):
+        for interleaved in (0, 1):
+            call = dict(p=pool(row_bytes=rb), type=type, interleaved=interleaved, q_rope=None, q=None, q_heads=0)
+            fake.fake_hold(0)  # the question fails, and is asked again by the next call
+            got.append([append(ntok=1, **call), -2, 0])
+            held += 1
+            fake.fake_hold(held)
+            for ntok in (1, 127, 5000, 152 * held * 4, 152 * held * 4 + 1, 131071, 1 << 30):
+                rc = append(ntok=ntok, **call)
+                blocks = fake.fake_grid(fake.fake_launches() - 1)[0]
+                per = -(-ntok // (152 * held * 4))  # a warp's tokens, the least that one wave can have
+                got.append([rc, 0, blocks - -(-(-(-ntok // per)) // 4)])
+                got.append([blocks > 152 * held, False, 0])
+""")
+    assert [x for x in got if x[0] != x[1] or x[2]] == []
