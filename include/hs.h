@@ -67,11 +67,12 @@ typedef struct hs_pool hs_pool;
 #define HS_ERR_CUDA (-2)        /* a CUDA runtime call or launch failed */
 #define HS_ERR_NOT_MAPPED (-3)  /* host_pool is not page-locked, device-mapped memory */
 #define HS_ERR_NO_MEMORY (-4)   /* host struct allocation failed */
-#define HS_ERR_UNSUPPORTED (-5) /* geometry needs more shared memory per block than the device offers */
+#define HS_ERR_UNSUPPORTED (-5) /* geometry needs more shared memory per block than the device offers, or row_bytes that the
+                                 * operator does not take */
 #define HS_ERR_TOO_LARGE (-6)   /* request larger than the fixed device scratch of hs_probe_link_static */
 
 /* Bits of the sticky device error word. */
-#define HS_DEVERR_RANGE 1 /* a selected token was >= ctx */
+#define HS_DEVERR_RANGE 1 /* a selected or appended token was >= ctx, or its request out of range */
 #define HS_DEVERR_DUP 2   /* a token appeared twice in one selection row */
 #define HS_DEVERR_STATE 4 /* metadata found inconsistent (never set by correct use) */
 #define HS_DEVERR_TIMEOUT 8 /* a kernel's bounded wait ran out and it stopped early (never set by correct use) */
@@ -346,7 +347,8 @@ typedef struct {
  * which must be writable, or the no-IO copy of a pool that has one), the paged rows when `paged` is given (list
  * req_ids[i]), and always the hot slot that the token occupies, if it occupies one, so that a resolve after a rewrite
  * (a rolled-back speculation, say) never serves the old row. (Of a no-IO pool the host copy is not written; of a pool
- * whose layers read overlapping host rows, the row that they share.) Norm and rotation are computed in 32 bits; each value is
+ * whose layers read overlapping host rows, the row that they share.) Norm and rotation are computed in 32 bits, the squares'
+ * sum too: with a norm it has to stay within their range (magnitudes below 2^59; above 2^-63 where norm_eps is 0). Each value is
  * rounded once.
  * A token with a negative position is padding: it touches nothing. One whose position is >= ctx or whose request is not
  * in 0 .. max_batch-1 is skipped whole, and the error word gets HS_DEVERR_RANGE. (request, position) pairs are distinct
@@ -373,13 +375,15 @@ int hs_append(hs_pool *pool, int32_t layer, int32_t ntok, const hs_append_desc *
  *   max_length: tokens, 0 .. 2^30 and <= page_stride * page_rows. prefix_length: NULL, or device int32 [1], the length to use
  *     (clamped to 0 .. max_length), read when the kernel runs: a captured graph can be replayed over a prefix that grew.
  *   own_out, own_lse: NULL, or the same requests' attention over rows of their own, as hs_mla_decode wrote it (fp32
- *     [batch][128][512], 16-byte aligned, and [batch][128]): out and lse are then those of both sets of rows together.
+ *     [batch][128][512], 16-byte aligned, and [batch][128]): out and lse are then those of both sets of rows together. The
+ *     sets are taken to be disjoint: a token of the prefix that a selection holds as well counts twice.
  *   out: [batch][128][512] of out_type (HS_TYPE_BF16 or HS_TYPE_F32), 16-byte aligned; lse: fp32 [batch][128]. They
  *     overlap no input, but with out_type HS_TYPE_F32 they may be own_out and own_lse themselves.
  *   workspace: device memory of hs_mla_prefix_workspace bytes or more for this batch and max_length (or of
  *     hs_mla_prefix_workspace_bound for the largest), 256-byte aligned (NULL where that is 0); its contents are scratch. Calls that may run at the same time (two streams, two graphs) need workspaces of their own.
- * The weights are rounded to bf16 before the value product; scores, sums and outputs accumulate in 32 bits, and lse sums
- * the unrounded weights. Results are deterministic for given batch, max_length and device. Enqueued on `stream` (of the
+ * The weights are rounded to bf16 before the value product, whose other operand is bf16 (2^-8 of each at most, which leaves
+ * outputs about 0.0013 off in the mean before their own rounding); scores, sums and outputs accumulate in 32 bits, and the
+ * normaliser and lse sum the unrounded weights. Results are deterministic for given batch, max_length and device. Enqueued on `stream` (of the
  * pool's device, which must be the current one); capturable; batch == 0 is a no-op. Basis: the "Hybrid HiSparse" card
  * (Timeline) serves resident rows from the ordinary KV blocks; requests that share blocks are its plainest case.
  */
