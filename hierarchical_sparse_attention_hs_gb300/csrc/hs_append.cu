@@ -410,6 +410,12 @@ bool hs_on_device(const hs_pool* p) {
   return dev == p->device;
 }
 
+int hs_launched(cudaError_t e) {
+  if (e == cudaSuccess) return HS_OK;
+  cudaGetLastError();
+  return HS_ERR_CUDA;
+}
+
 extern "C" int hs_append(hs_pool* pool, int32_t layer, int32_t ntok, const hs_append_desc* desc,
                          const hs_paged_rows* paged, int32_t to_history, hs_stream_t stream) {
   if (!pool || !desc || layer < 0 || layer >= pool->d.layers || ntok < 0) return HS_ERR_INVALID_ARG;
@@ -492,5 +498,5 @@ extern "C" int hs_append(hs_pool* pool, int32_t layer, int32_t ntok, const hs_ap
   attr.val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kernel, a) == cudaSuccess ? HS_OK : HS_ERR_CUDA;
+  return hs_launched(cudaLaunchKernelEx(&cfg, kernel, a));
 }

@@ -1042,14 +1042,13 @@ extern "C" int hs_mla_prefix(hs_pool* pool, int32_t batch, const void* q, const 
   attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  if (cudaLaunchKernelEx(&cfg, hs_prefix_kernel, a, qmap, map, map2, map1, small, omap, pmap) != cudaSuccess) return HS_ERR_CUDA;
-  if (!rest) return HS_OK;
+  const int rc = hs_launched(cudaLaunchKernelEx(&cfg, hs_prefix_kernel, a, qmap, map, map2, map1, small, omap, pmap));
+  if (rc != HS_OK || !rest) return rc;
   cfg.gridDim = dim3((unsigned)rest * HEADS, 1, 1);
   cfg.dynamicSmemBytes = 0;
   cfg.numAttrs = 1;
   const int groups = cut.nsplit <= 16 ? 1 : 4;
   cfg.blockDim = dim3((unsigned)groups * DV / 4, 1, 1);
-  const cudaError_t e = groups == 1 ? cudaLaunchKernelEx(&cfg, hs_prefix_join_kernel<1>, a)
-                                    : cudaLaunchKernelEx(&cfg, hs_prefix_join_kernel<4>, a);
-  return e == cudaSuccess ? HS_OK : HS_ERR_CUDA;
+  return hs_launched(groups == 1 ? cudaLaunchKernelEx(&cfg, hs_prefix_join_kernel<1>, a)
+                                 : cudaLaunchKernelEx(&cfg, hs_prefix_join_kernel<4>, a));
 }

@@ -14,7 +14,14 @@ int cudaGetDevice(int *device) {
   *device = 0;
   return 0;
 }
-int cudaGetLastError(void) { return 0; }
+static int last_error, fail_at; /* fail_at: launches from this one on fail (1: the next); 0: none does */
+void fake_fail(int at) { fail_at = at; }
+int fake_last_error(void) { return last_error; }
+int cudaGetLastError(void) {
+  const int e = last_error;
+  last_error = 0;
+  return e;
+}
 int cudaFuncSetAttribute(const void *f, int attr, int value) {
   (void)f, (void)attr, (void)value;
   return 0;
@@ -41,6 +48,8 @@ int cudaGetDriverEntryPointByVersion(const char *symbol, void **f, unsigned vers
 /* cudaLaunchConfig_t begins with the grid's three numbers */
 int cudaLaunchKernelExC(const void *config, const void *f, void **args) {
   (void)f, (void)args;
+  if (fail_at == 1) return last_error = 1;
+  if (fail_at > 1) --fail_at;
   for (int i = 0; i < 3; ++i) grid[launches % 64][i] = ((const unsigned *)config)[i];
   ++launches;
   return 0;
