@@ -116,3 +116,50 @@ def test_hot_slots_of_every_pool(row_bytes, noio):
     keep = ~changed
     assert torch.equal(hot.cpu()[keep], before.cpu()[keep]) and (hot[1, 0, int(slots[0, 8])] == 7).all()
     assert hs.hs_get_error(s.pool) == 0
+
+
+@pytest.mark.parametrize("page", [256, 65536])
+def test_large_pages(page):
+    s = Setup(60, ctx=700, page=page)
+    s.run()
+    s.check_all()
+
+
+def test_positions_in_mapped_host_memory():
+    """positions and req_ids are read over the host link and afresh by every call."""
+    s = Setup(40, heads=3)
+    s.desc()
+    pos, req = s.pos.pin_memory(), s.req.pin_memory()
+    d = hs.append_desc(s.kv, torch.from_numpy((10000.0 ** (-np.arange(0, 64, 2) / 64)).astype(np.float32)).cuda(), pos,
+                       req_ids=req, norm_weight=s.weight, norm_eps=1e-5, q_rope=s.q_rope, q=s.q)
+    for i in range(3):
+        if i:
+            s.pos = torch.cat([torch.randperm(s.ctx, generator=torch.Generator().manual_seed(i))[:40].int()])
+            s.pos[i] = -1
+            pos.copy_(s.pos)
+            s.rows.fill_(9)
+            s.buf.host.numpy()[:] = 7
+            s.q_before = s.q.clone()
+            torch.cuda.synchronize()
+        hs.hs_append(s.pool, 1, s.n, d, s.paged(), True)
+        torch.cuda.synchronize()
+        s.check_all()
+
+
+def test_two_appends_at_once():
+    """Two streams write different tokens of one pool at the same time."""
+    s = Setup(240, heads=4)
+    s.desc()
+    half, streams, descs = s.n // 2, [torch.cuda.Stream() for _ in range(2)], []
+    freq = torch.from_numpy((10000.0 ** (-np.arange(0, 64, 2) / 64)).astype(np.float32)).cuda()
+    for i in range(2):
+        at = slice(i * half, (i + 1) * half)
+        descs.append(hs.append_desc(s.kv[at], freq, s.pos_d[at], req_ids=s.req_d[at], norm_weight=s.weight, norm_eps=1e-5,
+                                    q_rope=s.q_rope[at], q=s.q[at]))
+    paged = s.paged()
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for d, stream in zip(descs, streams):
+            hs.hs_append(s.pool, 1, half, d, paged, True, stream=stream)
+    torch.cuda.synchronize()
+    s.check_all()

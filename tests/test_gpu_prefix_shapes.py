@@ -78,3 +78,95 @@ def test_fp32_outputs_and_in_place(pool, kind, batch, length):
     got = c.run(pool, hs.HS_TYPE_F32, out=c.own_out, lse=c.own_lse)
     torch.cuda.synchronize()
     assert all(torch.equal(x, y) for x, y in zip(got, want))
+
+
+def test_a_pool_without_rows(pool):
+    """count = 0, and a count below one page: no page is held."""
+    c = Case(3, 300, 16, seed=2).own()
+    c.at = c.at[:0]
+    for count in (0, 15):
+        p = hs.paged_rows(c.rows, c.pages, 16)
+        p.count = count
+        out = torch.empty(3, hs.MLA_HEADS, hs.MLA_D_V, device="cuda")
+        lse = torch.empty(3, hs.MLA_HEADS, device="cuda")
+        work = torch.empty(hs.hs_mla_prefix_workspace_bound(pool, 3, 300) or 16, dtype=torch.uint8, device="cuda")
+        hs.hs_mla_prefix(pool, 3, c.q, p, 300, None, c.scale, c.own_out, c.own_lse, out, hs.HS_TYPE_F32, lse, work)
+        c.check(out, lse)
+
+
+def test_outputs_past_four_gigabytes(pool):
+    """20,000 requests: the offsets of their queries pass 2 GB, those of their outputs 5 GB."""
+    batch, n, sample = 20000, 5, [0, 1, 9999, 16383, 16384, 19998, 19999]
+    c = Case(len(sample), n, 16, seed=4)
+    q = torch.zeros(batch, hs.MLA_HEADS, 576, dtype=torch.bfloat16, device="cuda")
+    q[sample] = c.q
+    out = torch.full((batch, hs.MLA_HEADS, hs.MLA_D_V), float("nan"), device="cuda")
+    lse = torch.full((batch, hs.MLA_HEADS), float("nan"), device="cuda")
+    assert hs.hs_mla_prefix_workspace(pool, batch, n) == 0
+    hs.hs_mla_prefix(pool, batch, q, hs.paged_rows(c.rows, c.pages, 16), n, None, c.scale, None, None, out, hs.HS_TYPE_F32,
+                     lse, None)
+    c.check(out[sample], lse[sample])
+    rest = torch.ones(batch, dtype=torch.bool, device="cuda")
+    rest[sample] = False
+    mean = c.rows[c.at.cuda(), :512].float().mean(0)  # scores of 0: every row weighs the same
+    assert ((out[rest] - mean).abs().amax(dim=(0, 1)) <= 2.0 ** -18 * c.rows[c.at.cuda(), :512].float().abs().mean(0) + 1e-6).all()
+    assert ((lse[rest] - torch.tensor(5.0).log().item()).abs() <= 2.0 ** -18).all()
+
+
+def test_a_captured_decode_step():
+    """Append, resolve, sparse attention and prefix attention as one graph, replayed for three steps whose positions,
+    selections and prefix length are refilled in place; each step against attention over the union."""
+    B, plen, ctx, k, page = 3, 200, 512, 16, 16
+    H, DV = hs.MLA_HEADS, hs.MLA_D_V
+    g = torch.Generator().manual_seed(7)
+    buf = hs.PoolBuffers(1, B, ctx, 64, k, 1152)
+    buf.host.numpy()[:] = 0
+    pool = buf.create()
+    freq = (10000.0 ** (-torch.arange(0, 64, 2) / 64)).float().cuda()
+    rows = torch.randn(20 * page, 576, generator=g).to(torch.bfloat16).cuda()
+    table = torch.randperm(20, generator=g)[: -(-plen // page)].int().cuda()
+    shared = hs.paged_rows(rows, table, page)
+    n = 40
+    own = torch.randn(B * n, 576, generator=g).to(torch.bfloat16).cuda()
+    d = hs.append_desc(own, freq, (plen + torch.arange(n)).repeat(B).int().cuda(), req_ids=torch.arange(B).repeat_interleave(n).int().cuda())
+    hs.hs_append(pool, 0, B * n, d, None, True)
+    new, q_in = torch.zeros(B, 576, dtype=torch.bfloat16, device="cuda"), torch.zeros(B, H, 576, dtype=torch.bfloat16, device="cuda")
+    q = torch.zeros_like(q_in)
+    pos, topk = torch.zeros(B, dtype=torch.int32, device="cuda"), torch.zeros(B, k, dtype=torch.int32, device="cuda")
+    length, slots = torch.zeros(1, dtype=torch.int32, device="cuda"), torch.empty(B, k, dtype=torch.int32, device="cuda")
+    step = hs.append_desc(new, freq, pos, q_rope=q_in[..., DV:], q=q)
+    out, lse = torch.empty(B, H, DV, device="cuda"), torch.empty(B, H, device="cuda")
+    work = torch.empty(hs.hs_mla_prefix_workspace_bound(pool, B, plen) or 16, dtype=torch.uint8, device="cuda")
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        q.copy_(q_in)
+        hs.hs_append(pool, 0, B, step, None, True)
+        hs.hs_step_begin(pool)
+        hs.hs_resolve(pool, 0, B, topk, k, slots)
+        hs.hs_mla_decode(pool, 0, B, q, slots, k, None, 0, 192 ** -0.5, out, lse)
+        hs.hs_mla_prefix(pool, B, q, shared, plen, length, 192 ** -0.5, out, lse, out, hs.HS_TYPE_F32, lse, work)
+    for i, used in enumerate((200, 77, 0)):
+        new.copy_(torch.randn(B, 576, generator=g))
+        q_in.copy_(torch.randn(B, H, 576, generator=g))
+        pos.fill_(plen + n + i)
+        sel = torch.stack([plen + torch.randperm(n + 1 + i, generator=g)[:k] for _ in range(B)])
+        sel[:, 0] = torch.where((sel == plen + n + i).any(1), sel[:, 0], plen + n + i)  # the step's own token is among them
+        topk.copy_(sel)
+        length.fill_(used)
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        hist = torch.from_numpy(buf.host.numpy().reshape(B, ctx, 1152)).view(torch.bfloat16).double()
+        t = torch.arange(used)
+        pre = rows.cpu().double()[table.cpu().long()[t // page] * page + t % page]
+        for b in range(B):
+            keys = torch.cat((pre, hist[b][sel[b]]))
+            assert hist[b][plen + n + i].any()
+            s = 192 ** -0.5 * q[b].cpu().double() @ keys.t()
+            p = torch.softmax(s, -1)
+            # hs_mla_decode rounds its weights and sums the rounded ones: 2 * 2^-8 of the mean at most
+            assert ((out[b].cpu().double() - p @ keys[:, :DV]).abs() <= 2.1 * 2.0 ** -8 * (p @ keys[:, :DV].abs())).all()
+            assert (lse[b].cpu().double() - torch.logsumexp(s, -1)).abs().max() <= 2.0 ** -7
+    assert hs.hs_get_error(pool) == 0
+    buf.close()
