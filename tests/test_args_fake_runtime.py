@@ -210,3 +210,32 @@ fake.fake_fail(0)
 got += [append(), prefix()]
 """)
     assert got == [-2, 0, -2, 0, -2, 0, -2, 0, 0, 0]
+
+
+def _cases(function):
+    """The keyword dicts that a test of test_append_prefix_args.py is run with."""
+    return [m.args[1] for m in function.pytestmark if m.name == "parametrize"][0]
+
+
+def test_every_refusal_is_of_its_argument(under):
+    """The refusals that test_append_prefix_args.py lists, each of a call that is good but for it."""
+    import test_append_prefix_args as listed
+
+    got = under("""
+nan = float("nan")
+got = dict(good=[append(), prefix(), append(paged=pages()), prefix(own_out=A, own_lse=A), prefix(length=A), prefix(work=None, nbytes=0)],
+           append=[append(**kw) for kw in %r], prefix=[prefix(**kw) for kw in %r],
+           paged=[[append(paged=pages(**kw)), prefix(paged=pages(**kw))] for kw in %r],
+           calls=[append(layer=-1), append(layer=2), append(layer=1), append(ntok=-1), append(ntok=(1 << 30) + 1),
+                  append(ntok=1 << 28, q_heads=81), append(ntok=1 << 28, q_heads=64), append(ntok=5, req_ids=None),
+                  append(ntok=4, req_ids=None), append(to_history=False, q_rope=None, q=None, q_heads=0),
+                  append(to_history=False), append(p=pool(row_bytes=1024)), append(p=pool(row_bytes=656)),
+                  prefix(p=pool(row_bytes=656)), prefix(batch=131072), prefix(max_length=160), prefix(max_length=0)],
+           space=[prefix(batch=1, max_length=9001, paged=pages(page_stride=1000), work=w, nbytes=n)
+                  for w, n in ((None, 1 << 40), (A + 16, 1 << 40), (A, 36 * 128 * 2056 - 1), (A, 36 * 128 * 2056))])
+""" % (_cases(listed.test_append_refuses), _cases(listed.test_prefix_refuses), _cases(listed.test_bad_paged_rows_are_refused)))
+    assert got["good"] == [0] * 6
+    assert got["append"] == [-1] * len(got["append"]) and got["prefix"] == [-1] * len(got["prefix"])
+    assert got["paged"] == [[-1, -1]] * len(got["paged"])
+    assert got["calls"] == [-1, -1, 0, -1, -1, -1, 0, -1, 0, -1, 0, -5, 0, -5, 0, 0, 0]
+    assert got["space"] == [-1, -1, -1, 0]
