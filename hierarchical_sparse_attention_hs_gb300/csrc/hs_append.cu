@@ -8,8 +8,9 @@
 // Angles. p * inv_freq is wanted modulo a full turn, and p reaches millions: a 32-bit product would be off by p * 2^-24
 // turns and more. inv_freq / 2 pi is taken once per warp, in 64 bits, as a fraction of a turn in fixed point (G / 2^64);
 // p * G modulo 2^64 is then the position's fraction of a turn by integer multiplication that wraps where the angle does.
-// The fraction's signed upper 32 bits, exact to 2^-32 turns, go to sincospif. (Double arithmetic per token would cost
-// more than the memory traffic: this device has few FP64 units.)
+// The fraction's signed upper 32 bits go to sincospif. They are off by 2^-32 turns, cut off, and by p * inv_freq * 2^-54, as
+// the rate passes through 53 bits: 2^-30 turns at p = 2^24 for inv_freq = 1. (Double arithmetic per token would cost more than
+// the memory traffic: this device has few FP64 units.)
 //
 // Work. One warp per row and one warp per 16 heads of a token's queries, each with several once there are many. A lane
 // holds 16 latents (two 16-byte chunks for 16-bit inputs) and one pair of the key, so a row is loaded and stored in
@@ -18,8 +19,9 @@
 //
 // Measured on one GB300 (reads and writes over the time): 1 to 32 tokens with 128 heads 2.1-2.2 us, a launch's own cost;
 // 256 2.8 us; 2,047 with 128 heads 18.5 us from fp32 (5.8 TB/s) and 13.5 from bf16; 131,071 without queries 50 us into bf16
-// rows (6.1 TB/s) and 50 into fp8 rows (4.8: issue-bound, 0.73 instructions a cycle and scheduler); 4,096 into host memory
-// 17.5 us for fp8 rows and 26 for bf16, 153 and 180 GB/s of writes over the link.
+// rows (6.1 TB/s) and 50 into fp8 rows (4.8: 339 instructions a row, which take 38 us where every scheduler issues one a
+// cycle; 0.73 are measured); 4,096 into host memory 17.5 us for fp8 rows and 26 for bf16, 153 and 180 GB/s of writes over the
+// link.
 
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
