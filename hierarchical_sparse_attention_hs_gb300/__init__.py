@@ -288,7 +288,8 @@ def paged_rows(rows, pages, page_rows: int) -> hs_paged_rows:
         raise ValueError("paged_rows takes contiguous tensors")
     row_bytes = rows.element_size() * math.prod(rows.shape[1:])
     if row_bytes not in KV_ROW_BYTES:
-        raise ValueError(f"rows is [count][...] with rows of 1152 or 656 bytes: {tuple(rows.shape)} of {rows.dtype} has {row_bytes}")
+        raise ValueError(f"rows is [count][...] with rows of 1152 or 656 bytes: {tuple(rows.shape)} of {rows.dtype} has "
+                         f"{row_bytes}")
     if pages.dtype != torch.int32:
         raise ValueError(f"pages is int32, not {pages.dtype}")
     if pages.dim() not in (1, 2) or pages.numel() == 0:
@@ -362,7 +363,7 @@ def _load_dtypes():
 
 def _fits(t, dtype, nbytes: int) -> bool:
     """Whether a tensor has this type and as many bytes, in order. (Of an address nothing is known; None is the library's.)"""
-    return t is None or type(t) is int or (t.dtype is dtype and t.nbytes >= nbytes and t.is_contiguous())
+    return t is None or isinstance(t, int) or (t.dtype is dtype and t.nbytes >= nbytes and t.is_contiguous())
 
 
 def hs_mla_prefix(pool: int, batch: int, q, prefix: hs_paged_rows, max_length: int, prefix_length, sm_scale: float,
@@ -376,7 +377,8 @@ def hs_mla_prefix(pool: int, batch: int, q, prefix: hs_paged_rows, max_length: i
             (own_out is None or _fits(own_out, f32, rows * MLA_D_V * 4) and _fits(own_lse, f32, rows * 4)) and
             (prefix_length is None or _fits(prefix_length, i32, 4))):
         raise ValueError(f"hs_mla_prefix of {batch} takes contiguous tensors: q bf16 [{batch}][128][576], out {out_dtype} "
-                         f"[{batch}][128][512], lse fp32 [{batch}][128], own_out and own_lse fp32 as out and lse, prefix_length int32")
+                         f"[{batch}][128][512], lse fp32 [{batch}][128], own_out and own_lse fp32 as out and lse, "
+                         f"prefix_length int32")
     _check(load().hs_mla_prefix(pool, batch, _addr(q), prefix, max_length, _addr(prefix_length), sm_scale,
                                 _addr(own_out), _addr(own_lse), _addr(out), out_type, _addr(lse), _addr(workspace),
                                 0 if workspace is None else workspace.nbytes, _stream(stream)), "hs_mla_prefix")

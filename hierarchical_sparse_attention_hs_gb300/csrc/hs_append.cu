@@ -48,14 +48,14 @@ constexpr int FP8_ROPE = LATENT + 4 * 4;         // byte offset of the rotary ke
 constexpr int Q_HEADS = 16;                      // heads of one warp's work item: four 16-byte loads a lane in flight
 constexpr int MAX_TOKENS = 1 << 30;              // and items of 16 heads of a token's queries
 constexpr int THREADS = 128, WARPS = THREADS / 32;
-// Blocks of a kernel that an SM holds at least. A launch of many tokens has as many blocks of rows as the device holds: all
-// warps get the same number of tokens, so time goes in whole waves, and in one wave a warp works its turn rates out once.
-// For 656-byte rows a bound of 7 (72 registers a thread) measured best; 131,071 / 16,384 / 8,191 rows in us: from 16 bits
-// 50.5 / 9.3 / 6.0 (a bound of 8 50.5 / 10.2 / 6.4, of 6 51.8 / 9.7 / 6.8, twelve blocks where seven fit 50.2 / 10.6 / 6.0), from fp32
-// 61.0 / 10.6 / 6.4 (of 6 63.2 / 11.1 / 7.3, of 5 64.5 / 11.3 / 6.7, twelve blocks 65.7 / 13.1 / 6.5). For 1152-byte rows the
-// compiler's own choice is kept, 8 blocks from 16 bits, 50.2 / 8.9 / 5.3 (a bound of 7 50.3 / 8.8 / 5.0, of 6 52.9 / 9.2 / 5.6; one of 8
-// took the queries of 256 and 2,047 tokens from 2.8 and 13.4 to 3.05 and 14.0), 6 from fp32, 70.3 / 11.4 / 6.4 (a bound of 7 73.4 / 10.9
-// / 5.6, of 5 70.9 / 11.7 / 5.8).
+// Blocks of a kernel that an SM holds at least. A launch of many tokens has as many blocks of rows as the device holds:
+// all warps get the same number of tokens, so time goes in whole waves, and in one wave a warp works its turn rates out
+// once. For 656-byte rows a bound of 7 (72 registers a thread) measured best; 131,071 / 16,384 / 8,191 rows in us: from
+// 16 bits 50.5 / 9.3 / 6.0 (a bound of 8 50.5 / 10.2 / 6.4, of 6 51.8 / 9.7 / 6.8, twelve blocks where seven fit 50.2 /
+// 10.6 / 6.0), from fp32 61.0 / 10.6 / 6.4 (of 6 63.2 / 11.1 / 7.3, of 5 64.5 / 11.3 / 6.7, twelve blocks 65.7 / 13.1 /
+// 6.5). For 1152-byte rows the compiler's own choice is kept, 8 blocks from 16 bits, 50.2 / 8.9 / 5.3 (a bound of 7 50.3
+// / 8.8 / 5.0, of 6 52.9 / 9.2 / 5.6; one of 8 took the queries of 256 and 2,047 tokens from 2.8 and 13.4 to 3.05 and
+// 14.0), 6 from fp32, 70.3 / 11.4 / 6.4 (a bound of 7 73.4 / 10.9 / 5.6, of 5 70.9 / 11.7 / 5.8).
 template <bool FP8>
 constexpr int MIN_BLOCKS = FP8 ? 7 : 0;  // 0: none
 constexpr int Q_BLOCKS = 16;  // blocks of queries an SM, at most

@@ -26,17 +26,17 @@
 // the next unit's rows, queries and first scores are under way while the last one's output is stored.
 //
 // Warp roles per CTA: 0-7 softmax (warp w: TMEM lanes 32 (w % 4) .. +31, that is head lane % 64 and key half lane / 64,
-// and keys 64 (w / 4) .. +63 of that half), 8 the issuer (the pair's first CTA issues for both), 9-15 the loaders. K and V
-// pass through one ring of 16 KB stages in the order in which the MMAs read them, with a loader for each slot (one
-// thread's wait, expectation and copies of a stage take about 310 cycles one after the other, more than the stage's MMAs):
-// a K stage is 64 columns of the CTA's 128 keys, a V stage 128 of its value columns of 64 keys; each feeds four MMAs, 256
-// cycles. The issuer runs the scores of tile g + 1 before the value product of tile g, so the softmax of a tile overlaps the
-// value product of the one before and the scores of the one after. P is rounded to bf16: one MMA takes operands of one
-// type, and V is bf16. Keeping more of P, as a second bf16 operand with what the rounding cuts off, would double the value
-// product, 512 of the 1,088 multiplications of a head and key. The rounding leaves an output 0.0010 to 0.0013 off in the mean (fp32
-// outputs, N(0, 1) rows; 0.00007 against the same sum with its weights rounded), against 0.0017 of the rounding to a bf16
-// output. Its normaliser sums the unrounded weights. O is rescaled only when a head's maximum has risen by more than 8 (log2), which
-// keeps P below 2^8.
+// and keys 64 (w / 4) .. +63 of that half), 8 the issuer (the pair's first CTA issues for both), 9-15 the loaders. K and
+// V pass through one ring of 16 KB stages in the order in which the MMAs read them, with a loader for each slot (one
+// thread's wait, expectation and copies of a stage take about 310 cycles one after the other, more than the stage's
+// MMAs): a K stage is 64 columns of the CTA's 128 keys, a V stage 128 of its value columns of 64 keys; each feeds four
+// MMAs, 256 cycles. The issuer runs the scores of tile g + 1 before the value product of tile g, so the softmax of a tile
+// overlaps the value product of the one before and the scores of the one after. P is rounded to bf16: one MMA takes
+// operands of one type, and V is bf16. Keeping more of P, as a second bf16 operand with what the rounding cuts off, would
+// double the value product, 512 of the 1,088 multiplications of a head and key. The rounding leaves an output 0.0010 to
+// 0.0013 off in the mean (fp32 outputs, N(0, 1) rows; 0.00007 against the same sum with its weights rounded), against
+// 0.0017 of the rounding to a bf16 output. Its normaliser sums the unrounded weights. O is rescaled only when a head's
+// maximum has risen by more than 8 (log2), which keeps P below 2^8.
 //
 // Loads are TMA boxes of 64 columns x min(page_rows, 64) rows, 128-byte swizzle; pages of one or two rows are gathered four
 // rows a copy. A box whose page the pool does not hold starts behind the last row of the tensor map: it reads nothing and
@@ -890,7 +890,8 @@ struct Cut {
 };
 // The cut with the shortest expected time, in tiles (1.2 to 2.6 us): a pair's units one after the other, each its tiles and
 // about one more (the softmax of its last tile and its store), and with splits their join, 1.5 and 0.025 for each. (What every
-// launch pays counts for all cuts alike and is left out.) Either all requests are cut, or as many as fill the pairs whole times over stay whole and the rest is cut.
+// launch pays counts for all cuts alike and is left out.) Either all requests are cut, or as many as fill the pairs whole
+// times over stay whole and the rest is cut.
 Cut cut_of(int pairs, int32_t batch, int32_t max_length) {
   const int tiles = (max_length + NK - 1) / NK, full = batch / pairs * pairs;
   Cut best = {batch, 1};

@@ -299,9 +299,9 @@ typedef struct {
 } hs_paged_rows;
 
 /*
- * What one append takes (of at least ntok tokens). Token i (0 <= i < ntok) belongs to request req_ids[i] (i itself when req_ids is NULL) at
- * position positions[i]. Arrays are device memory; req_ids and positions may be mapped host memory. 32-bit arrays are
- * 4-byte aligned.
+ * What one append takes (of at least ntok tokens). Token i (0 <= i < ntok) belongs to request req_ids[i] (i itself when
+ * req_ids is NULL) at position positions[i]. Arrays are device memory; req_ids and positions may be mapped host memory.
+ * 32-bit arrays are 4-byte aligned.
  *   type: HS_TYPE_* of kv and q_rope.
  *   interleaved: which values form the 32 pairs that turn: 0: (j, j + 32); 1: (2j, 2j + 1).
  *   kv: [ntok][576], the latent's 512 values and the rotary key's 64 before rotation; kv_stride: elements between
@@ -347,17 +347,18 @@ typedef struct {
  * which must be writable, or the no-IO copy of a pool that has one), the paged rows when `paged` is given (list
  * req_ids[i]), and always the hot slot that the token occupies, if it occupies one, so that a resolve after a rewrite
  * (a rolled-back speculation, say) never serves the old row. (Of a no-IO pool the host copy is not written; of a pool
- * whose layers read overlapping host rows, the row that they share.) Norm and rotation are computed in 32 bits, the squares'
- * sum too: with a norm it has to stay within their range (magnitudes below 2^59; above 2^-63 where norm_eps is 0). Each value is
- * rounded once.
- * A token with a negative position is padding: it touches nothing. One whose position is >= ctx or whose request is not
- * in 0 .. max_batch-1 is skipped whole, and the error word gets HS_DEVERR_RANGE. (request, position) pairs are distinct
- * within a call (not checked: rows of a repeated pair may mix). ntok == 0 is a no-op; ntok <= 2^30, and
- * so is ntok * ceil(q_heads / 16); with req_ids NULL ntok <= max_batch. At least one of `paged`, to_history and q_rope
- * is given. A token that `paged` has no row for is not written there. Enqueued on `stream` (of the pool's device, which must be the current one: HS_ERR_INVALID_ARG);
- * capturable. Order it before the resolve, prefetch, gather or attention that reads the rows. Basis: the full history
- * in host memory that the paper's cache sits on (Abstract) and the ordinary KV blocks of the "Hybrid HiSparse" card
- * (Timeline) have to be written by somebody; the pages name no writer.
+ * whose layers read overlapping host rows, the row that they share.) Norm and rotation are computed in 32 bits, the
+ * squares' sum too: with a norm it has to stay within their range (magnitudes below 2^59; above 2^-63 where norm_eps
+ * is 0). Each value is rounded once.
+ * A token with a negative position is padding: it touches nothing. One whose position is >= ctx or whose request is
+ * not in 0 .. max_batch-1 is skipped whole, and the error word gets HS_DEVERR_RANGE. (request, position) pairs are
+ * distinct within a call (not checked: rows of a repeated pair may mix). ntok == 0 is a no-op; ntok <= 2^30, and so
+ * is ntok * ceil(q_heads / 16); with req_ids NULL ntok <= max_batch. At least one of `paged`, to_history and q_rope
+ * is given. A token that `paged` has no row for is not written there. Enqueued on `stream` (of the pool's device,
+ * which must be the current one: HS_ERR_INVALID_ARG); capturable. Order it before the resolve, prefetch, gather or
+ * attention that reads the rows. Basis: the full history in host memory that the paper's cache sits on (Abstract) and
+ * the ordinary KV blocks of the "Hybrid HiSparse" card (Timeline) have to be written by somebody; the pages name no
+ * writer.
  */
 int hs_append(hs_pool *pool, int32_t layer, int32_t ntok, const hs_append_desc *desc, const hs_paged_rows *paged,
               int32_t to_history, hs_stream_t stream);
@@ -380,12 +381,14 @@ int hs_append(hs_pool *pool, int32_t layer, int32_t ntok, const hs_append_desc *
  *   out: [batch][128][512] of out_type (HS_TYPE_BF16 or HS_TYPE_F32), 16-byte aligned; lse: fp32 [batch][128]. They
  *     overlap no input, but with out_type HS_TYPE_F32 they may be own_out and own_lse themselves.
  *   workspace: device memory of hs_mla_prefix_workspace bytes or more for this batch and max_length (or of
- *     hs_mla_prefix_workspace_bound for the largest), 256-byte aligned (NULL where that is 0); its contents are scratch. Calls that may run at the same time (two streams, two graphs) need workspaces of their own.
- * The weights are rounded to bf16 before the value product, whose other operand is bf16 (2^-8 of each at most, which leaves
- * outputs about 0.0013 off in the mean before their own rounding); scores, sums and outputs accumulate in 32 bits, and the
- * normaliser and lse sum the unrounded weights. Results are deterministic for given batch, max_length and device. Enqueued on `stream` (of the
- * pool's device, which must be the current one); capturable; batch == 0 is a no-op. Basis: the "Hybrid HiSparse" card
- * (Timeline) serves resident rows from the ordinary KV blocks; requests that share blocks are its plainest case.
+ *     hs_mla_prefix_workspace_bound for the largest), 256-byte aligned (NULL where that is 0); its contents are scratch.
+ *     Calls that may run at the same time (two streams, two graphs) need workspaces of their own.
+ * The weights are rounded to bf16 before the value product, whose other operand is bf16 (2^-8 of each at most, which
+ * leaves outputs about 0.0013 off in the mean before their own rounding); scores, sums and outputs accumulate in 32
+ * bits, and the normaliser and lse sum the unrounded weights. Results are deterministic for given batch, max_length
+ * and device. Enqueued on `stream` (of the pool's device, which must be the current one); capturable; batch == 0 is a
+ * no-op. Basis: the "Hybrid HiSparse" card (Timeline) serves resident rows from the ordinary KV blocks; requests that
+ * share blocks are its plainest case.
  */
 int hs_mla_prefix(hs_pool *pool, int32_t batch, const void *q, const hs_paged_rows *prefix, int32_t max_length,
                   const int32_t *prefix_length, float sm_scale, const float *own_out, const float *own_lse, void *out,
