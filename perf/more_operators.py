@@ -1,14 +1,15 @@
 """Timed cases of the operators around a cache whose rows hold their latents in 4 bits: writing rows, reading rows back as
 numbers, and the sparse decode attention over them.
 
-A row of 416 bytes holds 512 latents as e2m1 codes (two a byte, the first in the low half), 32 scales, one for each 16
-latents (8 bits: 5 of exponent, 3 of fraction, no sign, which are the upper bits of a half), and the rotary key's 64 bf16
-values; a latent is its code's value times its scale. Rows of 656 bytes (e4m3 latents, a 32-bit scale for each 128) are
-read back as well.
+A row of 416 bytes holds 512 latents as whole numbers from -7 to 7 in 4 bits each, 32 scales, one for each 16 latents
+(8 bits: 5 of exponent, 3 of fraction, no sign, which are the upper bits of a half), and the rotary key's 64 bf16 values; a
+latent is its number times its scale. The 32-bit word i holds latents 8 i to 8 i + 7, each plus 8: the even ones at bits 0,
+4, 8, 12, the odd ones at bits 16, 20, 24, 28. Rows of 656 bytes (e4m3 latents, a 32-bit scale for each 128) are read back
+as well.
 
 Each case is a dict of plain values. ``prepare`` makes a case's inputs on the GPU from a seed, ``run`` makes one pass:
 through the library where ``own`` is true, else in elementary torch operations with 32-bit arithmetic (64-bit for the
-angles of far positions and for values next to a code's border). ``exact`` computes the same outputs in 64 bits, written
+angles of far positions and for values next to a border between two codes). ``exact`` computes the same outputs in 64 bits, written
 separately.
 """
 import math
@@ -22,7 +23,7 @@ WIDTH = LATENT + ROPE
 BLOCK = 16  # latents of one scale of a 4-bit row
 SCALE = 1.0 / math.sqrt(192.0)  # the query-key head dimension of the unabsorbed heads, 128 + 64
 TYPES = {"bf16": torch.bfloat16, "f16": torch.float16, "f32": torch.float32}
-ROW_BYTES = {"fp4": 416, "fp8": 656}
+ROW_BYTES = {"int4": 416, "fp8": 656}
 
 
 def listed():
@@ -37,13 +38,13 @@ def listed():
         dict(name="write_prompt_131071", op="write", tokens=131071, requests=1, start=0, type="bf16", heads=0, norm=False,
              interleaved=True, page=64, padded=0),
         # the rows a few requests selected, for a consumer that takes bf16 rows: some in the hot buffer, some in the paged rows
-        dict(name="read_tiered_3x257", op="read", row="fp4", source="tiered", batch=3, k=257, slots=512, type="bf16",
+        dict(name="read_tiered_3x257", op="read", row="int4", source="tiered", batch=3, k=257, slots=512, type="bf16",
              padded=0.05),
         # a decode batch's selections out of the hot buffer, fp8 rows, as 32-bit numbers
         dict(name="read_slots_32x2048_fp8", op="read", row="fp8", source="slots", batch=32, k=2048, slots=4096, type="f32",
              padded=0.0),
         # a whole long history in token order, for a prefill chunk that attends to all of it
-        dict(name="read_history_131072", op="read", row="fp4", source="history", batch=1, k=131072, slots=512,
+        dict(name="read_history_131072", op="read", row="int4", source="history", batch=1, k=131072, slots=512,
              type="bf16", padded=0.0),
         # one request whose selection is short: the smallest call
         dict(name="decode_1x65", op="decode", source="slots", batch=1, k=65, slots=512, padded=0.0),
@@ -78,7 +79,7 @@ def draw(rng):
     batch = _spread(rng, 1, 128)
     if op == "read":
         k = _spread(rng, 1, min(65535, 131072 // batch))
-        return dict(op="read", row=rng.choice(("fp4", "fp4", "fp8")), source=source, batch=batch, k=k, slots=k + 1 + k // 3,
+        return dict(op="read", row=rng.choice(("int4", "int4", "fp8")), source=source, batch=batch, k=k, slots=k + 1 + k // 3,
                     type=rng.choice(("bf16", "bf16", "f16", "f32")), padded=rng.choice((0.0, 0.0, 0.1)))
     k = _spread(rng, 1, min(16384, 98304 // batch))
     return dict(op="decode", source=source, batch=batch, k=k, slots=k + 1 + k // 3, padded=rng.choice((0.0, 0.0, 0.1)))
@@ -86,40 +87,28 @@ def draw(rng):
 
 # ---- the 4-bit format, in 64 bits
 
-_CODES = (0.0, 0.5, 1.0, 1.5, 2.0, 3.0, 4.0, 6.0)
-
-
 def _scale_of(z):
-    """The scale of each 16 latents [...][32]: their largest magnitude / 6, to 4 significant bits, within its range."""
-    a = z.double().unflatten(-1, (-1, BLOCK)).abs().amax(-1) / torch.full((), 6.0, dtype=torch.float64, device=z.device)
+    """The scale of each 16 latents [...][32]: their largest magnitude / 7, to 4 significant bits, within its range."""
+    a = z.double().unflatten(-1, (-1, BLOCK)).abs().amax(-1) / torch.full((), 7.0, dtype=torch.float64, device=z.device)
     step = torch.exp2(torch.frexp(a).exponent.clamp(min=-13).double() - 4)
-    return (torch.round(a / step) * step).clamp(2.0 ** -17, 10240.0)
-
-
-def _codes_of(z, scale):
-    """The e2m1 code nearest to each latent over its scale, ties to the even code."""
-    q = z.double() / scale.repeat_interleave(BLOCK, -1)
-    a = q.abs()
-    code = (a > 0.25).byte() + (a >= 0.75) + (a > 1.25) + (a >= 1.75) + (a > 2.5) + (a >= 3.5) + (a > 5.0)
-    return code | (q < 0).byte() << 3
+    return (torch.round(a / step) * step).clamp(2.0 ** -17, 3840.0)
 
 
 def _pack(z, key):
     """Rows of 416 bytes from latents [n][512] and rotary keys [n][64]."""
     scale = _scale_of(z)
-    code = _codes_of(z, scale)
-    return torch.cat((code[..., 0::2] | code[..., 1::2] << 4, (scale.half().view(torch.int16) >> 7).byte(),
-                      key.to(torch.bfloat16).view(torch.uint8)), -1)
+    code = (torch.round(z.double() / scale.repeat_interleave(BLOCK, -1)).clamp(-7, 7) + 8).byte().unflatten(-1, (-1, 8))
+    pair = code[..., [0, 4, 1, 5]] | code[..., [2, 6, 3, 7]] << 4
+    return torch.cat((pair.flatten(-2), (scale.half().view(torch.int16) >> 7).byte(), key.to(torch.bfloat16).view(torch.uint8)), -1)
 
 
 def _values(rows):
     """What rows [...][416 or 656] stand for, in 32 bits [...][576]."""
     if rows.shape[-1] == 416:
-        table = torch.tensor(_CODES + tuple(-v for v in _CODES), device=rows.device)
-        pair = rows[..., :LATENT // 2].int()
-        z = torch.stack((table[pair & 15], table[pair >> 4]), -1).flatten(-2)
+        pair = rows[..., :LATENT // 2].unflatten(-1, (-1, 4))
+        code = torch.cat((pair & 15, pair >> 4), -1)[..., [0, 2, 4, 6, 1, 3, 5, 7]]  # they are latents 0 4 1 5 2 6 3 7
         scale = (rows[..., LATENT // 2:LATENT // 2 + 32].short() << 7).view(torch.float16).float()
-        z = z * scale.repeat_interleave(BLOCK, -1)
+        z = (code.flatten(-2).float() - 8) * scale.repeat_interleave(BLOCK, -1)
     else:
         scale = rows[..., LATENT:LATENT + 16].contiguous().view(torch.float32)
         z = rows[..., :LATENT].contiguous().view(torch.float8_e4m3fn).float() * scale.repeat_interleave(128, -1)
@@ -134,7 +123,7 @@ def _random_rows(n, kind, gd):
         m = min(32768, n - i)
         z = torch.randn(m, LATENT, generator=gd, device="cuda") * channel
         key = torch.randn(m, ROPE, generator=gd, device="cuda")
-        if kind == "fp4":
+        if kind == "int4":
             out[i:i + m] = _pack(z, key)
         else:
             scale = z.view(m, 4, 128).abs().amax(-1) / 448
@@ -188,7 +177,7 @@ def _write_state(case, seed):
     s["at"] = row[alive].to(dev)
     # the list through which the rows are read back, as a resolve names rows of the paged pool
     s["entries"] = torch.where(row >= 0, -2 - row, -1).int().to(dev)
-    s["rows"] = torch.zeros(count * page, ROW_BYTES["fp4"], dtype=torch.uint8, device=dev)
+    s["rows"] = torch.zeros(count * page, ROW_BYTES["int4"], dtype=torch.uint8, device=dev)
     # the projections' outputs: latents of a varied scale where a norm follows, else of a normed size; the rotary key
     size = torch.exp(torch.randn(n, 1, generator=gd, device=dev)) if case["norm"] else 1.0
     s["kv"] = (torch.randn(n, WIDTH, generator=gd, device=dev) * size).to(t)
@@ -200,8 +189,8 @@ def _write_state(case, seed):
         s["q"] = torch.randn(n, case["heads"], WIDTH, generator=gd, device=dev, dtype=torch.bfloat16)
     s["values"] = torch.empty(n, WIDTH, dtype=torch.bfloat16, device=dev)
     if own:
-        s["hot"] = torch.zeros(reqs * 16 * ROW_BYTES["fp4"], dtype=torch.uint8, device=dev)
-        _pool(s, reqs, ctx, 16, ROW_BYTES["fp4"], s["hot"])
+        s["hot"] = torch.zeros(reqs * 16 * ROW_BYTES["int4"], dtype=torch.uint8, device=dev)
+        _pool(s, reqs, ctx, 16, ROW_BYTES["int4"], s["hot"])
         hs = s["hs"]
         s["desc"] = hs.append_desc(s["kv"], s["inv_freq"], s["pos"], req_ids=s["req"], norm_weight=s["weight"], norm_eps=1e-6,
                                    interleaved=case["interleaved"], q_rope=s["q_rope"], q=s["q"])
@@ -213,7 +202,7 @@ def _list_state(case, seed):
     """A hot buffer or a history, paged rows beside it, and every request's list of entries."""
     gd = torch.Generator(device="cuda").manual_seed(seed)
     batch, k, slots, dev = case["batch"], case["k"], case["slots"], "cuda"
-    kind = case.get("row", "fp4")
+    kind = case.get("row", "int4")
     history = case["source"] == "history"
     s = dict(case=case, ctx=slots if not history else max(slots, k + 5))
     per = s["ctx"] if history else slots
@@ -318,11 +307,11 @@ def _run_decode(s):
     if own:
         hs = s["hs"]
         if c["source"] == "history":
-            hs.hs_mla_decode_fp4_history(s["pool"], 0, c["batch"], s["q"], s["entries"], c["k"], SCALE, s["out"],
+            hs.hs_mla_decode_int4_history(s["pool"], 0, c["batch"], s["q"], s["entries"], c["k"], SCALE, s["out"],
                                          hs.HS_TYPE_BF16, s["lse"])
         else:
             r = s["resident"]
-            hs.hs_mla_decode_fp4(s["pool"], 0, c["batch"], s["q"], s["entries"], c["k"], r, 0 if r is None else r.shape[0],
+            hs.hs_mla_decode_int4(s["pool"], 0, c["batch"], s["q"], s["entries"], c["k"], r, 0 if r is None else r.shape[0],
                                  SCALE, s["out"], hs.HS_TYPE_BF16, s["lse"])
         return [s["out"], s["lse"]]
     rows, valid = _selected(s)
@@ -343,14 +332,14 @@ def work(case):
     if case["op"] == "write":
         n, size = case["tokens"] - case["padded"], {"bf16": 2, "f16": 2, "f32": 4}[case["type"]]
         # the projections in, the rows out, and their values
-        b = n * (WIDTH * size + ROW_BYTES["fp4"] + 12 + WIDTH * 2) + n * case["heads"] * ROPE * (size + 2)
+        b = n * (WIDTH * size + ROW_BYTES["int4"] + 12 + WIDTH * 2) + n * case["heads"] * ROPE * (size + 2)
         b += 4 * LATENT if case["norm"] else 0
         return {"bytes": b, "flops": n * ((7 if case["norm"] else 4) * LATENT + 6 * 32 * (1 + case["heads"]))}
     n = case["batch"] * case["k"] * (1 - case["padded"])
     if case["op"] == "read":
         size = {"bf16": 2, "f16": 2, "f32": 4}[case["type"]]
         return {"bytes": n * ROW_BYTES[case["row"]] + case["batch"] * case["k"] * (4 + WIDTH * size), "flops": n * LATENT}
-    b = n * ROW_BYTES["fp4"] + case["batch"] * (4 * case["k"] + HEADS * (WIDTH * 2 + LATENT * 2 + 4))
+    b = n * ROW_BYTES["int4"] + case["batch"] * (4 * case["k"] + HEADS * (WIDTH * 2 + LATENT * 2 + 4))
     return {"bytes": b, "flops": 2.0 * HEADS * n * (WIDTH + LATENT)}
 
 
@@ -361,10 +350,8 @@ def _exact_row(rows):
     d = torch.float64
     b = rows.to(torch.int64)
     if rows.shape[-1] == 416:
-        pair = b[..., :256]
-        code = torch.cat(((pair % 16)[..., None], torch.div(pair, 16, rounding_mode="floor")[..., None]), -1).flatten(-2)
-        ex, m, sign = (code // 2) % 4, (code % 2).to(d), 1 - 2 * (code // 8).to(d)
-        z = sign * torch.where(ex == 0, m / 2, (1 + m / 2) * torch.exp2(ex.to(d) - 1))
+        word = sum(b[..., i:256:4] << 8 * i for i in range(4))  # [...][64]
+        z = torch.stack([(word >> at) % 16 for at in (0, 16, 4, 20, 8, 24, 12, 28)], -1).flatten(-2).to(d) - 8
         f = b[..., 256:288]
         ex, m = f // 8, (f % 8).to(d)
         scale = torch.where(ex == 0, m / 8 * 2.0 ** -14, (1 + m / 8) * torch.exp2(ex.to(d) - 15))
@@ -389,25 +376,19 @@ def _exact_write(case, seed):
         r = torch.view_as_real(torch.view_as_complex(pair.contiguous()) * w)
         return r.flatten(-2) if case["interleaved"] else torch.cat((r[..., 0], r[..., 1]), -1)
 
-    # every scale that the format has, and every value of a code: the nearest of each is looked up
+    # every scale that the format has: the nearest is looked up
     f = torch.arange(1, 256, device="cuda")
     every = torch.where(f < 8, f / 8 * 2.0 ** -14, (1 + f % 8 / 8) * torch.exp2(f.to(d) // 8 - 15))
-    every = every[every <= 10240]
-    want = z.unflatten(-1, (32, 16)).abs().amax(-1) / 6
+    every = every[every <= 3840]
+    want = z.unflatten(-1, (32, 16)).abs().amax(-1) / 7
     hi = torch.searchsorted(every, want.contiguous()).clamp(1, len(every) - 1)
     lo, up = every[hi - 1], every[hi]
     odd = (hi + 1) % 2 == 1  # the code of `up` is hi + 1
     scale = torch.where((up - want < want - lo) | ((up - want == want - lo) & ~odd), up, lo)
-    q = z.unflatten(-1, (32, 16)) / scale[..., None]
-    near = torch.zeros_like(q)
-    for value in (0.5, 1.0, 1.5, 2.0, 3.0, 4.0, 6.0):
-        below = {0.5: 0.0, 1.0: 0.5, 1.5: 1.0, 2.0: 1.5, 3.0: 2.0, 4.0: 3.0, 6.0: 4.0}[value]
-        border = (value + below) / 2
-        up = q.abs() >= border if value in (1.0, 2.0, 4.0) else q.abs() > border
-        near = torch.where(up, value, near)
+    near = (z.unflatten(-1, (32, 16)) / scale[..., None]).round().clamp(-7, 7)
     values = torch.zeros(case["tokens"], WIDTH, dtype=d, device="cuda")
     live = s["live"]
-    values[live] = torch.cat(((near * q.sign() * scale[..., None]).flatten(-2), rotate(x[:, LATENT:], turn)), -1)[live]
+    values[live] = torch.cat(((near * scale[..., None]).flatten(-2), rotate(x[:, LATENT:], turn)), -1)[live]
     got = [values]
     if s["q"] is not None:
         q = s["q"].to(d)
