@@ -24,6 +24,7 @@ BLOCK = 16  # latents of one scale of a 4-bit row
 SCALE = 1.0 / math.sqrt(192.0)  # the query-key head dimension of the unabsorbed heads, 128 + 64
 TYPES = {"bf16": torch.bfloat16, "f16": torch.float16, "f32": torch.float32}
 ROW_BYTES = {"int4": 416, "fp8": 656}
+SLOTS_MOST = 8192  # slots of a request's hot buffer that every pool takes
 
 
 def listed():
@@ -228,7 +229,16 @@ def _list_state(case, seed):
         s["out"] = torch.empty(batch, HEADS, LATENT, dtype=torch.bfloat16, device=dev)
         s["lse"] = torch.empty(batch, HEADS, device=dev)
     if own:
-        if history:
+        s["list"], s["paged"] = s["entries"], s["resident"]
+        s["by_token"] = history
+        if not history and slots > SLOTS_MOST:
+            # more rows than a hot buffer has slots: the history's, or, beside rows of the paged pool, all in that pool
+            s["by_token"] = s["resident"] is None
+            if not s["by_token"]:
+                first = slots * torch.arange(batch, device=dev)[:, None]
+                s["list"] = torch.where(e >= 0, -2 - (e + first), torch.where(e <= -2, e - batch * slots, e)).int()
+                s["paged"] = torch.cat((s["rows"].flatten(0, 1), s["resident"]))
+        if s["by_token"] or slots > SLOTS_MOST:
             s["hot"] = torch.zeros(batch * 16 * ROW_BYTES[kind], dtype=torch.uint8, device=dev)
             _pool(s, batch, per, 16, ROW_BYTES[kind], s["hot"], s["rows"])
         else:
@@ -292,11 +302,11 @@ def _run_read(s):
     if own:
         hs = s["hs"]
         out_type = {"bf16": hs.HS_TYPE_BF16, "f16": hs.HS_TYPE_F16, "f32": hs.HS_TYPE_F32}[c["type"]]
-        if c["source"] == "history":
-            hs.hs_gather_values_history(s["pool"], 0, c["batch"], s["entries"], c["k"], s["out"], out_type)
+        if s["by_token"]:
+            hs.hs_gather_values_history(s["pool"], 0, c["batch"], s["list"], c["k"], s["out"], out_type)
         else:
-            r = s["resident"]
-            hs.hs_gather_values(s["pool"], 0, c["batch"], s["entries"], c["k"], r, 0 if r is None else r.shape[0], s["out"],
+            r = s["paged"]
+            hs.hs_gather_values(s["pool"], 0, c["batch"], s["list"], c["k"], r, 0 if r is None else r.shape[0], s["out"],
                                 out_type)
         return [s["out"]]
     return [_selected(s)[0].to(s["out"].dtype)]
@@ -306,13 +316,13 @@ def _run_decode(s):
     c = s["case"]
     if own:
         hs = s["hs"]
-        if c["source"] == "history":
-            hs.hs_mla_decode_int4_history(s["pool"], 0, c["batch"], s["q"], s["entries"], c["k"], SCALE, s["out"],
-                                         hs.HS_TYPE_BF16, s["lse"])
+        if s["by_token"]:
+            hs.hs_mla_decode_int4_history(s["pool"], 0, c["batch"], s["q"], s["list"], c["k"], SCALE, s["out"],
+                                          hs.HS_TYPE_BF16, s["lse"])
         else:
-            r = s["resident"]
-            hs.hs_mla_decode_int4(s["pool"], 0, c["batch"], s["q"], s["entries"], c["k"], r, 0 if r is None else r.shape[0],
-                                 SCALE, s["out"], hs.HS_TYPE_BF16, s["lse"])
+            r = s["paged"]
+            hs.hs_mla_decode_int4(s["pool"], 0, c["batch"], s["q"], s["list"], c["k"], r, 0 if r is None else r.shape[0],
+                                  SCALE, s["out"], hs.HS_TYPE_BF16, s["lse"])
         return [s["out"], s["lse"]]
     rows, valid = _selected(s)
     score = torch.matmul(s["q"].float(), rows.transpose(1, 2))
