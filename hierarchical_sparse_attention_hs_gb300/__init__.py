@@ -25,6 +25,7 @@ __all__ = [
     "hs_resolve_shared", "hs_resolve_tiered", "hs_mla_decode", "hs_mla_decode_history", "HS_DEVERR_TIMEOUT",
     "MLA_HEADS", "MLA_D_QK", "MLA_D_V", "hs_probe_launch", "hs_debug_attention", "hs_step_begin_fused", "hs_probe_link_static", "HS_ERR_TOO_LARGE",
     "hs_resolve_ids", "hs_prefetch_ids", "hs_append", "hs_append_desc", "append_desc", "hs_paged_rows", "paged_rows",
+    "hs_gather_values", "hs_gather_values_history", "hs_mla_decode_int4", "hs_mla_decode_int4_history",
     "hs_mla_prefix", "hs_mla_prefix_workspace", "hs_mla_prefix_workspace_bound", "HS_TYPE_BF16", "HS_TYPE_F16", "HS_TYPE_F32",
 ]
 
@@ -42,7 +43,8 @@ HS_DEVERR_TIMEOUT = 8
 HS_TYPE_BF16, HS_TYPE_F16, HS_TYPE_F32 = 0, 1, 2
 MLA_HEADS, MLA_D_QK, MLA_D_V = 128, 576, 512  # shape of the sparse MLA decode consumer
 
-KV_ROW_BYTES = (MLA_D_QK * 2, MLA_D_V + 4 * 4 + (MLA_D_QK - MLA_D_V) * 2)  # the row formats of hs_append: bf16, fp8
+# the row formats of hs_append: bf16, fp8, 4 bits
+KV_ROW_BYTES = (MLA_D_QK * 2, MLA_D_V + 4 * 4 + (MLA_D_QK - MLA_D_V) * 2, MLA_D_V // 2 + MLA_D_V // 16 + (MLA_D_QK - MLA_D_V) * 2)
 
 LIB_PATH = _build_mod.LIB_PATH
 _lib = None
@@ -127,6 +129,11 @@ def load():
             "hs_probe_link_static": (ctypes.c_int, [vp, sz, i32, vp, P(ctypes.c_double), P(ctypes.c_double)]),
             "hs_debug_attention": (ctypes.c_int, [ctypes.c_uint32, i32, P(i32)]),
             "hs_append": (ctypes.c_int, [vp, i32, i32, P(hs_append_desc), P(hs_paged_rows), i32, vp]),
+            "hs_gather_values": (ctypes.c_int, [vp, i32, i32, vp, i32, vp, ctypes.c_int64, vp, i32, vp]),
+            "hs_gather_values_history": (ctypes.c_int, [vp, i32, i32, vp, i32, vp, i32, vp]),
+            "hs_mla_decode_int4": (ctypes.c_int, [vp, i32, i32, vp, vp, i32, vp, ctypes.c_int64, ctypes.c_float, vp, i32, vp,
+                                                  vp]),
+            "hs_mla_decode_int4_history": (ctypes.c_int, [vp, i32, i32, vp, vp, i32, ctypes.c_float, vp, i32, vp, vp]),
             "hs_mla_prefix": (ctypes.c_int, [vp, i32, vp, P(hs_paged_rows), i32, vp, ctypes.c_float, vp, vp, vp, i32, vp,
                                              vp, sz, vp]),
             "hs_mla_prefix_workspace": (sz, [vp, i32, i32]),
@@ -279,8 +286,8 @@ def hs_gather_history(pool: int, layer: int, batch: int, topk_idx, k: int, dst, 
 
 
 def paged_rows(rows, pages, page_rows: int) -> hs_paged_rows:
-    """The struct of an ordinary paged pool: `rows` a tensor [count][...] of contiguous rows, each 1152 or 656 bytes (the
-    pool's row_bytes), `pages` int32 [lists][entries] (or [entries], one list, request 0's). It keeps both tensors alive;
+    """The struct of an ordinary paged pool: `rows` a tensor [count][...] of contiguous rows, each 1152 or 656 or 416
+    bytes (the pool's row_bytes), `pages` int32 [lists][entries] (or [entries], one list, request 0's). It keeps both tensors alive;
     build it once and pass it to every call."""
     import torch
 
@@ -288,7 +295,7 @@ def paged_rows(rows, pages, page_rows: int) -> hs_paged_rows:
         raise ValueError("paged_rows takes contiguous tensors")
     row_bytes = rows.element_size() * math.prod(rows.shape[1:])
     if row_bytes not in KV_ROW_BYTES:
-        raise ValueError(f"rows is [count][...] with rows of 1152 or 656 bytes: {tuple(rows.shape)} of {rows.dtype} has "
+        raise ValueError(f"rows is [count][...] with rows of 1152 or 656 or 416 bytes: {tuple(rows.shape)} of {rows.dtype} has "
                          f"{row_bytes}")
     if pages.dtype != torch.int32:
         raise ValueError(f"pages is int32, not {pages.dtype}")
@@ -350,14 +357,14 @@ def hs_append(pool: int, layer: int, ntok: int, desc: hs_append_desc, paged: hs_
     _check(load().hs_append(pool, layer, ntok, desc, paged, int(to_history), _stream(stream)), "hs_append")
 
 
-_dtypes = None  # torch's bf16, fp32 and int32, once torch is loaded
+_dtypes = None  # torch's bf16, fp32, int32 and fp16, once torch is loaded
 
 
 def _load_dtypes():
     global _dtypes
     import torch
 
-    _dtypes = torch.bfloat16, torch.float32, torch.int32
+    _dtypes = torch.bfloat16, torch.float32, torch.int32, torch.float16
     return _dtypes
 
 
@@ -369,7 +376,7 @@ def _fits(t, dtype, nbytes: int) -> bool:
 def hs_mla_prefix(pool: int, batch: int, q, prefix: hs_paged_rows, max_length: int, prefix_length, sm_scale: float,
                   own_out, own_lse, out, out_type: int, lse, workspace, stream=None) -> None:
     _check_row_bytes(pool, prefix)
-    bf16, f32, i32 = _dtypes or _load_dtypes()
+    bf16, f32, i32, _ = _dtypes or _load_dtypes()
     rows = batch * MLA_HEADS
     out_dtype = f32 if out_type == HS_TYPE_F32 else bf16
     if not (_fits(q, bf16, rows * MLA_D_QK * 2) and _fits(out, out_dtype, rows * MLA_D_V * out_dtype.itemsize) and
@@ -392,6 +399,63 @@ def hs_mla_prefix_workspace_bound(pool: int, batch: int, max_length: int) -> int
     n = ctypes.c_size_t()
     _check(load().hs_mla_prefix_workspace_bound(pool, batch, max_length, ctypes.byref(n)), "hs_mla_prefix_workspace_bound")
     return int(n.value)
+
+
+def _check_lists(what: str, pool: int, batch: int, entries, k: int, rows, count: int) -> None:
+    row_bytes = _pool_row_bytes.get(pool, 0)
+    i32 = (_dtypes or _load_dtypes())[2]
+    if not _fits(entries, i32, batch * k * 4):
+        raise ValueError(f"{what} takes a contiguous int32 list [{batch}][{k}]")
+    if rows is not None and not isinstance(rows, int) and not (rows.is_contiguous() and rows.nbytes >= count * row_bytes):
+        raise ValueError(f"{what} takes contiguous resident rows, {count} of {row_bytes} bytes")
+
+
+def _check_values(what: str, batch: int, k: int, dst, dst_type: int) -> None:
+    bf16, f32, _, f16 = _dtypes or _load_dtypes()
+    dtype = {HS_TYPE_BF16: bf16, HS_TYPE_F16: f16, HS_TYPE_F32: f32}.get(dst_type)
+    if dtype is not None and not _fits(dst, dtype, batch * k * MLA_D_QK * dtype.itemsize):
+        raise ValueError(f"{what} writes a contiguous {dtype} [{batch}][{k}][{MLA_D_QK}]")
+
+
+def hs_gather_values(pool: int, layer: int, batch: int, out_slots, k: int, resident_rows, resident_count: int, dst,
+                     dst_type: int, stream=None) -> None:
+    _check_lists("hs_gather_values", pool, batch, out_slots, k, resident_rows, resident_count)
+    _check_values("hs_gather_values", batch, k, dst, dst_type)
+    _check(load().hs_gather_values(pool, layer, batch, _addr(out_slots), k, _addr(resident_rows), resident_count, _addr(dst),
+                                   dst_type, _stream(stream)), "hs_gather_values")
+
+
+def hs_gather_values_history(pool: int, layer: int, batch: int, topk_idx, k: int, dst, dst_type: int, stream=None) -> None:
+    _check_lists("hs_gather_values_history", pool, batch, topk_idx, k, None, 0)
+    _check_values("hs_gather_values_history", batch, k, dst, dst_type)
+    _check(load().hs_gather_values_history(pool, layer, batch, _addr(topk_idx), k, _addr(dst), dst_type, _stream(stream)),
+           "hs_gather_values_history")
+
+
+def _check_heads(what: str, batch: int, q, out, out_type: int, lse) -> None:
+    bf16, f32, _, _ = _dtypes or _load_dtypes()
+    rows = batch * MLA_HEADS
+    dtype = f32 if out_type == HS_TYPE_F32 else bf16
+    if not (_fits(q, bf16, rows * MLA_D_QK * 2) and _fits(out, dtype, rows * MLA_D_V * dtype.itemsize) and
+            _fits(lse, f32, rows * 4)):
+        raise ValueError(f"{what} of {batch} takes contiguous tensors: q bf16 [{batch}][128][576], out {dtype} "
+                         f"[{batch}][128][512], lse fp32 [{batch}][128]")
+
+
+def hs_mla_decode_int4(pool: int, layer: int, batch: int, q, out_slots, k: int, resident_rows, resident_count: int,
+                       sm_scale: float, out, out_type: int, lse, stream=None) -> None:
+    _check_lists("hs_mla_decode_int4", pool, batch, out_slots, k, resident_rows, resident_count)
+    _check_heads("hs_mla_decode_int4", batch, q, out, out_type, lse)
+    _check(load().hs_mla_decode_int4(pool, layer, batch, _addr(q), _addr(out_slots), k, _addr(resident_rows), resident_count,
+                                     sm_scale, _addr(out), out_type, _addr(lse), _stream(stream)), "hs_mla_decode_int4")
+
+
+def hs_mla_decode_int4_history(pool: int, layer: int, batch: int, q, topk_idx, k: int, sm_scale: float, out, out_type: int,
+                               lse, stream=None) -> None:
+    _check_lists("hs_mla_decode_int4_history", pool, batch, topk_idx, k, None, 0)
+    _check_heads("hs_mla_decode_int4_history", batch, q, out, out_type, lse)
+    _check(load().hs_mla_decode_int4_history(pool, layer, batch, _addr(q), _addr(topk_idx), k, sm_scale, _addr(out), out_type,
+                                             _addr(lse), _stream(stream)), "hs_mla_decode_int4_history")
 
 
 def hs_get_error(pool: int, clear: bool = False) -> int:

@@ -2,8 +2,8 @@
 //
 // Token i at position p of request r: z = kv[i][0:512] (times weight / sqrt(mean(z^2) + eps) with a norm), and the 32
 // pairs of kv[i][512:576] turned by the angles p * inv_freq[j]. The row goes to every tier that holds the token, as 576
-// bf16 values or as 512 e4m3 values, a scale for each 128 and 64 bf16 (the pool's row_bytes says which). The queries'
-// rotary values of the same token turn by the same angles.
+// bf16 values, as 512 e4m3 values, a scale for each 128 and 64 bf16, or with its latents in 4 bits (hs_rows.cuh); the pool's
+// row_bytes says which. The queries' rotary values of the same token turn by the same angles.
 //
 // Angles. p * inv_freq is wanted modulo a full turn, and p reaches millions: a 32-bit product would be off by p * 2^-24
 // turns and more. inv_freq / 2 pi is taken once per warp, in 64 bits, as a fraction of a turn in fixed point (G / 2^64);
@@ -36,15 +36,16 @@
 #include "../../include/hs.h"
 #include "hs_internal.hpp"
 #include "hs_load.cuh"
+#include "hs_rows.cuh"
 
 namespace {
 
-using hs::ld_fresh;
+using namespace hs;
 
-constexpr int LATENT = 512, ROPE = 64, PAIRS = ROPE / 2, WIDTH = LATENT + ROPE;
-constexpr int ROW_BF16 = WIDTH * 2;              // 1152
-constexpr int ROW_FP8 = LATENT + 4 * 4 + ROPE * 2;  // 656
-constexpr int FP8_ROPE = LATENT + 4 * 4;         // byte offset of the rotary key in an fp8 row
+constexpr int PAIRS = ROPE / 2;
+enum Row { BF16, FP8, INT4 };  // a row's format
+template <Row R>
+constexpr int ROW_BYTES = R == BF16 ? ROW_BF16 : R == FP8 ? ROW_FP8 : ROW_INT4;
 constexpr int Q_HEADS = 16;                      // heads of one warp's work item: four 16-byte loads a lane in flight
 constexpr int MAX_TOKENS = 1 << 30;              // and items of 16 heads of a token's queries
 constexpr int THREADS = 128, WARPS = THREADS / 32;
@@ -56,8 +57,8 @@ constexpr int THREADS = 128, WARPS = THREADS / 32;
 // 6.5). For 1152-byte rows the compiler's own choice is kept, 8 blocks from 16 bits, 50.2 / 8.9 / 5.3 (a bound of 7 50.3
 // / 8.8 / 5.0, of 6 52.9 / 9.2 / 5.6; one of 8 took the queries of 256 and 2,047 tokens from 2.8 and 13.4 to 3.05 and
 // 14.0), 6 from fp32, 70.3 / 11.4 / 6.4 (a bound of 7 73.4 / 10.9 / 5.6, of 5 70.9 / 11.7 / 5.8).
-template <bool FP8>
-constexpr int MIN_BLOCKS = FP8 ? 7 : 0;  // 0: none
+template <Row R>
+constexpr int MIN_BLOCKS = R == FP8 ? 7 : 0;  // 0: none
 constexpr int Q_BLOCKS = 16;  // blocks of queries an SM, at most
 
 struct AppendArgs {
@@ -140,6 +141,20 @@ __device__ __forceinline__ uint32_t pack_e4m3(float a, float b, float c, float d
   return lo | hi << 16;
 }
 
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float m;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(m) : "f"(a), "f"(b));
+  return m;
+}
+// z / scale to the nearest whole number, ties to even, within -7 .. 7, plus 8; `inv` is 1 / scale. The quotient is corrected
+// once by its residual, which an fma has exactly (Markstein): where z / scale is a 32-bit number, a half among them, it is
+// that number, so ties are ties. Adding 1.5 * 2^23 leaves the whole number in the low bits.
+__device__ __forceinline__ uint32_t int4_of(float z, float scale, float inv) {
+  const float y = z * inv;
+  const float q = fminf(fmaxf(fmaf(fmaf(-y, scale, z), inv, y), -7.f), 7.f);
+  return __float_as_uint(q + (12582912.f + 8.f)) & 15u;
+}
+
 // Pair `lane`'s turns per position as a fraction of a turn in units of 2^-64 turns.
 __device__ __forceinline__ unsigned long long turn_rate(const float* inv_freq, int lane) {
   const double g = (double)__ldg(inv_freq + lane) * 0.15915494309189533577;  // 1 / 2 pi
@@ -161,9 +176,9 @@ __device__ __forceinline__ bool token_of(const AppendArgs& a, int i, int* req, i
 // A warp's `per` consecutive tokens. Where they go is looked up 32 tokens at a time, one lane each (position, request, then
 // slot and page: a chain of loads that every row would otherwise wait for), and a row's values are loaded while the one
 // before is worked on.
-template <class T, bool FP8, bool INTER>
+template <class T, Row R, bool INTER>
 __device__ __forceinline__ void append_rows(const AppendArgs& a, float* weight, int lane, int warp) {
-  constexpr int RB = FP8 ? ROW_FP8 : ROW_BF16;
+  constexpr int RB = ROW_BYTES<R>;
   constexpr uint32_t ALL = 0xffffffffu;
   const unsigned long long rate = turn_rate(a.inv_freq, lane);
   const int64_t begin = (int64_t)warp * a.per_warp;
@@ -247,7 +262,7 @@ __device__ __forceinline__ void append_rows(const AppendArgs& a, float* weight, 
         const float hi0 = __shfl_sync(0xffffffffu, t1, src), hi1 = __shfl_sync(0xffffffffu, t1, src + 1);
         kw = lane < 16 ? pack_bf16(lo0, lo1) : pack_bf16(hi0, hi1);
       }
-      if (FP8) {
+      if (R == FP8) {
         // lanes 0-15 hold groups 0 and 2 of 128 latents, lanes 16-31 groups 1 and 3
         uint2 w[2];
         float scale[2];
@@ -275,6 +290,36 @@ __device__ __forceinline__ void append_rows(const AppendArgs& a, float* weight, 
             sc[2] = scale[1];
           }
           *reinterpret_cast<uint32_t*>(o + FP8_ROPE + 4 * lane) = kw;
+        }
+      } else if (R == INT4) {
+        // two neighbouring lanes hold a block's 16 latents, this one word `lane` (and 32 + lane) of the row
+        uint32_t w[2], sc[2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          float m = 0.f;
+#pragma unroll
+          for (int e = 0; e < 8; ++e) m = max_nan(m, fabsf(z[h][e]));
+          m = max_nan(m, __shfl_xor_sync(ALL, m, 1));
+          const uint32_t code = int4_scale_code(m);
+          const float scale = int4_scale(code), inv = 1.f / scale;
+          w[h] = 0;
+#pragma unroll
+          for (int e = 0; e < 8; ++e) w[h] |= int4_of(z[h][e], scale, inv) << (16 * (e & 1) + 4 * (e >> 1));
+          // lanes 0, 8, 16 and 24 collect four scales each
+          uint32_t four = code | __shfl_down_sync(ALL, code, 2) << 8;
+          sc[h] = four | __shfl_down_sync(ALL, four, 4) << 16;
+        }
+#pragma unroll
+        for (int d = 0; d < 3; ++d) {
+          uint8_t* o = dst[d];
+          if (!o) continue;
+          *reinterpret_cast<uint32_t*>(o + 4 * lane) = w[0];
+          *reinterpret_cast<uint32_t*>(o + INT4_SCALES / 2 + 4 * lane) = w[1];
+          if ((lane & 7) == 0) {
+            *reinterpret_cast<uint32_t*>(o + INT4_SCALES + (lane >> 1)) = sc[0];
+            *reinterpret_cast<uint32_t*>(o + INT4_SCALES + 16 + (lane >> 1)) = sc[1];
+          }
+          *reinterpret_cast<uint32_t*>(o + INT4_ROPE + 4 * lane) = kw;
         }
       } else {
         uint4 w[2];
@@ -354,15 +399,15 @@ __device__ __forceinline__ void turn_queries(const AppendArgs& a, int lane, int 
   }
 }
 
-template <class T, bool FP8, bool INTER>
-__global__ void __launch_bounds__(THREADS, MIN_BLOCKS<FP8>) hs_append_kernel(const AppendArgs a) {
+template <class T, Row R, bool INTER>
+__global__ void __launch_bounds__(THREADS, MIN_BLOCKS<R>) hs_append_kernel(const AppendArgs a) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;");
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
   __shared__ __align__(16) float weight[LATENT];
   static_assert(THREADS * 4 == LATENT, "one 16-byte load a thread");
   if ((int)blockIdx.x < a.row_blocks)
-    append_rows<T, FP8, INTER>(a, weight, lane, (int)blockIdx.x * WARPS + w);
+    append_rows<T, R, INTER>(a, weight, lane, (int)blockIdx.x * WARPS + w);
   else
     turn_queries<T, INTER>(a, lane, ((int)blockIdx.x - a.row_blocks) * WARPS + w,
                            ((int)gridDim.x - a.row_blocks) * WARPS);
@@ -370,13 +415,14 @@ __global__ void __launch_bounds__(THREADS, MIN_BLOCKS<FP8>) hs_append_kernel(con
 
 using Kernel = void (*)(AppendArgs);
 template <class T>
-Kernel kernel_of(bool fp8, bool inter) {
-  if (fp8) return inter ? hs_append_kernel<T, true, true> : hs_append_kernel<T, true, false>;
-  return inter ? hs_append_kernel<T, false, true> : hs_append_kernel<T, false, false>;
+Kernel kernel_of(Row row, bool inter) {
+  if (row == FP8) return inter ? hs_append_kernel<T, FP8, true> : hs_append_kernel<T, FP8, false>;
+  if (row == INT4) return inter ? hs_append_kernel<T, INT4, true> : hs_append_kernel<T, INT4, false>;
+  return inter ? hs_append_kernel<T, BF16, true> : hs_append_kernel<T, BF16, false>;
 }
-// How many blocks of a kernel an SM of the device holds, cached per device and `form` (0 .. 11); 0 on an error.
+// How many blocks of a kernel an SM of the device holds, cached per device and `form` (0 .. 17); 0 on an error.
 int blocks_held(Kernel kernel, int form, int device) {
-  static std::atomic<int> cache[64][12];
+  static std::atomic<int> cache[64][18];
   if (device < 0 || device >= 64) return 0;
   int n = cache[device][form].load(std::memory_order_relaxed);
   if (n) return n;
@@ -421,7 +467,8 @@ int hs_launched(cudaError_t e) {
 extern "C" int hs_append(hs_pool* pool, int32_t layer, int32_t ntok, const hs_append_desc* desc,
                          const hs_paged_rows* paged, int32_t to_history, hs_stream_t stream) {
   if (!pool || !desc || layer < 0 || layer >= pool->d.layers || ntok < 0) return HS_ERR_INVALID_ARG;
-  if (pool->d.row_bytes != ROW_BF16 && pool->d.row_bytes != ROW_FP8) return HS_ERR_UNSUPPORTED;
+  const int rb = pool->d.row_bytes;
+  if (rb != ROW_BF16 && rb != ROW_FP8 && rb != ROW_INT4) return HS_ERR_UNSUPPORTED;
   const hs_append_desc& d = *desc;
   if (d.type < HS_TYPE_BF16 || d.type > HS_TYPE_F32 || (!paged && !to_history && !d.q_rope)) return HS_ERR_INVALID_ARG;
   if (paged && !hs_paged_ok(paged)) return HS_ERR_INVALID_ARG;
@@ -479,11 +526,12 @@ extern "C" int hs_append(hs_pool* pool, int32_t layer, int32_t ntok, const hs_ap
 
   // As many warps of rows as the device holds at once, each with its share of the tokens (and of the queries' items, whose
   // warps come on top): the turn rates (64-bit arithmetic) are worked out once per warp, not per row.
-  const bool fp8 = pool->d.row_bytes == ROW_FP8, inter = d.interleaved != 0;
-  const Kernel kernel = d.type == HS_TYPE_BF16  ? kernel_of<__nv_bfloat16>(fp8, inter)
-                        : d.type == HS_TYPE_F16 ? kernel_of<__half>(fp8, inter)
-                                                : kernel_of<float>(fp8, inter);
-  const int held = blocks_held(kernel, d.type * 4 + fp8 * 2 + inter, pool->device);
+  const Row row = rb == ROW_BF16 ? BF16 : rb == ROW_FP8 ? FP8 : INT4;
+  const bool inter = d.interleaved != 0;
+  const Kernel kernel = d.type == HS_TYPE_BF16  ? kernel_of<__nv_bfloat16>(row, inter)
+                        : d.type == HS_TYPE_F16 ? kernel_of<__half>(row, inter)
+                                                : kernel_of<float>(row, inter);
+  const int held = blocks_held(kernel, d.type * 6 + row * 2 + inter, pool->device);
   if (held < 1) return HS_ERR_CUDA;
   const int64_t most = (int64_t)pool->num_sms * held;
   const int64_t items = (int64_t)ntok * a.head_items;

@@ -342,6 +342,13 @@ typedef struct {
  *   656: 512 e4m3 latents, 4 fp32 scales, one for each 128 latents (their largest magnitude / 448, at
  *     least 2^-126; 1 where all are 0),
  *     64 bf16 of the rotary key; a latent is its e4m3 value times its scale.
+ *   416: 512 latents of 4 bits, 32 scales of 8 bits, one for each 16 latents, 64 bf16 of the rotary key; a latent is a whole
+ *     number from -7 to 7 times its scale. The 32-bit (little-endian) word i holds latents 8 i .. 8 i + 7, each number plus
+ *     8: the even ones at bits 0, 4, 8, 12, the odd ones at bits 16, 20, 24, 28. A scale is the latents' largest magnitude
+ *     / 7 in five bits of exponent (bias 15) and three of fraction, no sign (an fp16's bits 14 .. 7), to the nearest, at
+ *     least 2^-17 and at most 3840: larger magnitudes than 26880 are cut off. A number is the nearest to the latent over
+ *     its scale, the quotient taken in 32 bits; both round ties to even. Where one of the 16 latents is not finite their
+ *     scale is 255, a NaN, and so are all 16.
  *   Any other row_bytes: HS_ERR_UNSUPPORTED.
  * Every tier that holds the token gets the row: the pool's row source when `to_history` is non-zero (the host pool,
  * which must be writable, or the no-IO copy of a pool that has one), the paged rows when `paged` is given (list
@@ -362,6 +369,49 @@ typedef struct {
  */
 int hs_append(hs_pool *pool, int32_t layer, int32_t ntok, const hs_append_desc *desc, const hs_paged_rows *paged,
               int32_t to_history, hs_stream_t stream);
+
+/*
+ * Read rows back as numbers, whatever the pool's row format (1152, 656 or 416 bytes; any other row_bytes:
+ * HS_ERR_UNSUPPORTED): dst[b][i] = the 576 values (512 latents, 64 of the rotary key) of the row that entry i of request b's
+ * list names, zeros where it names none. It is hs_gather for a consumer that takes no quantised rows.
+ *   out_slots: int32 [batch][k] as a resolve wrote it (device or mapped host memory, 4-byte aligned): an entry >= 0 names
+ *     hot slot `entry` of `layer`, an entry <= -2 row -2 - entry of resident_rows (device memory, count rows of row_bytes,
+ *     16-byte aligned; NULL for none); anything else, or a row past the end, names none. k is not bound by topk_max.
+ *   dst: device memory [batch][k][576] of dst_type (any HS_TYPE_*), 16-byte aligned; it overlaps no input. Each value is rounded once: those
+ *     of 416-byte rows are exact in bf16 and fp16 (but for a rotary key past fp16's range), those of 1152-byte rows in
+ *     bf16; of 656-byte rows the product of value and scale is formed in 32 bits.
+ * batch * k <= 2^30; batch == 0 or k == 0 is a no-op. Enqueued on `stream` (of the pool's device, which must be the current
+ * one: HS_ERR_INVALID_ARG); capturable. Basis: as hs_gather; the pages leave the row format open.
+ */
+int hs_gather_values(hs_pool *pool, int32_t layer, int32_t batch, const int32_t *out_slots, int32_t k,
+                     const void *resident_rows, int64_t resident_count, void *dst, int32_t dst_type, hs_stream_t stream);
+
+/* The same from the full history: entry i of topk_idx names token i of request b's rows in the pool's row source (the no-IO
+ * copy when the pool has one, else the host pool); an entry < 0 or >= ctx names none. */
+int hs_gather_values_history(hs_pool *pool, int32_t layer, int32_t batch, const int32_t *topk_idx, int32_t k, void *dst,
+                             int32_t dst_type, hs_stream_t stream);
+
+/*
+ * hs_mla_decode over 416-byte rows (any other row_bytes: HS_ERR_UNSUPPORTED): the same attention with the latents read from
+ * their 4 bits. For request b < batch and head h < 128, over the entries i of its list that name a row (as for
+ * hs_gather_values):
+ *     s[i] = sm_scale * dot(q[b][h][0:576], row_i),  out[b][h][0:512] = sum_i softmax(s)[i] * row_i[0:512],
+ *     lse[b][h] = ln sum_i exp(s[i]).
+ * Rows that no entry names are not read, whatever they hold. With no row a head's output is zero and its lse -inf.
+ *   q: device bf16 [batch][128][576], 16-byte aligned. out: [batch][128][512] of out_type (HS_TYPE_BF16 or HS_TYPE_F32),
+ *     16-byte aligned; lse: fp32 [batch][128]. They overlap no input.
+ * batch <= 65536, k <= 2^30 and not bound by topk_max; batch == 0 or k == 0 is a no-op. Results are deterministic for given batch, k and
+ * device. Enqueued on `stream` (of the pool's device, which must be the current one: HS_ERR_INVALID_ARG); capturable.
+ * Basis: as hs_mla_decode.
+ */
+int hs_mla_decode_int4(hs_pool *pool, int32_t layer, int32_t batch, const void *q, const int32_t *out_slots, int32_t k,
+                       const void *resident_rows, int64_t resident_count, float sm_scale, void *out, int32_t out_type,
+                       float *lse, hs_stream_t stream);
+
+/* The same from the full history, as hs_gather_values_history names rows. Equal rows in the same order give bit-identical
+ * out and lse. */
+int hs_mla_decode_int4_history(hs_pool *pool, int32_t layer, int32_t batch, const void *q, const int32_t *topk_idx,
+                               int32_t k, float sm_scale, void *out, int32_t out_type, float *lse, hs_stream_t stream);
 
 /*
  * Attention of a whole batch over one prefix that all of its requests share (a system prompt, a document), read from the
