@@ -1,20 +1,50 @@
-// Sparse MLA decode attention over 4-bit rows, sm_103a.
+// Sparse MLA decode attention over 4-bit rows, sm_103a (tcgen05 tensor cores, TMEM).
 //
 // For request b and head h, over the rows that the request's list names:
 //     s[i] = sm_scale * q[b][h] . row_i,   out = sum softmax(s)[i] row_i[0:512],   lse = ln sum e^s[i],
-// the rows' latents being number times scale (hs_rows.cuh). One block takes eight heads of one request and walks the list
-// eight rows at a time, all in 32 bits on the CUDA cores.
+// the rows' latents being number times scale (hs_rows.cuh).
+//
+// What bounds it. A row is 416 bytes and serves 2 * 128 * (576 + 512) operations, 670 a byte: the tensor cores, once a
+// launch is long enough; one decode step's lists are short, and most of its time is the chain of one launch.
+//
+// Operands. The rows' latents become halves, exactly (at 2^-6 of their value), written into shared memory by the loader
+// warps; the rotary key stays bf16, and the scores' MMAs change from one type to the other within a sum. A head's query is
+// multiplied by a power of two, so that its largest value lies in [2^14, 2^15): its latent part is then exact in halves, but
+// for values 2^-28 below that one, which are rounded to 2^-40 of it; the score's scale takes the power back. The weights
+// are rounded to halves, 2^-11 of each (2^-31 of the largest, for those far below it): an output is 0.00014 off by that in
+// the mean, a tenth of its own rounding to bf16.
+//
+// A pair of CTAs takes one request's 128 heads, 64 for each CTA, over one split of its list, 256 entries a tile, with MMAs
+// of M = 128, N = 256 that both run together (cta_group::2): for S = Q K^T each CTA holds its 64 heads of Q and 128 of the
+// tile's rows, for O += P V its 64 heads of P and all 256 rows of 256 value columns. So the latents are unpacked 1.9 times:
+// once as K, and those of the half of the columns that a CTA has as V again.
+//
+// A list is cut into 1, 2, 4 or 8 splits, where pairs would otherwise be left over (cut_of): a cluster of as many pairs,
+// which leave their outputs in shared memory, unnormalised, with each head's maximum and normaliser, and join them:
+//     M = max m_s,   total = sum 2^(m_s - M) l_s,   out = sum 2^(m_s - M) O_s / total,   lse = ln 2 (M + log2 total).
+//
+// Warp roles per CTA: 0-7 softmax (warp w: TMEM lanes 32 (w % 4) .. +31, that is head lane % 64 and half lane / 64 of the
+// tile's rows, and rows 64 (w / 4) .. +63 of that half), 8 the issuer (the pair's first CTA issues for both), 9-15 the
+// loaders. K and V pass through one ring of 16 KB stages in the order in which the MMAs read them, a loader for each
+// slot: a K stage is 64 columns of the CTA's 128 rows, a V stage 128 of its value columns of 64 rows, both 128 rows of
+// 128 bytes, 128-byte swizzle; each feeds four MMAs, 256 cycles. A lane unpacks four of them; its next stage's words are
+// under way as soon as it has unpacked the ones before.
+//
+// Waits are bounded: on running out a role sets the abort flag, which ends every role, and the HS_DEVERR_TIMEOUT bit.
 
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
+#include <algorithm>
+#include <atomic>
 #include <cstdint>
 #include <cstring>
 
 #include "../../include/hs.h"
 #include "hs_internal.hpp"
 #include "hs_load.cuh"
+#include "hs_pair.cuh"
 #include "hs_rows.cuh"
 #include "hs_source.hpp"
 
@@ -22,88 +52,666 @@ namespace {
 
 using namespace hs;
 
-constexpr int HEADS = 128, GH = 8, KEYS = 8, THREADS = 128;
+constexpr int HEADS = 128;
+constexpr int NK = 256;            // rows of a tile
+constexpr int QH = HEADS / 2;      // heads of a CTA
+constexpr int KH = NK / 2;         // rows of a CTA's K half
+constexpr int DVH = LATENT / 2;    // value columns of a CTA
+constexpr int SEG = 64;            // a softmax thread's rows
+constexpr int NSEG = NK / SEG;
+constexpr int KBLK = WIDTH / 64;   // 64-column blocks of a row: K stages of a tile
+constexpr int BLK_BYTES = 64 * 128;      // 64 rows x 64 columns
+constexpr int STAGE_BYTES = 2 * BLK_BYTES;
+constexpr int NSTAGE = 7;          // stages of the ring
+constexpr int OFF_Q = 0;
+constexpr int OFF_RING = OFF_Q + KBLK * BLK_BYTES;
+constexpr int OFF_P = OFF_RING + NSTAGE * STAGE_BYTES;
+constexpr int OFF_BAR = OFF_P + NSEG * BLK_BYTES;
+// mbarriers: qfull full[7] empty[7] sfull[2] sfree[2] pfull pdone drain stall mx[2]
+constexpr int B_QFULL = 0, B_FULL = 1, B_EMPTY = B_FULL + NSTAGE, B_SFULL = B_EMPTY + NSTAGE,
+              B_SFREE = B_SFULL + 2, B_PFULL = B_SFREE + 2, B_PDONE = B_PFULL + 1, B_DRAIN = B_PDONE + 1,
+              B_STALL = B_DRAIN + 1, B_MX = B_STALL + 1, NBAR = B_MX + 2;
+constexpr int OFF_MISC = OFF_BAR + NBAR * 8;            // tensor-memory address, abort flag, the softmax warps' own
+constexpr int OFF_RED = (OFF_MISC + 12 + 15) & ~15;     // [2 parities][NSEG][QH] floats
+constexpr int OFF_QINV = OFF_RED + 2 * NSEG * QH * 4;   // [QH]: what the score of a head is multiplied by to undo its query's scale
+constexpr int OFF_ML = OFF_QINV + QH * 4;               // [QH] (m, l) of a split
+constexpr int SMEM_BYTES = OFF_ML + QH * 8;
+static_assert(NSTAGE <= KBLK, "the ring starts within the first K");
+static_assert(SMEM_BYTES <= 232448, "shared memory per block");
+constexpr int SOFTMAX_WARPS = 8, MMA_WARP = 8, LOAD_WARP0 = 9, THREADS = (LOAD_WARP0 + NSTAGE) * 32;
+static_assert(THREADS <= 512, "128 registers a thread");
+constexpr uint32_t TMEM_COLS = 512, TMEM_O = 0, TMEM_S = 256;  // O: 2 x 128 columns; S: two buffers of 128
+// A CTA's outputs take the place of Q and the ring: rows of a head, 16 bytes apart beyond their own size (no bank conflicts).
+constexpr int OUT_F32 = LATENT * 4 + 16, OUT_BF16 = LATENT * 2 + 16;
+static_assert(QH * OUT_F32 <= OFF_P, "a CTA's outputs fit in front of P");
+constexpr int MAX_SPLIT = 8;
+constexpr float P_SHIFT = 6.f;  // weights are kept at 2^6: their smallest half is then 2^-30 of a weight of the maximum's
+constexpr float UNSCALE = 64.f;  // latents are kept at 2^-6
 
 struct Decode4Args {
   const uint16_t* q;   // bf16 [batch][HEADS][WIDTH]
   const int32_t* idx;  // [batch][k]
   int32_t k;
   RowSource src;
-  float scale_log2;
+  float scale_log2;    // sm_scale * log2(e)
+  int32_t nsplit;
   void* out;
   int32_t out_f32;
   float* lse;
+  int32_t* err;
+  uint32_t wait_limit;
+  int32_t stall;
 };
 
-__global__ void __launch_bounds__(THREADS) hs_decode4_kernel(const Decode4Args a) {
+__host__ __device__ constexpr uint32_t idesc_f16(int m, int n, int a_mn, int b_mn) {
+  return idesc_bf16(m, n, a_mn, b_mn) & ~(1u << 7 | 1u << 10);
+}
+// (volatile, as every load of what an earlier kernel may have written: they stay behind the launch wait)
+__device__ __forceinline__ uint4 ld16(const uint8_t* p) {
+  uint4 v;
+  asm volatile("ld.global.cg.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
+  return v;
+}
+__device__ __forceinline__ uint32_t ld4(const uint8_t* p) {
+  uint32_t v;
+  asm volatile("ld.global.cg.u32 %0, [%1];" : "=r"(v) : "l"(p));
+  return v;
+}
+__device__ __forceinline__ float4 ld_peer(uint32_t addr) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr) : "memory");
+  return v;
+}
+__device__ __forceinline__ float2 ld_peer2(uint32_t addr) {
+  float2 v;
+  asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(addr) : "memory");
+  return v;
+}
+
+// A split's tiles, and where its stages lie in the order K(0) K(1) V(0) K(2) V(1) ... V(n - 1) of its tiles. Of the list's
+// last tile only the first `last_segs` segments hold entries: the others are neither loaded (their scores are masked,
+// whatever the buffer holds) nor multiplied with V.
+struct Tiles {
+  int first, n;      // the split's first tile, and how many it has
+  int last_segs;     // segments of its last tile
+  __device__ __forceinline__ int segs(int t) const { return t == n - 1 ? last_segs : NSEG; }
+};
+struct Order {
+  int kt = 0, vt = 0, c;  // the tile whose K is next or under way, the one whose V is; the stage's place within K or V
+  bool is_k = true;
+  __device__ __forceinline__ bool settle(const Tiles& t) {
+    for (;;) {
+      const int end = is_k ? KBLK : 2 * t.segs(vt);
+      if (c < end) return true;
+      c -= end;
+      if (is_k) {
+        is_k = kt == 0 && t.n > 1;
+        ++kt;
+      } else {
+        if (++vt == t.n) return false;
+        is_k = kt < t.n;
+      }
+    }
+  }
+};
+// A lane's four rows of a stage: 64 latents each (32 bytes and four scales) of the K half's rows lane, lane + 32, .., or of
+// rows lane and lane + 32 of a V segment, first one block of 64 columns, then the next.
+struct Quad {
+  uint4 a[4], b[4];
+  uint32_t s[4];
+};
+// 64 latents, unpacked, into row `row` of a stage.
+__device__ __forceinline__ void unpack(uint8_t* stage, int row, uint4 a, uint4 b, uint32_t scales) {
+  const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+  uint8_t* const dst = stage + row * 128;
+#pragma unroll
+  for (int g = 0; g < 4; ++g) {
+    Int4Scale k;
+    k.set(scales >> (8 * g) & 255u);
+#pragma unroll
+    for (int i = 2 * g; i < 2 * g + 2; ++i) {
+      const __half2 h[4] = {int4_pair<0>(w[i], k), int4_pair<1>(w[i], k), int4_pair<0>(w[i] >> 8, k), int4_pair<1>(w[i] >> 8, k)};
+      *reinterpret_cast<uint4*>(dst + ((i ^ (row & 7)) << 4)) = *reinterpret_cast<const uint4*>(h);
+    }
+  }
+}
+
+__global__ void __launch_bounds__(THREADS, 1) hs_decode4_kernel(const Decode4Args a) {
+  extern __shared__ __align__(1024) uint8_t smem[];
+  uint64_t* const bar = reinterpret_cast<uint64_t*>(smem + OFF_BAR);
+  volatile int* const abort_flag = reinterpret_cast<volatile int*>(smem + OFF_MISC + 4);
+  volatile int* const out_stop = abort_flag + 1;
+  float* const red = reinterpret_cast<float*>(smem + OFF_RED);
+  float* const qinv = reinterpret_cast<float*>(smem + OFF_QINV);
+  const int t = threadIdx.x, lane = t & 31;
+  const int warp = __shfl_sync(0xffffffffu, t >> 5, 0);  // the same in all lanes, and known to be
+  const uint32_t crank = cluster_rank(), rank = crank & 1u, first = crank & ~1u;
+  const unsigned lim = a.wait_limit;
+
+  if (t == 0) {
+    for (int i = 0; i < NBAR; ++i) bar_init(bar + i, 1);
+    // one arrival for each softmax warp of the pair, for each of its two loaders of a slot
+    bar_init(bar + B_QFULL, 2 * SOFTMAX_WARPS);
+    for (int i = 0; i < NSTAGE; ++i) bar_init(bar + B_FULL + i, 2);
+    for (int i = 0; i < 2; ++i) bar_init(bar + B_SFREE + i, 2 * SOFTMAX_WARPS);
+    bar_init(bar + B_PFULL, 2 * SOFTMAX_WARPS);
+    for (int i = 0; i < 2; ++i) bar_init(bar + B_MX + i, NSEG);  // the warps that hold the same heads
+    *abort_flag = *out_stop = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == MMA_WARP)
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(su32(smem + OFF_MISC)),
+                 "r"(TMEM_COLS)
+                 : "memory");
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();  // the CTAs' barriers are ready
+  tc_fence_after();
+  const uint32_t tmem = __shfl_sync(0xffffffffu, *reinterpret_cast<volatile uint32_t*>(smem + OFF_MISC), 0);
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;");
-  __shared__ float q[GH][WIDTH], row[KEYS][WIDTH], score[KEYS][GH];
-  __shared__ const uint8_t* at[KEYS];
-  const int b = blockIdx.x / (HEADS / GH), h0 = (blockIdx.x % (HEADS / GH)) * GH, t = threadIdx.x;
-  for (int i = t; i < GH * WIDTH; i += THREADS)
-    q[i / WIDTH][i % WIDTH] = __uint_as_float((uint32_t)a.q[((size_t)b * HEADS + h0) * WIDTH + i] << 16);
-  float m[GH], l[GH], o[GH][4] = {};
-  for (int h = 0; h < GH; ++h) m[h] = -INFINITY, l[h] = 0.f;
-  for (int i0 = 0; i0 < a.k; i0 += KEYS) {
-    __syncthreads();
-    if (t < KEYS) at[t] = i0 + t < a.k ? row_at(a.src, b, ld_fresh(a.idx + (size_t)b * a.k + i0 + t), ROW_INT4) : nullptr;
-    __syncthreads();
-    for (int i = t; i < KEYS * WIDTH; i += THREADS) {
-      const int j = i / WIDTH, c = i % WIDTH;
-      float v = 0.f;
-      if (at[j]) {
-        if (c < LATENT) {
-          const uint32_t w = __ldcg(reinterpret_cast<const uint32_t*>(at[j]) + c / 8);
-          const int e = c & 7;
-          v = (float)((int)(w >> (16 * (e & 1) + 4 * (e >> 1)) & 15u) - 8) * int4_scale(__ldcg(at[j] + INT4_SCALES + c / INT4_BLOCK));
-        } else {
-          v = __uint_as_float((uint32_t)__ldcg(reinterpret_cast<const uint16_t*>(at[j] + INT4_ROPE) + c - LATENT) << 16);
+
+  const uint32_t b = blockIdx.x / (uint32_t)(2 * a.nsplit);
+  const int split = (int)(crank >> 1), all = (a.k + NK - 1) / NK, per = all / a.nsplit, more = all - per * a.nsplit;
+  Tiles tiles;
+  tiles.n = per + (split < more ? 1 : 0);
+  tiles.first = split * per + min(split, more);
+  tiles.last_segs = min(NSEG, (a.k - (tiles.first + tiles.n - 1) * NK + SEG - 1) / SEG);
+  const int32_t* const list = a.idx + (size_t)b * a.k;
+  const uint32_t lead = peer_addr(bar, first);  // the first CTA's barriers
+  // test hook: the roles that would start a copy or an MMA first wait on a barrier that nothing completes
+  bool ok = true;
+
+  if (warp == MMA_WARP) {
+    // ---- the issuer, of the pair's first CTA. The whole warp walks the loop, so that the descriptors stay in uniform
+    //      registers; one lane issues: scores of tile g, then the value product of tile g - 1.
+    if (rank == 0) {
+      constexpr uint32_t ID_S = idesc_f16(HEADS, NK, 0, 0), ID_R = idesc_bf16(HEADS, NK, 0, 0), ID_O = idesc_f16(HEADS, 256, 0, 1);
+      const bool leader = elect_one();
+      const uint32_t both = 3u << first;
+      const uint64_t dq = sdesc128(su32(smem + OFF_Q), 0), dp = sdesc128(su32(smem + OFF_P), 0),
+                     dk = sdesc128(su32(smem + OFF_RING), 0), dv = sdesc128(su32(smem + OFF_RING), BLK_BYTES);
+      int st = 0;
+      unsigned ph = 0;
+      auto wait = [&](int i, unsigned parity) { return __all_sync(0xffffffffu, bar_wait(bar + i, parity, abort_flag, lim)); };
+      // four MMAs on the next stage: A's step of 32 bytes, B's of `step` (in units of 16), then the stage is free
+      auto four = [&](uint32_t d, uint64_t oa, uint64_t ob, int step, uint32_t id, uint32_t acc) {
+        if (leader) {
+          mma2(d, oa, ob, id, acc);
+          mma2(d, oa + 2, ob + step, id, 1u);
+          mma2(d, oa + 4, ob + 2 * step, id, 1u);
+          mma2(d, oa + 6, ob + 3 * step, id, 1u);
+          commit2(bar + B_EMPTY + st, both);
+        }
+        __syncwarp();
+        if (++st == NSTAGE) st = 0, ph ^= 1u;
+      };
+      ok = (!a.stall || wait(B_STALL, 0)) && wait(B_QFULL, 0);
+      for (int g = 0; g <= tiles.n && ok; ++g) {
+        if (g < tiles.n) {
+          if (g >= 2) ok = wait(B_SFREE + (g & 1), (unsigned)((g >> 1) - 1) & 1u);
+          tc_fence_after();
+          for (int c = 0; c < KBLK && ok; ++c) {
+            ok = wait(B_FULL + st, ph);
+            tc_fence_after();
+            if (ok) four(tmem + TMEM_S + (uint32_t)(g & 1) * KH, dq + (uint64_t)(c * (BLK_BYTES >> 4)),
+                         dk + (uint64_t)(st * (STAGE_BYTES >> 4)), 2, c < KBLK - 1 ? ID_S : ID_R, c != 0 ? 1u : 0u);
+          }
+          if (!ok) break;
+          if (leader) commit2(bar + B_SFULL + (g & 1), both);
+        }
+        if (g >= 1) {
+          ok = wait(B_PFULL, (unsigned)(g - 1) & 1u);
+          tc_fence_after();
+          const int nv = 2 * tiles.segs(g - 1);
+          for (int c = 0; c < nv && ok; ++c) {
+            // 64 rows: block c / 2 of P; 128 of the CTA's value columns, 16 rows a step
+            ok = wait(B_FULL + st, ph);
+            tc_fence_after();
+            if (ok) four(tmem + TMEM_O + (uint32_t)(c & 1) * 128, dp + (uint64_t)((c >> 1) * (BLK_BYTES >> 4)),
+                         dv + (uint64_t)(st * (STAGE_BYTES >> 4)), 128, ID_O, g > 1 || c > 1 ? 1u : 0u);
+          }
+          if (!ok) break;
+          if (leader) commit2(bar + B_PDONE, both);
         }
       }
-      row[j][c] = v;
+      __syncwarp();
+      if (leader) commit2(bar + B_DRAIN, both);
     }
-    __syncthreads();
-    if (t < KEYS * GH) {
-      const int j = t / GH, h = t % GH;
-      float s = 0.f;
-      for (int c = 0; c < WIDTH; ++c) s = fmaf(q[h][c], row[j][c], s);
-      score[j][h] = at[j] ? s * a.scale_log2 : -INFINITY;
-    }
-    __syncthreads();
-    for (int h = 0; h < GH; ++h) {
-      float top = m[h];
-      for (int j = 0; j < KEYS; ++j)
-        if (at[j]) top = fmaxf(top, score[j][h]);
-      const float ref = top == -INFINITY ? 0.f : top, f = exp2f(m[h] - ref);
-      m[h] = top;
-      l[h] *= f;
-      for (int e = 0; e < 4; ++e) o[h][e] *= f;
-      for (int j = 0; j < KEYS; ++j) {
-        if (!at[j]) continue;
-        const float p = exp2f(score[j][h] - ref);
-        l[h] += p;
-        for (int e = 0; e < 4; ++e) o[h][e] = fmaf(p, row[j][4 * t + e], o[h][e]);
+    __syncwarp();
+  } else if (warp >= LOAD_WARP0) {
+    // ---- the loader of ring slot s: every NSTAGE-th stage of the split's order.
+    ok = !a.stall || __all_sync(0xffffffffu, bar_wait(bar + B_STALL, 0, abort_flag, lim));
+    const int s = warp - LOAD_WARP0;
+    uint8_t* const stage = smem + OFF_RING + s * STAGE_BYTES;
+    const uint32_t full = lead + (B_FULL + s) * 8;
+    Order o;
+    o.c = s;
+    bool more_stages = o.settle(tiles);
+    int32_t e[4];               // the entries of the stage after the one that is unpacked
+    const uint8_t* row[4];
+    Quad w;
+    // the list's entries of a stage's rows
+    auto fetch = [&](const Order& x) {
+      const int base = (tiles.first + (x.is_k ? x.kt : x.vt)) * NK + (x.is_k ? (int)rank * KH : (x.c >> 1) * SEG) + lane;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int key = base + 32 * i;
+        if (x.is_k || i < 2) e[i] = key < a.k ? ld_fresh(list + key) : -1;
+      }
+      if (!x.is_k) e[2] = e[0], e[3] = e[1];
+    };
+    auto find = [&]() {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) row[i] = row_at(a.src, b, e[i], ROW_INT4);
+    };
+    // row i's words of a stage of latents
+    auto load = [&](const Order& x, int i) {
+      const int blk = x.is_k ? x.c : (int)rank * (DVH / 64) + (x.c & 1) * 2 + (i >> 1);
+      if (row[i]) {
+        w.a[i] = ld16(row[i] + 32 * blk);
+        w.b[i] = ld16(row[i] + 32 * blk + 16);
+        w.s[i] = ld4(row[i] + INT4_SCALES + 4 * blk);
+      } else {
+        w.a[i] = w.b[i] = make_uint4(0, 0, 0, 0);
+        w.s[i] = 0;
+      }
+    };
+    auto is_rope = [](const Order& x) { return x.is_k && x.c == KBLK - 1; };
+    if (more_stages && ok) {
+      fetch(o);
+      find();
+      if (!is_rope(o)) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) load(o, i);
       }
     }
-  }
-  for (int h = 0; h < GH; ++h) {
-    const size_t bh = (size_t)b * HEADS + h0 + h;
-    const float inv = l[h] != 0.f ? 1.f / l[h] : 0.f;
-    for (int e = 0; e < 4; ++e) {
-      if (a.out_f32)
-        static_cast<float*>(a.out)[bh * LATENT + 4 * t + e] = o[h][e] * inv;
-      else
-        static_cast<__nv_bfloat16*>(a.out)[bh * LATENT + 4 * t + e] = __float2bfloat16(o[h][e] * inv);
+    unsigned ph = 1;  // a barrier that has not completed a phase passes for the parity before its first
+    while (more_stages && ok) {
+      Order nx = o;
+      nx.c += NSTAGE;
+      const bool more_after = nx.settle(tiles);
+      if (more_after) fetch(nx);
+      ok = __all_sync(0xffffffffu, bar_wait(bar + B_EMPTY + s, ph, abort_flag, lim));  // the MMAs that read the slot have finished
+      if (!ok) break;
+      ph ^= 1u;
+      if (is_rope(o)) {
+        // the rotary keys as they are, 16 bytes a copy, eight lanes a row
+#pragma unroll 4
+        for (int it = 0; it < 32; ++it) {
+          const int r = 4 * it + (lane >> 3), j = lane & 7;
+          const unsigned long long p0 = reinterpret_cast<unsigned long long>(it < 16 ? (it < 8 ? row[0] : row[1]) : (it < 24 ? row[2] : row[3]));
+          const uint8_t* const src = reinterpret_cast<const uint8_t*>(__shfl_sync(0xffffffffu, p0, r & 31));
+          uint8_t* const dst = stage + r * 128 + ((j ^ (r & 7)) << 4);
+          if (src)
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(su32(dst)), "l"(src + INT4_ROPE + 16 * j) : "memory");
+          else
+            *reinterpret_cast<uint4*>(dst) = make_uint4(0, 0, 0, 0);
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+        if (more_after) find();
+        if (more_after) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) load(nx, i);
+        }
+        asm volatile("cp.async.wait_group 0;" ::: "memory");
+      } else {
+        const bool ahead = more_after && !is_rope(nx);
+        if (more_after) find();
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          unpack(stage, lane + 32 * i, w.a[i], w.b[i], w.s[i]);
+          if (ahead) load(nx, i);
+        }
+      }
+      fence_proxy_async();
+      __syncwarp();
+      if (lane == 0) arrive_lead(full);
+      o = nx;
+      more_stages = more_after;
     }
-    if (t == 0) a.lse[bh] = l[h] != 0.f ? ((m[h] == -INFINITY ? 0.f : m[h]) + log2f(l[h])) * 0.6931471805599453f : -INFINITY;
+    __syncwarp();
+  } else {
+    // ---- softmax: a thread holds head r of this CTA and 64 rows of every tile, segment sg
+    const int q = warp & 3, sub = warp >> 2, r = (q & 1) * 32 + lane, hf = q >> 1, sg = hf * 2 + sub;
+    const uint32_t trow = tmem + ((uint32_t)(q * 32) << 16);
+    uint8_t* const prows = smem + OFF_P + sg * BLK_BYTES + (q & 1) * 32 * 128;  // the warp's 32 rows of P
+    const size_t head0 = (size_t)b * HEADS + rank * QH;                         // the CTA's first
+    {
+      // Q: four threads a head, 18 chunks of eight values each (chunks 4 i + part: 64 of latents, 8 of the rotary part)
+      const int h = t >> 2, part = t & 3;
+      const uint8_t* const src = reinterpret_cast<const uint8_t*>(a.q + (head0 + h) * WIDTH);
+      uint4 v[KBLK * 2];
+      uint32_t top = 0;
+#pragma unroll
+      for (int i = 0; i < KBLK * 2; ++i) v[i] = ld16(src + 16 * (4 * i + part));
+#pragma unroll
+      for (int i = 0; i < KBLK * 2; ++i) {
+        const uint32_t x[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) top = max(top, max(x[j] & 0x7fffu, x[j] >> 16 & 0x7fffu));
+      }
+      top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+      top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+      const int f = min(14 + 127 - (int)(top >> 7), 100);  // the largest value's exponent becomes 14
+      const float mul = __uint_as_float((uint32_t)(127 + f) << 23);
+      if (part == 0) qinv[h] = __uint_as_float((uint32_t)(127 - f) << 23) * UNSCALE;
+#pragma unroll
+      for (int i = 0; i < KBLK * 2; ++i) {
+        const uint32_t x[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+        uint32_t y[4];
+        const int ch = 4 * i + part;
+        const bool rope = i >= 16;
+        const float m = rope ? mul * (1.f / UNSCALE) : mul;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const float lo = __uint_as_float(x[j] << 16) * m, hi = __uint_as_float(x[j] & 0xffff0000u) * m;
+          if (rope) {
+            const __nv_bfloat162 p = __floats2bfloat162_rn(lo, hi);
+            y[j] = *reinterpret_cast<const uint32_t*>(&p);
+          } else {
+            const __half2 p = __floats2half2_rn(lo, hi);
+            y[j] = *reinterpret_cast<const uint32_t*>(&p);
+          }
+        }
+        *reinterpret_cast<uint4*>(smem + OFF_Q + (ch >> 3) * BLK_BYTES + h * 128 + (((ch & 7) ^ (h & 7)) << 4)) =
+            make_uint4(y[0], y[1], y[2], y[3]);
+      }
+      fence_proxy_async();
+      named_sync(1, SOFTMAX_WARPS * 32);
+      if (lane == 0) arrive_lead(lead + B_QFULL * 8);
+    }
+    float m_run = -INFINITY, l_run = 0.f;
+    int nx = 0;  // exchanges
+    // hands `v` to the other three threads of the head
+    auto exchange = [&](float v) {
+      float* const share = red + (nx & 1) * NSEG * QH;
+      share[sg * QH + r] = v;
+      __syncwarp();
+      if (lane == 0) bar_arrive(bar + B_MX + (q & 1));
+      ok = __all_sync(0xffffffffu, bar_wait(bar + B_MX + (q & 1), (unsigned)nx & 1u, abort_flag, lim)) && ok;
+      ++nx;
+      return share + r;
+    };
+    const bool up = a.scale_log2 > 0.f;
+    const float factor = a.scale_log2 * qinv[r];  // of this head's scores
+    const float scale = up ? factor : 1.f;        // the maximum is taken before a positive scale; another is applied first
+    int32_t e0, e1;                               // the thread's entries of the tile's mask: rows lane and lane + 32 of its segment
+    auto entries = [&](int tile) {
+      const int key = (tiles.first + tile) * NK + sg * SEG + lane;
+      e0 = key < a.k ? ld_fresh(list + key) : -1;
+      e1 = key + 32 < a.k ? ld_fresh(list + key + 32) : -1;
+    };
+    entries(0);
+    for (int g = 0; g < tiles.n; ++g) {
+      const unsigned mlo = __ballot_sync(0xffffffffu, row_at(a.src, b, e0, ROW_INT4) != nullptr);
+      const unsigned mhi = __ballot_sync(0xffffffffu, row_at(a.src, b, e1, ROW_INT4) != nullptr);
+      if (g + 1 < tiles.n) entries(g + 1);
+      ok = __all_sync(0xffffffffu, bar_wait(bar + B_SFULL + (g & 1), (unsigned)(g >> 1) & 1u, abort_flag, lim));
+      if (!ok) break;
+      tc_fence_after();
+      // The scores are read twice, 32 at a time: for the maximum, and once the four threads of a head agree on it. (Holding
+      // all 64 across the exchange takes more registers than 16 warps leave.)
+      const uint32_t scol = trow + TMEM_S + (uint32_t)((g & 1) * KH + sub * SEG);
+      uint32_t sv[32];
+      float mb = -INFINITY;
+      auto load32 = [&](int h) {
+        tmem_ld32(scol + 32 * h, sv);
+        tmem_wait_ld();
+        if (!up) {
+#pragma unroll
+          for (int i = 0; i < 32; ++i) sv[i] = __float_as_uint(__uint_as_float(sv[i]) * factor);
+        }
+        const uint32_t m32 = h ? mhi : mlo;
+        if (~m32) {
+#pragma unroll
+          for (int i = 0; i < 32; ++i) sv[i] = m32 >> i & 1 ? sv[i] : 0xff800000u;
+        }
+      };
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        load32(h);
+#pragma unroll
+        for (int i = 0; i < 32; ++i) mb = fmaxf(mb, __uint_as_float(sv[i]));
+      }
+      const float* share = exchange(mb);
+      if (!ok) break;
+      mb = scale * fmaxf(fmaxf(share[0], share[QH]), fmaxf(share[2 * QH], share[3 * QH]));
+      // the maximum follows only when it has risen by more than 8 (log2), so that O is rarely rescaled: weights stay below
+      // 2^(8 + P_SHIFT), within a half
+      float m_new = m_run;
+      if (mb > -INFINITY && (m_run == -INFINITY || mb > m_run + 8.f)) m_new = mb;
+      const bool resc = m_new != m_run && m_run != -INFINITY;
+      const float ref = m_new == -INFINITY ? 0.f : m_new - P_SHIFT;  // no finite score yet: nothing to subtract, a NaN still shows
+      float sum[2] = {0.f, 0.f};
+      uint32_t p[SEG / 2];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        load32(h);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          const float p0 = ex2_approx(fmaf(__uint_as_float(sv[2 * i]), scale, -ref)),
+                      p1 = ex2_approx(fmaf(__uint_as_float(sv[2 * i + 1]), scale, -ref));
+          sum[i & 1] += p0 + p1;
+          const __half2 v = __floats2half2_rn(p0, p1);
+          p[16 * h + i] = *reinterpret_cast<const uint32_t*>(&v);
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) arrive_lead(lead + (B_SFREE + (g & 1)) * 8);
+      // P's buffer is free, and O holds the tiles before, once the value product of the tile before has finished
+      if (g >= 1) {
+        ok = __all_sync(0xffffffffu, bar_wait(bar + B_PDONE, (unsigned)(g - 1) & 1u, abort_flag, lim));
+        if (!ok) break;
+      }
+      if (__any_sync(0xffffffffu, resc)) {
+        // each of the two threads with the same lane takes half of its columns
+        tc_fence_after();
+        const float f = resc ? ex2_approx(m_run - m_new) : 1.f;
+#pragma unroll 1
+        for (int c = sub * (DVH / 2); c < (sub + 1) * (DVH / 2); c += 16) {
+          float o[16];
+          tmem_ld16(trow + TMEM_O + c, o);
+#pragma unroll
+          for (int i = 0; i < 16; ++i) o[i] *= f;
+          tmem_st16(trow + TMEM_O + c, o);
+        }
+        tmem_wait_st();
+        l_run *= f;
+      }
+      m_run = m_new;
+      l_run += sum[0] + sum[1];
+#pragma unroll
+      for (int c = 0; c < SEG / 8; ++c)
+        *reinterpret_cast<uint4*>(prows + lane * 128 + ((c ^ (lane & 7)) << 4)) =
+            make_uint4(p[4 * c], p[4 * c + 1], p[4 * c + 2], p[4 * c + 3]);
+      fence_proxy_async();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) arrive_lead(lead + B_PFULL * 8);
+    }
+    if (ok) ok = __all_sync(0xffffffffu, bar_wait(bar + B_PDONE, (unsigned)(tiles.n - 1) & 1u, abort_flag, lim));
+    if (ok) {
+      const float* const share = exchange(l_run);
+      if (ok) l_run = (share[0] + share[QH]) + (share[2 * QH] + share[3 * QH]);
+    }
+    if (!ok) *out_stop = 1;  // for all softmax warps alike: they meet at barriers below
+    // O, out of tensor memory into the head's row; every MMA of the pair has read Q and the ring by now, and every loader is
+    // done. Whole lists leave normalised, in the output's type; splits as they are.
+    named_sync(1, SOFTMAX_WARPS * 32);
+    if (*out_stop == 0) {
+      tc_fence_after();
+      const bool part = a.nsplit > 1, f32 = part || a.out_f32;
+      const float ref = m_run == -INFINITY ? 0.f : m_run - P_SHIFT;
+      const float f = part ? 1.f : l_run != 0.f ? UNSCALE / l_run : 0.f;
+      if (sg == 0) {
+        if (part)
+          reinterpret_cast<float2*>(smem + OFF_ML)[r] = make_float2(m_run == -INFINITY ? -INFINITY : ref, l_run);
+        else
+          a.lse[head0 + r] = l_run != 0.f ? (ref + log2f(l_run)) * 0.6931471805599453f : -INFINITY;
+      }
+      uint8_t* const orow = smem + r * (f32 ? OUT_F32 : OUT_BF16);
+#pragma unroll 1
+      for (int c = sub * (DVH / 2); c < (sub + 1) * (DVH / 2); c += 32) {
+        uint32_t v[32];
+        tmem_ld32(trow + TMEM_O + c, v);
+        tmem_wait_ld();
+        const int col = hf * DVH + c;
+        if (f32) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            *reinterpret_cast<float4*>(orow + 4 * col + 16 * i) =
+                make_float4(__uint_as_float(v[4 * i]) * f, __uint_as_float(v[4 * i + 1]) * f, __uint_as_float(v[4 * i + 2]) * f,
+                            __uint_as_float(v[4 * i + 3]) * f);
+        } else {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            uint32_t y[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const __nv_bfloat162 x = __floats2bfloat162_rn(__uint_as_float(v[8 * i + 2 * j]) * f, __uint_as_float(v[8 * i + 2 * j + 1]) * f);
+              y[j] = *reinterpret_cast<const uint32_t*>(&x);
+            }
+            *reinterpret_cast<uint4*>(orow + 2 * col + 16 * i) = make_uint4(y[0], y[1], y[2], y[3]);
+          }
+        }
+      }
+      tc_fence_before();
+      if (!part) {
+        fence_proxy_async();
+        named_sync(1 + 1 + (q & 1), SOFTMAX_WARPS * 16);  // the four warps of the same 32 heads
+        // eight rows a warp, one copy a lane
+        if (lane < 8) {
+          const int h = (q & 1) * 32 + sg * 8 + lane;
+          const uint32_t bytes = LATENT * (f32 ? 4 : 2);
+          asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;\n\tcp.async.bulk.commit_group;" ::"l"(
+                           static_cast<uint8_t*>(a.out) + (head0 + h) * bytes),
+                       "r"(su32(smem + h * (f32 ? OUT_F32 : OUT_BF16))), "r"(bytes)
+                       : "memory");
+          asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+        }
+      }
+    }
+    __syncwarp();
   }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == MMA_WARP) {  // every MMA has finished before the tensor memory is freed, after an abort too
+    bool drained = bar_test(bar + B_DRAIN, 0);
+    for (const uint64_t t0 = now_ns(); !drained && now_ns() - t0 < WAIT_NS;) drained = bar_test(bar + B_DRAIN, 0);
+    if (!drained) *abort_flag = 1;
+    __syncwarp();
+    if (*abort_flag && lane == 0) atomicOr(a.err, HS_DEVERR_TIMEOUT);
+    __syncwarp();
+  }
+  cluster_sync();
+  tc_fence_after();
+  if (a.nsplit > 1) {
+    // Join: this CTA's share of its 64 heads, from the splits' CTAs of the same heads; 128 threads a head, four values each.
+    const int share = QH / a.nsplit, c4 = (t & 127) * 16;
+    if (!*abort_flag) {
+#pragma unroll 1
+      for (int i = t >> 7; i < share; i += THREADS / 128) {
+        const int h = split * share + i;
+        const size_t bh = (size_t)b * HEADS + rank * QH + h;
+        float2 ml[MAX_SPLIT];
+        float4 v[MAX_SPLIT];
+        float mx = -INFINITY;
+#pragma unroll
+        for (int s = 0; s < MAX_SPLIT; ++s) {
+          if (s >= a.nsplit) break;
+          ml[s] = ld_peer2(peer_addr(smem + OFF_ML + h * 8, 2 * s + rank));
+          v[s] = ld_peer(peer_addr(smem + h * OUT_F32 + c4, 2 * s + rank));
+          if (ml[s].y != 0.f) mx = fmaxf(mx, ml[s].x);
+        }
+        const float ref = mx == -INFINITY ? 0.f : mx;
+        float total = 0.f;
+        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int s = 0; s < MAX_SPLIT; ++s) {
+          if (s >= a.nsplit) break;
+          if (ml[s].y == 0.f) continue;  // a split with no row
+          const float f = exp2f(ml[s].x == -INFINITY ? 0.f : ml[s].x - ref);
+          total = fmaf(f, ml[s].y, total);
+          o.x = fmaf(f, v[s].x, o.x);
+          o.y = fmaf(f, v[s].y, o.y);
+          o.z = fmaf(f, v[s].z, o.z);
+          o.w = fmaf(f, v[s].w, o.w);
+        }
+        const float inv = total != 0.f ? UNSCALE / total : 0.f;
+        o = make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
+        if (a.out_f32) {
+          *reinterpret_cast<float4*>(static_cast<uint8_t*>(a.out) + bh * LATENT * 4 + c4) = o;
+        } else {
+          const __nv_bfloat162 lo = __floats2bfloat162_rn(o.x, o.y), hi = __floats2bfloat162_rn(o.z, o.w);
+          *reinterpret_cast<uint2*>(static_cast<uint8_t*>(a.out) + bh * LATENT * 2 + c4 / 2) =
+              make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
+        }
+        if (c4 == 0) a.lse[bh] = total != 0.f ? (ref + log2f(total)) * 0.6931471805599453f : -INFINITY;
+      }
+    }
+    __syncwarp();
+    cluster_sync();  // the splits' shared memory stays until all have read it
+  }
+  if (warp == MMA_WARP)
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(TMEM_COLS) : "memory");
+}
+
+// How many clusters of 2 n CTAs (n = 1, 2, 4, 8) the current device holds at once, cached per device; 0 where it holds none.
+int resident(int n) {
+  static std::atomic<int> cache[64][4];  // 0: not yet asked, else the count + 1
+  const int slot = n == 1 ? 0 : n == 2 ? 1 : n == 4 ? 2 : 3;
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) {
+    cudaGetLastError();
+    return 0;
+  }
+  const int c = cache[dev][slot].load(std::memory_order_relaxed);
+  if (c) return c - 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(2 * n, 1, 1);
+  cfg.blockDim = dim3(THREADS, 1, 1);
+  cfg.dynamicSmemBytes = SMEM_BYTES;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim.x = 2 * n;
+  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  int got = 0;
+  if (cudaFuncSetAttribute(hs_decode4_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_BYTES) != cudaSuccess ||
+      (n == 8 && cudaFuncSetAttribute(hs_decode4_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess) ||
+      cudaOccupancyMaxActiveClusters(&got, hs_decode4_kernel, &cfg) != cudaSuccess) {
+    cudaGetLastError();
+    got = 0;
+  }
+  cache[dev][slot].store(got + 1, std::memory_order_relaxed);
+  return got;
+}
+
+// The splits of a list with the shortest expected time, in tiles: waves of clusters, each of its tiles and about two more
+// (its start, its last softmax and its output), and with splits the join.
+int cut_of(int32_t batch, int32_t k) {
+  const int tiles = (k + NK - 1) / NK;
+  int best = 0;
+  double least = 0;
+  for (int n = 1; n <= MAX_SPLIT && n <= tiles; n *= 2) {
+    const int held = resident(n);
+    if (held < 1) continue;
+    const double cost = (double)((batch + held - 1) / held) * ((tiles + n - 1) / n + 2 + (n > 1 ? 1 : 0));
+    if (best == 0 || cost < least) least = cost, best = n;
+  }
+  return best;
 }
 
 int launch(hs_pool* p, int32_t batch, const void* q, const int32_t* idx, int32_t k, const RowSource& src, float sm_scale,
            void* out, int32_t out_type, float* lse, hs_stream_t stream) {
   Decode4Args a;
   std::memset(&a, 0, sizeof(a));
+  a.nsplit = cut_of(batch, k);
+  if (a.nsplit < 1) return HS_ERR_UNSUPPORTED;
   a.q = static_cast<const uint16_t*>(q);
   a.idx = idx;
   a.k = k;
@@ -112,15 +720,21 @@ int launch(hs_pool* p, int32_t batch, const void* q, const int32_t* idx, int32_t
   a.out = out;
   a.out_f32 = out_type == HS_TYPE_F32;
   a.lse = lse;
+  a.err = p->err;
+  hs_attention_waits(&a.wait_limit, &a.stall);
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)batch * (HEADS / GH), 1, 1);
+  cfg.gridDim = dim3((unsigned)(2 * a.nsplit) * (unsigned)batch, 1, 1);
   cfg.blockDim = dim3(THREADS, 1, 1);
+  cfg.dynamicSmemBytes = SMEM_BYTES;
   cfg.stream = reinterpret_cast<cudaStream_t>(stream);
-  cudaLaunchAttribute attr;
-  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr.val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = (unsigned)(2 * a.nsplit);
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
   return hs_launched(cudaLaunchKernelEx(&cfg, hs_decode4_kernel, a));
 }
 
