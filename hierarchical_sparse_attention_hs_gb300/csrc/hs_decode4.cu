@@ -25,10 +25,9 @@
 //
 // Warp roles per CTA: 0-7 softmax (warp w: TMEM lanes 32 (w % 4) .. +31, that is head lane % 64 and half lane / 64 of the
 // tile's rows, and rows 64 (w / 4) .. +63 of that half), 8 the issuer (the pair's first CTA issues for both), 9-15 the
-// loaders. K and V pass through one ring of 16 KB stages in the order in which the MMAs read them, a loader for each
-// slot: a K stage is 64 columns of the CTA's 128 rows, a V stage 128 of its value columns of 64 rows, both 128 rows of
-// 128 bytes, 128-byte swizzle; each feeds four MMAs, 256 cycles. A lane unpacks four of them; its next stage's words are
-// under way as soon as it has unpacked the ones before.
+// loaders. K and V pass through one ring of 16 KB stages in the order in which the MMAs read them: a K stage
+// is 64 columns of the CTA's 128 rows, a V stage 128 of its value columns of 64 rows, both 128 rows of 128 bytes, 128-byte
+// swizzle; each feeds four MMAs, 256 cycles. The loaders take turns at jobs of 64 rows by 128 columns.
 //
 // Waits are bounded: on running out a role sets the abort flag, which ends every role, and the HS_DEVERR_TIMEOUT bit.
 
@@ -76,9 +75,9 @@ constexpr int OFF_RED = (OFF_MISC + 12 + 15) & ~15;     // [2 parities][NSEG][QH
 constexpr int OFF_QINV = OFF_RED + 2 * NSEG * QH * 4;   // [QH]: what the score of a head is multiplied by to undo its query's scale
 constexpr int OFF_ML = OFF_QINV + QH * 4;               // [QH] (m, l) of a split
 constexpr int SMEM_BYTES = OFF_ML + QH * 8;
-static_assert(NSTAGE <= KBLK, "the ring starts within the first K");
 static_assert(SMEM_BYTES <= 232448, "shared memory per block");
-constexpr int SOFTMAX_WARPS = 8, MMA_WARP = 8, LOAD_WARP0 = 9, THREADS = (LOAD_WARP0 + NSTAGE) * 32;
+constexpr int SOFTMAX_WARPS = 8, MMA_WARP = 8, LOAD_WARP0 = 9, LOADERS = 7, THREADS = (LOAD_WARP0 + LOADERS) * 32;
+constexpr int KJOBS = KBLK + 1;    // a loader's jobs of a K
 static_assert(THREADS <= 512, "128 registers a thread");
 constexpr uint32_t TMEM_COLS = 512, TMEM_O = 0, TMEM_S = 256;  // O: 2 x 128 columns; S: two buffers of 128
 // A CTA's outputs take the place of Q and the ring: rows of a head, 16 bytes apart beyond their own size (no bank conflicts).
@@ -112,9 +111,9 @@ __device__ __forceinline__ uint4 ld16(const uint8_t* p) {
   asm volatile("ld.global.cg.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
   return v;
 }
-__device__ __forceinline__ uint32_t ld4(const uint8_t* p) {
-  uint32_t v;
-  asm volatile("ld.global.cg.u32 %0, [%1];" : "=r"(v) : "l"(p));
+__device__ __forceinline__ uint32_t ld2(const uint8_t* p) {
+  uint16_t v;
+  asm volatile("ld.global.cg.u16 %0, [%1];" : "=h"(v) : "l"(p));
   return v;
 }
 __device__ __forceinline__ float4 ld_peer(uint32_t addr) {
@@ -136,42 +135,41 @@ struct Tiles {
   int last_segs;     // segments of its last tile
   __device__ __forceinline__ int segs(int t) const { return t == n - 1 ? last_segs : NSEG; }
 };
+// A loader's way through the jobs of that order. A job is 64 rows of 128 columns (K: half of two stages; V: a stage), or of
+// the rotary key (half of K's last stage): ten jobs of a K, two of each segment of a V.
 struct Order {
-  int kt = 0, vt = 0, c;  // the tile whose K is next or under way, the one whose V is; the stage's place within K or V
+  int kt = 0, vt = 0, c;  // the tile whose K is next or under way, the one whose V is; the job's place within K or V
+  int stage = 0;          // the number of K's or V's first stage
   bool is_k = true;
   __device__ __forceinline__ bool settle(const Tiles& t) {
     for (;;) {
-      const int end = is_k ? KBLK : 2 * t.segs(vt);
+      const int end = is_k ? KJOBS : 2 * t.segs(vt);
       if (c < end) return true;
       c -= end;
       if (is_k) {
+        stage += KBLK;
         is_k = kt == 0 && t.n > 1;
         ++kt;
       } else {
+        stage += end;
         if (++vt == t.n) return false;
         is_k = kt < t.n;
       }
     }
   }
+  __device__ __forceinline__ bool is_rope() const { return is_k && c >= KJOBS - 2; }
 };
-// A lane's four rows of a stage: 64 latents each (32 bytes and four scales) of the K half's rows lane, lane + 32, .., or of
-// rows lane and lane + 32 of a V segment, first one block of 64 columns, then the next.
-struct Quad {
-  uint4 a[4], b[4];
-  uint32_t s[4];
-};
-// 64 latents, unpacked, into row `row` of a stage.
-__device__ __forceinline__ void unpack(uint8_t* stage, int row, uint4 a, uint4 b, uint32_t scales) {
-  const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-  uint8_t* const dst = stage + row * 128;
+// 32 latents of a row, unpacked into four of the eight 16-byte chunks of a stage's row: chunks ch .. ch + 3.
+__device__ __forceinline__ void unpack(uint8_t* row, int swizzle, int ch, uint4 codes, uint32_t scales) {
+  const uint32_t w[4] = {codes.x, codes.y, codes.z, codes.w};
 #pragma unroll
-  for (int g = 0; g < 4; ++g) {
+  for (int g = 0; g < 2; ++g) {
     Int4Scale k;
     k.set(scales >> (8 * g) & 255u);
 #pragma unroll
     for (int i = 2 * g; i < 2 * g + 2; ++i) {
       const __half2 h[4] = {int4_pair<0>(w[i], k), int4_pair<1>(w[i], k), int4_pair<0>(w[i] >> 8, k), int4_pair<1>(w[i] >> 8, k)};
-      *reinterpret_cast<uint4*>(dst + ((i ^ (row & 7)) << 4)) = *reinterpret_cast<const uint4*>(h);
+      *reinterpret_cast<uint4*>(row + (((ch + i) ^ swizzle) << 4)) = *reinterpret_cast<const uint4*>(h);
     }
   }
 }
@@ -192,7 +190,7 @@ __global__ void __launch_bounds__(THREADS, 1) hs_decode4_kernel(const Decode4Arg
     for (int i = 0; i < NBAR; ++i) bar_init(bar + i, 1);
     // one arrival for each softmax warp of the pair, for each of its two loaders of a slot
     bar_init(bar + B_QFULL, 2 * SOFTMAX_WARPS);
-    for (int i = 0; i < NSTAGE; ++i) bar_init(bar + B_FULL + i, 2);
+    for (int i = 0; i < NSTAGE; ++i) bar_init(bar + B_FULL + i, 4);
     for (int i = 0; i < 2; ++i) bar_init(bar + B_SFREE + i, 2 * SOFTMAX_WARPS);
     bar_init(bar + B_PFULL, 2 * SOFTMAX_WARPS);
     for (int i = 0; i < 2; ++i) bar_init(bar + B_MX + i, NSEG);  // the warps that hold the same heads
@@ -280,95 +278,107 @@ __global__ void __launch_bounds__(THREADS, 1) hs_decode4_kernel(const Decode4Arg
     }
     __syncwarp();
   } else if (warp >= LOAD_WARP0) {
-    // ---- the loader of ring slot s: every NSTAGE-th stage of the split's order.
+    // ---- a loader: every LOADERS-th job. Eight lanes hold eight rows, four such groups 32 columns each (16 bytes of codes, two
+    //      scales): a load instruction then touches eight rows' lines, not 32, and stores have no bank conflicts. The next
+    //      job's words are under way as soon as this job's are unpacked.
     ok = !a.stall || __all_sync(0xffffffffu, bar_wait(bar + B_STALL, 0, abort_flag, lim));
-    const int s = warp - LOAD_WARP0;
-    uint8_t* const stage = smem + OFF_RING + s * STAGE_BYTES;
-    const uint32_t full = lead + (B_FULL + s) * 8;
+    const int r8 = lane & 7, qd = lane >> 3;
     Order o;
-    o.c = s;
-    bool more_stages = o.settle(tiles);
-    int32_t e[4];               // the entries of the stage after the one that is unpacked
-    const uint8_t* row[4];
-    Quad w;
-    // the list's entries of a stage's rows
+    o.c = warp - LOAD_WARP0;
+    bool more_jobs = o.settle(tiles);
+    int32_t e[2];                     // the list's entries of the next job's rows: lane and lane + 32
+    unsigned long long row[2] = {};   // and where they are
+    uint4 w[8];
+    uint32_t sc[8];
     auto fetch = [&](const Order& x) {
-      const int base = (tiles.first + (x.is_k ? x.kt : x.vt)) * NK + (x.is_k ? (int)rank * KH : (x.c >> 1) * SEG) + lane;
+      const int base = (tiles.first + (x.is_k ? x.kt : x.vt)) * NK + (x.is_k ? (int)rank * KH + (x.c & 1) * 64 : (x.c >> 1) * SEG) + lane;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int key = base + 32 * i;
-        if (x.is_k || i < 2) e[i] = key < a.k ? ld_fresh(list + key) : -1;
-      }
-      if (!x.is_k) e[2] = e[0], e[3] = e[1];
+      for (int i = 0; i < 2; ++i) e[i] = base + 32 * i < a.k ? ld_fresh(list + base + 32 * i) : -1;
     };
     auto find = [&]() {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) row[i] = row_at(a.src, b, e[i], ROW_INT4);
+      for (int i = 0; i < 2; ++i) row[i] = reinterpret_cast<unsigned long long>(row_at(a.src, b, e[i], ROW_INT4));
     };
-    // row i's words of a stage of latents
+    // the lane's words of row 8 i + r8 of a job of latents
     auto load = [&](const Order& x, int i) {
-      const int blk = x.is_k ? x.c : (int)rank * (DVH / 64) + (x.c & 1) * 2 + (i >> 1);
-      if (row[i]) {
-        w.a[i] = ld16(row[i] + 32 * blk);
-        w.b[i] = ld16(row[i] + 32 * blk + 16);
-        w.s[i] = ld4(row[i] + INT4_SCALES + 4 * blk);
-      } else {
-        w.a[i] = w.b[i] = make_uint4(0, 0, 0, 0);
-        w.s[i] = 0;
+      const int col = x.is_k ? (x.c >> 1) * 128 : (int)rank * DVH + (x.c & 1) * 128;
+      const uint8_t* const p = reinterpret_cast<const uint8_t*>(__shfl_sync(0xffffffffu, row[i >> 2], (8 * i + r8) & 31));
+      w[i] = make_uint4(0, 0, 0, 0);
+      sc[i] = 0;
+      if (p) {
+        w[i] = ld16(p + col / 2 + 16 * qd);
+        sc[i] = ld2(p + INT4_SCALES + col / INT4_BLOCK + 2 * qd);
       }
     };
-    auto is_rope = [](const Order& x) { return x.is_k && x.c == KBLK - 1; };
-    if (more_stages && ok) {
+    if (more_jobs && ok) {
       fetch(o);
       find();
-      if (!is_rope(o)) {
+      if (!o.is_rope()) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) load(o, i);
+        for (int i = 0; i < 8; ++i) load(o, i);
       }
     }
-    unsigned ph = 1;  // a barrier that has not completed a phase passes for the parity before its first
-    while (more_stages && ok) {
+    while (more_jobs && ok) {
       Order nx = o;
-      nx.c += NSTAGE;
+      nx.c += LOADERS;
       const bool more_after = nx.settle(tiles);
       if (more_after) fetch(nx);
-      ok = __all_sync(0xffffffffu, bar_wait(bar + B_EMPTY + s, ph, abort_flag, lim));  // the MMAs that read the slot have finished
+      // the job's stages, free once the MMAs that read them have finished (a barrier that has not completed a phase passes
+      // for the parity before its first)
+      const int n0 = o.stage + (o.is_k ? o.c & ~1 : o.c), s0 = n0 % NSTAGE, s1 = (n0 + 1) % NSTAGE;
+      const bool rope = o.is_rope(), two = o.is_k && !rope;
+      const int sr = rope ? (o.stage + KBLK - 1) % NSTAGE : s0;
+      ok = bar_wait(bar + B_EMPTY + sr, (unsigned)((rope ? o.stage + KBLK - 1 : n0) / NSTAGE & 1) ^ 1u, abort_flag, lim);
+      if (two) ok = ok && bar_wait(bar + B_EMPTY + s1, (unsigned)((n0 + 1) / NSTAGE & 1) ^ 1u, abort_flag, lim);
+      ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
-      ph ^= 1u;
-      if (is_rope(o)) {
+      if (rope) {
         // the rotary keys as they are, 16 bytes a copy, eight lanes a row
-#pragma unroll 4
-        for (int it = 0; it < 32; ++it) {
-          const int r = 4 * it + (lane >> 3), j = lane & 7;
-          const unsigned long long p0 = reinterpret_cast<unsigned long long>(it < 16 ? (it < 8 ? row[0] : row[1]) : (it < 24 ? row[2] : row[3]));
-          const uint8_t* const src = reinterpret_cast<const uint8_t*>(__shfl_sync(0xffffffffu, p0, r & 31));
-          uint8_t* const dst = stage + r * 128 + ((j ^ (r & 7)) << 4);
-          if (src)
-            asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(su32(dst)), "l"(src + INT4_ROPE + 16 * j) : "memory");
+        uint8_t* const dst = smem + OFF_RING + sr * STAGE_BYTES + (o.c & 1) * BLK_BYTES;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          const int r = 4 * i + qd;
+          const unsigned long long p = __shfl_sync(0xffffffffu, row[i >> 3], r & 31);
+          uint8_t* const d = dst + r * 128 + ((r8 ^ (r & 7)) << 4);
+          if (p)
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(su32(d)), "l"(p + INT4_ROPE + 16 * r8) : "memory");
           else
-            *reinterpret_cast<uint4*>(dst) = make_uint4(0, 0, 0, 0);
+            *reinterpret_cast<uint4*>(d) = make_uint4(0, 0, 0, 0);
         }
         asm volatile("cp.async.commit_group;" ::: "memory");
-        if (more_after) find();
         if (more_after) {
+          find();
+          if (!nx.is_rope()) {
 #pragma unroll
-          for (int i = 0; i < 4; ++i) load(nx, i);
+            for (int i = 0; i < 8; ++i) load(nx, i);
+          }
         }
         asm volatile("cp.async.wait_group 0;" ::: "memory");
       } else {
-        const bool ahead = more_after && !is_rope(nx);
+        const bool ahead = more_after && !nx.is_rope();
         if (more_after) find();
+        // K: the upper 64 columns lie in the stage after; V: behind the lower 64
+        uint8_t* const dst = smem + OFF_RING + (two && qd >> 1 ? s1 : s0) * STAGE_BYTES +
+                             (two ? (o.c & 1) : qd >> 1) * BLK_BYTES + r8 * 128;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          unpack(stage, lane + 32 * i, w.a[i], w.b[i], w.s[i]);
+        for (int i = 0; i < 8; ++i) {
+          unpack(dst + i * 1024, r8, (qd & 1) * 4, w[i], sc[i]);
           if (ahead) load(nx, i);
         }
       }
       fence_proxy_async();
       __syncwarp();
-      if (lane == 0) arrive_lead(full);
+      if (lane == 0) {
+        // a stage is full with four arrivals: two for each CTA
+        if (o.is_k) {
+          arrive_lead(lead + (B_FULL + sr) * 8);
+          if (two) arrive_lead(lead + (B_FULL + s1) * 8);
+        } else {
+          arrive_lead(lead + (B_FULL + s0) * 8, 2);
+        }
+      }
       o = nx;
-      more_stages = more_after;
+      more_jobs = more_after;
     }
     __syncwarp();
   } else {
@@ -378,43 +388,47 @@ __global__ void __launch_bounds__(THREADS, 1) hs_decode4_kernel(const Decode4Arg
     uint8_t* const prows = smem + OFF_P + sg * BLK_BYTES + (q & 1) * 32 * 128;  // the warp's 32 rows of P
     const size_t head0 = (size_t)b * HEADS + rank * QH;                         // the CTA's first
     {
-      // Q: four threads a head, 18 chunks of eight values each (chunks 4 i + part: 64 of latents, 8 of the rotary part)
-      const int h = t >> 2, part = t & 3;
-      const uint8_t* const src = reinterpret_cast<const uint8_t*>(a.q + (head0 + h) * WIDTH);
+      // Q. A warp takes eight heads, 18 chunks of eight values a lane, one behind the other: eight neighbouring lanes hold
+      // chunks of one head (of its 72: 64 of latents, 8 of the rotary part), and share the largest magnitude among them.
+      const int h8 = warp * 8;
+      const uint8_t* const src = reinterpret_cast<const uint8_t*>(a.q + (head0 + h8) * WIDTH);
+      uint32_t* const top = reinterpret_cast<uint32_t*>(smem + OFF_ML) + h8;
       uint4 v[KBLK * 2];
-      uint32_t top = 0;
+      if (lane < 8) top[lane] = 0;
+      __syncwarp();
 #pragma unroll
-      for (int i = 0; i < KBLK * 2; ++i) v[i] = ld16(src + 16 * (4 * i + part));
+      for (int i = 0; i < KBLK * 2; ++i) v[i] = ld16(src + 16 * (32 * i + lane));
 #pragma unroll
       for (int i = 0; i < KBLK * 2; ++i) {
-        const uint32_t x[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+        const uint32_t x[4] = {v[i].x & 0x7fff7fffu, v[i].y & 0x7fff7fffu, v[i].z & 0x7fff7fffu, v[i].w & 0x7fff7fffu};
+        uint32_t m = __vmaxu2(__vmaxu2(x[0], x[1]), __vmaxu2(x[2], x[3]));
+        m = max(m & 0xffffu, m >> 16);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) top = max(top, max(x[j] & 0x7fffu, x[j] >> 16 & 0x7fffu));
+        for (int d = 4; d; d >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, d));
+        if ((lane & 7) == 0) atomicMax(top + (32 * i + lane) / (KBLK * 8), m);
       }
-      top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
-      top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
-      const int f = min(14 + 127 - (int)(top >> 7), 100);  // the largest value's exponent becomes 14
-      const float mul = __uint_as_float((uint32_t)(127 + f) << 23);
-      if (part == 0) qinv[h] = __uint_as_float((uint32_t)(127 - f) << 23) * UNSCALE;
+      __syncwarp();
+      if (lane < 8) {
+        const int f = min(14 + 127 - (int)(top[lane] >> 7), 100);  // the largest value's exponent becomes 14
+        qinv[h8 + lane] = __uint_as_float((uint32_t)(127 - f) << 23) * UNSCALE;
+        top[lane] = (uint32_t)(127 + f) << 23;
+      }
+      __syncwarp();
 #pragma unroll
       for (int i = 0; i < KBLK * 2; ++i) {
         const uint32_t x[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
         uint32_t y[4];
-        const int ch = 4 * i + part;
-        const bool rope = i >= 16;
-        const float m = rope ? mul * (1.f / UNSCALE) : mul;
+        const int h = (32 * i + lane) / (KBLK * 8), ch = 32 * i + lane - h * (KBLK * 8);
+        const bool rope = ch >= LATENT / 8;
+        const float m = __uint_as_float(top[h]) * (rope ? 1.f / UNSCALE : 1.f);
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           const float lo = __uint_as_float(x[j] << 16) * m, hi = __uint_as_float(x[j] & 0xffff0000u) * m;
-          if (rope) {
-            const __nv_bfloat162 p = __floats2bfloat162_rn(lo, hi);
-            y[j] = *reinterpret_cast<const uint32_t*>(&p);
-          } else {
-            const __half2 p = __floats2half2_rn(lo, hi);
-            y[j] = *reinterpret_cast<const uint32_t*>(&p);
-          }
+          const __nv_bfloat162 pr = __floats2bfloat162_rn(lo, hi);
+          const __half2 pl = __floats2half2_rn(lo, hi);
+          y[j] = rope ? *reinterpret_cast<const uint32_t*>(&pr) : *reinterpret_cast<const uint32_t*>(&pl);
         }
-        *reinterpret_cast<uint4*>(smem + OFF_Q + (ch >> 3) * BLK_BYTES + h * 128 + (((ch & 7) ^ (h & 7)) << 4)) =
+        *reinterpret_cast<uint4*>(smem + OFF_Q + (ch >> 3) * BLK_BYTES + (h8 + h) * 128 + (((ch & 7) ^ h) << 4)) =
             make_uint4(y[0], y[1], y[2], y[3]);
       }
       fence_proxy_async();

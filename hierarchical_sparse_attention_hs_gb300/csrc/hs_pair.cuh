@@ -35,6 +35,9 @@ __device__ __forceinline__ void commit2(uint64_t* b, uint32_t mask = 3) {
 __device__ __forceinline__ void arrive_lead(uint32_t addr) {
   asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
 }
+__device__ __forceinline__ void arrive_lead(uint32_t addr, uint32_t count) {
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0], %1;" ::"r"(addr), "r"(count) : "memory");
+}
 // One lane of a converged warp, the same at every call.
 __device__ __forceinline__ bool elect_one() {
   uint32_t p;
