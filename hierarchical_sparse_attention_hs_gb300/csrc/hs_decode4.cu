@@ -7,12 +7,10 @@
 // What bounds it. A row is 416 bytes and serves 2 * 128 * (576 + 512) operations, 670 a byte: the tensor cores, once a
 // launch is long enough; one decode step's lists are short, and most of its time is the chain of one launch.
 //
-// Operands. The rows' latents become halves, exactly (at 2^-6 of their value), written into shared memory by the loader
-// warps; the rotary key stays bf16, and the scores' MMAs change from one type to the other within a sum. A head's query is
-// multiplied by a power of two, so that its largest value lies in [2^14, 2^15): its latent part is then exact in halves, but
-// for values 2^-28 below that one, which are rounded to 2^-40 of it; the score's scale takes the power back. The weights
-// are rounded to halves, 2^-11 of each (2^-31 of the largest, for those far below it): an output is 0.00014 off by that in
-// the mean, a tenth of its own rounding to bf16.
+// Operands, all of them exact. For the scores the rows' latents become bf16, beside the queries and rotary keys that are; for
+// the value product they become halves, at 2^-6 of their value, beside weights in halves. Rounding the weights, 2^-11 of
+// each (2^-31 of the largest, for those far below it), leaves an output 0.00014 off in the mean, a tenth of its own rounding
+// to bf16; weights in bf16 would leave 0.0011.
 //
 // A pair of CTAs takes one request's 128 heads, 64 for each CTA, over one split of its list, 256 entries a tile, with MMAs
 // of M = 128, N = 256 that both run together (cta_group::2): for S = Q K^T each CTA holds its 64 heads of Q and 128 of the
@@ -39,6 +37,7 @@
 #include <atomic>
 #include <cstdint>
 #include <cstring>
+#include <type_traits>
 
 #include "../../include/hs.h"
 #include "hs_internal.hpp"
@@ -61,24 +60,25 @@ constexpr int NSEG = NK / SEG;
 constexpr int KBLK = WIDTH / 64;   // 64-column blocks of a row: K stages of a tile
 constexpr int BLK_BYTES = 64 * 128;      // 64 rows x 64 columns
 constexpr int STAGE_BYTES = 2 * BLK_BYTES;
-constexpr int NSTAGE = 7;          // stages of the ring
+constexpr int NSTAGE = 5;          // stages of the ring
 constexpr int OFF_Q = 0;
 constexpr int OFF_RING = OFF_Q + KBLK * BLK_BYTES;
 constexpr int OFF_P = OFF_RING + NSTAGE * STAGE_BYTES;
-constexpr int OFF_BAR = OFF_P + NSEG * BLK_BYTES;
-// mbarriers: qfull full[7] empty[7] sfull[2] sfree[2] pfull pdone drain stall mx[2]
+constexpr int SOFTMAX_WARPS = 8, MMA_WARP = 8, LOAD_WARP0 = 9, LOADERS = 7, THREADS = (LOAD_WARP0 + LOADERS) * 32;
+static_assert(THREADS <= 512, "128 registers a thread");
+constexpr int KJOBS = KBLK + 1;    // a loader's jobs of a K
+constexpr int RAW_CODES = 64 * 64, RAW_SCALES = 64 * 8, RAW_BYTES = RAW_CODES + 2 * RAW_SCALES;  // a loader's rows as they are
+constexpr int OFF_RAW = OFF_P + NSEG * BLK_BYTES;
+constexpr int OFF_BAR = OFF_RAW + LOADERS * RAW_BYTES;
+// mbarriers: qfull full[] empty[] sfull[2] sfree[2] pfull pdone drain stall mx[2]
 constexpr int B_QFULL = 0, B_FULL = 1, B_EMPTY = B_FULL + NSTAGE, B_SFULL = B_EMPTY + NSTAGE,
               B_SFREE = B_SFULL + 2, B_PFULL = B_SFREE + 2, B_PDONE = B_PFULL + 1, B_DRAIN = B_PDONE + 1,
               B_STALL = B_DRAIN + 1, B_MX = B_STALL + 1, NBAR = B_MX + 2;
 constexpr int OFF_MISC = OFF_BAR + NBAR * 8;            // tensor-memory address, abort flag, the softmax warps' own
 constexpr int OFF_RED = (OFF_MISC + 12 + 15) & ~15;     // [2 parities][NSEG][QH] floats
-constexpr int OFF_QINV = OFF_RED + 2 * NSEG * QH * 4;   // [QH]: what the score of a head is multiplied by to undo its query's scale
-constexpr int OFF_ML = OFF_QINV + QH * 4;               // [QH] (m, l) of a split
+constexpr int OFF_ML = OFF_RED + 2 * NSEG * QH * 4;     // [QH] (m, l) of a split
 constexpr int SMEM_BYTES = OFF_ML + QH * 8;
 static_assert(SMEM_BYTES <= 232448, "shared memory per block");
-constexpr int SOFTMAX_WARPS = 8, MMA_WARP = 8, LOAD_WARP0 = 9, LOADERS = 7, THREADS = (LOAD_WARP0 + LOADERS) * 32;
-constexpr int KJOBS = KBLK + 1;    // a loader's jobs of a K
-static_assert(THREADS <= 512, "128 registers a thread");
 constexpr uint32_t TMEM_COLS = 512, TMEM_O = 0, TMEM_S = 256;  // O: 2 x 128 columns; S: two buffers of 128
 // A CTA's outputs take the place of Q and the ring: rows of a head, 16 bytes apart beyond their own size (no bank conflicts).
 constexpr int OUT_F32 = LATENT * 4 + 16, OUT_BF16 = LATENT * 2 + 16;
@@ -88,7 +88,6 @@ constexpr float P_SHIFT = 6.f;  // weights are kept at 2^6: their smallest half 
 constexpr float UNSCALE = 64.f;  // latents are kept at 2^-6
 
 struct Decode4Args {
-  const uint16_t* q;   // bf16 [batch][HEADS][WIDTH]
   const int32_t* idx;  // [batch][k]
   int32_t k;
   RowSource src;
@@ -105,16 +104,18 @@ struct Decode4Args {
 __host__ __device__ constexpr uint32_t idesc_f16(int m, int n, int a_mn, int b_mn) {
   return idesc_bf16(m, n, a_mn, b_mn) & ~(1u << 7 | 1u << 10);
 }
-// (volatile, as every load of what an earlier kernel may have written: they stay behind the launch wait)
-__device__ __forceinline__ uint4 ld16(const uint8_t* p) {
-  uint4 v;
-  asm volatile("ld.global.cg.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
-  return v;
+// 16 and 8 bytes into shared memory (volatile: behind the launch wait, like every load of what an earlier kernel may have
+// written).
+__device__ __forceinline__ void copy16(uint32_t dst, unsigned long long src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
-__device__ __forceinline__ uint32_t ld2(const uint8_t* p) {
-  uint16_t v;
-  asm volatile("ld.global.cg.u16 %0, [%1];" : "=h"(v) : "l"(p));
-  return v;
+__device__ __forceinline__ void copy8(uint32_t dst, unsigned long long src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copies_wait() {  // all but the last N groups
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 __device__ __forceinline__ float4 ld_peer(uint32_t addr) {
   float4 v;
@@ -159,28 +160,37 @@ struct Order {
   }
   __device__ __forceinline__ bool is_rope() const { return is_k && c >= KJOBS - 2; }
 };
-// 32 latents of a row, unpacked into four of the eight 16-byte chunks of a stage's row: chunks ch .. ch + 3.
+// 32 latents of a row, unpacked into four of the eight 16-byte chunks of a stage's row, from chunk ch on: as bf16 for the
+// scores, as halves at 2^-6 for the values.
+template <bool K>
 __device__ __forceinline__ void unpack(uint8_t* row, int swizzle, int ch, uint4 codes, uint32_t scales) {
   const uint32_t w[4] = {codes.x, codes.y, codes.z, codes.w};
 #pragma unroll
   for (int g = 0; g < 2; ++g) {
-    Int4Scale k;
-    k.set(scales >> (8 * g) & 255u);
+    const uint32_t code = g ? scales >> 8 : scales & 255u;
+    std::conditional_t<K, Int4Bf16, Int4Half> k;
+    k.set(code);
 #pragma unroll
     for (int i = 2 * g; i < 2 * g + 2; ++i) {
-      const __half2 h[4] = {int4_pair<0>(w[i], k), int4_pair<1>(w[i], k), int4_pair<0>(w[i] >> 8, k), int4_pair<1>(w[i] >> 8, k)};
-      *reinterpret_cast<uint4*>(row + (((ch + i) ^ swizzle) << 4)) = *reinterpret_cast<const uint4*>(h);
+      uint4 v;
+      if constexpr (K) {
+        const __nv_bfloat162 h[4] = {int4_pair(w[i], k), int4_pair(w[i] >> 4, k), int4_pair(w[i] >> 8, k), int4_pair(w[i] >> 12, k)};
+        v = *reinterpret_cast<const uint4*>(h);
+      } else {
+        const __half2 h[4] = {int4_pair<0>(w[i], k), int4_pair<1>(w[i], k), int4_pair<0>(w[i] >> 8, k), int4_pair<1>(w[i] >> 8, k)};
+        v = *reinterpret_cast<const uint4*>(h);
+      }
+      *reinterpret_cast<uint4*>(row + (((ch + i) ^ swizzle) << 4)) = v;
     }
   }
 }
 
-__global__ void __launch_bounds__(THREADS, 1) hs_decode4_kernel(const Decode4Args a) {
+__global__ void __launch_bounds__(THREADS, 1) hs_decode4_kernel(const Decode4Args a, const __grid_constant__ CUtensorMap qmap) {
   extern __shared__ __align__(1024) uint8_t smem[];
   uint64_t* const bar = reinterpret_cast<uint64_t*>(smem + OFF_BAR);
   volatile int* const abort_flag = reinterpret_cast<volatile int*>(smem + OFF_MISC + 4);
   volatile int* const out_stop = abort_flag + 1;
   float* const red = reinterpret_cast<float*>(smem + OFF_RED);
-  float* const qinv = reinterpret_cast<float*>(smem + OFF_QINV);
   const int t = threadIdx.x, lane = t & 31;
   const int warp = __shfl_sync(0xffffffffu, t >> 5, 0);  // the same in all lanes, and known to be
   const uint32_t crank = cluster_rank(), rank = crank & 1u, first = crank & ~1u;
@@ -188,8 +198,7 @@ __global__ void __launch_bounds__(THREADS, 1) hs_decode4_kernel(const Decode4Arg
 
   if (t == 0) {
     for (int i = 0; i < NBAR; ++i) bar_init(bar + i, 1);
-    // one arrival for each softmax warp of the pair, for each of its two loaders of a slot
-    bar_init(bar + B_QFULL, 2 * SOFTMAX_WARPS);
+    // one arrival for each softmax warp of the pair; two of each CTA for a stage
     for (int i = 0; i < NSTAGE; ++i) bar_init(bar + B_FULL + i, 4);
     for (int i = 0; i < 2; ++i) bar_init(bar + B_SFREE + i, 2 * SOFTMAX_WARPS);
     bar_init(bar + B_PFULL, 2 * SOFTMAX_WARPS);
@@ -224,7 +233,7 @@ __global__ void __launch_bounds__(THREADS, 1) hs_decode4_kernel(const Decode4Arg
     // ---- the issuer, of the pair's first CTA. The whole warp walks the loop, so that the descriptors stay in uniform
     //      registers; one lane issues: scores of tile g, then the value product of tile g - 1.
     if (rank == 0) {
-      constexpr uint32_t ID_S = idesc_f16(HEADS, NK, 0, 0), ID_R = idesc_bf16(HEADS, NK, 0, 0), ID_O = idesc_f16(HEADS, 256, 0, 1);
+      constexpr uint32_t ID_S = idesc_bf16(HEADS, NK, 0, 0), ID_O = idesc_f16(HEADS, 256, 0, 1);
       const bool leader = elect_one();
       const uint32_t both = 3u << first;
       const uint64_t dq = sdesc128(su32(smem + OFF_Q), 0), dp = sdesc128(su32(smem + OFF_P), 0),
@@ -253,7 +262,7 @@ __global__ void __launch_bounds__(THREADS, 1) hs_decode4_kernel(const Decode4Arg
             ok = wait(B_FULL + st, ph);
             tc_fence_after();
             if (ok) four(tmem + TMEM_S + (uint32_t)(g & 1) * KH, dq + (uint64_t)(c * (BLK_BYTES >> 4)),
-                         dk + (uint64_t)(st * (STAGE_BYTES >> 4)), 2, c < KBLK - 1 ? ID_S : ID_R, c != 0 ? 1u : 0u);
+                         dk + (uint64_t)(st * (STAGE_BYTES >> 4)), 2, ID_S, c != 0 ? 1u : 0u);
           }
           if (!ok) break;
           if (leader) commit2(bar + B_SFULL + (g & 1), both);
@@ -278,18 +287,27 @@ __global__ void __launch_bounds__(THREADS, 1) hs_decode4_kernel(const Decode4Arg
     }
     __syncwarp();
   } else if (warp >= LOAD_WARP0) {
-    // ---- a loader: every LOADERS-th job. Eight lanes hold eight rows, four such groups 32 columns each (16 bytes of codes, two
-    //      scales): a load instruction then touches eight rows' lines, not 32, and stores have no bank conflicts. The next
-    //      job's words are under way as soon as this job's are unpacked.
+    // ---- a loader: every LOADERS-th job. A job's rows come into the warp's own 64 x 64 bytes of codes (row r: 16-byte chunk j at
+    //      j ^ (r / 2 % 4)) and 64 x 8 of scales, and are unpacked from there, 32 rows at a time: eight lanes hold eight rows,
+    //      four such groups 32 columns each. The same half of the next job is under way as soon as this job's has been read (a
+    //      group of copies each, so that all but the last are done when the next half is due).
     ok = !a.stall || __all_sync(0xffffffffu, bar_wait(bar + B_STALL, 0, abort_flag, lim));
-    const int r8 = lane & 7, qd = lane >> 3;
+    const int r8 = lane & 7, qd = lane >> 3, wl = warp - LOAD_WARP0;
+    if (wl == 0 && lane == 0 && ok) {
+      if (rank == 0) bar_arrive_expect(bar + B_QFULL, 2 * KBLK * BLK_BYTES);
+      for (int i = 0; i < KBLK; i += 3)
+        tma_box(su32(smem + OFF_Q + i * BLK_BYTES), &qmap, i, (int)b * HEADS + (int)rank * QH, lead + B_QFULL * 8);
+    }
+    __syncwarp();
+    uint8_t* const raw = smem + OFF_RAW + wl * RAW_BYTES;
+    const uint8_t* const codes_at = raw + r8 * 64 + ((qd ^ (r8 >> 1 & 3)) << 4);
+    const uint32_t codes_to = su32(raw + (lane >> 2) * 64 + (((lane & 3) ^ (lane >> 3 & 3)) << 4));
     Order o;
-    o.c = warp - LOAD_WARP0;
+    o.c = wl;
     bool more_jobs = o.settle(tiles);
+    int parity = 0;                   // of the job: where its scales are
     int32_t e[2];                     // the list's entries of the next job's rows: lane and lane + 32
     unsigned long long row[2] = {};   // and where they are
-    uint4 w[8];
-    uint32_t sc[8];
     auto fetch = [&](const Order& x) {
       const int base = (tiles.first + (x.is_k ? x.kt : x.vt)) * NK + (x.is_k ? (int)rank * KH + (x.c & 1) * 64 : (x.c >> 1) * SEG) + lane;
 #pragma unroll
@@ -299,71 +317,105 @@ __global__ void __launch_bounds__(THREADS, 1) hs_decode4_kernel(const Decode4Arg
 #pragma unroll
       for (int i = 0; i < 2; ++i) row[i] = reinterpret_cast<unsigned long long>(row_at(a.src, b, e[i], ROW_INT4));
     };
-    // the lane's words of row 8 i + r8 of a job of latents
-    auto load = [&](const Order& x, int i) {
-      const int col = x.is_k ? (x.c >> 1) * 128 : (int)rank * DVH + (x.c & 1) * 128;
-      const uint8_t* const p = reinterpret_cast<const uint8_t*>(__shfl_sync(0xffffffffu, row[i >> 2], (8 * i + r8) & 31));
-      w[i] = make_uint4(0, 0, 0, 0);
-      sc[i] = 0;
-      if (p) {
-        w[i] = ld16(p + col / 2 + 16 * qd);
-        sc[i] = ld2(p + INT4_SCALES + col / INT4_BLOCK + 2 * qd);
+    auto first_col = [&](const Order& x) { return x.is_k ? (x.c >> 1) * 128 : (int)rank * DVH + (x.c & 1) * 128; };
+    // the scales of a job's rows: zeros without a row, whose numbers may then be anything
+    auto get_scales = [&](int col, int par) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        uint8_t* const d = raw + RAW_CODES + par * RAW_SCALES + (lane + 32 * i) * 8;
+        if (row[i])
+          copy8(su32(d), row[i] + INT4_SCALES + col / INT4_BLOCK);
+        else
+          *reinterpret_cast<uint2*>(d) = make_uint2(0, 0);
+      }
+    };
+    // the codes of 32 rows, four lanes a row
+    auto get_codes = [&](int col, int h) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const unsigned long long p = __shfl_sync(0xffffffffu, h ? row[1] : row[0], 8 * i + (lane >> 2));
+        if (p) copy16(codes_to + h * 2048 + i * 512, p + col / 2 + 16 * (lane & 3));
+      }
+    };
+    auto get_job = [&](const Order& x, bool there, int par) {
+      if (there) get_scales(first_col(x), par);
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        if (there) get_codes(first_col(x), h);
+        copies_commit();
+      }
+    };
+    // Waits until the MMAs that read stage x have finished. A barrier's parity tells its last two phases apart, so a wait for
+    // stage x needs that of the stage before in the same slot to be known.
+    int known = -1;
+    auto need = [&](int x) {
+      while (x > known && ok) {
+        const int y = min(x, known + NSTAGE);
+        ok = __all_sync(0xffffffffu, bar_wait(bar + B_EMPTY + y % NSTAGE, (unsigned)(y / NSTAGE) & 1u, abort_flag, lim));
+        known = y;
       }
     };
     if (more_jobs && ok) {
       fetch(o);
       find();
-      if (!o.is_rope()) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) load(o, i);
-      }
+      get_job(o, !o.is_rope(), parity);
     }
     while (more_jobs && ok) {
       Order nx = o;
       nx.c += LOADERS;
-      const bool more_after = nx.settle(tiles);
+      const bool more_after = nx.settle(tiles), ahead = more_after && !nx.is_rope();
       if (more_after) fetch(nx);
-      // the job's stages, free once the MMAs that read them have finished (a barrier that has not completed a phase passes
-      // for the parity before its first)
-      const int n0 = o.stage + (o.is_k ? o.c & ~1 : o.c), s0 = n0 % NSTAGE, s1 = (n0 + 1) % NSTAGE;
+      const int next_col = first_col(nx);
       const bool rope = o.is_rope(), two = o.is_k && !rope;
-      const int sr = rope ? (o.stage + KBLK - 1) % NSTAGE : s0;
-      ok = bar_wait(bar + B_EMPTY + sr, (unsigned)((rope ? o.stage + KBLK - 1 : n0) / NSTAGE & 1) ^ 1u, abort_flag, lim);
-      if (two) ok = ok && bar_wait(bar + B_EMPTY + s1, (unsigned)((n0 + 1) / NSTAGE & 1) ^ 1u, abort_flag, lim);
-      ok = __all_sync(0xffffffffu, ok);
+      const int n0 = o.stage + (rope ? KBLK - 1 : o.is_k ? o.c & ~1 : o.c), n1 = n0 + (two ? 1 : 0);
+      const int s0 = n0 % NSTAGE, s1 = n1 % NSTAGE;
+      need(n1 - NSTAGE);
       if (!ok) break;
       if (rope) {
         // the rotary keys as they are, 16 bytes a copy, eight lanes a row
-        uint8_t* const dst = smem + OFF_RING + sr * STAGE_BYTES + (o.c & 1) * BLK_BYTES;
-#pragma unroll
+        uint8_t* const dst = smem + OFF_RING + s0 * STAGE_BYTES + (o.c & 1) * BLK_BYTES;
+#pragma unroll 4
         for (int i = 0; i < 16; ++i) {
           const int r = 4 * i + qd;
-          const unsigned long long p = __shfl_sync(0xffffffffu, row[i >> 3], r & 31);
+          const unsigned long long p = __shfl_sync(0xffffffffu, i < 8 ? row[0] : row[1], r & 31);
           uint8_t* const d = dst + r * 128 + ((r8 ^ (r & 7)) << 4);
           if (p)
-            asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(su32(d)), "l"(p + INT4_ROPE + 16 * r8) : "memory");
+            copy16(su32(d), p + INT4_ROPE + 16 * r8);
           else
             *reinterpret_cast<uint4*>(d) = make_uint4(0, 0, 0, 0);
         }
-        asm volatile("cp.async.commit_group;" ::: "memory");
-        if (more_after) {
-          find();
-          if (!nx.is_rope()) {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) load(nx, i);
-          }
-        }
-        asm volatile("cp.async.wait_group 0;" ::: "memory");
+        copies_commit();
+        if (more_after) find();
+        get_job(nx, ahead, parity ^ 1);
+        copies_wait<2>();
       } else {
-        const bool ahead = more_after && !nx.is_rope();
         if (more_after) find();
         // K: the upper 64 columns lie in the stage after; V: behind the lower 64
-        uint8_t* const dst = smem + OFF_RING + (two && qd >> 1 ? s1 : s0) * STAGE_BYTES +
-                             (two ? (o.c & 1) : qd >> 1) * BLK_BYTES + r8 * 128;
+        uint8_t* const dst = smem + OFF_RING + (qd >> 1 ? s1 : s0) * STAGE_BYTES + (two ? (o.c & 1) : qd >> 1) * BLK_BYTES + r8 * 128;
+        const uint8_t* const scales_at = raw + RAW_CODES + parity * RAW_SCALES + r8 * 8 + 2 * qd;
+        if (ahead) get_scales(next_col, parity ^ 1);
+        auto half = [&](auto is_k, int h) {
+          copies_wait<1>();
+          __syncwarp();
+          uint4 c[4];
+          uint32_t sc[4];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          unpack(dst + i * 1024, r8, (qd & 1) * 4, w[i], sc[i]);
-          if (ahead) load(nx, i);
+          for (int i = 0; i < 4; ++i) {
+            c[i] = *reinterpret_cast<const uint4*>(codes_at + h * 2048 + i * 512);
+            sc[i] = *reinterpret_cast<const uint16_t*>(scales_at + h * 256 + i * 64);
+          }
+          __syncwarp();
+          if (ahead) get_codes(next_col, h);
+          copies_commit();
+#pragma unroll
+          for (int i = 0; i < 4; ++i) unpack<decltype(is_k)::value>(dst + h * 4096 + i * 1024, r8, (qd & 1) * 4, c[i], sc[i]);
+        };
+        if (o.is_k) {
+#pragma unroll 1
+          for (int h = 0; h < 2; ++h) half(std::true_type{}, h);
+        } else {
+#pragma unroll 1
+          for (int h = 0; h < 2; ++h) half(std::false_type{}, h);
         }
       }
       fence_proxy_async();
@@ -371,7 +423,7 @@ __global__ void __launch_bounds__(THREADS, 1) hs_decode4_kernel(const Decode4Arg
       if (lane == 0) {
         // a stage is full with four arrivals: two for each CTA
         if (o.is_k) {
-          arrive_lead(lead + (B_FULL + sr) * 8);
+          arrive_lead(lead + (B_FULL + s0) * 8);
           if (two) arrive_lead(lead + (B_FULL + s1) * 8);
         } else {
           arrive_lead(lead + (B_FULL + s0) * 8, 2);
@@ -379,7 +431,9 @@ __global__ void __launch_bounds__(THREADS, 1) hs_decode4_kernel(const Decode4Arg
       }
       o = nx;
       more_jobs = more_after;
+      parity ^= 1;
     }
+    copies_wait<0>();
     __syncwarp();
   } else {
     // ---- softmax: a thread holds head r of this CTA and 64 rows of every tile, segment sg
@@ -387,54 +441,6 @@ __global__ void __launch_bounds__(THREADS, 1) hs_decode4_kernel(const Decode4Arg
     const uint32_t trow = tmem + ((uint32_t)(q * 32) << 16);
     uint8_t* const prows = smem + OFF_P + sg * BLK_BYTES + (q & 1) * 32 * 128;  // the warp's 32 rows of P
     const size_t head0 = (size_t)b * HEADS + rank * QH;                         // the CTA's first
-    {
-      // Q. A warp takes eight heads, 18 chunks of eight values a lane, one behind the other: eight neighbouring lanes hold
-      // chunks of one head (of its 72: 64 of latents, 8 of the rotary part), and share the largest magnitude among them.
-      const int h8 = warp * 8;
-      const uint8_t* const src = reinterpret_cast<const uint8_t*>(a.q + (head0 + h8) * WIDTH);
-      uint32_t* const top = reinterpret_cast<uint32_t*>(smem + OFF_ML) + h8;
-      uint4 v[KBLK * 2];
-      if (lane < 8) top[lane] = 0;
-      __syncwarp();
-#pragma unroll
-      for (int i = 0; i < KBLK * 2; ++i) v[i] = ld16(src + 16 * (32 * i + lane));
-#pragma unroll
-      for (int i = 0; i < KBLK * 2; ++i) {
-        const uint32_t x[4] = {v[i].x & 0x7fff7fffu, v[i].y & 0x7fff7fffu, v[i].z & 0x7fff7fffu, v[i].w & 0x7fff7fffu};
-        uint32_t m = __vmaxu2(__vmaxu2(x[0], x[1]), __vmaxu2(x[2], x[3]));
-        m = max(m & 0xffffu, m >> 16);
-#pragma unroll
-        for (int d = 4; d; d >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, d));
-        if ((lane & 7) == 0) atomicMax(top + (32 * i + lane) / (KBLK * 8), m);
-      }
-      __syncwarp();
-      if (lane < 8) {
-        const int f = min(14 + 127 - (int)(top[lane] >> 7), 100);  // the largest value's exponent becomes 14
-        qinv[h8 + lane] = __uint_as_float((uint32_t)(127 - f) << 23) * UNSCALE;
-        top[lane] = (uint32_t)(127 + f) << 23;
-      }
-      __syncwarp();
-#pragma unroll
-      for (int i = 0; i < KBLK * 2; ++i) {
-        const uint32_t x[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
-        uint32_t y[4];
-        const int h = (32 * i + lane) / (KBLK * 8), ch = 32 * i + lane - h * (KBLK * 8);
-        const bool rope = ch >= LATENT / 8;
-        const float m = __uint_as_float(top[h]) * (rope ? 1.f / UNSCALE : 1.f);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const float lo = __uint_as_float(x[j] << 16) * m, hi = __uint_as_float(x[j] & 0xffff0000u) * m;
-          const __nv_bfloat162 pr = __floats2bfloat162_rn(lo, hi);
-          const __half2 pl = __floats2half2_rn(lo, hi);
-          y[j] = rope ? *reinterpret_cast<const uint32_t*>(&pr) : *reinterpret_cast<const uint32_t*>(&pl);
-        }
-        *reinterpret_cast<uint4*>(smem + OFF_Q + (ch >> 3) * BLK_BYTES + (h8 + h) * 128 + (((ch & 7) ^ h) << 4)) =
-            make_uint4(y[0], y[1], y[2], y[3]);
-      }
-      fence_proxy_async();
-      named_sync(1, SOFTMAX_WARPS * 32);
-      if (lane == 0) arrive_lead(lead + B_QFULL * 8);
-    }
     float m_run = -INFINITY, l_run = 0.f;
     int nx = 0;  // exchanges
     // hands `v` to the other three threads of the head
@@ -448,8 +454,7 @@ __global__ void __launch_bounds__(THREADS, 1) hs_decode4_kernel(const Decode4Arg
       return share + r;
     };
     const bool up = a.scale_log2 > 0.f;
-    const float factor = a.scale_log2 * qinv[r];  // of this head's scores
-    const float scale = up ? factor : 1.f;        // the maximum is taken before a positive scale; another is applied first
+    const float factor = a.scale_log2, scale = up ? factor : 1.f;  // the maximum is taken before a positive scale; another is applied first
     int32_t e0, e1;                               // the thread's entries of the tile's mask: rows lane and lane + 32 of its segment
     auto entries = [&](int tile) {
       const int key = (tiles.first + tile) * NK + sg * SEG + lane;
@@ -617,7 +622,11 @@ __global__ void __launch_bounds__(THREADS, 1) hs_decode4_kernel(const Decode4Arg
     for (const uint64_t t0 = now_ns(); !drained && now_ns() - t0 < WAIT_NS;) drained = bar_test(bar + B_DRAIN, 0);
     if (!drained) *abort_flag = 1;
     __syncwarp();
-    if (*abort_flag && lane == 0) atomicOr(a.err, HS_DEVERR_TIMEOUT);
+    if (*abort_flag) {
+      // a wait ran out: let the copies in flight land before the shared memory goes, and report
+      for (int i = 0; i < 50; ++i) __nanosleep(1000);
+      if (lane == 0) atomicOr(a.err, HS_DEVERR_TIMEOUT);
+    }
     __syncwarp();
   }
   cluster_sync();
@@ -726,7 +735,6 @@ int launch(hs_pool* p, int32_t batch, const void* q, const int32_t* idx, int32_t
   std::memset(&a, 0, sizeof(a));
   a.nsplit = cut_of(batch, k);
   if (a.nsplit < 1) return HS_ERR_UNSUPPORTED;
-  a.q = static_cast<const uint16_t*>(q);
   a.idx = idx;
   a.k = k;
   a.src = src;
@@ -736,6 +744,10 @@ int launch(hs_pool* p, int32_t batch, const void* q, const int32_t* idx, int32_t
   a.lse = lse;
   a.err = p->err;
   hs_attention_waits(&a.wait_limit, &a.stall);
+  CUtensorMap qmap;
+  const EncodeFn encode = encoder();
+  if (!encode) return HS_ERR_UNSUPPORTED;
+  if (!make_map(encode, &qmap, q, (uint64_t)batch * HEADS, QH, 3)) return HS_ERR_INVALID_ARG;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(2 * a.nsplit) * (unsigned)batch, 1, 1);
   cfg.blockDim = dim3(THREADS, 1, 1);
@@ -749,7 +761,7 @@ int launch(hs_pool* p, int32_t batch, const void* q, const int32_t* idx, int32_t
   attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  return hs_launched(cudaLaunchKernelEx(&cfg, hs_decode4_kernel, a));
+  return hs_launched(cudaLaunchKernelEx(&cfg, hs_decode4_kernel, a, qmap));
 }
 
 // HS_OK, or what the call is refused with; *empty for one that has nothing to do.

@@ -10,13 +10,15 @@
 // 2.8 cycles an SM for a warp's pairs (measured), ten times the two instructions below. q has 3 bits and s 4: the product
 // is exact in bf16 and in f16, so all readers of a row see the same numbers, none of them rounded.
 //
-// Arithmetic in halves, at 2^-6 of the value (so that nothing below leaves their range): two numbers at bits 0 and 16 under
-// the exponent of 1024 are 1024 + q + 8, at bits 4 and 20 under that of 64 they are 64 + q + 8 (q + 8 shifted left by four
-// counts 16 / 1024 of 64); fma(x, s, -1032 s) and fma(x, s, -72 s) leave q s. Every term is exact: 1032 = 129 * 8 and 72 =
-// 9 * 8, with four bits of s at most 11 bits; s <= 3840 keeps 1032 * 2^-6 s below 65504, and the smallest, 2^-17 * 2^-6, is a
-// multiple of 2^-24.
+// In halves, at 2^-6 of the value (so that nothing below leaves their range): two numbers at bits 0 and 16 under the exponent
+// of 16 are 16 + (q + 8) / 64, at bits 4 and 20 under that of 1 they are 1 + (q + 8) / 64; fma(x, s, -16.125 s) and fma(x, s,
+// -1.125 s) leave q s / 64. Every term is exact: 16.125 = 129 / 8 and 1.125 = 9 / 8, with four bits of s at most 11 bits; s <=
+// 3840 keeps 16.125 s below 65504, and the smallest, 2^-17 * 2^-6, is a multiple of 2^-24. In bf16, at the value itself: under
+// the exponent of 128 they are 128 + q + 8 (the four bits have to lie at bits 0 and 16), and fma(x, s, -136 s) leaves q s; 136
+// = 17 * 8, and 17 times four bits of s has 8.
 #pragma once
 
+#include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
@@ -48,22 +50,40 @@ __device__ __forceinline__ float int4_scale(uint32_t code) {
   return __half2float(__ushort_as_half((unsigned short)(code << 7)));
 }
 
-// Two scales' worth of constants, in both halves: 2^-6 s, and what takes the offsets of the two places out.
-struct Int4Scale {
+// (w & mask) | magic in one instruction, which takes one of the two from a register: written out as an expression it became
+// two, and the unpacking of a row a third slower.
+__device__ __forceinline__ uint32_t and_or(uint32_t w, uint32_t mask, uint32_t magic) {
+  uint32_t x;
+  asm("lop3.b32 %0, %1, %2, %3, 0xea;" : "=r"(x) : "r"(w), "r"(mask), "r"(magic));
+  return x;
+}
+// A scale in both halves of a register, and what takes the numbers' offsets out.
+struct Int4Half {
   __half2 s, c0, c1;
   __device__ __forceinline__ void set(uint32_t code) {
-    const uint32_t b = code << 7;
-    const uint32_t two = b | b << 16;
-    s = __hmul2(*reinterpret_cast<const __half2*>(&two), __float2half2_rn(0.015625f));
-    c0 = __hmul2(s, __float2half2_rn(-1032.f));
-    c1 = __hmul2(s, __float2half2_rn(-72.f));
+    const uint32_t two = code * 0x00800080u;
+    s = *reinterpret_cast<const __half2*>(&two);
+    c0 = __hmul2(s, __float2half2_rn(-16.125f));
+    c1 = __hmul2(s, __float2half2_rn(-1.125f));
   }
 };
 // Latents 2p and 2p + 1 of a word, p = 0 or 1 (2 and 3: of the word shifted right by 8), at 2^-6 of their value.
 template <int P>
-__device__ __forceinline__ __half2 int4_pair(uint32_t w, const Int4Scale& k) {
-  const uint32_t x = P == 0 ? (w & 0x000f000fu) | 0x64006400u : (w & 0x00f000f0u) | 0x54005400u;
+__device__ __forceinline__ __half2 int4_pair(uint32_t w, const Int4Half& k) {
+  const uint32_t x = P == 0 ? and_or(w, 0x000f000fu, 0x4c004c00u) : and_or(w, 0x00f000f0u, 0x3c003c00u);
   return __hfma2(*reinterpret_cast<const __half2*>(&x), k.s, P == 0 ? k.c0 : k.c1);
+}
+struct Int4Bf16 {
+  __nv_bfloat162 s, c;
+  __device__ __forceinline__ void set(uint32_t code) {
+    s = __float2bfloat162_rn(int4_scale(code));
+    c = __hmul2(s, __float2bfloat162_rn(-136.f));
+  }
+};
+// Latents 2p and 2p + 1 of a word shifted right by 4 p.
+__device__ __forceinline__ __nv_bfloat162 int4_pair(uint32_t w, const Int4Bf16& k) {
+  const uint32_t x = and_or(w, 0x000f000fu, 0x43004300u);
+  return __hfma2(*reinterpret_cast<const __nv_bfloat162*>(&x), k.s, k.c);
 }
 
 }  // namespace hs

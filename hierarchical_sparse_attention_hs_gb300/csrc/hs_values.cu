@@ -85,7 +85,7 @@ struct Part {
   // chunk t in 32 bits
   __device__ __forceinline__ void get(int t, int lane, float (&x)[V]) const {
     if constexpr (RB == ROW_INT4) {
-      Int4Scale k;
+      Int4Half k;
       k.set(scale[t]);
       const uint32_t w = V == 8 ? codes[t] : codes[t] >> (8 * (lane & 1));  // four of a word's eight where a chunk is four
 #pragma unroll
