@@ -25,7 +25,7 @@
 // tile's rows, and rows 64 (w / 4) .. +63 of that half), 8 the issuer (the pair's first CTA issues for both), 9-15 the
 // loaders. K and V pass through one ring of 16 KB stages in the order in which the MMAs read them: a K stage
 // is 64 columns of the CTA's 128 rows, a V stage 128 of its value columns of 64 rows, both 128 rows of 128 bytes, 128-byte
-// swizzle; each feeds four MMAs, 256 cycles. The loaders take turns at jobs of 64 rows by 128 columns.
+// swizzle; each feeds four MMAs, 256 cycles. The loaders take turns at jobs of 32 rows by 128 columns.
 //
 // Waits are bounded: on running out a role sets the abort flag, which ends every role, and the HS_DEVERR_TIMEOUT bit.
 
@@ -64,10 +64,11 @@ constexpr int NSTAGE = 5;          // stages of the ring
 constexpr int OFF_Q = 0;
 constexpr int OFF_RING = OFF_Q + KBLK * BLK_BYTES;
 constexpr int OFF_P = OFF_RING + NSTAGE * STAGE_BYTES;
-constexpr int SOFTMAX_WARPS = 8, MMA_WARP = 8, LOAD_WARP0 = 9, LOADERS = 7, THREADS = (LOAD_WARP0 + LOADERS) * 32;
-static_assert(THREADS <= 512, "128 registers a thread");
-constexpr int KJOBS = KBLK + 1;    // a loader's jobs of a K
-constexpr int RAW_CODES = 64 * 64, RAW_SCALES = 64 * 8, RAW_BYTES = RAW_CODES + 2 * RAW_SCALES;  // a loader's rows as they are
+constexpr int SOFTMAX_WARPS = 8, MMA_WARP = 8, LOAD_WARP0 = 9, LOADERS = 11, THREADS = (LOAD_WARP0 + LOADERS) * 32;
+static_assert(THREADS <= 640, "96 registers a thread");
+constexpr int KPAIRS = LATENT / 128, KJOBS = 4 * (KPAIRS + 1);  // pairs of K's stages of latents; a loader's jobs of a K
+// A loader's rows of a job as they are: 64 bytes of codes and eight scales each.
+constexpr int JOB_ROWS = 32, RAW_CODES = JOB_ROWS * 64, RAW_BYTES = RAW_CODES + JOB_ROWS * 8;
 constexpr int OFF_RAW = OFF_P + NSEG * BLK_BYTES;
 constexpr int OFF_BAR = OFF_RAW + LOADERS * RAW_BYTES;
 // mbarriers: qfull full[] empty[] sfull[2] sfree[2] pfull pdone drain stall mx[2]
@@ -136,15 +137,15 @@ struct Tiles {
   int last_segs;     // segments of its last tile
   __device__ __forceinline__ int segs(int t) const { return t == n - 1 ? last_segs : NSEG; }
 };
-// A loader's way through the jobs of that order. A job is 64 rows of 128 columns (K: half of two stages; V: a stage), or of
-// the rotary key (half of K's last stage): ten jobs of a K, two of each segment of a V.
+// A loader's way through the jobs of that order. A job is 32 rows of 128 columns (K: a quarter of the rows of two stages; V:
+// half of a stage), or of the rotary key (a quarter of K's last stage).
 struct Order {
   int kt = 0, vt = 0, c;  // the tile whose K is next or under way, the one whose V is; the job's place within K or V
   int stage = 0;          // the number of K's or V's first stage
   bool is_k = true;
   __device__ __forceinline__ bool settle(const Tiles& t) {
     for (;;) {
-      const int end = is_k ? KJOBS : 2 * t.segs(vt);
+      const int end = is_k ? KJOBS : 4 * t.segs(vt);
       if (c < end) return true;
       c -= end;
       if (is_k) {
@@ -152,13 +153,19 @@ struct Order {
         is_k = kt == 0 && t.n > 1;
         ++kt;
       } else {
-        stage += end;
+        stage += 2 * t.segs(vt);
         if (++vt == t.n) return false;
         is_k = kt < t.n;
       }
     }
   }
-  __device__ __forceinline__ bool is_rope() const { return is_k && c >= KJOBS - 2; }
+  __device__ __forceinline__ bool is_rope() const { return is_k && c >= 4 * KPAIRS; }
+  __device__ __forceinline__ int first_stage() const { return stage + (is_k ? c >> 2 << 1 : c >> 1); }
+  // of the job's rows, among the tile's rows
+  __device__ __forceinline__ int first_row(int rank) const {
+    return is_k ? rank * KH + (c & 3) * JOB_ROWS : (c >> 2) * SEG + (c & 1) * JOB_ROWS;
+  }
+  __device__ __forceinline__ int first_col(int rank) const { return is_k ? (c >> 2) * 128 : rank * DVH + (c >> 1 & 1) * 128; }
 };
 // 32 latents of a row, unpacked into four of the eight 16-byte chunks of a stage's row, from chunk ch on: as bf16 for the
 // scores, as halves at 2^-6 for the values.
@@ -198,8 +205,8 @@ __global__ void __launch_bounds__(THREADS, 1) hs_decode4_kernel(const Decode4Arg
 
   if (t == 0) {
     for (int i = 0; i < NBAR; ++i) bar_init(bar + i, 1);
-    // one arrival for each softmax warp of the pair; two of each CTA for a stage
-    for (int i = 0; i < NSTAGE; ++i) bar_init(bar + B_FULL + i, 4);
+    // one arrival for each softmax warp of the pair; four of each CTA for a stage
+    for (int i = 0; i < NSTAGE; ++i) bar_init(bar + B_FULL + i, 8);
     for (int i = 0; i < 2; ++i) bar_init(bar + B_SFREE + i, 2 * SOFTMAX_WARPS);
     bar_init(bar + B_PFULL, 2 * SOFTMAX_WARPS);
     for (int i = 0; i < 2; ++i) bar_init(bar + B_MX + i, NSEG);  // the warps that hold the same heads
@@ -228,7 +235,6 @@ __global__ void __launch_bounds__(THREADS, 1) hs_decode4_kernel(const Decode4Arg
   const uint32_t lead = peer_addr(bar, first);  // the first CTA's barriers
   // test hook: the roles that would start a copy or an MMA first wait on a barrier that nothing completes
   bool ok = true;
-
   if (warp == MMA_WARP) {
     // ---- the issuer, of the pair's first CTA. The whole warp walks the loop, so that the descriptors stay in uniform
     //      registers; one lane issues: scores of tile g, then the value product of tile g - 1.
@@ -287,10 +293,8 @@ __global__ void __launch_bounds__(THREADS, 1) hs_decode4_kernel(const Decode4Arg
     }
     __syncwarp();
   } else if (warp >= LOAD_WARP0) {
-    // ---- a loader: every LOADERS-th job. A job's rows come into the warp's own 64 x 64 bytes of codes (row r: 16-byte chunk j at
-    //      j ^ (r / 2 % 4)) and 64 x 8 of scales, and are unpacked from there, 32 rows at a time: eight lanes hold eight rows,
-    //      four such groups 32 columns each. The same half of the next job is under way as soon as this job's has been read (a
-    //      group of copies each, so that all but the last are done when the next half is due).
+    // ---- a loader: every LOADERS-th job. A job's rows come into shared memory of the warp's own, codes (row r: 16-byte chunk j
+    //      at j ^ (r / 2 % 4)) and scales, one job ahead, and are unpacked from there, a lane 32 columns of every eighth row.
     ok = !a.stall || __all_sync(0xffffffffu, bar_wait(bar + B_STALL, 0, abort_flag, lim));
     const int r8 = lane & 7, qd = lane >> 3, wl = warp - LOAD_WARP0;
     if (wl == 0 && lane == 0 && ok) {
@@ -300,50 +304,40 @@ __global__ void __launch_bounds__(THREADS, 1) hs_decode4_kernel(const Decode4Arg
     }
     __syncwarp();
     uint8_t* const raw = smem + OFF_RAW + wl * RAW_BYTES;
-    const uint8_t* const codes_at = raw + r8 * 64 + ((qd ^ (r8 >> 1 & 3)) << 4);
-    const uint32_t codes_to = su32(raw + (lane >> 2) * 64 + (((lane & 3) ^ (lane >> 3 & 3)) << 4));
-    Order o;
-    o.c = wl;
-    bool more_jobs = o.settle(tiles);
-    int parity = 0;                   // of the job: where its scales are
-    int32_t e[2];                     // the list's entries of the next job's rows: lane and lane + 32
-    unsigned long long row[2] = {};   // and where they are
-    auto fetch = [&](const Order& x) {
-      const int base = (tiles.first + (x.is_k ? x.kt : x.vt)) * NK + (x.is_k ? (int)rank * KH + (x.c & 1) * 64 : (x.c >> 1) * SEG) + lane;
-#pragma unroll
-      for (int i = 0; i < 2; ++i) e[i] = base + 32 * i < a.k ? ld_fresh(list + base + 32 * i) : -1;
+    // a job, and the lane's entry of the list for it: none where there is no job
+    struct Job : Order {
+      bool more;
+      int32_t e;
     };
-    auto find = [&]() {
-#pragma unroll
-      for (int i = 0; i < 2; ++i) row[i] = reinterpret_cast<unsigned long long>(row_at(a.src, b, e[i], ROW_INT4));
+    auto entry = [&](Job& x) {
+      const int i = (tiles.first + (x.is_k ? x.kt : x.vt)) * NK + x.first_row((int)rank) + lane;
+      x.e = x.more && i < a.k ? ld_fresh(list + i) : -1;
     };
-    auto first_col = [&](const Order& x) { return x.is_k ? (x.c >> 1) * 128 : (int)rank * DVH + (x.c & 1) * 128; };
-    // the scales of a job's rows: zeros without a row, whose numbers may then be anything
-    auto get_scales = [&](int col, int par) {
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        uint8_t* const d = raw + RAW_CODES + par * RAW_SCALES + (lane + 32 * i) * 8;
-        if (row[i])
-          copy8(su32(d), row[i] + INT4_SCALES + col / INT4_BLOCK);
+    auto after = [&](const Job& x) {
+      Job y = x;
+      y.c += LOADERS;
+      if (x.more) y.more = y.settle(tiles);
+      return y;
+    };
+    // The codes and scales of a job's rows on their way: four lanes a row; where there is no row its scales are zeros (and the
+    // numbers may be anything).
+    auto get = [&](const Job& x) {
+      if (x.more && !x.is_rope()) {
+        const int col = x.first_col((int)rank);
+        const unsigned long long mine = reinterpret_cast<unsigned long long>(row_at(a.src, b, x.e, ROW_INT4));
+        uint8_t* const scales = raw + RAW_CODES + lane * 8;
+        if (mine)
+          copy8(su32(scales), mine + INT4_SCALES + col / INT4_BLOCK);
         else
-          *reinterpret_cast<uint2*>(d) = make_uint2(0, 0);
-      }
-    };
-    // the codes of 32 rows, four lanes a row
-    auto get_codes = [&](int col, int h) {
+          *reinterpret_cast<uint2*>(scales) = make_uint2(0, 0);
+        const uint32_t to = su32(raw + (lane >> 2) * 64 + (((lane & 3) ^ (lane >> 3 & 3)) << 4));
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const unsigned long long p = __shfl_sync(0xffffffffu, h ? row[1] : row[0], 8 * i + (lane >> 2));
-        if (p) copy16(codes_to + h * 2048 + i * 512, p + col / 2 + 16 * (lane & 3));
+        for (int i = 0; i < 4; ++i) {
+          const unsigned long long p = __shfl_sync(0xffffffffu, mine, 8 * i + (lane >> 2));
+          if (p) copy16(to + i * 512, p + col / 2 + 16 * (lane & 3));
+        }
       }
-    };
-    auto get_job = [&](const Order& x, bool there, int par) {
-      if (there) get_scales(first_col(x), par);
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        if (there) get_codes(first_col(x), h);
-        copies_commit();
-      }
+      copies_commit();
     };
     // Waits until the MMAs that read stage x have finished. A barrier's parity tells its last two phases apart, so a wait for
     // stage x needs that of the stage before in the same slot to be known.
@@ -355,73 +349,65 @@ __global__ void __launch_bounds__(THREADS, 1) hs_decode4_kernel(const Decode4Arg
         known = y;
       }
     };
-    if (more_jobs && ok) {
-      fetch(o);
-      find();
-      get_job(o, !o.is_rope(), parity);
-    }
-    while (more_jobs && ok) {
-      Order nx = o;
-      nx.c += LOADERS;
-      const bool more_after = nx.settle(tiles), ahead = more_after && !nx.is_rope();
-      if (more_after) fetch(nx);
-      const int next_col = first_col(nx);
+    Job o, o1;  // this job and the next
+    o.c = wl;
+    o.more = o.settle(tiles) && ok;
+    entry(o);
+    o1 = after(o);
+    entry(o1);
+    get(o);
+    while (o.more) {
+      Job o2 = after(o1);
+      entry(o2);
       const bool rope = o.is_rope(), two = o.is_k && !rope;
-      const int n0 = o.stage + (rope ? KBLK - 1 : o.is_k ? o.c & ~1 : o.c), n1 = n0 + (two ? 1 : 0);
-      const int s0 = n0 % NSTAGE, s1 = n1 % NSTAGE;
-      need(n1 - NSTAGE);
-      if (!ok) break;
+      const int n0 = o.first_stage(), n1 = n0 + (two ? 1 : 0), s0 = n0 % NSTAGE, s1 = n1 % NSTAGE;
       if (rope) {
         // the rotary keys as they are, 16 bytes a copy, eight lanes a row
-        uint8_t* const dst = smem + OFF_RING + s0 * STAGE_BYTES + (o.c & 1) * BLK_BYTES;
-#pragma unroll 4
-        for (int i = 0; i < 16; ++i) {
-          const int r = 4 * i + qd;
-          const unsigned long long p = __shfl_sync(0xffffffffu, i < 8 ? row[0] : row[1], r & 31);
-          uint8_t* const d = dst + r * 128 + ((r8 ^ (r & 7)) << 4);
+        const unsigned long long mine = reinterpret_cast<unsigned long long>(row_at(a.src, b, o.e, ROW_INT4));
+        uint8_t* const dst = smem + OFF_RING + s0 * STAGE_BYTES + ((o.c & 3) * JOB_ROWS + qd) * 128;
+        need(n1 - NSTAGE);
+        if (!ok) break;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const unsigned long long p = __shfl_sync(0xffffffffu, mine, 4 * i + qd);
+          uint8_t* const d = dst + i * 512 + ((r8 ^ ((4 * i + qd) & 7)) << 4);
           if (p)
             copy16(su32(d), p + INT4_ROPE + 16 * r8);
           else
             *reinterpret_cast<uint4*>(d) = make_uint4(0, 0, 0, 0);
         }
         copies_commit();
-        if (more_after) find();
-        get_job(nx, ahead, parity ^ 1);
-        copies_wait<2>();
+        get(o1);
+        copies_wait<1>();
       } else {
-        if (more_after) find();
+        copies_wait<0>();
+        __syncwarp();
+        uint4 c[4];
+        uint32_t sc[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          c[i] = *reinterpret_cast<const uint4*>(raw + i * 512 + r8 * 64 + ((qd ^ (r8 >> 1 & 3)) << 4));
+          sc[i] = *reinterpret_cast<const uint16_t*>(raw + RAW_CODES + i * 64 + r8 * 8 + 2 * qd);
+        }
+        __syncwarp();
+        get(o1);
+        need(n1 - NSTAGE);
+        if (!ok) break;
         // K: the upper 64 columns lie in the stage after; V: behind the lower 64
-        uint8_t* const dst = smem + OFF_RING + (qd >> 1 ? s1 : s0) * STAGE_BYTES + (two ? (o.c & 1) : qd >> 1) * BLK_BYTES + r8 * 128;
-        const uint8_t* const scales_at = raw + RAW_CODES + parity * RAW_SCALES + r8 * 8 + 2 * qd;
-        if (ahead) get_scales(next_col, parity ^ 1);
-        auto half = [&](auto is_k, int h) {
-          copies_wait<1>();
-          __syncwarp();
-          uint4 c[4];
-          uint32_t sc[4];
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            c[i] = *reinterpret_cast<const uint4*>(codes_at + h * 2048 + i * 512);
-            sc[i] = *reinterpret_cast<const uint16_t*>(scales_at + h * 256 + i * 64);
-          }
-          __syncwarp();
-          if (ahead) get_codes(next_col, h);
-          copies_commit();
-#pragma unroll
-          for (int i = 0; i < 4; ++i) unpack<decltype(is_k)::value>(dst + h * 4096 + i * 1024, r8, (qd & 1) * 4, c[i], sc[i]);
-        };
+        uint8_t* const dst = smem + OFF_RING + (qd >> 1 ? s1 : s0) * STAGE_BYTES +
+                             ((two ? o.c & 3 : (qd >> 1) * 2 + (o.c & 1)) * JOB_ROWS + r8) * 128;
         if (o.is_k) {
-#pragma unroll 1
-          for (int h = 0; h < 2; ++h) half(std::true_type{}, h);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) unpack<true>(dst + i * 1024, r8, (qd & 1) * 4, c[i], sc[i]);
         } else {
-#pragma unroll 1
-          for (int h = 0; h < 2; ++h) half(std::false_type{}, h);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) unpack<false>(dst + i * 1024, r8, (qd & 1) * 4, c[i], sc[i]);
         }
       }
       fence_proxy_async();
       __syncwarp();
       if (lane == 0) {
-        // a stage is full with four arrivals: two for each CTA
+        // a stage is full with eight arrivals, four for each CTA
         if (o.is_k) {
           arrive_lead(lead + (B_FULL + s0) * 8);
           if (two) arrive_lead(lead + (B_FULL + s1) * 8);
@@ -429,9 +415,8 @@ __global__ void __launch_bounds__(THREADS, 1) hs_decode4_kernel(const Decode4Arg
           arrive_lead(lead + (B_FULL + s0) * 8, 2);
         }
       }
-      o = nx;
-      more_jobs = more_after;
-      parity ^= 1;
+      o = o1;
+      o1 = o2;
     }
     copies_wait<0>();
     __syncwarp();
@@ -631,55 +616,69 @@ __global__ void __launch_bounds__(THREADS, 1) hs_decode4_kernel(const Decode4Arg
   }
   cluster_sync();
   tc_fence_after();
+  if (warp == MMA_WARP)
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(TMEM_COLS) : "memory");
   if (a.nsplit > 1) {
-    // Join: this CTA's share of its 64 heads, from the splits' CTAs of the same heads; 128 threads a head, four values each.
-    const int share = QH / a.nsplit, c4 = (t & 127) * 16;
-    if (!*abort_flag) {
+    // Join: this CTA's share of its 64 heads, from the splits' CTAs of the same heads. Thread t holds outputs 4 (t % 128) .. +3
+    // of every fourth head of them, eight loads from the other CTAs in flight; the weights of all 64 pairs of head and
+    // split are worked out by 64 threads meanwhile.
+    const int n = a.nsplit, lg = n == 2 ? 1 : n == 4 ? 2 : 3, share = QH >> lg, grp = t >> 7, c4 = (t & 127) * 16;
+    float* const weight = red;
+    const uint8_t* const mine = smem + split * share * OUT_F32 + c4;
+    float4 v[8];
+    auto load8 = [&](int x0) {
+#pragma unroll
+      for (int u = 0; u < 8; ++u) {
+        const int x = x0 + u;  // of the group's pairs: its heads grp, grp + 4, ..
+        v[u] = ld_peer(peer_addr(mine + ((x >> lg) * 4 + grp) * OUT_F32, 2 * (x & (n - 1)) + rank));
+      }
+    };
+    if (grp < 4) load8(0);
+    if (t < QH) {
+      const int h = split * share + (t >> lg);
+      const float2 ml = ld_peer2(peer_addr(smem + OFF_ML + h * 8, 2 * (t & (n - 1)) + rank));
+      const bool some = ml.y != 0.f;  // (a split with no row has no weight, and zeros)
+      float mx = some ? ml.x : -INFINITY;
+      for (int d = 1; d < n; d <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
+      const float ref = mx == -INFINITY ? 0.f : mx;
+      const float f = some ? exp2f(ml.x == -INFINITY ? 0.f : ml.x - ref) : 0.f;
+      float total = some ? f * ml.y : 0.f;
+      for (int d = 1; d < n; d <<= 1) total += __shfl_xor_sync(0xffffffffu, total, d);
+      weight[t] = total != 0.f ? f * (UNSCALE / total) : 0.f;
+      if ((t & (n - 1)) == 0) a.lse[(size_t)b * HEADS + rank * QH + h] = total != 0.f ? (ref + log2f(total)) * 0.6931471805599453f : -INFINITY;
+    }
+    __syncthreads();
+    if (grp < 4) {
+      float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 1
-      for (int i = t >> 7; i < share; i += THREADS / 128) {
-        const int h = split * share + i;
-        const size_t bh = (size_t)b * HEADS + rank * QH + h;
-        float2 ml[MAX_SPLIT];
-        float4 v[MAX_SPLIT];
-        float mx = -INFINITY;
+      for (int x0 = 0; x0 < 16; x0 += 8) {
+        if (x0) load8(x0);
 #pragma unroll
-        for (int s = 0; s < MAX_SPLIT; ++s) {
-          if (s >= a.nsplit) break;
-          ml[s] = ld_peer2(peer_addr(smem + OFF_ML + h * 8, 2 * s + rank));
-          v[s] = ld_peer(peer_addr(smem + h * OUT_F32 + c4, 2 * s + rank));
-          if (ml[s].y != 0.f) mx = fmaxf(mx, ml[s].x);
+        for (int u = 0; u < 8; ++u) {
+          const int x = x0 + u, i = (x >> lg) * 4 + grp;
+          const float w = weight[(i << lg) + (x & (n - 1))];
+          o.x = fmaf(w, v[u].x, o.x);
+          o.y = fmaf(w, v[u].y, o.y);
+          o.z = fmaf(w, v[u].z, o.z);
+          o.w = fmaf(w, v[u].w, o.w);
+          if ((x & (n - 1)) == n - 1) {
+            const size_t bh = (size_t)b * HEADS + rank * QH + split * share + i;
+            if (*abort_flag) {
+            } else if (a.out_f32) {
+              *reinterpret_cast<float4*>(static_cast<uint8_t*>(a.out) + bh * LATENT * 4 + c4) = o;
+            } else {
+              const __nv_bfloat162 lo = __floats2bfloat162_rn(o.x, o.y), hi = __floats2bfloat162_rn(o.z, o.w);
+              *reinterpret_cast<uint2*>(static_cast<uint8_t*>(a.out) + bh * LATENT * 2 + c4 / 2) =
+                  make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
+            }
+            o = make_float4(0.f, 0.f, 0.f, 0.f);
+          }
         }
-        const float ref = mx == -INFINITY ? 0.f : mx;
-        float total = 0.f;
-        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-        for (int s = 0; s < MAX_SPLIT; ++s) {
-          if (s >= a.nsplit) break;
-          if (ml[s].y == 0.f) continue;  // a split with no row
-          const float f = exp2f(ml[s].x == -INFINITY ? 0.f : ml[s].x - ref);
-          total = fmaf(f, ml[s].y, total);
-          o.x = fmaf(f, v[s].x, o.x);
-          o.y = fmaf(f, v[s].y, o.y);
-          o.z = fmaf(f, v[s].z, o.z);
-          o.w = fmaf(f, v[s].w, o.w);
-        }
-        const float inv = total != 0.f ? UNSCALE / total : 0.f;
-        o = make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
-        if (a.out_f32) {
-          *reinterpret_cast<float4*>(static_cast<uint8_t*>(a.out) + bh * LATENT * 4 + c4) = o;
-        } else {
-          const __nv_bfloat162 lo = __floats2bfloat162_rn(o.x, o.y), hi = __floats2bfloat162_rn(o.z, o.w);
-          *reinterpret_cast<uint2*>(static_cast<uint8_t*>(a.out) + bh * LATENT * 2 + c4 / 2) =
-              make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
-        }
-        if (c4 == 0) a.lse[bh] = total != 0.f ? (ref + log2f(total)) * 0.6931471805599453f : -INFINITY;
       }
     }
     __syncwarp();
     cluster_sync();  // the splits' shared memory stays until all have read it
   }
-  if (warp == MMA_WARP)
-    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(TMEM_COLS) : "memory");
 }
 
 // How many clusters of 2 n CTAs (n = 1, 2, 4, 8) the current device holds at once, cached per device; 0 where it holds none.
