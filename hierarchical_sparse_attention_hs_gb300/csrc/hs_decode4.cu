@@ -25,7 +25,7 @@
 // tile's rows, and rows 64 (w / 4) .. +63 of that half), 8 the issuer (the pair's first CTA issues for both), 9-15 the
 // loaders. K and V pass through one ring of 16 KB stages in the order in which the MMAs read them: a K stage
 // is 64 columns of the CTA's 128 rows, a V stage 128 of its value columns of 64 rows, both 128 rows of 128 bytes, 128-byte
-// swizzle; each feeds four MMAs, 256 cycles. The loaders take turns at jobs of 32 rows by 128 columns.
+// swizzle; each feeds four MMAs, 256 cycles. The loaders work side by side, 32 rows by 128 columns each.
 //
 // Waits are bounded: on running out a role sets the abort flag, which ends every role, and the HS_DEVERR_TIMEOUT bit.
 
@@ -58,19 +58,20 @@ constexpr int DVH = LATENT / 2;    // value columns of a CTA
 constexpr int SEG = 64;            // a softmax thread's rows
 constexpr int NSEG = NK / SEG;
 constexpr int KBLK = WIDTH / 64;   // 64-column blocks of a row: K stages of a tile
+constexpr int ROPE_AT = 4;         // the K stage of the rotary keys
 constexpr int BLK_BYTES = 64 * 128;      // 64 rows x 64 columns
 constexpr int STAGE_BYTES = 2 * BLK_BYTES;
 constexpr int NSTAGE = 5;          // stages of the ring
 constexpr int OFF_Q = 0;
 constexpr int OFF_RING = OFF_Q + KBLK * BLK_BYTES;
 constexpr int OFF_P = OFF_RING + NSTAGE * STAGE_BYTES;
-constexpr int SOFTMAX_WARPS = 8, MMA_WARP = 8, LOAD_WARP0 = 9, LOADERS = 11, THREADS = (LOAD_WARP0 + LOADERS) * 32;
-static_assert(THREADS <= 640, "96 registers a thread");
-constexpr int KPAIRS = LATENT / 128, KJOBS = 4 * (KPAIRS + 1);  // pairs of K's stages of latents; a loader's jobs of a K
-// A loader's rows of a job as they are: 64 bytes of codes and eight scales each.
-constexpr int JOB_ROWS = 32, RAW_CODES = JOB_ROWS * 64, RAW_BYTES = RAW_CODES + JOB_ROWS * 8;
+constexpr int SOFTMAX_WARPS = 8, MMA_WARP = 8, LOAD_WARP0 = 9, LOADERS = 8, KEY_WARP = LOAD_WARP0 + LOADERS, KEY_WARPS = 2, THREADS = (KEY_WARP + KEY_WARPS) * 32;
+static_assert(THREADS <= 640, "96 registers a thread: five warps a scheduler");
+// A loader's two jobs as their rows are in memory, 64 bytes of codes (row r: 16-byte chunk j at j ^ (r / 2 % 4)) and eight scales
+// each.
+constexpr int RAW_CODES = 32 * 64, RAW_JOB = RAW_CODES + 32 * 8;
 constexpr int OFF_RAW = OFF_P + NSEG * BLK_BYTES;
-constexpr int OFF_BAR = OFF_RAW + LOADERS * RAW_BYTES;
+constexpr int OFF_BAR = OFF_RAW + LOADERS * 2 * RAW_JOB;
 // mbarriers: qfull full[] empty[] sfull[2] sfree[2] pfull pdone drain stall mx[2]
 constexpr int B_QFULL = 0, B_FULL = 1, B_EMPTY = B_FULL + NSTAGE, B_SFULL = B_EMPTY + NSTAGE,
               B_SFREE = B_SFULL + 2, B_PFULL = B_SFREE + 2, B_PDONE = B_PFULL + 1, B_DRAIN = B_PDONE + 1,
@@ -105,8 +106,7 @@ struct Decode4Args {
 __host__ __device__ constexpr uint32_t idesc_f16(int m, int n, int a_mn, int b_mn) {
   return idesc_bf16(m, n, a_mn, b_mn) & ~(1u << 7 | 1u << 10);
 }
-// 16 and 8 bytes into shared memory (volatile: behind the launch wait, like every load of what an earlier kernel may have
-// written).
+// Copies into shared memory (volatile: they stay behind the launch wait).
 __device__ __forceinline__ void copy16(uint32_t dst, unsigned long long src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
@@ -129,43 +129,14 @@ __device__ __forceinline__ float2 ld_peer2(uint32_t addr) {
   return v;
 }
 
-// A split's tiles, and where its stages lie in the order K(0) K(1) V(0) K(2) V(1) ... V(n - 1) of its tiles. Of the list's
-// last tile only the first `last_segs` segments hold entries: the others are neither loaded (their scores are masked,
-// whatever the buffer holds) nor multiplied with V.
+// A split's tiles, and where their stages lie in the order K(0) K(1) V(0) K(2) V(1) ... V(n - 1): K's rotary keys in the
+// middle of its latents (stage ROPE_AT). Of the list's last tile only the first `last_segs` segments hold entries: the others are not multiplied with V.
 struct Tiles {
   int first, n;      // the split's first tile, and how many it has
   int last_segs;     // segments of its last tile
   __device__ __forceinline__ int segs(int t) const { return t == n - 1 ? last_segs : NSEG; }
-};
-// A loader's way through the jobs of that order. A job is 32 rows of 128 columns (K: a quarter of the rows of two stages; V:
-// half of a stage), or of the rotary key (a quarter of K's last stage).
-struct Order {
-  int kt = 0, vt = 0, c;  // the tile whose K is next or under way, the one whose V is; the job's place within K or V
-  int stage = 0;          // the number of K's or V's first stage
-  bool is_k = true;
-  __device__ __forceinline__ bool settle(const Tiles& t) {
-    for (;;) {
-      const int end = is_k ? KJOBS : 4 * t.segs(vt);
-      if (c < end) return true;
-      c -= end;
-      if (is_k) {
-        stage += KBLK;
-        is_k = kt == 0 && t.n > 1;
-        ++kt;
-      } else {
-        stage += 2 * t.segs(vt);
-        if (++vt == t.n) return false;
-        is_k = kt < t.n;
-      }
-    }
-  }
-  __device__ __forceinline__ bool is_rope() const { return is_k && c >= 4 * KPAIRS; }
-  __device__ __forceinline__ int first_stage() const { return stage + (is_k ? c >> 2 << 1 : c >> 1); }
-  // of the job's rows, among the tile's rows
-  __device__ __forceinline__ int first_row(int rank) const {
-    return is_k ? rank * KH + (c & 3) * JOB_ROWS : (c >> 2) * SEG + (c & 1) * JOB_ROWS;
-  }
-  __device__ __forceinline__ int first_col(int rank) const { return is_k ? (c >> 2) * 128 : rank * DVH + (c >> 1 & 1) * 128; }
+  __device__ __forceinline__ int k_stage(int t) const { return t == 0 ? 0 : t * (KBLK + 2 * NSEG) - 2 * NSEG; }
+  __device__ __forceinline__ int v_stage(int t) const { return (t + 1) * (KBLK + 2 * NSEG) + (t == n - 1 ? -2 * NSEG : 1); }
 };
 // 32 latents of a row, unpacked into four of the eight 16-byte chunks of a stage's row, from chunk ch on: as bf16 for the
 // scores, as halves at 2^-6 for the values.
@@ -267,7 +238,7 @@ __global__ void __launch_bounds__(THREADS, 1) hs_decode4_kernel(const Decode4Arg
           for (int c = 0; c < KBLK && ok; ++c) {
             ok = wait(B_FULL + st, ph);
             tc_fence_after();
-            if (ok) four(tmem + TMEM_S + (uint32_t)(g & 1) * KH, dq + (uint64_t)(c * (BLK_BYTES >> 4)),
+            if (ok) four(tmem + TMEM_S + (uint32_t)(g & 1) * KH, dq + (uint64_t)((c < ROPE_AT ? c : c == ROPE_AT ? KBLK - 1 : c - 1) * (BLK_BYTES >> 4)),
                          dk + (uint64_t)(st * (STAGE_BYTES >> 4)), 2, ID_S, c != 0 ? 1u : 0u);
           }
           if (!ok) break;
@@ -292,133 +263,194 @@ __global__ void __launch_bounds__(THREADS, 1) hs_decode4_kernel(const Decode4Arg
       if (leader) commit2(bar + B_DRAIN, both);
     }
     __syncwarp();
-  } else if (warp >= LOAD_WARP0) {
-    // ---- a loader: every LOADERS-th job. A job's rows come into shared memory of the warp's own, codes (row r: 16-byte chunk j
-    //      at j ^ (r / 2 % 4)) and scales, one job ahead, and are unpacked from there, a lane 32 columns of every eighth row.
+  } else if (warp >= KEY_WARP) {
+    // ---- the rotary keys of the CTA's half of every tile, 64 rows a warp, as they are: 16 bytes a copy, eight lanes a row. Their stage's place is
+    //      free when the V before this K has been multiplied (of the second K: when the first one has). The rows as a whole come
+    //      into L2 two tiles ahead: their words come in nine pieces, over the time of a tile.
     ok = !a.stall || __all_sync(0xffffffffu, bar_wait(bar + B_STALL, 0, abort_flag, lim));
-    const int r8 = lane & 7, qd = lane >> 3, wl = warp - LOAD_WARP0;
+    const int r8 = lane & 7, qd = lane >> 3, part = warp - KEY_WARP;
+    unsigned long long row[2], later[2];  // of the lane's rows: of this tile, and of the next
+    int32_t e[2];                         // the entries of the tile after that
+    auto entries = [&](int tile) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int x = (tiles.first + tile) * NK + (int)rank * KH + part * 64 + lane + 32 * i;
+        e[i] = tile < tiles.n && x < a.k ? ld_fresh(list + x) : -1;
+      }
+    };
+    auto find = [&](unsigned long long (&to)[2]) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i) to[i] = reinterpret_cast<unsigned long long>(row_at(a.src, b, e[i], ROW_INT4));
+    };
+    auto prefetch = [&](const unsigned long long (&of)[2]) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        if (!of[i]) continue;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) asm volatile("prefetch.global.L2 [%0];" ::"l"((of[i] & ~127ull) + j * 128) : "memory");
+      }
+    };
+    entries(0);
+    find(row);
+    entries(1);
+    for (int t = 0; t < tiles.n && ok; ++t) {
+      if (t == 1) ok = __all_sync(0xffffffffu, bar_wait(bar + B_SFULL, 0, abort_flag, lim));
+      if (t >= 2) ok = __all_sync(0xffffffffu, bar_wait(bar + B_PDONE, (unsigned)(t - 2) & 1u, abort_flag, lim));
+      if (!ok) break;
+      const int slot = (tiles.k_stage(t) + ROPE_AT) % NSTAGE;
+      uint8_t* const dst = smem + OFF_RING + slot * STAGE_BYTES + (part * 64 + qd) * 128;
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        const int r = 4 * i + qd;
+        const unsigned long long p = __shfl_sync(0xffffffffu, row[i >> 3], r & 31);
+        uint8_t* const d = dst + i * 512 + ((r8 ^ (r & 7)) << 4);
+        if (p)
+          copy16(su32(d), p + INT4_ROPE + 16 * r8);
+        else
+          *reinterpret_cast<uint4*>(d) = make_uint4(0, 0, 0, 0);
+      }
+      copies_commit();
+      if (t == 0) {
+        find(later);
+        prefetch(later);
+        entries(2);
+      }
+      copies_wait<0>();
+      fence_proxy_async();
+      __syncwarp();
+      if (lane == 0) arrive_lead(lead + (B_FULL + slot) * 8, 2);
+#pragma unroll
+      for (int i = 0; i < 2; ++i) row[i] = later[i];
+      find(later);
+      prefetch(later);
+      entries(t + 3);
+    }
+    copies_wait<0>();
+    __syncwarp();
+  } else if (warp >= LOAD_WARP0) {
+    // ---- a loader. All of them work side by side, a job each: of K's latents first on 128 columns a group of four (32 rows
+    //      each), then on the other two 128s; of V on two segments (32 rows by 128 columns each), then on the other two. The next
+    //      job's words are under way while this job's are unpacked.
+    ok = !a.stall || __all_sync(0xffffffffu, bar_wait(bar + B_STALL, 0, abort_flag, lim));
+    const int r8 = lane & 7, qd = lane >> 3, wl = warp - LOAD_WARP0, grp = wl >> 2;
     if (wl == 0 && lane == 0 && ok) {
       if (rank == 0) bar_arrive_expect(bar + B_QFULL, 2 * KBLK * BLK_BYTES);
       for (int i = 0; i < KBLK; i += 3)
         tma_box(su32(smem + OFF_Q + i * BLK_BYTES), &qmap, i, (int)b * HEADS + (int)rank * QH, lead + B_QFULL * 8);
     }
     __syncwarp();
-    uint8_t* const raw = smem + OFF_RAW + wl * RAW_BYTES;
-    // a job, and the lane's entry of the list for it: none where there is no job
-    struct Job : Order {
-      bool more;
-      int32_t e;
+    using Address = unsigned long long;
+    // the list's entry of the lane's row, `row` of a tile, and where that row is
+    auto entry = [&](int tile, int row) {
+      const int i = (tiles.first + tile) * NK + row + lane;
+      return tile < tiles.n && i < a.k ? ld_fresh(list + i) : -1;
     };
-    auto entry = [&](Job& x) {
-      const int i = (tiles.first + (x.is_k ? x.kt : x.vt)) * NK + x.first_row((int)rank) + lane;
-      x.e = x.more && i < a.k ? ld_fresh(list + i) : -1;
-    };
-    auto after = [&](const Job& x) {
-      Job y = x;
-      y.c += LOADERS;
-      if (x.more) y.more = y.settle(tiles);
-      return y;
-    };
-    // The codes and scales of a job's rows on their way: four lanes a row; where there is no row its scales are zeros (and the
-    // numbers may be anything).
-    auto get = [&](const Job& x) {
-      if (x.more && !x.is_rope()) {
-        const int col = x.first_col((int)rank);
-        const unsigned long long mine = reinterpret_cast<unsigned long long>(row_at(a.src, b, x.e, ROW_INT4));
-        uint8_t* const scales = raw + RAW_CODES + lane * 8;
-        if (mine)
-          copy8(su32(scales), mine + INT4_SCALES + col / INT4_BLOCK);
-        else
-          *reinterpret_cast<uint2*>(scales) = make_uint2(0, 0);
-        const uint32_t to = su32(raw + (lane >> 2) * 64 + (((lane & 3) ^ (lane >> 3 & 3)) << 4));
+    auto at = [&](int32_t e) { return reinterpret_cast<Address>(row_at(a.src, b, e, ROW_INT4)); };
+    const int krow = (int)rank * KH + (wl & 3) * 32, vrow = grp * SEG + (wl & 1) * 32;
+    // The words of 128 columns from `col` on, on their way into buffer `par`: four lanes a row; where there is no row its scales
+    // are zeros (and the numbers may be anything).
+    uint8_t* const raw = smem + OFF_RAW + wl * 2 * RAW_JOB;
+    auto load = [&](int par, Address mine, int col) {
+      uint8_t* const scales = raw + par * RAW_JOB + RAW_CODES + lane * 8;
+      if (mine)
+        copy8(su32(scales), mine + INT4_SCALES + col / INT4_BLOCK);
+      else
+        *reinterpret_cast<uint2*>(scales) = make_uint2(0, 0);
+      const uint32_t to = su32(raw + par * RAW_JOB + (lane >> 2) * 64 + (((lane & 3) ^ (lane >> 3 & 3)) << 4));
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const unsigned long long p = __shfl_sync(0xffffffffu, mine, 8 * i + (lane >> 2));
-          if (p) copy16(to + i * 512, p + col / 2 + 16 * (lane & 3));
-        }
+      for (int i = 0; i < 4; ++i) {
+        const Address p = __shfl_sync(0xffffffffu, mine, 8 * i + (lane >> 2));
+        if (p) copy16(to + i * 512, p + col / 2 + 16 * (lane & 3));
       }
       copies_commit();
     };
-    // Waits until the MMAs that read stage x have finished. A barrier's parity tells its last two phases apart, so a wait for
-    // stage x needs that of the stage before in the same slot to be known.
-    int known = -1;
-    auto need = [&](int x) {
-      while (x > known && ok) {
-        const int y = min(x, known + NSTAGE);
-        ok = __all_sync(0xffffffffu, bar_wait(bar + B_EMPTY + y % NSTAGE, (unsigned)(y / NSTAGE) & 1u, abort_flag, lim));
-        known = y;
+    // a lane's part of a buffer: 32 latents of rows lane % 8, + 8, + 16 and + 24
+    auto read = [&](int par, uint4 (&codes)[4], uint32_t (&scales)[4]) {
+      __syncwarp();
+      const uint8_t* const from = raw + par * RAW_JOB;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        codes[i] = *reinterpret_cast<const uint4*>(from + i * 512 + r8 * 64 + ((qd ^ (r8 >> 1 & 3)) << 4));
+        scales[i] = *reinterpret_cast<const uint16_t*>(from + RAW_CODES + i * 64 + r8 * 8 + 2 * qd);
       }
+      __syncwarp();
     };
-    Job o, o1;  // this job and the next
-    o.c = wl;
-    o.more = o.settle(tiles) && ok;
-    entry(o);
-    o1 = after(o);
-    entry(o1);
-    get(o);
-    while (o.more) {
-      Job o2 = after(o1);
-      entry(o2);
-      const bool rope = o.is_rope(), two = o.is_k && !rope;
-      const int n0 = o.first_stage(), n1 = n0 + (two ? 1 : 0), s0 = n0 % NSTAGE, s1 = n1 % NSTAGE;
-      if (rope) {
-        // the rotary keys as they are, 16 bytes a copy, eight lanes a row
-        const unsigned long long mine = reinterpret_cast<unsigned long long>(row_at(a.src, b, o.e, ROW_INT4));
-        uint8_t* const dst = smem + OFF_RING + s0 * STAGE_BYTES + ((o.c & 3) * JOB_ROWS + qd) * 128;
-        need(n1 - NSTAGE);
-        if (!ok) break;
+    // Waits until the MMAs that read the stage NSTAGE before stage n have finished: n takes its place. A barrier's parity tells
+    // its last two phases apart, so the wait holds only if that place's phase before is over; it is, as a loader has a part in
+    // at least one of any NSTAGE stages in a row, and waited for one of those before that.
+    auto need = [&](int n) {
+      if (n >= NSTAGE && ok)
+        ok = __all_sync(0xffffffffu, bar_wait(bar + B_EMPTY + n % NSTAGE, (unsigned)(n / NSTAGE - 1) & 1u, abort_flag, lim));
+    };
+    // a stage is full with eight arrivals, four for each CTA
+    auto full = [&](int stage, uint32_t count) { arrive_lead(lead + (B_FULL + stage % NSTAGE) * 8, count); };
+    // 32 rows by 128 columns of K into stages n and n + 1, or of V into stage n, the upper 64 columns behind the lower
+    auto put = [&](auto k, const uint4 (&codes)[4], const uint32_t (&scales)[4], int n) {
+      constexpr bool K = decltype(k)::value;
+      need(n);
+      if (K) need(n + 1);
+      if (!ok) return;
+      uint8_t* const dst = smem + OFF_RING + (K ? n + (qd >> 1) : n) % NSTAGE * STAGE_BYTES +
+                           ((K ? (wl & 3) * 32 : (qd >> 1) * SEG + (wl & 1) * 32) + r8) * 128;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const unsigned long long p = __shfl_sync(0xffffffffu, mine, 4 * i + qd);
-          uint8_t* const d = dst + i * 512 + ((r8 ^ ((4 * i + qd) & 7)) << 4);
-          if (p)
-            copy16(su32(d), p + INT4_ROPE + 16 * r8);
-          else
-            *reinterpret_cast<uint4*>(d) = make_uint4(0, 0, 0, 0);
-        }
-        copies_commit();
-        get(o1);
-        copies_wait<1>();
-      } else {
-        copies_wait<0>();
-        __syncwarp();
-        uint4 c[4];
-        uint32_t sc[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          c[i] = *reinterpret_cast<const uint4*>(raw + i * 512 + r8 * 64 + ((qd ^ (r8 >> 1 & 3)) << 4));
-          sc[i] = *reinterpret_cast<const uint16_t*>(raw + RAW_CODES + i * 64 + r8 * 8 + 2 * qd);
-        }
-        __syncwarp();
-        get(o1);
-        need(n1 - NSTAGE);
-        if (!ok) break;
-        // K: the upper 64 columns lie in the stage after; V: behind the lower 64
-        uint8_t* const dst = smem + OFF_RING + (qd >> 1 ? s1 : s0) * STAGE_BYTES +
-                             ((two ? o.c & 3 : (qd >> 1) * 2 + (o.c & 1)) * JOB_ROWS + r8) * 128;
-        if (o.is_k) {
-#pragma unroll
-          for (int i = 0; i < 4; ++i) unpack<true>(dst + i * 1024, r8, (qd & 1) * 4, c[i], sc[i]);
-        } else {
-#pragma unroll
-          for (int i = 0; i < 4; ++i) unpack<false>(dst + i * 1024, r8, (qd & 1) * 4, c[i], sc[i]);
-        }
-      }
+      for (int i = 0; i < 4; ++i) unpack<K>(dst + i * 1024, r8, (qd & 1) * 4, codes[i], scales[i]);
       fence_proxy_async();
       __syncwarp();
       if (lane == 0) {
-        // a stage is full with eight arrivals, four for each CTA
-        if (o.is_k) {
-          arrive_lead(lead + (B_FULL + s0) * 8);
-          if (two) arrive_lead(lead + (B_FULL + s1) * 8);
-        } else {
-          arrive_lead(lead + (B_FULL + s0) * 8, 2);
+        full(n, K ? 1 : 2);
+        if (K) full(n + 1, 1);
+      }
+    };
+    const std::true_type K;
+    const std::false_type V;
+    const int kcol = grp * 128, vcol = (int)rank * DVH + (wl >> 1 & 1) * 128;
+    uint4 w[4];
+    uint32_t sc[4];
+    Address krows = at(entry(0, krow));
+    int32_t ek = entry(1, krow), ev0 = entry(0, vrow), ev1 = entry(0, vrow + 2 * SEG);
+    // Two jobs are on their way, each in the buffer of the one before the last: a job's words are awaited, read, the buffer's next
+    // copies started, and the words unpacked.
+    load(0, krows, kcol);
+    load(1, krows, kcol + 256);
+    // step t: K(t), then V(t - 1)
+    for (int t = 0; t <= tiles.n && ok; ++t) {
+      const bool k_next = t + 1 < tiles.n;  // what comes after V(t - 1): K(t + 1), or the last V
+      if (t < tiles.n) {
+        const int n = tiles.k_stage(t);
+        krows = at(ek);
+        ek = entry(t + 2, krow);
+        // after K(t) comes V(t - 1), or K(1) or V(0)
+        const bool v_next = t > 0 || !k_next;
+        copies_wait<1>();
+        read(0, w, sc);
+        load(0, v_next ? at(ev0) : krows, v_next ? vcol : kcol);
+        put(K, w, sc, n + 2 * grp);
+        if (!ok) break;
+        copies_wait<1>();
+        read(1, w, sc);
+        load(1, v_next ? at(ev1) : krows, v_next ? vcol : kcol + 256);
+        put(K, w, sc, n + ROPE_AT + 1 + 2 * grp);
+        if (!ok) break;
+        if (t > 0) {
+          ev0 = entry(t, vrow);
+          ev1 = entry(t, vrow + 2 * SEG);
         }
       }
-      o = o1;
-      o1 = o2;
+      if (t > 0) {
+        const int n = tiles.v_stage(t - 1) + 2 * grp + (wl >> 1 & 1), segs = tiles.segs(t - 1);
+        copies_wait<1>();
+        read(0, w, sc);
+        load(0, t == tiles.n ? 0 : k_next ? krows : at(ev0), k_next ? kcol : vcol);
+        if (grp < segs) put(V, w, sc, n);
+        if (!ok) break;
+        copies_wait<1>();
+        read(1, w, sc);
+        load(1, t == tiles.n ? 0 : k_next ? krows : at(ev1), k_next ? kcol + 256 : vcol);
+        if (grp + 2 < segs) put(V, w, sc, n + 4);
+        if (!ok) break;
+      }
     }
-    copies_wait<0>();
+    asm volatile("cp.async.wait_all;" ::: "memory");
     __syncwarp();
   } else {
     // ---- softmax: a thread holds head r of this CTA and 64 rows of every tile, segment sg
