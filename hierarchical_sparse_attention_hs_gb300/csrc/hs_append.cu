@@ -141,18 +141,22 @@ __device__ __forceinline__ uint32_t pack_e4m3(float a, float b, float c, float d
   return lo | hi << 16;
 }
 
-__device__ __forceinline__ float max_nan(float a, float b) {
+// The largest of three magnitudes; NaN if one is.
+__device__ __forceinline__ float max_nan(float a, float b, float c) {
   float m;
-  asm("max.NaN.f32 %0, %1, %2;" : "=f"(m) : "f"(a), "f"(b));
+  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(m) : "f"(fabsf(a)), "f"(fabsf(b)), "f"(fabsf(c)));
   return m;
 }
-// z / scale to the nearest whole number, ties to even, within -7 .. 7, plus 8; `inv` is 1 / scale. The quotient is corrected
-// once by its residual, which an fma has exactly (Markstein): where z / scale is a 32-bit number, a half among them, it is
-// that number, so ties are ties. Adding 1.5 * 2^23 leaves the whole number in the low bits.
+// The quotient z / scale, `inv` being 1 / scale, corrected once by its residual, which an fma has exactly (Markstein): where z /
+// scale is a 32-bit number, a half of a whole number among them, it is that number, so ties are ties. Adding 1.5 * 2^23 + 8
+// leaves the nearest whole number, ties to even, plus 8 in the low bits.
 __device__ __forceinline__ uint32_t int4_of(float z, float scale, float inv) {
   const float y = z * inv;
-  const float q = fminf(fmaxf(fmaf(fmaf(-y, scale, z), inv, y), -7.f), 7.f);
-  return __float_as_uint(q + (12582912.f + 8.f)) & 15u;
+  return __float_as_uint(fmaf(fmaf(-y, scale, z), inv, y) + (12582912.f + 8.f));
+}
+// Four of them at bits 0, 4, 8 and 12: above the number a float's bits hold a multiple of 2^22, which shifts out of the low 16.
+__device__ __forceinline__ uint32_t int4_four(float a, float b, float c, float d, float scale, float inv) {
+  return ((int4_of(d, scale, inv) * 16 + int4_of(c, scale, inv)) * 16 + int4_of(b, scale, inv)) * 16 + int4_of(a, scale, inv);
 }
 
 // Pair `lane`'s turns per position as a fraction of a turn in units of 2^-64 turns.
@@ -294,20 +298,32 @@ __device__ __forceinline__ void append_rows(const AppendArgs& a, float* weight, 
       } else if (R == INT4) {
         // two neighbouring lanes hold a block's 16 latents, this one word `lane` (and 32 + lane) of the row
         uint32_t w[2], sc[2];
+        float scale[2];
+        bool wide = false;
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          float m = 0.f;
-#pragma unroll
-          for (int e = 0; e < 8; ++e) m = max_nan(m, fabsf(z[h][e]));
-          m = max_nan(m, __shfl_xor_sync(ALL, m, 1));
+          float m = max_nan(max_nan(z[h][0], z[h][1], z[h][2]), max_nan(z[h][3], z[h][4], z[h][5]), max_nan(z[h][6], z[h][7], 0.f));
+          m = max_nan(m, __shfl_xor_sync(ALL, m, 1), 0.f);
           const uint32_t code = int4_scale_code(m);
-          const float scale = int4_scale(code), inv = 1.f / scale;
-          w[h] = 0;
-#pragma unroll
-          for (int e = 0; e < 8; ++e) w[h] |= int4_of(z[h][e], scale, inv) << (16 * (e & 1) + 4 * (e >> 1));
+          scale[h] = int4_scale(code);
+          wide = wide || !(m < 7.5f * scale[h]);
           // lanes 0, 8, 16 and 24 collect four scales each
-          uint32_t four = code | __shfl_down_sync(ALL, code, 2) << 8;
-          sc[h] = four | __shfl_down_sync(ALL, four, 4) << 16;
+          const uint32_t two = code | __shfl_down_sync(ALL, code, 2) << 8;
+          sc[h] = two | __shfl_down_sync(ALL, two, 4) << 16;
+        }
+        // A number past 7 comes only of the largest scale or of one below 2^-14, whose steps are wide: the scale is otherwise within a
+        // sixteenth of the seventh part of the largest.
+        if (__any_sync(ALL, wide)) {
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int e = 0; e < 8; ++e) z[h][e] = fminf(fmaxf(z[h][e], -7.f * scale[h]), 7.f * scale[h]);
+        }
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const float inv = 1.f / scale[h];
+          w[h] = __byte_perm(int4_four(z[h][0], z[h][2], z[h][4], z[h][6], scale[h], inv),
+                             int4_four(z[h][1], z[h][3], z[h][5], z[h][7], scale[h], inv), 0x5410);
         }
 #pragma unroll
         for (int d = 0; d < 3; ++d) {

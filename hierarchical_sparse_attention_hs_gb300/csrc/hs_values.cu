@@ -9,6 +9,9 @@
 // Work. A warp takes ROWS consecutive entries at a time: their list entries in one load, then all their rows' loads in
 // flight together, then the stores. A lane's values lie 32 lanes' worth apart (chunk t of a lane: values (32 t + lane) V on),
 // so that every store instruction of a warp fills 512 consecutive bytes, and every load of codes 128 (4-bit) to 512.
+//
+// Measured on one GB300 (reads and writes over the time): 131,072 4-bit rows into bf16 32.9 us, 6.25 TB/s, 0.92 of the
+// measured copy; 65,536 fp8 rows into fp32 33.6 us, 5.8 TB/s; 771 rows 2.2 us, a launch's own cost.
 
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -32,7 +35,10 @@ using namespace hs;
 
 constexpr int THREADS = 256, WARPS = THREADS / 32;
 constexpr int ROWS = 4;          // rows of a warp in flight
-constexpr int BLOCKS = 8;        // blocks an SM, at most
+// Blocks an SM, at most: 131,072 4-bit rows into bf16 took 32.9 us with 16 (37.0 with 8, 32.6 with 32), 65,536 fp8 rows into
+// fp32 33.6 with 8 (34.4 with 16, 35.2 with 4). Four rows in flight: 37.0 and 33.6 us with eight blocks, against 36.3 and 34.3
+// with two rows, 34.6 and 38.3 with eight.
+constexpr int BLOCKS_16 = 16, BLOCKS_32 = 8;
 constexpr int64_t MAX_ENTRIES = 1 << 30;
 
 struct ValuesArgs {
@@ -195,7 +201,7 @@ int launch_values(hs_pool* p, int32_t batch, const int32_t* idx, int32_t k, cons
   a.dst = static_cast<uint8_t*>(dst);
   cudaLaunchConfig_t cfg = {};
   const uint32_t per = WARPS * ROWS;
-  cfg.gridDim = dim3(std::min<uint32_t>((a.entries + per - 1) / per, (uint32_t)p->num_sms * BLOCKS), 1, 1);
+  cfg.gridDim = dim3(std::min<uint32_t>((a.entries + per - 1) / per, (uint32_t)p->num_sms * (type == HS_TYPE_F32 ? BLOCKS_32 : BLOCKS_16)), 1, 1);
   cfg.blockDim = dim3(THREADS, 1, 1);
   cfg.stream = reinterpret_cast<cudaStream_t>(stream);
   cudaLaunchAttribute attr;
