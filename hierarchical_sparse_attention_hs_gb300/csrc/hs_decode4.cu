@@ -4,8 +4,9 @@
 //     s[i] = sm_scale * q[b][h] . row_i,   out = sum softmax(s)[i] row_i[0:512],   lse = ln sum e^s[i],
 // the rows' latents being number times scale (hs_rows.cuh).
 //
-// What bounds it. A row is 416 bytes and serves 2 * 128 * (576 + 512) operations, 670 a byte: the tensor cores, once a
-// launch is long enough; one decode step's lists are short, and most of its time is the chain of one launch.
+// What bounds it. A row is 416 bytes and serves 2 * 128 * (576 + 512) operations, 670 a byte: the tensor cores and the shared
+// memory that feeds them. A decode step's lists are short, though, and much of its time is the chain of one launch: the
+// list, the rows it names, the first scores, and at the end the last product, its store and the join of splits.
 //
 // Operands, all of them exact. For the scores the rows' latents become bf16, beside the queries and rotary keys that are; for
 // the value product they become halves, at 2^-6 of their value, beside weights in halves. Rounding the weights, 2^-11 of
@@ -22,10 +23,21 @@
 //     M = max m_s,   total = sum 2^(m_s - M) l_s,   out = sum 2^(m_s - M) O_s / total,   lse = ln 2 (M + log2 total).
 //
 // Warp roles per CTA: 0-7 softmax (warp w: TMEM lanes 32 (w % 4) .. +31, that is head lane % 64 and half lane / 64 of the
-// tile's rows, and rows 64 (w / 4) .. +63 of that half), 8 the issuer (the pair's first CTA issues for both), 9-15 the
-// loaders. K and V pass through one ring of 16 KB stages in the order in which the MMAs read them: a K stage
-// is 64 columns of the CTA's 128 rows, a V stage 128 of its value columns of 64 rows, both 128 rows of 128 bytes, 128-byte
-// swizzle; each feeds four MMAs, 256 cycles. The loaders work side by side, 32 rows by 128 columns each.
+// tile's rows, and rows 64 (w / 4) .. +63 of that half), 8 the issuer (the pair's first CTA issues for both), 9-16 the
+// loaders, which unpack latents, 17 and 18 the rotary keys. K and V pass through one ring of 16 KB stages in the order in which
+// the MMAs read them: a K stage is 64 columns of the CTA's 128 rows, a V stage 128 of its value columns of 64 rows, both 128
+// rows of 128 bytes, 128-byte swizzle; each feeds four MMAs, 256 cycles. The rows' words come into shared memory as they are,
+// by asynchronous copies a job ahead (through registers they were waited for as soon as they were asked for), and are unpacked
+// from there.
+//
+// Measured on one GB300 (replayed graphs): a tile takes 4.1 us, 7,700 cycles, of which its MMAs are 4,352 at their full rate.
+// Shared memory is what it waits for: 2,200 cycles of stores of unpacked rows, 1,100 of the words' way through it, and 96 of its
+// 128 bytes a cycle that MMAs of this shape read while they run, 3,300 or more. 32 requests of 2,048 entries 29.1 us (628
+// TFLOP/s; four tiles a pair, the start, the join), one 16.3, seven 17.8, five of 16,384 46.5, one of 65 8.9. Steps that brought
+// it there, for 32 requests of 2,048: lanes that load a row each 62 us; eight rows by four lanes 40; copies into shared memory,
+// scores in bf16, queries by TMA 34; jobs of 32 rows in a fixed order, the keys by warps of their own 29.1. Not kept: eleven
+// loaders with 96 registers or fewer that take jobs in turn, 30.2 (and a wait that could be lapped); all loaders on one stage
+// pair, 16 rows each, 36; rows brought into L2 by bulk prefetches, whose issue took a warp 2,000 cycles for 32.
 //
 // Waits are bounded: on running out a role sets the abort flag, which ends every role, and the HS_DEVERR_TIMEOUT bit.
 
@@ -65,7 +77,8 @@ constexpr int NSTAGE = 5;          // stages of the ring
 constexpr int OFF_Q = 0;
 constexpr int OFF_RING = OFF_Q + KBLK * BLK_BYTES;
 constexpr int OFF_P = OFF_RING + NSTAGE * STAGE_BYTES;
-constexpr int SOFTMAX_WARPS = 8, MMA_WARP = 8, LOAD_WARP0 = 9, LOADERS = 8, KEY_WARP = LOAD_WARP0 + LOADERS, KEY_WARPS = 2, THREADS = (KEY_WARP + KEY_WARPS) * 32;
+constexpr int SOFTMAX_WARPS = 8, MMA_WARP = 8, LOAD_WARP0 = 9, LOADERS = 8, KEY_WARP = LOAD_WARP0 + LOADERS, KEY_WARPS = 2,
+              THREADS = (KEY_WARP + KEY_WARPS) * 32;
 static_assert(THREADS <= 640, "96 registers a thread: five warps a scheduler");
 // A loader's two jobs as their rows are in memory, 64 bytes of codes (row r: 16-byte chunk j at j ^ (r / 2 % 4)) and eight scales
 // each.
@@ -130,7 +143,8 @@ __device__ __forceinline__ float2 ld_peer2(uint32_t addr) {
 }
 
 // A split's tiles, and where their stages lie in the order K(0) K(1) V(0) K(2) V(1) ... V(n - 1): K's rotary keys in the
-// middle of its latents (stage ROPE_AT). Of the list's last tile only the first `last_segs` segments hold entries: the others are not multiplied with V.
+// middle of its latents (stage ROPE_AT). Of the list's last tile only the first `last_segs` segments hold entries: the others
+// are not multiplied with V.
 struct Tiles {
   int first, n;      // the split's first tile, and how many it has
   int last_segs;     // segments of its last tile
@@ -176,7 +190,7 @@ __global__ void __launch_bounds__(THREADS, 1) hs_decode4_kernel(const Decode4Arg
 
   if (t == 0) {
     for (int i = 0; i < NBAR; ++i) bar_init(bar + i, 1);
-    // one arrival for each softmax warp of the pair; four of each CTA for a stage
+    // one arrival for each softmax warp of the pair; four of each CTA's loaders for a stage
     for (int i = 0; i < NSTAGE; ++i) bar_init(bar + B_FULL + i, 8);
     for (int i = 0; i < 2; ++i) bar_init(bar + B_SFREE + i, 2 * SOFTMAX_WARPS);
     bar_init(bar + B_PFULL, 2 * SOFTMAX_WARPS);
@@ -238,7 +252,8 @@ __global__ void __launch_bounds__(THREADS, 1) hs_decode4_kernel(const Decode4Arg
           for (int c = 0; c < KBLK && ok; ++c) {
             ok = wait(B_FULL + st, ph);
             tc_fence_after();
-            if (ok) four(tmem + TMEM_S + (uint32_t)(g & 1) * KH, dq + (uint64_t)((c < ROPE_AT ? c : c == ROPE_AT ? KBLK - 1 : c - 1) * (BLK_BYTES >> 4)),
+            const int blk = c < ROPE_AT ? c : c == ROPE_AT ? KBLK - 1 : c - 1;
+            if (ok) four(tmem + TMEM_S + (uint32_t)(g & 1) * KH, dq + (uint64_t)(blk * (BLK_BYTES >> 4)),
                          dk + (uint64_t)(st * (STAGE_BYTES >> 4)), 2, ID_S, c != 0 ? 1u : 0u);
           }
           if (!ok) break;
@@ -264,9 +279,10 @@ __global__ void __launch_bounds__(THREADS, 1) hs_decode4_kernel(const Decode4Arg
     }
     __syncwarp();
   } else if (warp >= KEY_WARP) {
-    // ---- the rotary keys of the CTA's half of every tile, 64 rows a warp, as they are: 16 bytes a copy, eight lanes a row. Their stage's place is
-    //      free when the V before this K has been multiplied (of the second K: when the first one has). The rows as a whole come
-    //      into L2 two tiles ahead: their words come in nine pieces, over the time of a tile.
+    // ---- the rotary keys of the CTA's half of every tile, 64 rows a warp, as they are: 16 bytes a copy, eight lanes a row. Their
+    //      place in the ring is free when the V before this K has been multiplied (of the second K: when the first one has;
+    //      either wait is for a phase that the next one of its barrier cannot follow before these keys are there). The rows as a
+    //      whole come into L2 a tile ahead of their first words, which are asked for in nine pieces over the time of a tile.
     ok = !a.stall || __all_sync(0xffffffffu, bar_wait(bar + B_STALL, 0, abort_flag, lim));
     const int r8 = lane & 7, qd = lane >> 3, part = warp - KEY_WARP;
     unsigned long long row[2], later[2];  // of the lane's rows: of this tile, and of the next
@@ -328,9 +344,8 @@ __global__ void __launch_bounds__(THREADS, 1) hs_decode4_kernel(const Decode4Arg
     copies_wait<0>();
     __syncwarp();
   } else if (warp >= LOAD_WARP0) {
-    // ---- a loader. All of them work side by side, a job each: of K's latents first on 128 columns a group of four (32 rows
-    //      each), then on the other two 128s; of V on two segments (32 rows by 128 columns each), then on the other two. The next
-    //      job's words are under way while this job's are unpacked.
+    // ---- a loader. All of them work side by side, 32 rows by 128 columns each: of K's latents first on 128 columns a group of four,
+    //      then on the other two 128s; of V on two segments, then on the other two. Two jobs' words are on their way.
     ok = !a.stall || __all_sync(0xffffffffu, bar_wait(bar + B_STALL, 0, abort_flag, lim));
     const int r8 = lane & 7, qd = lane >> 3, wl = warp - LOAD_WARP0, grp = wl >> 2;
     if (wl == 0 && lane == 0 && ok) {
@@ -358,7 +373,7 @@ __global__ void __launch_bounds__(THREADS, 1) hs_decode4_kernel(const Decode4Arg
         *reinterpret_cast<uint2*>(scales) = make_uint2(0, 0);
       const uint32_t to = su32(raw + par * RAW_JOB + (lane >> 2) * 64 + (((lane & 3) ^ (lane >> 3 & 3)) << 4));
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
+      for (int i = 0; i < 4; ++i) {  // (the swizzle of rows 8 apart is the same)
         const Address p = __shfl_sync(0xffffffffu, mine, 8 * i + (lane >> 2));
         if (p) copy16(to + i * 512, p + col / 2 + 16 * (lane & 3));
       }
@@ -375,9 +390,9 @@ __global__ void __launch_bounds__(THREADS, 1) hs_decode4_kernel(const Decode4Arg
       }
       __syncwarp();
     };
-    // Waits until the MMAs that read the stage NSTAGE before stage n have finished: n takes its place. A barrier's parity tells
-    // its last two phases apart, so the wait holds only if that place's phase before is over; it is, as a loader has a part in
-    // at least one of any NSTAGE stages in a row, and waited for one of those before that.
+    // Waits until the MMAs that read the stage NSTAGE before stage n have finished: n takes its place. A barrier's parity only
+    // tells a phase from its neighbours. The phase after cannot be over: it takes this loader's part of stage n. The phase
+    // before is: stages that a loader has a part in are at most four apart, and it has waited for the last one's place.
     auto need = [&](int n) {
       if (n >= NSTAGE && ok)
         ok = __all_sync(0xffffffffu, bar_wait(bar + B_EMPTY + n % NSTAGE, (unsigned)(n / NSTAGE - 1) & 1u, abort_flag, lim));
@@ -408,8 +423,7 @@ __global__ void __launch_bounds__(THREADS, 1) hs_decode4_kernel(const Decode4Arg
     uint32_t sc[4];
     Address krows = at(entry(0, krow));
     int32_t ek = entry(1, krow), ev0 = entry(0, vrow), ev1 = entry(0, vrow + 2 * SEG);
-    // Two jobs are on their way, each in the buffer of the one before the last: a job's words are awaited, read, the buffer's next
-    // copies started, and the words unpacked.
+    // A job's words are awaited and read, the copies of the job after the next started into their place, and the words unpacked.
     load(0, krows, kcol);
     load(1, krows, kcol + 256);
     // step t: K(t), then V(t - 1)
@@ -471,8 +485,9 @@ __global__ void __launch_bounds__(THREADS, 1) hs_decode4_kernel(const Decode4Arg
       return share + r;
     };
     const bool up = a.scale_log2 > 0.f;
-    const float factor = a.scale_log2, scale = up ? factor : 1.f;  // the maximum is taken before a positive scale; another is applied first
-    int32_t e0, e1;                               // the thread's entries of the tile's mask: rows lane and lane + 32 of its segment
+    // the maximum is taken before a positive scale; another is applied first
+    const float factor = a.scale_log2, scale = up ? factor : 1.f;
+    int32_t e0, e1;  // the thread's entries of the tile's mask: rows lane and lane + 32 of its segment
     auto entries = [&](int tile) {
       const int key = (tiles.first + tile) * NK + sg * SEG + lane;
       e0 = key < a.k ? ld_fresh(list + key) : -1;
@@ -745,8 +760,9 @@ int resident(int n) {
   return got;
 }
 
-// The splits of a list with the shortest expected time, in tiles: waves of clusters, each of its tiles and about two more
-// (its start, its last softmax and its output), and with splits the join.
+// The splits of a list with the shortest expected time, in tiles (4.1 us): waves of clusters, each of its tiles and about two
+// more (its start, its last softmax and its output), and with splits the join (2.8 us of two, 5 of eight). One request of 2,048:
+// 38.2, 25.3, 18.1 and 16.3 us with 1, 2, 4 and 8; 32 of them 40.3, 28.9 and 28.8 with 1, 2 and 4.
 int cut_of(int32_t batch, int32_t k) {
   const int tiles = (k + NK - 1) / NK;
   int best = 0;
