@@ -459,12 +459,13 @@ int hs_mla_prefix_workspace_bound(hs_pool *pool, int32_t batch, int32_t max_leng
  * out it stops every role, frees its tensor memory, returns and sets HS_DEVERR_TIMEOUT.
  *   wait_limit: polling rounds after which a wait of the kernel's roles gives up (0 restores the default, 2^20); it also
  *     gives up after two seconds.
- *   stall != 0: the tensor-core issuer of every CTA (and the loaders of hs_mla_prefix) first waits on a barrier that
+ *   stall != 0: the tensor-core issuer of every CTA (and the loaders of hs_mla_prefix and hs_mla_decode_int4) first waits on a barrier that
  *     nothing completes, so that wait runs out before any tensor-core work or row copy of the kernel is issued, and
  *     the abort path runs with nothing in flight. 0 restores normal operation.
  *   split_max_batch: if non-NULL, receives the largest batch for which hs_mla_decode splits a request's keys over
  *     two CTA pairs on the current device (larger batches run one pair per request).
- * Applies to the hs_mla_decode / hs_mla_decode_history / hs_mla_prefix calls made after it.
+ * Applies to the hs_mla_decode / hs_mla_decode_history / hs_mla_decode_int4 (and its history form) / hs_mla_prefix calls made
+ * after it.
  */
 int hs_debug_attention(uint32_t wait_limit, int32_t stall, int32_t *split_max_batch);
 

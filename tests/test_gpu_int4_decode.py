@@ -359,3 +359,83 @@ def test_a_decode_step():
             assert np.array_equal(now[b, int(pos[b]), :288], ora.pack(kv[b:b + 1, :512].float().cpu().numpy())[0])
         assert hs.hs_get_error(pool) == 0
     buf.close()
+
+
+@pytest.mark.parametrize("batch,k", [(1, 200), (1, 3000), (20, 1100)])
+def test_a_wait_that_runs_out(batch, k):
+    """With the stall hook nothing is copied or multiplied: every role's wait runs out, the kernel returns, the error word says
+    so, and the next call is right."""
+    c = Case(batch, k, slots=300, seed=50)
+    hs.hs_debug_attention(64, True)
+    try:
+        c.run()
+        torch.cuda.synchronize()
+    finally:
+        hs.hs_debug_attention()
+    assert hs.hs_get_error(c.pool, clear=True) == hs.HS_DEVERR_TIMEOUT
+    c.check(*c.run(), requests=sorted({0, batch - 1}))
+    c.close()
+
+
+def test_captured_before_any_other_call():
+    """Nothing has been called before in the process: the first call of each operator is captured, and replayed."""
+    import os
+    import subprocess
+    import sys
+
+    code = """
+import sys
+sys.path[:0] = [%r, %r]
+import torch, hierarchical_sparse_attention_hs_gb300 as hs
+import test_gpu_int4_decode as t, test_gpu_int4_rows as rows
+cases = [t.Case(1, 2048, slots=2048, seed=60), t.Case(3, 40, slots=64, seed=61)]
+outs = [[torch.zeros(c.batch, 128, 512, dtype=torch.bfloat16, device="cuda"), torch.zeros(c.batch, 128, device="cuda")] for c in cases]
+vals = torch.zeros(3, 40, 576, device="cuda")
+s = torch.cuda.Stream()
+torch.cuda.synchronize()
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g, stream=s):
+    for c, o in zip(cases, outs):
+        c.run(out=o[0], lse=o[1])
+    hs.hs_gather_values(cases[1].pool, 1, 3, cases[1].e, 40, None, 0, vals, hs.HS_TYPE_F32)
+for _ in range(2):
+    g.replay()
+for c, o in zip(cases, outs):
+    c.check(*o)
+want = t.ora.values(cases[1].rows(2))
+assert (vals[2].double().cpu().numpy() == want).all()
+print("right")
+""" % (os.path.dirname(os.path.dirname(os.path.abspath(__file__))), os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and "right" in r.stdout, r.stderr[-2000:]
+
+
+def test_back_to_back_calls_read_what_the_call_before_wrote():
+    """Appends and attention by turns on one stream, without a pause: each attention sees the rows of the append before it."""
+    batch, ctx = 3, 600
+    buf = hs.PoolBuffers(1, batch, ctx, 16, 8, 416, noio=True)
+    buf.host.numpy()[:] = model_rows(batch * ctx, 70).reshape(-1)
+    buf.upload_noio()
+    pool = buf.create()
+    freq = torch.zeros(32, device="cuda")
+    g = torch.Generator().manual_seed(7)
+    steps = [torch.randn(batch * ctx, 576, generator=g).to(torch.bfloat16).cuda() for _ in range(4)]
+    req = torch.arange(batch, dtype=torch.int32).repeat_interleave(ctx).cuda()
+    pos = torch.arange(ctx, dtype=torch.int32).repeat(batch).cuda()
+    topk = torch.stack([torch.randperm(ctx, generator=g) for _ in range(batch)]).int().cuda()
+    q = torch.randn(batch, H, DQK, generator=g).to(torch.bfloat16).cuda()
+    outs = [(torch.empty(batch, H, DV, device="cuda"), torch.empty(batch, H, device="cuda")) for _ in steps]
+    descs = [hs.append_desc(kv, freq, pos, req_ids=req) for kv in steps]
+    torch.cuda.synchronize()
+    for d, (out, lse) in zip(descs, outs):
+        hs.hs_append(pool, 0, batch * ctx, d, None, True)
+        hs.hs_mla_decode_int4_history(pool, 0, batch, q, topk, ctx, SCALE, out, hs.HS_TYPE_F32, lse)
+    torch.cuda.synchronize()
+    for kv, (out, lse) in zip(steps, outs):
+        kv = kv.float().cpu().numpy()
+        for b in range(batch):
+            mine = kv[b * ctx:(b + 1) * ctx]
+            key = torch.from_numpy(mine[:, 512:]).to(torch.bfloat16).view(torch.uint8).numpy()
+            rows = ora.values(np.concatenate([ora.pack(mine[:, :512]), key], 1))
+            check_request(q[b], rows[topk[b].cpu().numpy()], SCALE, out[b], lse[b], b)
+    buf.close()
