@@ -20,7 +20,7 @@
 // Measured on one GB300 (reads and writes over the time): 1 to 32 tokens with 128 heads 2.1-2.2 us, a launch's own cost;
 // 256 2.8 us; 2,047 with 128 heads 18.5 us from fp32 (5.8 TB/s) and 13.5 from bf16; 131,071 without queries 50 us into bf16
 // rows (6.1 TB/s) and 50 into fp8 rows (4.8: 339 instructions a row, which take 38 us where every scheduler issues one a
-// cycle; 0.73 are measured); 4,096 into host memory 17.5 us for fp8 rows and 26 for bf16, 153 and 180 GB/s of writes over the
+// cycle; 0.73 are measured); 131,071 into 4-bit rows 54 with a norm and 47 without (4.4 TB/s), issue too; 4,096 into host memory 17.5 us for fp8 rows and 26 for bf16, 153 and 180 GB/s of writes over the
 // link.
 
 #include <cuda_bf16.h>
@@ -56,9 +56,10 @@ constexpr int THREADS = 128, WARPS = THREADS / 32;
 // 10.6 / 6.0), from fp32 61.0 / 10.6 / 6.4 (of 6 63.2 / 11.1 / 7.3, of 5 64.5 / 11.3 / 6.7, twelve blocks 65.7 / 13.1 /
 // 6.5). For 1152-byte rows the compiler's own choice is kept, 8 blocks from 16 bits, 50.2 / 8.9 / 5.3 (a bound of 7 50.3
 // / 8.8 / 5.0, of 6 52.9 / 9.2 / 5.6; one of 8 took the queries of 256 and 2,047 tokens from 2.8 and 13.4 to 3.05 and
-// 14.0), 6 from fp32, 70.3 / 11.4 / 6.4 (a bound of 7 73.4 / 10.9 / 5.6, of 5 70.9 / 11.7 / 5.8).
+// 14.0), 6 from fp32, 70.3 / 11.4 / 6.4 (a bound of 7 73.4 / 10.9 / 5.6, of 5 70.9 / 11.7 / 5.8). For 416-byte rows a
+// bound of 7, from 16 bits with a norm 54.3 / 9.5 / 6.2 (none 54.9 / 10.6 / 6.7, one of 8 55.1 / 10.6 / 6.7).
 template <Row R>
-constexpr int MIN_BLOCKS = R == FP8 ? 7 : 0;  // 0: none
+constexpr int MIN_BLOCKS = R == BF16 ? 0 : 7;  // 0: none
 constexpr int Q_BLOCKS = 16;  // blocks of queries an SM, at most
 
 struct AppendArgs {
@@ -147,12 +148,9 @@ __device__ __forceinline__ float max_nan(float a, float b, float c) {
   asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(m) : "f"(fabsf(a)), "f"(fabsf(b)), "f"(fabsf(c)));
   return m;
 }
-// The quotient z / scale, `inv` being 1 / scale, corrected once by its residual, which an fma has exactly (Markstein): where z /
-// scale is a 32-bit number, a half of a whole number among them, it is that number, so ties are ties. Adding 1.5 * 2^23 + 8
-// leaves the nearest whole number, ties to even, plus 8 in the low bits.
+// z / scale to the nearest whole number, ties to even, plus 8, in the low bits: adding 1.5 * 2^23 leaves it there.
 __device__ __forceinline__ uint32_t int4_of(float z, float scale, float inv) {
-  const float y = z * inv;
-  return __float_as_uint(fmaf(fmaf(-y, scale, z), inv, y) + (12582912.f + 8.f));
+  return __float_as_uint(quotient(z, scale, inv) + (12582912.f + 8.f));
 }
 // Four of them at bits 0, 4, 8 and 12: above the number a float's bits hold a multiple of 2^22, which shifts out of the low 16.
 __device__ __forceinline__ uint32_t int4_four(float a, float b, float c, float d, float scale, float inv) {
@@ -321,7 +319,8 @@ __device__ __forceinline__ void append_rows(const AppendArgs& a, float* weight, 
         }
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          const float inv = 1.f / scale[h];
+          float inv;
+          asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(scale[h]));
           w[h] = __byte_perm(int4_four(z[h][0], z[h][2], z[h][4], z[h][6], scale[h], inv),
                              int4_four(z[h][1], z[h][3], z[h][5], z[h][7], scale[h], inv), 0x5410);
         }

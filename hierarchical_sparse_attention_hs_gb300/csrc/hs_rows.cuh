@@ -36,11 +36,19 @@ constexpr int ROW_INT4 = INT4_ROPE + ROPE * 2;      // 416
 constexpr float INT4_SCALE_MIN = 7.62939453125e-06f, INT4_SCALE_MAX = 3840.f;  // 2^-17 and 1.875 * 2^11
 constexpr uint32_t INT4_SCALE_NAN = 255;            // a block with a latent that is not finite: it reads back as NaN
 
+// z / d, `inv` being 1 / d to a unit in its last place: the product, corrected once by its residual, which an fma has exactly
+// (Markstein). Where z / d is a 32-bit number the result is that number, so that what lies halfway between two codes does.
+__device__ __forceinline__ float quotient(float z, float d, float inv) {
+  const float y = z * inv;
+  return fmaf(fmaf(-y, d, z), inv, y);
+}
+
 // The code of the scale for a largest magnitude (a NaN or an infinity: that of NaN): amax / 7 to the nearest scale, ties to
 // the even code.
 __device__ __forceinline__ uint32_t int4_scale_code(float amax) {
   if (!(amax <= 3.4028234664e38f)) return INT4_SCALE_NAN;
-  const float a = fminf(fmaxf(__fdiv_rn(amax, 7.f), INT4_SCALE_MIN), INT4_SCALE_MAX);
+  const float m = fminf(fmaxf(amax, 7.f * INT4_SCALE_MIN), 7.f * INT4_SCALE_MAX);
+  const float a = quotient(m, 7.f, 1.f / 7.f);
   if (a < 6.103515625e-05f) return (uint32_t)__float2int_rn(a * 131072.f);  // below 2^-14: multiples of 2^-17
   uint32_t b = __float_as_uint(a);
   b += 0x7ffffu + (b >> 20 & 1u);
