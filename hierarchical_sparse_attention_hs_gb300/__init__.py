@@ -401,43 +401,52 @@ def hs_mla_prefix_workspace_bound(pool: int, batch: int, max_length: int) -> int
     return int(n.value)
 
 
-def _check_lists(what: str, pool: int, batch: int, entries, k: int, rows, count: int) -> None:
-    row_bytes = _pool_row_bytes.get(pool, 0)
-    i32 = (_dtypes or _load_dtypes())[2]
-    if not _fits(entries, i32, batch * k * 4):
+_value_types = None  # of each HS_TYPE_*: torch's type, and the bytes of 576 values
+
+
+def _load_value_types():
+    global _value_types
+    bf16, f32, _, f16 = _dtypes or _load_dtypes()
+    _value_types = {HS_TYPE_BF16: (bf16, 2 * MLA_D_QK), HS_TYPE_F16: (f16, 2 * MLA_D_QK), HS_TYPE_F32: (f32, 4 * MLA_D_QK)}
+    return _value_types
+
+
+def _check_lists(what: str, pool: int, batch: int, entries, k: int, rows=None, count: int = 0) -> None:
+    if not _fits(entries, (_dtypes or _load_dtypes())[2], batch * k * 4):
         raise ValueError(f"{what} takes a contiguous int32 list [{batch}][{k}]")
-    if rows is not None and not isinstance(rows, int) and not (rows.is_contiguous() and rows.nbytes >= count * row_bytes):
-        raise ValueError(f"{what} takes contiguous resident rows, {count} of {row_bytes} bytes")
+    if rows is not None and not isinstance(rows, int):
+        row_bytes = _pool_row_bytes.get(pool, 0)
+        if rows.nbytes < count * row_bytes or not rows.is_contiguous():
+            raise ValueError(f"{what} takes contiguous resident rows, {count} of {row_bytes} bytes")
 
 
 def _check_values(what: str, batch: int, k: int, dst, dst_type: int) -> None:
-    bf16, f32, _, f16 = _dtypes or _load_dtypes()
-    dtype = {HS_TYPE_BF16: bf16, HS_TYPE_F16: f16, HS_TYPE_F32: f32}.get(dst_type)
-    if dtype is not None and not _fits(dst, dtype, batch * k * MLA_D_QK * dtype.itemsize):
-        raise ValueError(f"{what} writes a contiguous {dtype} [{batch}][{k}][{MLA_D_QK}]")
+    # (of a type that there is not the library says so)
+    t = (_value_types or _load_value_types()).get(dst_type)
+    if t is not None and not _fits(dst, t[0], batch * k * t[1]):
+        raise ValueError(f"{what} writes a contiguous {t[0]} [{batch}][{k}][{MLA_D_QK}]")
 
 
 def hs_gather_values(pool: int, layer: int, batch: int, out_slots, k: int, resident_rows, resident_count: int, dst,
                      dst_type: int, stream=None) -> None:
     _check_lists("hs_gather_values", pool, batch, out_slots, k, resident_rows, resident_count)
     _check_values("hs_gather_values", batch, k, dst, dst_type)
-    _check(load().hs_gather_values(pool, layer, batch, _addr(out_slots), k, _addr(resident_rows), resident_count, _addr(dst),
-                                   dst_type, _stream(stream)), "hs_gather_values")
+    _check((_lib or load()).hs_gather_values(pool, layer, batch, _addr(out_slots), k, _addr(resident_rows), resident_count,
+                                             _addr(dst), dst_type, _stream(stream)), "hs_gather_values")
 
 
 def hs_gather_values_history(pool: int, layer: int, batch: int, topk_idx, k: int, dst, dst_type: int, stream=None) -> None:
-    _check_lists("hs_gather_values_history", pool, batch, topk_idx, k, None, 0)
+    _check_lists("hs_gather_values_history", pool, batch, topk_idx, k)
     _check_values("hs_gather_values_history", batch, k, dst, dst_type)
-    _check(load().hs_gather_values_history(pool, layer, batch, _addr(topk_idx), k, _addr(dst), dst_type, _stream(stream)),
-           "hs_gather_values_history")
+    _check((_lib or load()).hs_gather_values_history(pool, layer, batch, _addr(topk_idx), k, _addr(dst), dst_type,
+                                                     _stream(stream)), "hs_gather_values_history")
 
 
 def _check_heads(what: str, batch: int, q, out, out_type: int, lse) -> None:
     bf16, f32, _, _ = _dtypes or _load_dtypes()
     rows = batch * MLA_HEADS
-    dtype = f32 if out_type == HS_TYPE_F32 else bf16
-    if not (_fits(q, bf16, rows * MLA_D_QK * 2) and _fits(out, dtype, rows * MLA_D_V * dtype.itemsize) and
-            _fits(lse, f32, rows * 4)):
+    dtype, size = (f32, 4) if out_type == HS_TYPE_F32 else (bf16, 2)
+    if not (_fits(q, bf16, rows * (2 * MLA_D_QK)) and _fits(out, dtype, rows * (size * MLA_D_V)) and _fits(lse, f32, rows * 4)):
         raise ValueError(f"{what} of {batch} takes contiguous tensors: q bf16 [{batch}][128][576], out {dtype} "
                          f"[{batch}][128][512], lse fp32 [{batch}][128]")
 
@@ -446,16 +455,17 @@ def hs_mla_decode_int4(pool: int, layer: int, batch: int, q, out_slots, k: int, 
                        sm_scale: float, out, out_type: int, lse, stream=None) -> None:
     _check_lists("hs_mla_decode_int4", pool, batch, out_slots, k, resident_rows, resident_count)
     _check_heads("hs_mla_decode_int4", batch, q, out, out_type, lse)
-    _check(load().hs_mla_decode_int4(pool, layer, batch, _addr(q), _addr(out_slots), k, _addr(resident_rows), resident_count,
-                                     sm_scale, _addr(out), out_type, _addr(lse), _stream(stream)), "hs_mla_decode_int4")
+    _check((_lib or load()).hs_mla_decode_int4(pool, layer, batch, _addr(q), _addr(out_slots), k, _addr(resident_rows),
+                                               resident_count, sm_scale, _addr(out), out_type, _addr(lse), _stream(stream)),
+           "hs_mla_decode_int4")
 
 
 def hs_mla_decode_int4_history(pool: int, layer: int, batch: int, q, topk_idx, k: int, sm_scale: float, out, out_type: int,
                                lse, stream=None) -> None:
-    _check_lists("hs_mla_decode_int4_history", pool, batch, topk_idx, k, None, 0)
+    _check_lists("hs_mla_decode_int4_history", pool, batch, topk_idx, k)
     _check_heads("hs_mla_decode_int4_history", batch, q, out, out_type, lse)
-    _check(load().hs_mla_decode_int4_history(pool, layer, batch, _addr(q), _addr(topk_idx), k, sm_scale, _addr(out), out_type,
-                                             _addr(lse), _stream(stream)), "hs_mla_decode_int4_history")
+    _check((_lib or load()).hs_mla_decode_int4_history(pool, layer, batch, _addr(q), _addr(topk_idx), k, sm_scale, _addr(out),
+                                                       out_type, _addr(lse), _stream(stream)), "hs_mla_decode_int4_history")
 
 
 def hs_get_error(pool: int, clear: bool = False) -> int:

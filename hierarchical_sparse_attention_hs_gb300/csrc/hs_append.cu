@@ -17,11 +17,11 @@
 // whole 128-byte segments and the norm's sum and the scales' maxima are warp shuffles. Only the norm's weights
 // pass through shared memory.
 //
-// Measured on one GB300 (reads and writes over the time): 1 to 32 tokens with 128 heads 2.1-2.2 us, a launch's own cost;
-// 256 2.8 us; 2,047 with 128 heads 18.5 us from fp32 (5.8 TB/s) and 13.5 from bf16; 131,071 without queries 50 us into bf16
-// rows (6.1 TB/s) and 50 into fp8 rows (4.8: 339 instructions a row, which take 38 us where every scheduler issues one a
-// cycle; 0.73 are measured); 131,071 into 4-bit rows 54 with a norm and 47 without (4.4 TB/s), issue too; 4,096 into host memory 17.5 us for fp8 rows and 26 for bf16, 153 and 180 GB/s of writes over the
-// link.
+// Measured on one GB300 (reads and writes over the time): 1 to 32 tokens with 128 heads 2.1-2.2 us, a launch's own cost; 256
+// 2.8 us; 2,047 with 128 heads 18.5 us from fp32 (5.8 TB/s) and 13.5 from bf16; 131,071 without queries 50 us into bf16 rows
+// (6.1 TB/s) and 50 into fp8 rows (4.8: 339 instructions a row, which take 38 us where every scheduler issues one a cycle;
+// 0.73 are measured); 131,071 into 4-bit rows 54 with a norm and 47 without (4.4 TB/s), issue too; 4,096 into host memory
+// 17.5 us for fp8 rows and 26 for bf16, 153 and 180 GB/s of writes over the link.
 
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>

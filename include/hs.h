@@ -377,9 +377,9 @@ int hs_append(hs_pool *pool, int32_t layer, int32_t ntok, const hs_append_desc *
  *   out_slots: int32 [batch][k] as a resolve wrote it (device or mapped host memory, 4-byte aligned): an entry >= 0 names
  *     hot slot `entry` of `layer`, an entry <= -2 row -2 - entry of resident_rows (device memory, count rows of row_bytes,
  *     16-byte aligned; NULL for none); anything else, or a row past the end, names none. k is not bound by topk_max.
- *   dst: device memory [batch][k][576] of dst_type (any HS_TYPE_*), 16-byte aligned; it overlaps no input. Each value is rounded once: those
- *     of 416-byte rows are exact in bf16 and fp16 (but for a rotary key past fp16's range), those of 1152-byte rows in
- *     bf16; of 656-byte rows the product of value and scale is formed in 32 bits.
+ *   dst: device memory [batch][k][576] of dst_type (any HS_TYPE_*), 16-byte aligned; it overlaps no input. Each value is
+ *     rounded once: latents of 416-byte rows are exact in bf16 and fp16, and 1152-byte rows and every rotary key in bf16
+ *     (past fp16's range a value becomes infinite); of 656-byte rows the product of value and scale is formed in 32 bits.
  * batch * k <= 2^30; batch == 0 or k == 0 is a no-op. Enqueued on `stream` (of the pool's device, which must be the current
  * one: HS_ERR_INVALID_ARG); capturable. Basis: as hs_gather; the pages leave the row format open.
  */
@@ -400,9 +400,12 @@ int hs_gather_values_history(hs_pool *pool, int32_t layer, int32_t batch, const 
  * Rows that no entry names are not read, whatever they hold. With no row a head's output is zero and its lse -inf.
  *   q: device bf16 [batch][128][576], 16-byte aligned. out: [batch][128][512] of out_type (HS_TYPE_BF16 or HS_TYPE_F32),
  *     16-byte aligned; lse: fp32 [batch][128]. They overlap no input.
- * batch <= 65536, k <= 2^30 and not bound by topk_max; batch == 0 or k == 0 is a no-op. Results are deterministic for given batch, k and
- * device. Enqueued on `stream` (of the pool's device, which must be the current one: HS_ERR_INVALID_ARG); capturable.
- * Basis: as hs_mla_decode.
+ * batch <= 65536, k <= 2^30 and not bound by topk_max; batch == 0 or k == 0 is a no-op (out and lse stay as they are). The
+ * weights are rounded to fp16 before the value product, whose other operand is exact in fp16 (2^-11 of each weight, which
+ * leaves outputs about 0.00014 off in the mean before their own rounding); scores are of exact operands, and scores, sums
+ * and outputs accumulate in 32 bits; the normaliser and lse sum the unrounded weights. Results are deterministic for given
+ * batch, k and device. Enqueued on `stream` (of the pool's device, which must be the current one: HS_ERR_INVALID_ARG);
+ * capturable. Basis: as hs_mla_decode.
  */
 int hs_mla_decode_int4(hs_pool *pool, int32_t layer, int32_t batch, const void *q, const int32_t *out_slots, int32_t k,
                        const void *resident_rows, int64_t resident_count, float sm_scale, void *out, int32_t out_type,
@@ -459,9 +462,9 @@ int hs_mla_prefix_workspace_bound(hs_pool *pool, int32_t batch, int32_t max_leng
  * out it stops every role, frees its tensor memory, returns and sets HS_DEVERR_TIMEOUT.
  *   wait_limit: polling rounds after which a wait of the kernel's roles gives up (0 restores the default, 2^20); it also
  *     gives up after two seconds.
- *   stall != 0: the tensor-core issuer of every CTA (and the loaders of hs_mla_prefix and hs_mla_decode_int4) first waits on a barrier that
- *     nothing completes, so that wait runs out before any tensor-core work or row copy of the kernel is issued, and
- *     the abort path runs with nothing in flight. 0 restores normal operation.
+ *   stall != 0: the tensor-core issuer of every CTA (and the loaders of hs_mla_prefix and hs_mla_decode_int4) first waits
+ *     on a barrier that nothing completes, so that wait runs out before any tensor-core work or row copy of the kernel is
+ *     issued, and the abort path runs with nothing in flight. 0 restores normal operation.
  *   split_max_batch: if non-NULL, receives the largest batch for which hs_mla_decode splits a request's keys over
  *     two CTA pairs on the current device (larger batches run one pair per request).
  * Applies to the hs_mla_decode / hs_mla_decode_history / hs_mla_decode_int4 (and its history form) / hs_mla_prefix calls made

@@ -119,6 +119,7 @@ got = dict(values=[grid(values, batch=1, k=k) for k in (1, 32, 33, 64, 65, 1 << 
 def test_the_binding_refuses_tensors_of_another_type_or_size(monkeypatch):
     """Refused before the library is called; addresses pass, as nothing is known of them."""
     monkeypatch.setitem(hs._pool_row_bytes, 7, 416)
+    monkeypatch.setattr(hs, "_lib", None)
     monkeypatch.setattr(hs, "load", lambda: (_ for _ in ()).throw(KeyError("called")))
     idx, rows = torch.zeros(2, 3, dtype=torch.int32), torch.zeros(9, 416, dtype=torch.uint8)
     dst, q = torch.zeros(2, 3, 576, dtype=torch.bfloat16), torch.zeros(2, 128, 576, dtype=torch.bfloat16)
