@@ -133,7 +133,10 @@ __device__ __forceinline__ void copies_wait() {  // all but the last N groups
 }
 __device__ __forceinline__ float4 ld_peer(uint32_t addr) {
   float4 v;
-  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr) : "memory");
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(addr)
+               : "memory");
   return v;
 }
 __device__ __forceinline__ float2 ld_peer2(uint32_t addr) {
@@ -166,10 +169,12 @@ __device__ __forceinline__ void unpack(uint8_t* row, int swizzle, int ch, uint4 
     for (int i = 2 * g; i < 2 * g + 2; ++i) {
       uint4 v;
       if constexpr (K) {
-        const __nv_bfloat162 h[4] = {int4_pair(w[i], k), int4_pair(w[i] >> 4, k), int4_pair(w[i] >> 8, k), int4_pair(w[i] >> 12, k)};
+        const __nv_bfloat162 h[4] = {int4_pair(w[i], k), int4_pair(w[i] >> 4, k), int4_pair(w[i] >> 8, k),
+                                     int4_pair(w[i] >> 12, k)};
         v = *reinterpret_cast<const uint4*>(h);
       } else {
-        const __half2 h[4] = {int4_pair<0>(w[i], k), int4_pair<1>(w[i], k), int4_pair<0>(w[i] >> 8, k), int4_pair<1>(w[i] >> 8, k)};
+        const __half2 h[4] = {int4_pair<0>(w[i], k), int4_pair<1>(w[i], k), int4_pair<0>(w[i] >> 8, k),
+                              int4_pair<1>(w[i] >> 8, k)};
         v = *reinterpret_cast<const uint4*>(h);
       }
       *reinterpret_cast<uint4*>(row + (((ch + i) ^ swizzle) << 4)) = v;
@@ -279,10 +284,10 @@ __global__ void __launch_bounds__(THREADS, 1) hs_decode4_kernel(const Decode4Arg
     }
     __syncwarp();
   } else if (warp >= KEY_WARP) {
-    // ---- the rotary keys of the CTA's half of every tile, 64 rows a warp, as they are: 16 bytes a copy, eight lanes a row. Their
-    //      place in the ring is free when the V before this K has been multiplied (of the second K: when the first one has;
-    //      either wait is for a phase that the next one of its barrier cannot follow before these keys are there). The rows as a
-    //      whole come into L2 a tile ahead of their first words, which are asked for in nine pieces over the time of a tile.
+    // ---- the rotary keys of the CTA's half of every tile, 64 rows a warp, as they are: 16 bytes a copy, eight lanes a row.
+    //      Their place in the ring is free when the V before this K has been multiplied (of the second K: when the first one
+    //      has; either wait is for a phase that the next one of its barrier cannot follow before these keys are there). The
+    //      rows as a whole come into L2 a tile ahead of their first words, asked for in nine pieces over the time of a tile.
     ok = !a.stall || __all_sync(0xffffffffu, bar_wait(bar + B_STALL, 0, abort_flag, lim));
     const int r8 = lane & 7, qd = lane >> 3, part = warp - KEY_WARP;
     unsigned long long row[2], later[2];  // of the lane's rows: of this tile, and of the next
@@ -344,8 +349,8 @@ __global__ void __launch_bounds__(THREADS, 1) hs_decode4_kernel(const Decode4Arg
     copies_wait<0>();
     __syncwarp();
   } else if (warp >= LOAD_WARP0) {
-    // ---- a loader. All of them work side by side, 32 rows by 128 columns each: of K's latents first on 128 columns a group of four,
-    //      then on the other two 128s; of V on two segments, then on the other two. Two jobs' words are on their way.
+    // ---- a loader. All of them work side by side, 32 rows by 128 columns each: of K's latents first on 128 columns a group of
+    //      four, then on the other two 128s; of V on two segments, then on the other two. Two jobs' words are on their way.
     ok = !a.stall || __all_sync(0xffffffffu, bar_wait(bar + B_STALL, 0, abort_flag, lim));
     const int r8 = lane & 7, qd = lane >> 3, wl = warp - LOAD_WARP0, grp = wl >> 2;
     if (wl == 0 && lane == 0 && ok) {
@@ -533,7 +538,8 @@ __global__ void __launch_bounds__(THREADS, 1) hs_decode4_kernel(const Decode4Arg
       float m_new = m_run;
       if (mb > -INFINITY && (m_run == -INFINITY || mb > m_run + 8.f)) m_new = mb;
       const bool resc = m_new != m_run && m_run != -INFINITY;
-      const float ref = m_new == -INFINITY ? 0.f : m_new - P_SHIFT;  // no finite score yet: nothing to subtract, a NaN still shows
+      // (no finite score yet: nothing to subtract, and a NaN still shows)
+      const float ref = m_new == -INFINITY ? 0.f : m_new - P_SHIFT;
       float sum[2] = {0.f, 0.f};
       uint32_t p[SEG / 2];
 #pragma unroll
@@ -621,7 +627,8 @@ __global__ void __launch_bounds__(THREADS, 1) hs_decode4_kernel(const Decode4Arg
             uint32_t y[4];
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-              const __nv_bfloat162 x = __floats2bfloat162_rn(__uint_as_float(v[8 * i + 2 * j]) * f, __uint_as_float(v[8 * i + 2 * j + 1]) * f);
+              const __nv_bfloat162 x =
+                  __floats2bfloat162_rn(__uint_as_float(v[8 * i + 2 * j]) * f, __uint_as_float(v[8 * i + 2 * j + 1]) * f);
               y[j] = *reinterpret_cast<const uint32_t*>(&x);
             }
             *reinterpret_cast<uint4*>(orow + 2 * col + 16 * i) = make_uint4(y[0], y[1], y[2], y[3]);
@@ -692,7 +699,8 @@ __global__ void __launch_bounds__(THREADS, 1) hs_decode4_kernel(const Decode4Arg
       float total = some ? f * ml.y : 0.f;
       for (int d = 1; d < n; d <<= 1) total += __shfl_xor_sync(0xffffffffu, total, d);
       weight[t] = total != 0.f ? f * (UNSCALE / total) : 0.f;
-      if ((t & (n - 1)) == 0) a.lse[(size_t)b * HEADS + rank * QH + h] = total != 0.f ? (ref + log2f(total)) * 0.6931471805599453f : -INFINITY;
+      if ((t & (n - 1)) == 0)
+        a.lse[(size_t)b * HEADS + rank * QH + h] = total != 0.f ? (ref + log2f(total)) * 0.6931471805599453f : -INFINITY;
     }
     __syncthreads();
     if (grp < 4) {

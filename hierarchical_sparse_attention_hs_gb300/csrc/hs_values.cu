@@ -187,7 +187,9 @@ Kernel of_type(int32_t type) {
 }
 template <bool HOST>
 Kernel kernel_of(int rb, int32_t type) {
-  return rb == ROW_BF16 ? of_type<ROW_BF16, HOST>(type) : rb == ROW_FP8 ? of_type<ROW_FP8, HOST>(type) : of_type<ROW_INT4, HOST>(type);
+  return rb == ROW_BF16  ? of_type<ROW_BF16, HOST>(type)
+         : rb == ROW_FP8 ? of_type<ROW_FP8, HOST>(type)
+                         : of_type<ROW_INT4, HOST>(type);
 }
 
 int launch_values(hs_pool* p, int32_t batch, const int32_t* idx, int32_t k, const RowSource& src, bool host, void* dst,
@@ -200,8 +202,8 @@ int launch_values(hs_pool* p, int32_t batch, const int32_t* idx, int32_t k, cons
   a.src = src;
   a.dst = static_cast<uint8_t*>(dst);
   cudaLaunchConfig_t cfg = {};
-  const uint32_t per = WARPS * ROWS;
-  cfg.gridDim = dim3(std::min<uint32_t>((a.entries + per - 1) / per, (uint32_t)p->num_sms * (type == HS_TYPE_F32 ? BLOCKS_32 : BLOCKS_16)), 1, 1);
+  const uint32_t per = WARPS * ROWS, most = (uint32_t)p->num_sms * (type == HS_TYPE_F32 ? BLOCKS_32 : BLOCKS_16);
+  cfg.gridDim = dim3(std::min<uint32_t>((a.entries + per - 1) / per, most), 1, 1);
   cfg.blockDim = dim3(THREADS, 1, 1);
   cfg.stream = reinterpret_cast<cudaStream_t>(stream);
   cudaLaunchAttribute attr;

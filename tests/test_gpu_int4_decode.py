@@ -439,3 +439,35 @@ def test_back_to_back_calls_read_what_the_call_before_wrote():
             rows = ora.values(np.concatenate([ora.pack(mine[:, :512]), key], 1))
             check_request(q[b], rows[topk[b].cpu().numpy()], SCALE, out[b], lse[b], b)
     buf.close()
+
+
+def test_host_rows_rewritten_between_replays():
+    """The history as the host leaves it before each replay, rows and list: nothing of the pass before is read again."""
+    batch, k, ctx = 2, 900, 1000
+    buf = hs.PoolBuffers(1, batch, ctx, 16, 8, 416)
+    pool = buf.create()
+    history = buf.host.numpy().reshape(batch, ctx, 416)
+    mem = hs.HostBuffer(batch * k * 4)
+    entries = np.ctypeslib.as_array((np.ctypeslib.ctypes.c_int32 * (batch * k)).from_address(mem.ptr)).reshape(batch, k)
+    q = torch.randn(batch, H, DQK, generator=torch.Generator().manual_seed(5)).to(torch.bfloat16).cuda()
+    out, lse = torch.empty(batch, H, DV, device="cuda"), torch.empty(batch, H, device="cuda")
+    values = torch.empty(batch, k, 576, device="cuda")
+    entries[:] = -1
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        hs.hs_mla_decode_int4_history(pool, 0, batch, q, mem.ptr, k, SCALE, out, hs.HS_TYPE_F32, lse)
+        hs.hs_gather_values_history(pool, 0, batch, mem.ptr, k, values, hs.HS_TYPE_F32)
+    for seed in range(4):
+        history[:] = model_rows(batch * ctx, 50 + seed).reshape(batch, ctx, 416)
+        for b in range(batch):
+            entries[b] = np.random.default_rng(seed + 9 * b).permutation(ctx)[:k]
+        entries[1, 10 + 200 * seed:] = ctx + seed  # past the end: no row
+        graph.replay()
+        torch.cuda.synchronize()
+        for b in range(batch):
+            named = ora.values(history[b][entries[b][entries[b] < ctx]])
+            check_request(q[b], named, SCALE, out[b], lse[b], (seed, b))
+            assert np.array_equal(values[b, :len(named)].double().cpu().numpy(), named) and not values[b, len(named):].any()
+    assert hs.hs_get_error(pool) == 0
+    mem.close()
+    buf.close()
