@@ -33,11 +33,13 @@
 // Measured on one GB300 (replayed graphs): a tile takes 4.1 us, 7,700 cycles, of which its MMAs are 4,352 at their full rate.
 // Shared memory is what it waits for: 2,200 cycles of stores of unpacked rows, 1,100 of the words' way through it, and 96 of its
 // 128 bytes a cycle that MMAs of this shape read while they run, 3,300 or more. 32 requests of 2,048 entries 29.1 us (628
-// TFLOP/s; four tiles a pair, the start, the join), one 16.3, seven 17.8, five of 16,384 46.5, one of 65 8.9. Steps that brought
+// TFLOP/s; four tiles a pair, the start, the join), one 15.9, seven 17.1, five of 16,384 46.2, one of 65 9.3. Steps that brought
 // it there, for 32 requests of 2,048: lanes that load a row each 62 us; eight rows by four lanes 40; copies into shared memory,
 // scores in bf16, queries by TMA 34; jobs of 32 rows in a fixed order, the keys by warps of their own 29.1. Not kept: eleven
 // loaders with 96 registers or fewer that take jobs in turn, 30.2 (and a wait that could be lapped); all loaders on one stage
-// pair, 16 rows each, 36; rows brought into L2 by bulk prefetches, whose issue took a warp 2,000 cycles for 32.
+// pair, 16 rows each, 36; rows brought into L2 by bulk prefetches, whose issue took a warp 2,000 cycles for 32; first loads
+// ahead of the cluster's start, 29.2 against 28.9 (programmatic launch hides that start already); the second tile's prefetch
+// behind the first tile's keys, 29.5; the join by bulk copies into the CTA that sums a head, 31 (one request 16.7 or more).
 //
 // Waits are bounded: on running out a role sets the abort flag, which ends every role, and the HS_DEVERR_TIMEOUT bit.
 
@@ -675,8 +677,10 @@ __global__ void __launch_bounds__(THREADS, 1) hs_decode4_kernel(const Decode4Arg
   if (a.nsplit > 1) {
     // Join: this CTA's share of its 64 heads, from the splits' CTAs of the same heads. Thread t holds outputs 4 (t % 128) .. +3
     // of every fourth head of them, eight loads from the other CTAs in flight; the weights of all 64 pairs of head and
-    // split are worked out by 64 threads meanwhile.
+    // split are worked out by 64 threads meanwhile. Each CTA and group begins with another split, `turn` (all of them with
+    // the first: one request of 2,048 0.5 us more).
     const int n = a.nsplit, lg = n == 2 ? 1 : n == 4 ? 2 : 3, share = QH >> lg, grp = t >> 7, c4 = (t & 127) * 16;
+    const int turn = split + grp;
     float* const weight = red;
     const uint8_t* const mine = smem + split * share * OUT_F32 + c4;
     float4 v[8];
@@ -684,7 +688,7 @@ __global__ void __launch_bounds__(THREADS, 1) hs_decode4_kernel(const Decode4Arg
 #pragma unroll
       for (int u = 0; u < 8; ++u) {
         const int x = x0 + u;  // of the group's pairs: its heads grp, grp + 4, ..
-        v[u] = ld_peer(peer_addr(mine + ((x >> lg) * 4 + grp) * OUT_F32, 2 * (x & (n - 1)) + rank));
+        v[u] = ld_peer(peer_addr(mine + ((x >> lg) * 4 + grp) * OUT_F32, 2 * ((x + turn) & (n - 1)) + rank));
       }
     };
     if (grp < 4) load8(0);
@@ -711,7 +715,7 @@ __global__ void __launch_bounds__(THREADS, 1) hs_decode4_kernel(const Decode4Arg
 #pragma unroll
         for (int u = 0; u < 8; ++u) {
           const int x = x0 + u, i = (x >> lg) * 4 + grp;
-          const float w = weight[(i << lg) + (x & (n - 1))];
+          const float w = weight[(i << lg) + ((x + turn) & (n - 1))];
           o.x = fmaf(w, v[u].x, o.x);
           o.y = fmaf(w, v[u].y, o.y);
           o.z = fmaf(w, v[u].z, o.z);
@@ -769,8 +773,8 @@ int resident(int n) {
 }
 
 // The splits of a list with the shortest expected time, in tiles (4.1 us): waves of clusters, each of its tiles and about two
-// more (its start, its last softmax and its output), and with splits the join (2.8 us of two, 5 of eight). One request of 2,048:
-// 38.2, 25.3, 18.1 and 16.3 us with 1, 2, 4 and 8; 32 of them 40.3, 28.9 and 28.8 with 1, 2 and 4.
+// more (its start, its last softmax and its output), and with splits the join (3.2 us of two, 6 of eight). One request of 2,048:
+// 38.4, 25.4, 18.1 and 15.9 us with 1, 2, 4 and 8; 32 of them 40.3, 29.2, 59 and 86.
 int cut_of(int32_t batch, int32_t k) {
   const int tiles = (k + NK - 1) / NK;
   int best = 0;
