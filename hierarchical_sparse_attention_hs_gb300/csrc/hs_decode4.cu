@@ -32,14 +32,16 @@
 //
 // Measured on one GB300 (replayed graphs): a tile takes 4.1 us, 7,700 cycles, of which its MMAs are 4,352 at their full rate.
 // Shared memory is what it waits for: 2,200 cycles of stores of unpacked rows, 1,100 of the words' way through it, and 96 of its
-// 128 bytes a cycle that MMAs of this shape read while they run, 3,300 or more. 32 requests of 2,048 entries 29.1 us (628
-// TFLOP/s; four tiles a pair, the start, the join), one 15.9, seven 17.1, five of 16,384 46.2, one of 65 9.3. Steps that brought
+// 128 bytes a cycle that MMAs of this shape read while they run, 3,300 or more. 32 requests of 2,048 entries 28.2 us (647
+// TFLOP/s; four tiles a pair, the start, the join), one 15.4, seven 16.7, five of 16,384 46.3, one of 65 9.1. Steps that brought
 // it there, for 32 requests of 2,048: lanes that load a row each 62 us; eight rows by four lanes 40; copies into shared memory,
-// scores in bf16, queries by TMA 34; jobs of 32 rows in a fixed order, the keys by warps of their own 29.1. Not kept: eleven
-// loaders with 96 registers or fewer that take jobs in turn, 30.2 (and a wait that could be lapped); all loaders on one stage
-// pair, 16 rows each, 36; rows brought into L2 by bulk prefetches, whose issue took a warp 2,000 cycles for 32; first loads
-// ahead of the cluster's start, 29.2 against 28.9 (programmatic launch hides that start already); the second tile's prefetch
-// behind the first tile's keys, 29.5; the join by bulk copies into the CTA that sums a head, 31 (one request 16.7 or more).
+// scores in bf16, queries by TMA 34; jobs of 32 rows in a fixed order, the keys by warps of their own 29.1; the code of a
+// loader's two jobs and of the join once each, 78 KB for 94 (what a launch runs once waits for its instructions) 28.2. Not kept:
+// eleven loaders with 96 registers or fewer that take jobs in turn, 30.2 (and a wait that could be lapped); all loaders on one
+// stage pair, 16 rows each, 36; rows brought into L2 by bulk prefetches, whose issue took a warp 2,000 cycles for 32; first
+// copies ahead of the cluster's start, 29.2 against 28.9 (programmatic launch hides that start already); the second tile's
+// prefetch behind the first tile's keys, 29.5; a job's copies started after the job before is unpacked, 29.5 against 28.2; the
+// join by bulk copies into the CTA that sums a head, 31.
 //
 // Waits are bounded: on running out a role sets the abort flag, which ends every role, and the HS_DEVERR_TIMEOUT bit.
 
@@ -442,15 +444,13 @@ __global__ void __launch_bounds__(THREADS, 1) hs_decode4_kernel(const Decode4Arg
         ek = entry(t + 2, krow);
         // after K(t) comes V(t - 1), or K(1) or V(0)
         const bool v_next = t > 0 || !k_next;
-        copies_wait<1>();
-        read(0, w, sc);
-        load(0, v_next ? at(ev0) : krows, v_next ? vcol : kcol);
-        put(K, w, sc, n + 2 * grp);
-        if (!ok) break;
-        copies_wait<1>();
-        read(1, w, sc);
-        load(1, v_next ? at(ev1) : krows, v_next ? vcol : kcol + 256);
-        put(K, w, sc, n + ROPE_AT + 1 + 2 * grp);
+#pragma unroll 1
+        for (int h = 0; h < 2 && ok; ++h) {
+          copies_wait<1>();
+          read(h, w, sc);
+          load(h, v_next ? at(h ? ev1 : ev0) : krows, v_next ? vcol : kcol + 256 * h);
+          put(K, w, sc, n + (ROPE_AT + 1) * h + 2 * grp);
+        }
         if (!ok) break;
         if (t > 0) {
           ev0 = entry(t, vrow);
@@ -459,16 +459,13 @@ __global__ void __launch_bounds__(THREADS, 1) hs_decode4_kernel(const Decode4Arg
       }
       if (t > 0) {
         const int n = tiles.v_stage(t - 1) + 2 * grp + (wl >> 1 & 1), segs = tiles.segs(t - 1);
-        copies_wait<1>();
-        read(0, w, sc);
-        load(0, t == tiles.n ? 0 : k_next ? krows : at(ev0), k_next ? kcol : vcol);
-        if (grp < segs) put(V, w, sc, n);
-        if (!ok) break;
-        copies_wait<1>();
-        read(1, w, sc);
-        load(1, t == tiles.n ? 0 : k_next ? krows : at(ev1), k_next ? kcol + 256 : vcol);
-        if (grp + 2 < segs) put(V, w, sc, n + 4);
-        if (!ok) break;
+#pragma unroll 1
+        for (int h = 0; h < 2 && ok; ++h) {
+          copies_wait<1>();
+          read(h, w, sc);
+          load(h, t == tiles.n ? 0 : k_next ? krows : at(h ? ev1 : ev0), k_next ? kcol + 256 * h : vcol);
+          if (grp + 2 * h < segs) put(V, w, sc, n + 4 * h);
+        }
       }
     }
     asm volatile("cp.async.wait_all;" ::: "memory");
@@ -683,55 +680,54 @@ __global__ void __launch_bounds__(THREADS, 1) hs_decode4_kernel(const Decode4Arg
     const int turn = split + grp;
     float* const weight = red;
     const uint8_t* const mine = smem + split * share * OUT_F32 + c4;
-    float4 v[8];
-    auto load8 = [&](int x0) {
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    const size_t head0 = (size_t)b * HEADS + rank * QH + split * share;  // the CTA's first
+    bool write = false;
+#pragma unroll 1
+    for (int x0 = 0; x0 < 16; x0 += 8) {  // of the group's pairs: its heads grp, grp + 4, ..
+      float4 v[8];
+      if (grp < 4) {
+#pragma unroll
+        for (int u = 0; u < 8; ++u)
+          v[u] = ld_peer(peer_addr(mine + (((x0 + u) >> lg) * 4 + grp) * OUT_F32, 2 * ((u + turn) & (n - 1)) + rank));
+      }
+      if (x0 == 0) {
+        if (t < QH) {
+          const int h = split * share + (t >> lg);
+          const float2 ml = ld_peer2(peer_addr(smem + OFF_ML + h * 8, 2 * (t & (n - 1)) + rank));
+          const bool some = ml.y != 0.f;  // (a split with no row has no weight, and zeros)
+          float mx = some ? ml.x : -INFINITY;
+          for (int d = 1; d < n; d <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
+          const float ref = mx == -INFINITY ? 0.f : mx;
+          const float f = some ? exp2f(ml.x == -INFINITY ? 0.f : ml.x - ref) : 0.f;
+          float total = some ? f * ml.y : 0.f;
+          for (int d = 1; d < n; d <<= 1) total += __shfl_xor_sync(0xffffffffu, total, d);
+          weight[t] = total != 0.f ? f * (UNSCALE / total) : 0.f;
+          if ((t & (n - 1)) == 0)
+            a.lse[(size_t)b * HEADS + rank * QH + h] = total != 0.f ? (ref + log2f(total)) * 0.6931471805599453f : -INFINITY;
+        }
+        __syncthreads();
+        write = grp < 4 && *abort_flag == 0;
+      }
+      if (!write) continue;
 #pragma unroll
       for (int u = 0; u < 8; ++u) {
-        const int x = x0 + u;  // of the group's pairs: its heads grp, grp + 4, ..
-        v[u] = ld_peer(peer_addr(mine + ((x >> lg) * 4 + grp) * OUT_F32, 2 * ((x + turn) & (n - 1)) + rank));
-      }
-    };
-    if (grp < 4) load8(0);
-    if (t < QH) {
-      const int h = split * share + (t >> lg);
-      const float2 ml = ld_peer2(peer_addr(smem + OFF_ML + h * 8, 2 * (t & (n - 1)) + rank));
-      const bool some = ml.y != 0.f;  // (a split with no row has no weight, and zeros)
-      float mx = some ? ml.x : -INFINITY;
-      for (int d = 1; d < n; d <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
-      const float ref = mx == -INFINITY ? 0.f : mx;
-      const float f = some ? exp2f(ml.x == -INFINITY ? 0.f : ml.x - ref) : 0.f;
-      float total = some ? f * ml.y : 0.f;
-      for (int d = 1; d < n; d <<= 1) total += __shfl_xor_sync(0xffffffffu, total, d);
-      weight[t] = total != 0.f ? f * (UNSCALE / total) : 0.f;
-      if ((t & (n - 1)) == 0)
-        a.lse[(size_t)b * HEADS + rank * QH + h] = total != 0.f ? (ref + log2f(total)) * 0.6931471805599453f : -INFINITY;
-    }
-    __syncthreads();
-    if (grp < 4) {
-      float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 1
-      for (int x0 = 0; x0 < 16; x0 += 8) {
-        if (x0) load8(x0);
-#pragma unroll
-        for (int u = 0; u < 8; ++u) {
-          const int x = x0 + u, i = (x >> lg) * 4 + grp;
-          const float w = weight[(i << lg) + ((x + turn) & (n - 1))];
-          o.x = fmaf(w, v[u].x, o.x);
-          o.y = fmaf(w, v[u].y, o.y);
-          o.z = fmaf(w, v[u].z, o.z);
-          o.w = fmaf(w, v[u].w, o.w);
-          if ((x & (n - 1)) == n - 1) {
-            const size_t bh = (size_t)b * HEADS + rank * QH + split * share + i;
-            if (*abort_flag) {
-            } else if (a.out_f32) {
-              *reinterpret_cast<float4*>(static_cast<uint8_t*>(a.out) + bh * LATENT * 4 + c4) = o;
-            } else {
-              const __nv_bfloat162 lo = __floats2bfloat162_rn(o.x, o.y), hi = __floats2bfloat162_rn(o.z, o.w);
-              *reinterpret_cast<uint2*>(static_cast<uint8_t*>(a.out) + bh * LATENT * 2 + c4 / 2) =
-                  make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
-            }
-            o = make_float4(0.f, 0.f, 0.f, 0.f);
+        const int i = ((x0 + u) >> lg) * 4 + grp;
+        const float w = weight[(i << lg) + ((u + turn) & (n - 1))];
+        o.x = fmaf(w, v[u].x, o.x);
+        o.y = fmaf(w, v[u].y, o.y);
+        o.z = fmaf(w, v[u].z, o.z);
+        o.w = fmaf(w, v[u].w, o.w);
+        if ((u & (n - 1)) == n - 1) {
+          uint8_t* const to = static_cast<uint8_t*>(a.out) + (((head0 + i) * LATENT * 4 + c4) >> (a.out_f32 ? 0 : 1));
+          if (a.out_f32) {
+            *reinterpret_cast<float4*>(to) = o;
+          } else {
+            const __nv_bfloat162 lo = __floats2bfloat162_rn(o.x, o.y), hi = __floats2bfloat162_rn(o.z, o.w);
+            *reinterpret_cast<uint2*>(to) =
+                make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
           }
+          o = make_float4(0.f, 0.f, 0.f, 0.f);
         }
       }
     }
