@@ -18,8 +18,10 @@
 // tile's rows, for O += P V its 64 heads of P and all 256 rows of 256 value columns. So the latents are unpacked 1.9 times:
 // once as K, and those of the half of the columns that a CTA has as V again.
 //
-// A list is cut into 1, 2, 4 or 8 splits, where pairs would otherwise be left over (cut_of): a cluster of as many pairs,
-// which leave their outputs in shared memory, unnormalised, with each head's maximum and normaliser, and join them:
+// A request is cut where pairs would otherwise be left over (cut_of): its list into 1, 2, 4 or 8 splits, and a split's value
+// columns into halves, whose two pairs take 128 columns a CTA and both work out all scores. Halves do not have to be joined,
+// and make what splits join half as large. A cluster of up to eight pairs leaves the splits' outputs in shared memory,
+// unnormalised, with each head's maximum and normaliser, and joins them:
 //     M = max m_s,   total = sum 2^(m_s - M) l_s,   out = sum 2^(m_s - M) O_s / total,   lse = ln 2 (M + log2 total).
 //
 // Warp roles per CTA: 0-7 softmax (warp w: TMEM lanes 32 (w % 4) .. +31, that is head lane % 64 and half lane / 64 of the
@@ -31,17 +33,21 @@
 // from there.
 //
 // Measured on one GB300 (replayed graphs): a tile takes 4.1 us, 7,700 cycles, of which its MMAs are 4,352 at their full rate.
-// Shared memory is what it waits for: 2,200 cycles of stores of unpacked rows, 1,100 of the words' way through it, and 96 of its
-// 128 bytes a cycle that MMAs of this shape read while they run, 3,300 or more. 32 requests of 2,048 entries 28.2 us (647
-// TFLOP/s; four tiles a pair, the start, the join), one 15.4, seven 16.7, five of 16,384 46.3, one of 65 9.1. Steps that brought
-// it there, for 32 requests of 2,048: lanes that load a row each 62 us; eight rows by four lanes 40; copies into shared memory,
-// scores in bf16, queries by TMA 34; jobs of 32 rows in a fixed order, the keys by warps of their own 29.1; the code of a
-// loader's two jobs and of the join once each, 78 KB for 94 (what a launch runs once waits for its instructions) 28.2. Not kept:
-// eleven loaders with 96 registers or fewer that take jobs in turn, 30.2 (and a wait that could be lapped); all loaders on one
-// stage pair, 16 rows each, 36; rows brought into L2 by bulk prefetches, whose issue took a warp 2,000 cycles for 32; first
-// copies ahead of the cluster's start, 29.2 against 28.9 (programmatic launch hides that start already); the second tile's
-// prefetch behind the first tile's keys, 29.5; a job's copies started after the job before is unpacked, 29.5 against 28.2; the
-// join by bulk copies into the CTA that sums a head, 31.
+// Shared memory is what it waits for: 2,200 cycles of stores of unpacked rows, 1,100 of the words' way through it, and 96 of
+// its 128 bytes a cycle that MMAs of this shape read while they run, 3,300 or more. 32 requests of 2,048 entries 28.0 us (652
+// TFLOP/s; four tiles a pair, the start, the join), one 14.7, seven 16.4, five of 16,384 46.0, one of 65 8.2.
+//
+// Steps that brought it there, for 32 requests of 2,048: lanes that load a row each 62 us; eight rows by four lanes 40; copies
+// into shared memory, scores in bf16, queries by TMA 34; jobs of 32 rows in a fixed order, the keys by warps of their own
+// 29.1; the code of a loader's two jobs and of the join once each, 78 KB for 94 (what a launch runs once waits for its
+// instructions) 28.0. Halves of the value columns: one request of 2,048 14.7 from 15.3, of 1,000 12.0 from 14.4, of 65 8.2
+// from 9.1; as an argument in place of a template's the others took 28.4 to 28.7.
+//
+// Not kept: eleven loaders with 96 registers or fewer that take jobs in turn, 30.2 (and a wait that could be lapped); all
+// loaders on one stage pair, 16 rows each, 36; rows brought into L2 by bulk prefetches, whose issue took a warp 2,000 cycles
+// for 32; first copies ahead of the cluster's start, 29.2 against 28.9 (programmatic launch hides that start already); the
+// second tile's prefetch behind the first tile's keys, 29.5; a job's copies started after the job before is unpacked, 29.5
+// against 28.2; waits as calls of a function 28.7; the join by bulk copies into the CTA that sums a head, 31.
 //
 // Waits are bounded: on running out a role sets the abort flag, which ends every role, and the HS_DEVERR_TIMEOUT bit.
 
@@ -102,7 +108,7 @@ constexpr uint32_t TMEM_COLS = 512, TMEM_O = 0, TMEM_S = 256;  // O: 2 x 128 col
 // A CTA's outputs take the place of Q and the ring: rows of a head, 16 bytes apart beyond their own size (no bank conflicts).
 constexpr int OUT_F32 = LATENT * 4 + 16, OUT_BF16 = LATENT * 2 + 16;
 static_assert(QH * OUT_F32 <= OFF_P, "a CTA's outputs fit in front of P");
-constexpr int MAX_SPLIT = 8;
+constexpr int MAX_PAIRS_LOG = 3;  // of a cluster: 16 CTAs
 constexpr float P_SHIFT = 6.f;  // weights are kept at 2^6: their smallest half is then 2^-30 of a weight of the maximum's
 constexpr float UNSCALE = 64.f;  // latents are kept at 2^-6
 
@@ -111,7 +117,7 @@ struct Decode4Args {
   int32_t k;
   RowSource src;
   float scale_log2;    // sm_scale * log2(e)
-  int32_t nsplit;
+  int32_t nsplit;      // splits of the list
   void* out;
   int32_t out_f32;
   float* lse;
@@ -151,13 +157,15 @@ __device__ __forceinline__ float2 ld_peer2(uint32_t addr) {
 
 // A split's tiles, and where their stages lie in the order K(0) K(1) V(0) K(2) V(1) ... V(n - 1): K's rotary keys in the
 // middle of its latents (stage ROPE_AT). Of the list's last tile only the first `last_segs` segments hold entries: the others
-// are not multiplied with V.
+// are not multiplied with V. (lv, here and below: 1 with the value columns in halves.)
+template <int lv>
 struct Tiles {
+  static constexpr int vstages = (2 * NSEG) >> lv;  // V stages of a whole tile
   int first, n;      // the split's first tile, and how many it has
   int last_segs;     // segments of its last tile
   __device__ __forceinline__ int segs(int t) const { return t == n - 1 ? last_segs : NSEG; }
-  __device__ __forceinline__ int k_stage(int t) const { return t == 0 ? 0 : t * (KBLK + 2 * NSEG) - 2 * NSEG; }
-  __device__ __forceinline__ int v_stage(int t) const { return (t + 1) * (KBLK + 2 * NSEG) + (t == n - 1 ? -2 * NSEG : 1); }
+  __device__ __forceinline__ int k_stage(int t) const { return t == 0 ? 0 : t * (KBLK + vstages) - vstages; }
+  __device__ __forceinline__ int v_stage(int t) const { return (t + 1) * (KBLK + vstages) - vstages + (t == n - 1 ? 0 : KBLK); }
 };
 // 32 latents of a row, unpacked into four of the eight 16-byte chunks of a stage's row, from chunk ch on: as bf16 for the
 // scores, as halves at 2^-6 for the values.
@@ -186,6 +194,7 @@ __device__ __forceinline__ void unpack(uint8_t* row, int swizzle, int ch, uint4 
   }
 }
 
+template <int lv>
 __global__ void __launch_bounds__(THREADS, 1) hs_decode4_kernel(const Decode4Args a, const __grid_constant__ CUtensorMap qmap) {
   extern __shared__ __align__(1024) uint8_t smem[];
   uint64_t* const bar = reinterpret_cast<uint64_t*>(smem + OFF_BAR);
@@ -219,9 +228,10 @@ __global__ void __launch_bounds__(THREADS, 1) hs_decode4_kernel(const Decode4Arg
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;");
 
-  const uint32_t b = blockIdx.x / (uint32_t)(2 * a.nsplit);
-  const int split = (int)(crank >> 1), all = (a.k + NK - 1) / NK, per = all / a.nsplit, more = all - per * a.nsplit;
-  Tiles tiles;
+  const int half = (int)(crank >> 1) & lv;  // the pair's half of the value columns
+  const uint32_t b = blockIdx.x / (uint32_t)((2 * a.nsplit) << lv);
+  const int split = (int)(crank >> 1) >> lv, all = (a.k + NK - 1) / NK, per = all / a.nsplit, more = all - per * a.nsplit;
+  Tiles<lv> tiles;
   tiles.n = per + (split < more ? 1 : 0);
   tiles.first = split * per + min(split, more);
   tiles.last_segs = min(NSEG, (a.k - (tiles.first + tiles.n - 1) * NK + SEG - 1) / SEG);
@@ -271,13 +281,13 @@ __global__ void __launch_bounds__(THREADS, 1) hs_decode4_kernel(const Decode4Arg
         if (g >= 1) {
           ok = wait(B_PFULL, (unsigned)(g - 1) & 1u);
           tc_fence_after();
-          const int nv = 2 * tiles.segs(g - 1);
+          const int nv = (2 * tiles.segs(g - 1)) >> lv, two = 1 - lv;
           for (int c = 0; c < nv && ok; ++c) {
-            // 64 rows: block c / 2 of P; 128 of the CTA's value columns, 16 rows a step
+            // 64 rows: a block of P; 128 of the CTA's value columns, 16 rows a step
             ok = wait(B_FULL + st, ph);
             tc_fence_after();
-            if (ok) four(tmem + TMEM_O + (uint32_t)(c & 1) * 128, dp + (uint64_t)((c >> 1) * (BLK_BYTES >> 4)),
-                         dv + (uint64_t)(st * (STAGE_BYTES >> 4)), 128, ID_O, g > 1 || c > 1 ? 1u : 0u);
+            if (ok) four(tmem + TMEM_O + (uint32_t)(c & two) * 128, dp + (uint64_t)((c >> two) * (BLK_BYTES >> 4)),
+                         dv + (uint64_t)(st * (STAGE_BYTES >> 4)), 128, ID_O, g > 1 || c > two ? 1u : 0u);
           }
           if (!ok) break;
           if (leader) commit2(bar + B_PDONE, both);
@@ -354,7 +364,8 @@ __global__ void __launch_bounds__(THREADS, 1) hs_decode4_kernel(const Decode4Arg
     __syncwarp();
   } else if (warp >= LOAD_WARP0) {
     // ---- a loader. All of them work side by side, 32 rows by 128 columns each: of K's latents first on 128 columns a group of
-    //      four, then on the other two 128s; of V on two segments, then on the other two. Two jobs' words are on their way.
+    //      four, then on the other two 128s; of V on two segments, then on the other two (of half of the columns on all four).
+    //      Two jobs' words are on their way.
     ok = !a.stall || __all_sync(0xffffffffu, bar_wait(bar + B_STALL, 0, abort_flag, lim));
     const int r8 = lane & 7, qd = lane >> 3, wl = warp - LOAD_WARP0, grp = wl >> 2;
     if (wl == 0 && lane == 0 && ok) {
@@ -370,7 +381,8 @@ __global__ void __launch_bounds__(THREADS, 1) hs_decode4_kernel(const Decode4Arg
       return tile < tiles.n && i < a.k ? ld_fresh(list + i) : -1;
     };
     auto at = [&](int32_t e) { return reinterpret_cast<Address>(row_at(a.src, b, e, ROW_INT4)); };
-    const int krow = (int)rank * KH + (wl & 3) * 32, vrow = grp * SEG + (wl & 1) * 32;
+    // a loader's rows of K, the first of its segments of V, its columns of either, and its stage among a tile's V
+    const int krow = (int)rank * KH + (wl & 3) * 32, vseg = lv ? wl >> 1 : grp, vrow = vseg * SEG + (wl & 1) * 32;
     // The words of 128 columns from `col` on, on their way into buffer `par`: four lanes a row; where there is no row its scales
     // are zeros (and the numbers may be anything).
     uint8_t* const raw = smem + OFF_RAW + wl * 2 * RAW_JOB;
@@ -427,17 +439,19 @@ __global__ void __launch_bounds__(THREADS, 1) hs_decode4_kernel(const Decode4Arg
     };
     const std::true_type K;
     const std::false_type V;
-    const int kcol = grp * 128, vcol = (int)rank * DVH + (wl >> 1 & 1) * 128;
+    const int kcol = grp * 128, vcol = (int)rank * DVH + (lv ? half : wl >> 1 & 1) * 128;
+    const int vstage = lv ? vseg : 2 * grp + (wl >> 1 & 1);
     uint4 w[4];
     uint32_t sc[4];
     Address krows = at(entry(0, krow));
     int32_t ek = entry(1, krow), ev0 = entry(0, vrow), ev1 = entry(0, vrow + 2 * SEG);
-    // A job's words are awaited and read, the copies of the job after the next started into their place, and the words unpacked.
-    load(0, krows, kcol);
-    load(1, krows, kcol + 256);
-    // step t: K(t), then V(t - 1)
+#pragma unroll 1
+    for (int h = 0; h < 2; ++h) load(h, krows, kcol + 256 * h);
+    // Step t: the two halves of K(t), then V(t - 1), of all columns in two jobs, of half of them in one. A job's words are
+    // awaited and read, the copies of the job after the next started into their place, and the words unpacked.
     for (int t = 0; t <= tiles.n && ok; ++t) {
-      const bool k_next = t + 1 < tiles.n;  // what comes after V(t - 1): K(t + 1), or the last V
+      const int odd = t > 0 ? lv & (t + 1) : 0;  // with single jobs of V: 3 t - 1 jobs come before step t
+      const bool k_next = t + 1 < tiles.n;       // what comes after V(t - 1): K(t + 1), or the last V
       if (t < tiles.n) {
         const int n = tiles.k_stage(t);
         krows = at(ek);
@@ -446,25 +460,30 @@ __global__ void __launch_bounds__(THREADS, 1) hs_decode4_kernel(const Decode4Arg
         const bool v_next = t > 0 || !k_next;
 #pragma unroll 1
         for (int h = 0; h < 2 && ok; ++h) {
+          const int par = h ^ odd;  // the job's buffer
+          const bool past = lv && h;  // the job after the next is the one behind a V that is a single job
+          const bool v = past ? t > 0 && !k_next : v_next;
           copies_wait<1>();
-          read(h, w, sc);
-          load(h, v_next ? at(h ? ev1 : ev0) : krows, v_next ? vcol : kcol + 256 * h);
+          read(par, w, sc);
+          load(par, v ? at(h > lv ? ev1 : ev0) : past && !k_next ? 0 : krows, v ? vcol : past && t > 0 ? kcol : kcol + 256 * h);
+          if (lv && h == 0 && t > 0) ev0 = entry(t, vrow);
           put(K, w, sc, n + (ROPE_AT + 1) * h + 2 * grp);
         }
         if (!ok) break;
-        if (t > 0) {
+        if (t > 0 && !lv) {
           ev0 = entry(t, vrow);
           ev1 = entry(t, vrow + 2 * SEG);
         }
       }
       if (t > 0) {
-        const int n = tiles.v_stage(t - 1) + 2 * grp + (wl >> 1 & 1), segs = tiles.segs(t - 1);
+        const int n = tiles.v_stage(t - 1) + vstage, segs = tiles.segs(t - 1);
 #pragma unroll 1
-        for (int h = 0; h < 2 && ok; ++h) {
+        for (int h = 0; h < 2 - lv && ok; ++h) {
+          const int par = h ^ odd;  // the job's buffer
           copies_wait<1>();
-          read(h, w, sc);
-          load(h, t == tiles.n ? 0 : k_next ? krows : at(h ? ev1 : ev0), k_next ? kcol + 256 * h : vcol);
-          if (grp + 2 * h < segs) put(V, w, sc, n + 4 * h);
+          read(par, w, sc);
+          load(par, k_next ? krows : lv || t == tiles.n ? 0 : at(h ? ev1 : ev0), k_next ? kcol + 256 * (h | lv) : vcol);
+          if (vseg + 2 * h < segs) put(V, w, sc, n + 4 * h);
         }
       }
     }
@@ -477,6 +496,7 @@ __global__ void __launch_bounds__(THREADS, 1) hs_decode4_kernel(const Decode4Arg
     uint8_t* const prows = smem + OFF_P + sg * BLK_BYTES + (q & 1) * 32 * 128;  // the warp's 32 rows of P
     const size_t head0 = (size_t)b * HEADS + rank * QH;                         // the CTA's first
     float m_run = -INFINITY, l_run = 0.f;
+    const int o_cols = (DVH / 2) >> lv;  // columns of O of a thread
     int nx = 0;  // exchanges
     // hands `v` to the other three threads of the head
     auto exchange = [&](float v) {
@@ -566,7 +586,7 @@ __global__ void __launch_bounds__(THREADS, 1) hs_decode4_kernel(const Decode4Arg
         tc_fence_after();
         const float f = resc ? ex2_approx(m_run - m_new) : 1.f;
 #pragma unroll 1
-        for (int c = sub * (DVH / 2); c < (sub + 1) * (DVH / 2); c += 16) {
+        for (int c = sub * o_cols; c < (sub + 1) * o_cols; c += 16) {
           float o[16];
           tmem_ld16(trow + TMEM_O + c, o);
 #pragma unroll
@@ -604,16 +624,16 @@ __global__ void __launch_bounds__(THREADS, 1) hs_decode4_kernel(const Decode4Arg
       if (sg == 0) {
         if (part)
           reinterpret_cast<float2*>(smem + OFF_ML)[r] = make_float2(m_run == -INFINITY ? -INFINITY : ref, l_run);
-        else
+        else if (half == 0)
           a.lse[head0 + r] = l_run != 0.f ? (ref + log2f(l_run)) * 0.6931471805599453f : -INFINITY;
       }
       uint8_t* const orow = smem + r * (f32 ? OUT_F32 : OUT_BF16);
 #pragma unroll 1
-      for (int c = sub * (DVH / 2); c < (sub + 1) * (DVH / 2); c += 32) {
+      for (int c = sub * o_cols; c < (sub + 1) * o_cols; c += 32) {
         uint32_t v[32];
         tmem_ld32(trow + TMEM_O + c, v);
         tmem_wait_ld();
-        const int col = hf * DVH + c;
+        const int col = hf * 2 * o_cols + c;
         if (f32) {
 #pragma unroll
           for (int i = 0; i < 8; ++i)
@@ -638,13 +658,13 @@ __global__ void __launch_bounds__(THREADS, 1) hs_decode4_kernel(const Decode4Arg
       if (!part) {
         fence_proxy_async();
         named_sync(1 + 1 + (q & 1), SOFTMAX_WARPS * 16);  // the four warps of the same 32 heads
-        // eight rows a warp, one copy a lane
-        if (lane < 8) {
-          const int h = (q & 1) * 32 + sg * 8 + lane;
-          const uint32_t bytes = LATENT * (f32 ? 4 : 2);
+        // eight rows a warp, one copy a lane; half of the columns are two pieces of a row
+        if (lane < 8 << lv) {
+          const int h = (q & 1) * 32 + sg * 8 + (lane & 7), piece = lane >> 3, size = f32 ? 4 : 2;
+          const uint32_t bytes = (uint32_t)(size * (lv ? LATENT / 4 : LATENT));
           asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;\n\tcp.async.bulk.commit_group;" ::"l"(
-                           static_cast<uint8_t*>(a.out) + (head0 + h) * bytes),
-                       "r"(su32(smem + h * (f32 ? OUT_F32 : OUT_BF16))), "r"(bytes)
+                           static_cast<uint8_t*>(a.out) + ((head0 + h) * LATENT + piece * DVH + half * (DVH / 2)) * size),
+                       "r"(su32(smem + h * (f32 ? OUT_F32 : OUT_BF16) + piece * bytes)), "r"(bytes)
                        : "memory");
           asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
         }
@@ -672,29 +692,32 @@ __global__ void __launch_bounds__(THREADS, 1) hs_decode4_kernel(const Decode4Arg
   if (warp == MMA_WARP)
     asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(TMEM_COLS) : "memory");
   if (a.nsplit > 1) {
-    // Join: this CTA's share of its 64 heads, from the splits' CTAs of the same heads. Thread t holds outputs 4 (t % 128) .. +3
-    // of every fourth head of them, eight loads from the other CTAs in flight; the weights of all 64 pairs of head and
-    // split are worked out by 64 threads meanwhile. Each CTA and group begins with another split, `turn` (all of them with
-    // the first: one request of 2,048 0.5 us more).
-    const int n = a.nsplit, lg = n == 2 ? 1 : n == 4 ? 2 : 3, share = QH >> lg, grp = t >> 7, c4 = (t & 127) * 16;
+    // Join: this CTA's share of its 64 heads, from the splits' CTAs of the same heads and columns. A group of threads, 128 for
+    // all columns or 64 for half of them, holds every fourth or eighth head of them, a thread four outputs, eight loads from
+    // the other CTAs in flight; the weights of all 64 pairs of head and split are worked out by 64 threads meanwhile. Each CTA
+    // and group begins with another split, `turn` (all of them with the first: one request of 2,048 0.5 us more).
+    const int n = a.nsplit, lg = n == 2 ? 1 : n == 4 ? 2 : 3, share = QH >> lg, groups = 4 << lv,
+              grp = t >> (7 - lv), c = 4 * (t & (127 >> lv));
     const int turn = split + grp;
+    auto pair_of = [&](int of) { return 2u * (uint32_t)((of << lv) + half) + rank; };  // this CTA's like in another split
     float* const weight = red;
-    const uint8_t* const mine = smem + split * share * OUT_F32 + c4;
+    const uint8_t* const mine = smem + split * share * OUT_F32 + 4 * c;
+    const int col = lv ? (c >> 7) * DVH + half * (DVH / 2) + (c & 127) : c;
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
     const size_t head0 = (size_t)b * HEADS + rank * QH + split * share;  // the CTA's first
     bool write = false;
 #pragma unroll 1
-    for (int x0 = 0; x0 < 16; x0 += 8) {  // of the group's pairs: its heads grp, grp + 4, ..
+    for (int x0 = 0; x0 < 16 >> lv; x0 += 8) {  // of the group's pairs: its heads grp, grp + groups, ..
       float4 v[8];
-      if (grp < 4) {
+      if (grp < groups) {
 #pragma unroll
         for (int u = 0; u < 8; ++u)
-          v[u] = ld_peer(peer_addr(mine + (((x0 + u) >> lg) * 4 + grp) * OUT_F32, 2 * ((u + turn) & (n - 1)) + rank));
+          v[u] = ld_peer(peer_addr(mine + (((x0 + u) >> lg) * groups + grp) * OUT_F32, pair_of((u + turn) & (n - 1))));
       }
       if (x0 == 0) {
         if (t < QH) {
           const int h = split * share + (t >> lg);
-          const float2 ml = ld_peer2(peer_addr(smem + OFF_ML + h * 8, 2 * (t & (n - 1)) + rank));
+          const float2 ml = ld_peer2(peer_addr(smem + OFF_ML + h * 8, pair_of(t & (n - 1))));
           const bool some = ml.y != 0.f;  // (a split with no row has no weight, and zeros)
           float mx = some ? ml.x : -INFINITY;
           for (int d = 1; d < n; d <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
@@ -703,23 +726,23 @@ __global__ void __launch_bounds__(THREADS, 1) hs_decode4_kernel(const Decode4Arg
           float total = some ? f * ml.y : 0.f;
           for (int d = 1; d < n; d <<= 1) total += __shfl_xor_sync(0xffffffffu, total, d);
           weight[t] = total != 0.f ? f * (UNSCALE / total) : 0.f;
-          if ((t & (n - 1)) == 0)
+          if ((t & (n - 1)) == 0 && half == 0)
             a.lse[(size_t)b * HEADS + rank * QH + h] = total != 0.f ? (ref + log2f(total)) * 0.6931471805599453f : -INFINITY;
         }
         __syncthreads();
-        write = grp < 4 && *abort_flag == 0;
+        write = grp < groups && *abort_flag == 0;
       }
       if (!write) continue;
 #pragma unroll
       for (int u = 0; u < 8; ++u) {
-        const int i = ((x0 + u) >> lg) * 4 + grp;
+        const int i = ((x0 + u) >> lg) * groups + grp;
         const float w = weight[(i << lg) + ((u + turn) & (n - 1))];
         o.x = fmaf(w, v[u].x, o.x);
         o.y = fmaf(w, v[u].y, o.y);
         o.z = fmaf(w, v[u].z, o.z);
         o.w = fmaf(w, v[u].w, o.w);
         if ((u & (n - 1)) == n - 1) {
-          uint8_t* const to = static_cast<uint8_t*>(a.out) + (((head0 + i) * LATENT * 4 + c4) >> (a.out_f32 ? 0 : 1));
+          uint8_t* const to = static_cast<uint8_t*>(a.out) + ((((head0 + i) * LATENT + col) * 4) >> (a.out_f32 ? 0 : 1));
           if (a.out_f32) {
             *reinterpret_cast<float4*>(to) = o;
           } else {
@@ -736,51 +759,63 @@ __global__ void __launch_bounds__(THREADS, 1) hs_decode4_kernel(const Decode4Arg
   }
 }
 
-// How many clusters of 2 n CTAs (n = 1, 2, 4, 8) the current device holds at once, cached per device; 0 where it holds none.
-int resident(int n) {
-  static std::atomic<int> cache[64][4];  // 0: not yet asked, else the count + 1
-  const int slot = n == 1 ? 0 : n == 2 ? 1 : n == 4 ? 2 : 3;
+using Kernel = void (*)(Decode4Args, CUtensorMap);
+const Kernel KERNELS[2] = {hs_decode4_kernel<0>, hs_decode4_kernel<1>};
+
+// How many clusters of 2^lg splits the current device holds at once, cached per device; 0 where it holds none.
+int resident(int lg, int halves) {
+  static std::atomic<int> cache[64][2][MAX_PAIRS_LOG + 1];  // 0: not yet asked, else the count + 1
+  const unsigned ctas = 2u << (lg + halves);
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) {
     cudaGetLastError();
     return 0;
   }
-  const int c = cache[dev][slot].load(std::memory_order_relaxed);
+  const int c = cache[dev][halves][lg].load(std::memory_order_relaxed);
   if (c) return c - 1;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(2 * n, 1, 1);
+  cfg.gridDim = dim3(ctas, 1, 1);
   cfg.blockDim = dim3(THREADS, 1, 1);
   cfg.dynamicSmemBytes = SMEM_BYTES;
   cudaLaunchAttribute attr;
   attr.id = cudaLaunchAttributeClusterDimension;
-  attr.val.clusterDim.x = 2 * n;
+  attr.val.clusterDim.x = ctas;
   attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
   int got = 0;
-  if (cudaFuncSetAttribute(hs_decode4_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_BYTES) != cudaSuccess ||
-      (n == 8 && cudaFuncSetAttribute(hs_decode4_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess) ||
-      cudaOccupancyMaxActiveClusters(&got, hs_decode4_kernel, &cfg) != cudaSuccess) {
+  const Kernel kernel = KERNELS[halves];
+  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_BYTES) != cudaSuccess ||
+      (ctas > 8 && cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess) ||
+      cudaOccupancyMaxActiveClusters(&got, kernel, &cfg) != cudaSuccess) {
     cudaGetLastError();
     got = 0;
   }
-  cache[dev][slot].store(got + 1, std::memory_order_relaxed);
+  cache[dev][halves][lg].store(got + 1, std::memory_order_relaxed);
   return got;
 }
 
-// The splits of a list with the shortest expected time, in tiles (4.1 us): waves of clusters, each of its tiles and about two
-// more (its start, its last softmax and its output), and with splits the join (3.2 us of two, 6 of eight). One request of 2,048:
-// 38.4, 25.4, 18.1 and 15.9 us with 1, 2, 4 and 8; 32 of them 40.3, 29.2, 59 and 86.
-int cut_of(int32_t batch, int32_t k) {
+// How a request is cut: the splits of its list, and whether two pairs of CTAs share the value columns of each.
+struct Cut {
+  int splits, halves;
+};
+// The cut with the shortest expected time: waves of clusters, each of its start, its last softmax and its output (5 us), its
+// tiles (4.2 us, 3.4 with half of the value columns) and the join of splits. Measured, in us, as splits / splits with halves:
+// one request of 65 entries 9.4 / 8.3; of 400, one 13.6 / 11.6, two 13.3 / 10.9; of 2,048, one 39 / 32, two 25.7 / 20.7, four
+// 18.3 / 14.9, eight 15.8; 9 of 2,048 (more clusters of 16 CTAs than the device holds), two 26.1 / 21.6, four 19.3 / 30.6; 32 of
+// 2,048, one 41 / 34, two 27.9 / 65; 76 of 2,048, one 45 / 100.
+Cut cut_of(int32_t batch, int32_t k) {
   const int tiles = (k + NK - 1) / NK;
-  int best = 0;
+  Cut best = {0, 0};
   double least = 0;
-  for (int n = 1; n <= MAX_SPLIT && n <= tiles; n *= 2) {
-    const int held = resident(n);
-    if (held < 1) continue;
-    const double cost = (double)((batch + held - 1) / held) * ((tiles + n - 1) / n + 2 + (n > 1 ? 1 : 0));
-    if (best == 0 || cost < least) least = cost, best = n;
-  }
+  for (int halves = 0; halves < 2; ++halves)
+    for (int lg = 0; lg + halves <= MAX_PAIRS_LOG && 1 << lg <= tiles; ++lg) {
+      const int n = 1 << lg, held = resident(lg, halves);
+      if (held < 1) continue;
+      const double join = lg == 0 ? 0. : halves ? 1.5 + 1.1 * lg : 2.6 + 1.3 * lg;
+      const double cost = (double)((batch + held - 1) / held) * (5. + (tiles + n - 1) / n * (halves ? 3.4 : 4.2) + join);
+      if (best.splits == 0 || cost < least) least = cost, best = {n, halves};
+    }
   return best;
 }
 
@@ -788,8 +823,10 @@ int launch(hs_pool* p, int32_t batch, const void* q, const int32_t* idx, int32_t
            void* out, int32_t out_type, float* lse, hs_stream_t stream) {
   Decode4Args a;
   std::memset(&a, 0, sizeof(a));
-  a.nsplit = cut_of(batch, k);
-  if (a.nsplit < 1) return HS_ERR_UNSUPPORTED;
+  const Cut cut = cut_of(batch, k);
+  if (cut.splits < 1) return HS_ERR_UNSUPPORTED;
+  a.nsplit = cut.splits;
+  const unsigned ctas = (2u * (unsigned)cut.splits) << cut.halves;  // of a request: a cluster
   a.idx = idx;
   a.k = k;
   a.src = src;
@@ -804,7 +841,7 @@ int launch(hs_pool* p, int32_t batch, const void* q, const int32_t* idx, int32_t
   if (!encode) return HS_ERR_UNSUPPORTED;
   if (!make_map(encode, &qmap, q, (uint64_t)batch * HEADS, QH, 3)) return HS_ERR_INVALID_ARG;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(2 * a.nsplit) * (unsigned)batch, 1, 1);
+  cfg.gridDim = dim3(ctas * (unsigned)batch, 1, 1);
   cfg.blockDim = dim3(THREADS, 1, 1);
   cfg.dynamicSmemBytes = SMEM_BYTES;
   cfg.stream = reinterpret_cast<cudaStream_t>(stream);
@@ -812,11 +849,11 @@ int launch(hs_pool* p, int32_t batch, const void* q, const int32_t* idx, int32_t
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = (unsigned)(2 * a.nsplit);
+  attr[1].val.clusterDim.x = ctas;
   attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  return hs_launched(cudaLaunchKernelEx(&cfg, hs_decode4_kernel, a, qmap));
+  return hs_launched(cudaLaunchKernelEx(&cfg, KERNELS[cut.halves], a, qmap));
 }
 
 // HS_OK, or what the call is refused with; *empty for one that has nothing to do.

@@ -134,7 +134,8 @@ def test_lengths(batch, k):
     c.close()
 
 
-@pytest.mark.parametrize("batch,k", [(2, 2048), (1, 4097), (9, 1500), (17, 700), (20, 513), (39, 600), (77, 300), (160, 70)])
+@pytest.mark.parametrize("batch,k", [(2, 2048), (1, 4097), (9, 1500), (9, 2100), (17, 700), (20, 513), (30, 1100), (39, 600),
+                                     (77, 300), (160, 70)])
 def test_batches(batch, k):
     c = Case(batch, k, slots=600, away=50, seed=batch, padded=0.05)
     c.check(*c.run(hs.HS_TYPE_F32 if batch % 2 else hs.HS_TYPE_BF16), requests=sorted({0, 1, batch // 2, batch - 1} & set(range(batch))))

@@ -98,8 +98,8 @@ got["append"] = [append(p=pool(row_bytes=416)), append(p=pool(row_bytes=416), pa
 
 
 def test_grids(under):  # noqa: F811
-    """Rows read back: a warp for four entries, at most a device full of blocks. Attention: a cluster for each request, cut into
-    splits while the device (76 clusters of any size) holds them all."""
+    """Rows read back: a warp for four entries, at most a device full of blocks. Attention: a cluster for each request, its list
+    cut into splits and its value columns into halves while the device (76 clusters of any size) holds them all."""
     got = under(CALLS + """
 def grid(f, *a, **kw):
     rc = f(*a, **kw)
@@ -111,7 +111,7 @@ got = dict(values=[grid(values, batch=1, k=k) for k in (1, 32, 33, 64, 65, 1 << 
            many=[grid(decode, p=big, batch=b, k=2048) for b in (76, 77, 200)])
 """)
     assert got["values"] == [[0, 1], [0, 1], [0, 2], [0, 2], [0, 3], [0, 152 * 16]] and got["f32"] == [0, 152 * 8]
-    assert got["decode"] == [[0, 2], [0, 2], [0, 2], [0, 16], [0, 16]]
+    assert got["decode"] == [[0, 4], [0, 4], [0, 8], [0, 16], [0, 16]]  # halves of the columns for short lists
     assert [rc for rc, _ in got["many"]] == [0, 0, 0] and all(g % 2 == 0 and g // 2 % b == 0 for (_, g), b in
                                                               zip(got["many"], (76, 77, 200)))
 
@@ -175,20 +175,43 @@ def test_paged_rows_of_416_bytes(monkeypatch):
         hs.hs_append(7, 0, 1, hs.hs_append_desc(), hs.paged_rows(torch.zeros(64, 656, dtype=torch.uint8), pages, 16), False, 0)
 
 
-def test_stages_of_a_loader_are_at_most_four_apart():
+def test_stages_of_a_loader_are_close():
     """The attention's loaders wait for a place of the ring by its barrier's parity, which holds as long as the stages that a loader
-    has a part in are no further apart than the ring has places (five): their order, as hs_decode4.cu walks it."""
-    def gap(n, last, grp, pair):
-        k = lambda t: 0 if t == 0 else 17 * t - 8  # noqa: E731
-        v = lambda t: 17 * (t + 1) + (-8 if t == n - 1 else 1)  # noqa: E731
-        of = []
-        for t in range(n + 1):
-            if t < n:
-                of += [k(t) + 2 * grp, k(t) + 2 * grp + 1, k(t) + 5 + 2 * grp, k(t) + 6 + 2 * grp]
-            if t > 0:
-                segs = last if t == n else 4
-                of += [v(t - 1) + 2 * s + pair for s in (grp, grp + 2) if s < segs]
-        assert of == sorted(of) and of[0] < 5
-        return max([b - a for a, b in zip(of, of[1:])])
+    has a part in are no further apart than the ring has places (five): their order, as hs_decode4.cu walks it, with all value
+    columns to a pair of CTAs or half of them."""
+    def walk(n, half):
+        t = p = 0
+        while t <= n:
+            yield t, p
+            p += 1
+            if p == 4 - half or (p == 2 and t == 0):
+                t, p = t + 1, 0
+            if p == 0 and t >= n:
+                p = 2
 
-    assert max(gap(n, last, grp, pair) for n in range(1, 6) for last in range(1, 5) for grp in (0, 1) for pair in (0, 1)) <= 5
+    def stages(n, last, loader, half):
+        v = 8 >> half
+        grp, pair = loader >> 2, loader >> 1 & 1
+        for t, p in walk(n, half):
+            if p < 2:
+                at = (t * (9 + v) - v if t else 0) + 5 * p + 2 * grp
+                yield from (at, at + 1)
+            else:
+                segment = (loader >> 1 if half else grp) + 2 * (p - 2)
+                if segment < (last if t == n else 4):
+                    yield t * (9 + v) - v + (0 if t == n else 9) + (segment if half else 2 * segment + pair)
+
+    for half in (0, 1):
+        for n in range(1, 6):
+            order = [(t, p) for t in range(n + 1) for p in range(4 - half) if (t < n if p < 2 else t > 0)]
+            assert list(walk(n, half)) == order
+            for last in range(1, 5):
+                filled = [0] * (n * 9 + (n - 1) * (8 >> half) + (2 * last >> half))
+                for loader in range(8):
+                    of = list(stages(n, last, loader, half))
+                    assert of == sorted(of) and of[0] < 5 and all(b - a <= 5 for a, b in zip(of, of[1:]))
+                    for x in of:
+                        filled[x] += 1
+                keys = {(t * (9 + (8 >> half)) - (8 >> half) if t else 0) + 4 for t in range(n)}
+                # four loaders of a CTA for a stage of K, two for one of V, none for the rotary keys
+                assert all(c == 0 if x in keys else c in (2, 4) for x, c in enumerate(filled))
