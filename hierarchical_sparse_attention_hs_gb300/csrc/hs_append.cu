@@ -20,7 +20,7 @@
 // Measured on one GB300 (reads and writes over the time): 1 to 32 tokens with 128 heads 2.1-2.2 us, a launch's own cost; 256
 // 2.8 us; 2,047 with 128 heads 18.5 us from fp32 (5.8 TB/s) and 13.5 from bf16; 131,071 without queries 50 us into bf16 rows
 // (6.1 TB/s) and 50 into fp8 rows (4.8: 339 instructions a row, which take 38 us where every scheduler issues one a cycle;
-// 0.73 are measured); 131,071 into 4-bit rows 54 with a norm and 47 without (4.4 TB/s), issue too; 4,096 into host memory
+// 0.73 are measured); 131,071 into 4-bit rows 51.8 with a norm and 44.4 without (4.7 TB/s), issue too; 4,096 into host memory
 // 17.5 us for fp8 rows and 26 for bf16, 153 and 180 GB/s of writes over the link.
 
 #include <cuda_bf16.h>
@@ -57,7 +57,8 @@ constexpr int THREADS = 128, WARPS = THREADS / 32;
 // 6.5). For 1152-byte rows the compiler's own choice is kept, 8 blocks from 16 bits, 50.2 / 8.9 / 5.3 (a bound of 7 50.3
 // / 8.8 / 5.0, of 6 52.9 / 9.2 / 5.6; one of 8 took the queries of 256 and 2,047 tokens from 2.8 and 13.4 to 3.05 and
 // 14.0), 6 from fp32, 70.3 / 11.4 / 6.4 (a bound of 7 73.4 / 10.9 / 5.6, of 5 70.9 / 11.7 / 5.8). For 416-byte rows a
-// bound of 7, from 16 bits with a norm 54.3 / 9.5 / 6.2 (none 54.9 / 10.6 / 6.7, one of 8 55.1 / 10.6 / 6.7).
+// bound of 7, from 16 bits with a norm 51.8 / 9.4 / 6.0 (before packed arithmetic 54.3 / 9.5 / 6.2; no bound 54.9 / 10.6 / 6.7,
+// one of 8 55.1 / 10.6 / 6.7).
 template <Row R>
 constexpr int MIN_BLOCKS = R == BF16 ? 0 : 7;  // 0: none
 constexpr int Q_BLOCKS = 16;  // blocks of queries an SM, at most
@@ -148,13 +149,48 @@ __device__ __forceinline__ float max_nan(float a, float b, float c) {
   asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(m) : "f"(fabsf(a)), "f"(fabsf(b)), "f"(fabsf(c)));
   return m;
 }
-// z / scale to the nearest whole number, ties to even, plus 8, in the low bits: adding 1.5 * 2^23 leaves it there.
-__device__ __forceinline__ uint32_t int4_of(float z, float scale, float inv) {
-  return __float_as_uint(quotient(z, scale, inv) + (12582912.f + 8.f));
+// Two 32-bit values that one instruction multiplies or adds, each rounded as by itself.
+struct F2 {
+  unsigned long long v;
+};
+__device__ __forceinline__ F2 f2(float a, float b) {
+  F2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(a), "f"(b));
+  return r;
 }
-// Four of them at bits 0, 4, 8 and 12: above the number a float's bits hold a multiple of 2^22, which shifts out of the low 16.
-__device__ __forceinline__ uint32_t int4_four(float a, float b, float c, float d, float scale, float inv) {
-  return ((int4_of(d, scale, inv) * 16 + int4_of(c, scale, inv)) * 16 + int4_of(b, scale, inv)) * 16 + int4_of(a, scale, inv);
+__device__ __forceinline__ void split(F2 a, float& x, float& y) { asm("mov.b64 {%0, %1}, %2;" : "=f"(x), "=f"(y) : "l"(a.v)); }
+__device__ __forceinline__ F2 mul(F2 a, F2 b) {
+  F2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+  return r;
+}
+__device__ __forceinline__ F2 add(F2 a, F2 b) {
+  F2 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+  return r;
+}
+__device__ __forceinline__ F2 fma(F2 a, F2 b, F2 c) {
+  F2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+  return r;
+}
+
+// A word of eight latents: z / scale, as quotient() has it, to the nearest whole number, ties to even, plus 8. Adding 1.5 * 2^23
+// leaves a number in the low bits; above it a float's bits hold a multiple of 2^22, which shifts out of the low 16.
+__device__ __forceinline__ uint32_t int4_word(const float (&z)[8], float scale) {
+  float inv;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(scale));
+  const F2 i2 = f2(inv, inv), minus = f2(-scale, -scale), up = f2(12582912.f + 8.f, 12582912.f + 8.f);
+  uint32_t even = 0, odd = 0;
+#pragma unroll
+  for (int e = 3; e >= 0; --e) {
+    const F2 x = f2(z[2 * e], z[2 * e + 1]), y = mul(x, i2);
+    float a, b;
+    split(add(fma(fma(y, minus, x), i2, y), up), a, b);
+    even = even * 16 + __float_as_uint(a);
+    odd = odd * 16 + __float_as_uint(b);
+  }
+  return __byte_perm(even, odd, 0x5410);
 }
 
 // Pair `lane`'s turns per position as a fraction of a turn in units of 2^-64 turns.
@@ -245,10 +281,8 @@ __device__ __forceinline__ void append_rows(const AppendArgs& a, float* weight, 
 #pragma unroll
           for (int e = 0; e < 8; e += 4) {
             const float4 w = *reinterpret_cast<const float4*>(weight + h * (LATENT / 2) + 8 * lane + e);
-            z[h][e] *= r * w.x;
-            z[h][e + 1] *= r * w.y;
-            z[h][e + 2] *= r * w.z;
-            z[h][e + 3] *= r * w.w;
+            split(mul(f2(z[h][e], z[h][e + 1]), mul(f2(r, r), f2(w.x, w.y))), z[h][e], z[h][e + 1]);
+            split(mul(f2(z[h][e + 2], z[h][e + 3]), mul(f2(r, r), f2(w.z, w.w))), z[h][e + 2], z[h][e + 3]);
           }
       }
       // the rotary key: lane j turns pair j; lane l then writes the values 2l and 2l + 1
@@ -318,12 +352,7 @@ __device__ __forceinline__ void append_rows(const AppendArgs& a, float* weight, 
             for (int e = 0; e < 8; ++e) z[h][e] = fminf(fmaxf(z[h][e], -7.f * scale[h]), 7.f * scale[h]);
         }
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          float inv;
-          asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(scale[h]));
-          w[h] = __byte_perm(int4_four(z[h][0], z[h][2], z[h][4], z[h][6], scale[h], inv),
-                             int4_four(z[h][1], z[h][3], z[h][5], z[h][7], scale[h], inv), 0x5410);
-        }
+        for (int h = 0; h < 2; ++h) w[h] = int4_word(z[h], scale[h]);
 #pragma unroll
         for (int d = 0; d < 3; ++d) {
           uint8_t* o = dst[d];
