@@ -148,19 +148,26 @@ def load():
 
 
 def _addr(x) -> int | None:
-    if x is None:
-        return None
-    if isinstance(x, int):
-        return x
-    return x.data_ptr()
+    return x if x is None or isinstance(x, int) else x.data_ptr()
+
+
+_current = None  # torch's current stream of a device and its current device, once torch is loaded
+
+
+def _load_current():
+    global _current
+    import torch
+
+    torch.cuda.current_device()  # starts CUDA; from then on the bare call under it is enough
+    # the handle alone: making a Stream object of it takes longer than a small kernel
+    _current = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
+    return _current
 
 
 def _stream(s) -> int | None:
     if s is None:
-        import torch
-
-        # the handle alone: making a Stream object of it takes longer than a small kernel
-        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+        handle, device = _current or _load_current()
+        return handle(device())
     if isinstance(s, int):
         return s
     return s.cuda_stream
