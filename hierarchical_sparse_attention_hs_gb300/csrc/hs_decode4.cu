@@ -762,15 +762,10 @@ __global__ void __launch_bounds__(THREADS, 1) hs_decode4_kernel(const Decode4Arg
 using Kernel = void (*)(Decode4Args, CUtensorMap);
 const Kernel KERNELS[2] = {hs_decode4_kernel<0>, hs_decode4_kernel<1>};
 
-// How many clusters of 2^lg splits the current device holds at once, cached per device; 0 where it holds none.
-int resident(int lg, int halves) {
+// How many clusters of 2^lg splits the current device, `dev`, holds at once, cached per device; 0 where it holds none.
+int resident(int dev, int lg, int halves) {
   static std::atomic<int> cache[64][2][MAX_PAIRS_LOG + 1];  // 0: not yet asked, else the count + 1
   const unsigned ctas = 2u << (lg + halves);
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) {
-    cudaGetLastError();
-    return 0;
-  }
   const int c = cache[dev][halves][lg].load(std::memory_order_relaxed);
   if (c) return c - 1;
   cudaLaunchConfig_t cfg = {};
@@ -807,10 +802,15 @@ struct Cut {
 Cut cut_of(int32_t batch, int32_t k) {
   const int tiles = (k + NK - 1) / NK;
   Cut best = {0, 0};
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) {
+    cudaGetLastError();
+    return best;
+  }
   double least = 0;
   for (int halves = 0; halves < 2; ++halves)
     for (int lg = 0; lg + halves <= MAX_PAIRS_LOG && 1 << lg <= tiles; ++lg) {
-      const int n = 1 << lg, held = resident(lg, halves);
+      const int n = 1 << lg, held = resident(dev, lg, halves);
       if (held < 1) continue;
       const double join = lg == 0 ? 0. : halves ? 1.5 + 1.1 * lg : 2.6 + 1.3 * lg;
       const double cost = (double)((batch + held - 1) / held) * (5. + (tiles + n - 1) / n * (halves ? 3.4 : 4.2) + join);

@@ -472,3 +472,17 @@ def test_host_rows_rewritten_between_replays():
     assert hs.hs_get_error(pool) == 0
     mem.close()
     buf.close()
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("batch,k", [(1, 65), (1, 700), (2, 2048), (1, 5000), (30, 1100), (77, 300)])
+def test_only_the_batch_is_written(batch, k, dtype):
+    """Outputs beside the batch's, the rows and the list stay as they are, however a request is cut."""
+    c = Case(batch, k, slots=700, seed=3, padded=0.1, max_batch=batch + 1)
+    out, lse = torch.full((batch + 2, H, DV), 7.0, device="cuda", dtype=dtype), torch.full((batch + 2, H), 7.0, device="cuda")
+    hot, e, q = c.buf.hot.clone(), c.e.clone(), c.q.clone()
+    c.run(hs.HS_TYPE_F32 if dtype == torch.float32 else hs.HS_TYPE_BF16, out=out[1:-1], lse=lse[1:-1])
+    c.check(out[1:-1], lse[1:-1], requests=sorted({0, batch - 1}))
+    assert (out[[0, -1]] == 7).all() and (lse[[0, -1]] == 7).all()
+    assert torch.equal(hot, c.buf.hot) and torch.equal(e, c.e) and torch.equal(q, c.q)
+    c.close()
