@@ -790,52 +790,66 @@ int resident(int dev, int lg, int halves) {
   return got;
 }
 
-// How a request is cut: the splits of its list, and whether two pairs of CTAs share the value columns of each.
+// How the requests of a grid are cut: the splits of a list, and whether two pairs of CTAs share the value columns of each.
 struct Cut {
   int splits, halves;
 };
-// The cut with the shortest expected time: waves of clusters, each of its start, its last softmax and its output (5 us), its
-// tiles (4.2 us, 3.4 with half of the value columns) and the join of splits. Measured, in us, as splits / splits with halves:
-// one request of 65 entries 9.4 / 8.3; of 400, one 13.6 / 11.6, two 13.3 / 10.9; of 2,048, one 39 / 32, two 25.7 / 20.7, four
-// 18.3 / 14.9, eight 15.8; 9 of 2,048 (more clusters of 16 CTAs than the device holds), two 26.1 / 21.6, four 19.3 / 30.6; 32 of
-// 2,048, one 41 / 34, two 27.9 / 65; 76 of 2,048, one 45 / 100.
-Cut cut_of(int32_t batch, int32_t k) {
-  const int tiles = (k + NK - 1) / NK;
+// Calls f(lg, halves, clusters held at once, us of one wave of them) for every way to cut lists of `tiles` tiles into 2^lg
+// splits. A wave takes its start, its last softmax and its output (5 us), its tiles (4.2 us, 3.4 with half of the value columns) and
+// the join of splits. Measured, in us, as splits / splits with halves: one request of 65 entries 9.4 / 8.3; of 400, one 13.6 /
+// 11.6, two 13.3 / 10.9; of 2,048, one 39 / 32, two 25.7 / 20.7, four 18.3 / 14.9, eight 15.8; 9 of 2,048 (more clusters of 16
+// CTAs than the device holds), two 26.1 / 21.6, four 19.3 / 30.6; 32 of 2,048, one 41 / 34, two 27.9 / 65; 76 of 2,048, one 45 /
+// 100.
+template <class F>
+void each_cut(int dev, int tiles, F f) {
+  for (int halves = 0; halves < 2; ++halves)
+    for (int lg = 0; lg + halves <= MAX_PAIRS_LOG && 1 << lg <= tiles; ++lg) {
+      const int held = resident(dev, lg, halves);
+      const double join = lg == 0 ? 0. : halves ? 1.5 + 1.1 * lg : 2.6 + 1.3 * lg;
+      if (held > 0) f(lg, halves, held, 5. + (((tiles - 1) >> lg) + 1) * (halves ? 3.4 : 4.2) + join);
+    }
+}
+// The cut of one grid with the shortest expected time, which goes to *us.
+Cut cut_of(int dev, int32_t batch, int tiles, double* us) {
   Cut best = {0, 0};
+  each_cut(dev, tiles, [&](int lg, int halves, int held, double wave) {
+    const double cost = (batch + held - 1) / held * wave;
+    if (best.splits == 0 || cost < *us) *us = cost, best = {1 << lg, halves};
+  });
+  return best;
+}
+// A call is one grid, or two where the requests of a last, partly filled wave do better with a cut of their own (a second grid
+// costs GRID_US: with 1.5 77 requests of 300 took 27.1 us in place of 26.4). 80 of 2,048 62.5 us from 81.3, 160 106 from 124,
+// 100 of 1,111 53.1 from 56.0.
+struct Plan {
+  int32_t first;  // requests of the first grid
+  Cut cut[2];
+};
+constexpr double GRID_US = 3;
+Plan plan_of(int32_t batch, int32_t k) {
+  const int tiles = (k + NK - 1) / NK;
+  Plan plan = {batch, {{0, 0}, {0, 0}}};
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) {
     cudaGetLastError();
-    return best;
+    return plan;
   }
   double least = 0;
-  for (int halves = 0; halves < 2; ++halves)
-    for (int lg = 0; lg + halves <= MAX_PAIRS_LOG && 1 << lg <= tiles; ++lg) {
-      const int n = 1 << lg, held = resident(dev, lg, halves);
-      if (held < 1) continue;
-      const double join = lg == 0 ? 0. : halves ? 1.5 + 1.1 * lg : 2.6 + 1.3 * lg;
-      const double cost = (double)((batch + held - 1) / held) * (5. + (tiles + n - 1) / n * (halves ? 3.4 : 4.2) + join);
-      if (best.splits == 0 || cost < least) least = cost, best = {n, halves};
-    }
-  return best;
+  plan.cut[0] = cut_of(dev, batch, tiles, &least);
+  each_cut(dev, tiles, [&](int lg, int halves, int held, double wave) {
+    const int32_t waves = batch / held, rest = batch - waves * held;
+    if (waves == 0 || rest == 0 || waves * wave + GRID_US >= least) return;
+    double us = 0;
+    const Cut last = cut_of(dev, rest, tiles, &us);
+    us += waves * wave + GRID_US;
+    if (us < least) least = us, plan = {waves * held, {{1 << lg, halves}, last}};
+  });
+  return plan;
 }
 
-int launch(hs_pool* p, int32_t batch, const void* q, const int32_t* idx, int32_t k, const RowSource& src, float sm_scale,
-           void* out, int32_t out_type, float* lse, hs_stream_t stream) {
-  Decode4Args a;
-  std::memset(&a, 0, sizeof(a));
-  const Cut cut = cut_of(batch, k);
-  if (cut.splits < 1) return HS_ERR_UNSUPPORTED;
+int launch_part(Decode4Args a, int32_t batch, const Cut& cut, const void* q, hs_stream_t stream) {
   a.nsplit = cut.splits;
   const unsigned ctas = (2u * (unsigned)cut.splits) << cut.halves;  // of a request: a cluster
-  a.idx = idx;
-  a.k = k;
-  a.src = src;
-  a.scale_log2 = sm_scale * 1.4426950408889634f;
-  a.out = out;
-  a.out_f32 = out_type == HS_TYPE_F32;
-  a.lse = lse;
-  a.err = p->err;
-  hs_attention_waits(&a.wait_limit, &a.stall);
   CUtensorMap qmap;
   const EncodeFn encode = encoder();
   if (!encode) return HS_ERR_UNSUPPORTED;
@@ -854,6 +868,31 @@ int launch(hs_pool* p, int32_t batch, const void* q, const int32_t* idx, int32_t
   cfg.attrs = attr;
   cfg.numAttrs = 2;
   return hs_launched(cudaLaunchKernelEx(&cfg, KERNELS[cut.halves], a, qmap));
+}
+
+int launch(hs_pool* p, int32_t batch, const void* q, const int32_t* idx, int32_t k, const RowSource& src, float sm_scale,
+           void* out, int32_t out_type, float* lse, hs_stream_t stream) {
+  const Plan plan = plan_of(batch, k);
+  if (plan.cut[0].splits < 1) return HS_ERR_UNSUPPORTED;
+  Decode4Args a;
+  std::memset(&a, 0, sizeof(a));
+  a.idx = idx;
+  a.k = k;
+  a.src = src;
+  a.scale_log2 = sm_scale * 1.4426950408889634f;
+  a.out = out;
+  a.out_f32 = out_type == HS_TYPE_F32;
+  a.lse = lse;
+  a.err = p->err;
+  hs_attention_waits(&a.wait_limit, &a.stall);
+  const int rc = launch_part(a, plan.first, plan.cut[0], q, stream);
+  if (rc != HS_OK || plan.first == batch) return rc;
+  const size_t heads = (size_t)plan.first * HEADS;
+  a.idx += (size_t)plan.first * (size_t)k;
+  a.src.rows += (size_t)plan.first * (size_t)src.req_stride;
+  a.out = static_cast<uint8_t*>(out) + heads * LATENT * (a.out_f32 ? 4 : 2);
+  a.lse += heads;
+  return launch_part(a, batch - plan.first, plan.cut[1], static_cast<const uint8_t*>(q) + heads * (WIDTH * 2), stream);
 }
 
 // HS_OK, or what the call is refused with; *empty for one that has nothing to do.

@@ -135,7 +135,7 @@ def test_lengths(batch, k):
 
 
 @pytest.mark.parametrize("batch,k", [(2, 2048), (1, 4097), (9, 1500), (9, 2100), (17, 700), (20, 513), (30, 1100), (39, 600),
-                                     (77, 300), (160, 70)])
+                                     (77, 300), (80, 1300), (160, 70), (190, 500)])
 def test_batches(batch, k):
     c = Case(batch, k, slots=600, away=50, seed=batch, padded=0.05)
     c.check(*c.run(hs.HS_TYPE_F32 if batch % 2 else hs.HS_TYPE_BF16), requests=sorted({0, 1, batch // 2, batch - 1} & set(range(batch))))
@@ -475,7 +475,7 @@ def test_host_rows_rewritten_between_replays():
 
 
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
-@pytest.mark.parametrize("batch,k", [(1, 65), (1, 700), (2, 2048), (1, 5000), (30, 1100), (77, 300)])
+@pytest.mark.parametrize("batch,k", [(1, 65), (1, 700), (2, 2048), (1, 5000), (30, 1100), (77, 300), (80, 1300)])
 def test_only_the_batch_is_written(batch, k, dtype):
     """Outputs beside the batch's, the rows and the list stay as they are, however a request is cut."""
     c = Case(batch, k, slots=700, seed=3, padded=0.1, max_batch=batch + 1)
@@ -485,4 +485,20 @@ def test_only_the_batch_is_written(batch, k, dtype):
     c.check(out[1:-1], lse[1:-1], requests=sorted({0, batch - 1}))
     assert (out[[0, -1]] == 7).all() and (lse[[0, -1]] == 7).all()
     assert torch.equal(hot, c.buf.hot) and torch.equal(e, c.e) and torch.equal(q, c.q)
+    c.close()
+
+
+def test_a_large_batch_from_the_history():
+    """More requests than the device holds at once, the last of them in a grid of their own: from the history as from hot slots."""
+    batch, k, ctx = 80, 530, 600
+    c = Case(batch, k, slots=ctx, seed=41, padded=0.02, garbage=False)
+    buf = hs.PoolBuffers(2, batch, ctx, 16, 8, 416)
+    pool = buf.create()
+    buf.host.numpy().reshape(2, batch, ctx, 416)[1] = c.hot
+    want = c.run()
+    got = torch.empty_like(want[0]), torch.empty_like(want[1])
+    hs.hs_mla_decode_int4_history(pool, 1, batch, c.q, c.e, k, SCALE, got[0], hs.HS_TYPE_BF16, got[1])
+    c.check(*got, requests=[0, 1, 37, 75, 76, 77, 79])
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1]) and hs.hs_get_error(pool) == 0
+    buf.close()
     c.close()
