@@ -418,61 +418,82 @@ def _load_value_types():
     return _value_types
 
 
-def _check_lists(what: str, pool: int, batch: int, entries, k: int, rows=None, count: int = 0) -> None:
-    if not _fits(entries, (_dtypes or _load_dtypes())[2], batch * k * 4):
+def _tensor(t, dtype, nbytes: int):
+    """The address of a tensor that _fits, or False."""
+    if t is None or isinstance(t, int):
+        return t
+    return t.dtype is dtype and t.nbytes >= nbytes and t.is_contiguous() and t.data_ptr()
+
+
+def _entries(what: str, batch: int, entries, k: int):
+    at = _tensor(entries, (_dtypes or _load_dtypes())[2], batch * k * 4)
+    if at is False:
         raise ValueError(f"{what} takes a contiguous int32 list [{batch}][{k}]")
-    if rows is not None and not isinstance(rows, int):
-        row_bytes = _pool_row_bytes.get(pool, 0)
-        if rows.nbytes < count * row_bytes or not rows.is_contiguous():
-            raise ValueError(f"{what} takes contiguous resident rows, {count} of {row_bytes} bytes")
+    return at
 
 
-def _check_values(what: str, batch: int, k: int, dst, dst_type: int) -> None:
+def _resident(what: str, pool: int, rows, count: int):
+    if rows is None or isinstance(rows, int):
+        return rows
+    row_bytes = _pool_row_bytes.get(pool, 0)
+    if rows.nbytes < count * row_bytes or not rows.is_contiguous():
+        raise ValueError(f"{what} takes contiguous resident rows, {count} of {row_bytes} bytes")
+    return rows.data_ptr()
+
+
+def _values(what: str, batch: int, k: int, dst, dst_type: int):
     # (of a type that there is not the library says so)
     t = (_value_types or _load_value_types()).get(dst_type)
-    if t is not None and not _fits(dst, t[0], batch * k * t[1]):
+    if t is None:
+        return _addr(dst)
+    at = _tensor(dst, t[0], batch * k * t[1])
+    if at is False:
         raise ValueError(f"{what} writes a contiguous {t[0]} [{batch}][{k}][{MLA_D_QK}]")
+    return at
 
 
 def hs_gather_values(pool: int, layer: int, batch: int, out_slots, k: int, resident_rows, resident_count: int, dst,
                      dst_type: int, stream=None) -> None:
-    _check_lists("hs_gather_values", pool, batch, out_slots, k, resident_rows, resident_count)
-    _check_values("hs_gather_values", batch, k, dst, dst_type)
-    _check((_lib or load()).hs_gather_values(pool, layer, batch, _addr(out_slots), k, _addr(resident_rows), resident_count,
-                                             _addr(dst), dst_type, _stream(stream)), "hs_gather_values")
+    entries = _entries("hs_gather_values", batch, out_slots, k)
+    rows = _resident("hs_gather_values", pool, resident_rows, resident_count)
+    values = _values("hs_gather_values", batch, k, dst, dst_type)
+    _check((_lib or load()).hs_gather_values(pool, layer, batch, entries, k, rows, resident_count, values, dst_type,
+                                             _stream(stream)), "hs_gather_values")
 
 
 def hs_gather_values_history(pool: int, layer: int, batch: int, topk_idx, k: int, dst, dst_type: int, stream=None) -> None:
-    _check_lists("hs_gather_values_history", pool, batch, topk_idx, k)
-    _check_values("hs_gather_values_history", batch, k, dst, dst_type)
-    _check((_lib or load()).hs_gather_values_history(pool, layer, batch, _addr(topk_idx), k, _addr(dst), dst_type,
-                                                     _stream(stream)), "hs_gather_values_history")
+    entries = _entries("hs_gather_values_history", batch, topk_idx, k)
+    values = _values("hs_gather_values_history", batch, k, dst, dst_type)
+    _check((_lib or load()).hs_gather_values_history(pool, layer, batch, entries, k, values, dst_type, _stream(stream)),
+           "hs_gather_values_history")
 
 
-def _check_heads(what: str, batch: int, q, out, out_type: int, lse) -> None:
+def _heads(what: str, batch: int, q, out, out_type: int, lse):
     bf16, f32, _, _ = _dtypes or _load_dtypes()
     rows = batch * MLA_HEADS
     dtype, size = (f32, 4) if out_type == HS_TYPE_F32 else (bf16, 2)
-    if not (_fits(q, bf16, rows * (2 * MLA_D_QK)) and _fits(out, dtype, rows * (size * MLA_D_V)) and _fits(lse, f32, rows * 4)):
+    at = _tensor(q, bf16, rows * (2 * MLA_D_QK)), _tensor(out, dtype, rows * (size * MLA_D_V)), _tensor(lse, f32, rows * 4)
+    if at[0] is False or at[1] is False or at[2] is False:
         raise ValueError(f"{what} of {batch} takes contiguous tensors: q bf16 [{batch}][128][576], out {dtype} "
                          f"[{batch}][128][512], lse fp32 [{batch}][128]")
+    return at
 
 
 def hs_mla_decode_int4(pool: int, layer: int, batch: int, q, out_slots, k: int, resident_rows, resident_count: int,
                        sm_scale: float, out, out_type: int, lse, stream=None) -> None:
-    _check_lists("hs_mla_decode_int4", pool, batch, out_slots, k, resident_rows, resident_count)
-    _check_heads("hs_mla_decode_int4", batch, q, out, out_type, lse)
-    _check((_lib or load()).hs_mla_decode_int4(pool, layer, batch, _addr(q), _addr(out_slots), k, _addr(resident_rows),
-                                               resident_count, sm_scale, _addr(out), out_type, _addr(lse), _stream(stream)),
-           "hs_mla_decode_int4")
+    entries = _entries("hs_mla_decode_int4", batch, out_slots, k)
+    rows = _resident("hs_mla_decode_int4", pool, resident_rows, resident_count)
+    q, out, lse = _heads("hs_mla_decode_int4", batch, q, out, out_type, lse)
+    _check((_lib or load()).hs_mla_decode_int4(pool, layer, batch, q, entries, k, rows, resident_count, sm_scale, out, out_type,
+                                               lse, _stream(stream)), "hs_mla_decode_int4")
 
 
 def hs_mla_decode_int4_history(pool: int, layer: int, batch: int, q, topk_idx, k: int, sm_scale: float, out, out_type: int,
                                lse, stream=None) -> None:
-    _check_lists("hs_mla_decode_int4_history", pool, batch, topk_idx, k)
-    _check_heads("hs_mla_decode_int4_history", batch, q, out, out_type, lse)
-    _check((_lib or load()).hs_mla_decode_int4_history(pool, layer, batch, _addr(q), _addr(topk_idx), k, sm_scale, _addr(out),
-                                                       out_type, _addr(lse), _stream(stream)), "hs_mla_decode_int4_history")
+    entries = _entries("hs_mla_decode_int4_history", batch, topk_idx, k)
+    q, out, lse = _heads("hs_mla_decode_int4_history", batch, q, out, out_type, lse)
+    _check((_lib or load()).hs_mla_decode_int4_history(pool, layer, batch, q, entries, k, sm_scale, out, out_type, lse,
+                                                       _stream(stream)), "hs_mla_decode_int4_history")
 
 
 def hs_get_error(pool: int, clear: bool = False) -> int:
