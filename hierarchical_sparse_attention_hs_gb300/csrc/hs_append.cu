@@ -19,9 +19,10 @@
 //
 // Measured on one GB300 (reads and writes over the time): 1 to 32 tokens with 128 heads 2.1-2.2 us, a launch's own cost; 256
 // 2.8 us; 2,047 with 128 heads 18.5 us from fp32 (5.8 TB/s) and 13.5 from bf16; 131,071 without queries 50 us into bf16 rows
-// (6.1 TB/s) and 50 into fp8 rows (4.8: 339 instructions a row, which take 38 us where every scheduler issues one a cycle;
-// 0.73 are measured); 131,071 into 4-bit rows 51.8 with a norm and 44.4 without (4.7 TB/s), issue too; 4,096 into host memory
-// 17.5 us for fp8 rows and 26 for bf16, 153 and 180 GB/s of writes over the link.
+// (6.1 TB/s) and 49.6 into fp8 rows (4.8 TB/s; 50.1 and 339 instructions a row before the norm's products went two an
+// instruction, which take 38 us where every scheduler issues one a cycle: 0.73 were measured); 131,071 into 4-bit rows 51.8
+// with a norm and 44.4 without (4.7 TB/s), issue too; 4,096 into host memory 17.5 us for fp8 rows and 26 for bf16, 153 and
+// 180 GB/s of writes over the link.
 
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
