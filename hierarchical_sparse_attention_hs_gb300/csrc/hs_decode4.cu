@@ -34,8 +34,8 @@
 //
 // Measured on one GB300 (replayed graphs): a tile takes 4.1 us, 7,700 cycles, of which its MMAs are 4,352 at their full rate.
 // Shared memory is what it waits for: 2,200 cycles of stores of unpacked rows, 1,100 of the words' way through it, and 96 of
-// its 128 bytes a cycle that MMAs of this shape read while they run, 3,300 or more. 32 requests of 2,048 entries 28.0 us (652
-// TFLOP/s; four tiles a pair, the start, the join), one 14.7, seven 16.4, five of 16,384 46.0, one of 65 8.2.
+// its 128 bytes a cycle that MMAs of this shape read while they run, 3,300 or more. 32 requests of 2,048 entries 27.8 us (657
+// TFLOP/s; four tiles a pair, the start, the join), one 14.4, seven 16.3, five of 16,384 45.5, one of 65 8.3.
 //
 // Steps that brought it there, for 32 requests of 2,048: lanes that load a row each 62 us; eight rows by four lanes 40; copies
 // into shared memory, scores in bf16, queries by TMA 34; jobs of 32 rows in a fixed order, the keys by warps of their own
@@ -300,12 +300,11 @@ __global__ void __launch_bounds__(THREADS, 1) hs_decode4_kernel(const Decode4Arg
   } else if (warp >= KEY_WARP) {
     // ---- the rotary keys of the CTA's half of every tile, 64 rows a warp, as they are: 16 bytes a copy, eight lanes a row.
     //      Their place in the ring is free when the V before this K has been multiplied (of the second K: when the first one
-    //      has; either wait is for a phase that the next one of its barrier cannot follow before these keys are there). The
-    //      rows as a whole come into L2 a tile ahead of their first words, asked for in nine pieces over the time of a tile.
+    //      has; either wait is for a phase that the next one of its barrier cannot follow before these keys are there). (Rows
+    //      as a whole brought into L2 a tile or two ahead: 46.2 us for five requests of 16,384 against 45.6, cold and warm.)
     ok = !a.stall || __all_sync(0xffffffffu, bar_wait(bar + B_STALL, 0, abort_flag, lim));
     const int r8 = lane & 7, qd = lane >> 3, part = warp - KEY_WARP;
-    unsigned long long row[2], later[2];  // of the lane's rows: of this tile, and of the next
-    int32_t e[2];                         // the entries of the tile after that
+    int32_t e[2];  // the entries of the lane's rows, a tile ahead
     auto entries = [&](int tile) {
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
@@ -313,22 +312,12 @@ __global__ void __launch_bounds__(THREADS, 1) hs_decode4_kernel(const Decode4Arg
         e[i] = tile < tiles.n && x < a.k ? ld_fresh(list + x) : -1;
       }
     };
-    auto find = [&](unsigned long long (&to)[2]) {
-#pragma unroll
-      for (int i = 0; i < 2; ++i) to[i] = reinterpret_cast<unsigned long long>(row_at(a.src, b, e[i], ROW_INT4));
-    };
-    auto prefetch = [&](const unsigned long long (&of)[2]) {
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        if (!of[i]) continue;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) asm volatile("prefetch.global.L2 [%0];" ::"l"((of[i] & ~127ull) + j * 128) : "memory");
-      }
-    };
     entries(0);
-    find(row);
-    entries(1);
     for (int t = 0; t < tiles.n && ok; ++t) {
+      unsigned long long row[2];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) row[i] = reinterpret_cast<unsigned long long>(row_at(a.src, b, e[i], ROW_INT4));
+      entries(t + 1);
       if (t == 1) ok = __all_sync(0xffffffffu, bar_wait(bar + B_SFULL, 0, abort_flag, lim));
       if (t >= 2) ok = __all_sync(0xffffffffu, bar_wait(bar + B_PDONE, (unsigned)(t - 2) & 1u, abort_flag, lim));
       if (!ok) break;
@@ -345,20 +334,10 @@ __global__ void __launch_bounds__(THREADS, 1) hs_decode4_kernel(const Decode4Arg
           *reinterpret_cast<uint4*>(d) = make_uint4(0, 0, 0, 0);
       }
       copies_commit();
-      if (t == 0) {
-        find(later);
-        prefetch(later);
-        entries(2);
-      }
       copies_wait<0>();
       fence_proxy_async();
       __syncwarp();
       if (lane == 0) arrive_lead(lead + (B_FULL + slot) * 8, 2);
-#pragma unroll
-      for (int i = 0; i < 2; ++i) row[i] = later[i];
-      find(later);
-      prefetch(later);
-      entries(t + 3);
     }
     copies_wait<0>();
     __syncwarp();
