@@ -500,5 +500,13 @@ def test_a_large_batch_from_the_history():
     hs.hs_mla_decode_int4_history(pool, 1, batch, c.q, c.e, k, SCALE, got[0], hs.HS_TYPE_BF16, got[1])
     c.check(*got, requests=[0, 1, 37, 75, 76, 77, 79])
     assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1]) and hs.hs_get_error(pool) == 0
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        c.run(out=got[0], lse=got[1])
+    for seed in range(2):  # another list in the captured one's place
+        c.entries = np.ascontiguousarray(np.roll(c.entries, 7, axis=0))
+        c.e.copy_(torch.from_numpy(c.entries))
+        graph.replay()
+        c.check(*got, requests=[0, 74, 75, 76, 79])
     buf.close()
     c.close()
