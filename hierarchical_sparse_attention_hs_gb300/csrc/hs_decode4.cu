@@ -741,7 +741,8 @@ __global__ void __launch_bounds__(THREADS, 1) hs_decode4_kernel(const Decode4Arg
 using Kernel = void (*)(Decode4Args, CUtensorMap);
 const Kernel KERNELS[2] = {hs_decode4_kernel<0>, hs_decode4_kernel<1>};
 
-// How many clusters of 2^lg splits the current device, `dev`, holds at once, cached per device; 0 where it holds none.
+// How many clusters of 2^lg splits the current device, `dev`, holds at once, cached per device; 0 where it holds none, or takes
+// none that large. -1 where it could not be asked: not cached, so that equal calls are cut alike before and after.
 int resident(int dev, int lg, int halves) {
   static std::atomic<int> cache[64][2][MAX_PAIRS_LOG + 1];  // 0: not yet asked, else the count + 1
   const unsigned ctas = 2u << (lg + halves);
@@ -759,11 +760,18 @@ int resident(int dev, int lg, int halves) {
   cfg.numAttrs = 1;
   int got = 0;
   const Kernel kernel = KERNELS[halves];
-  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_BYTES) != cudaSuccess ||
-      (ctas > 8 && cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess) ||
-      cudaOccupancyMaxActiveClusters(&got, kernel, &cfg) != cudaSuccess) {
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_BYTES);
+  if (e == cudaSuccess && ctas > 8) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+  if (e == cudaSuccess) {
+    e = cudaOccupancyMaxActiveClusters(&got, kernel, &cfg);
+    if (e == cudaErrorInvalidClusterSize) {
+      cudaGetLastError();
+      got = 0, e = cudaSuccess;
+    }
+  }
+  if (e != cudaSuccess) {
     cudaGetLastError();
-    got = 0;
+    return -1;
   }
   cache[dev][halves][lg].store(got + 1, std::memory_order_relaxed);
   return got;
@@ -774,28 +782,30 @@ struct Cut {
   int splits, halves;
 };
 // Calls f(lg, halves, clusters held at once, us of one wave of them) for every way to cut lists of `tiles` tiles into 2^lg
-// splits. A wave takes its start, its last softmax and its output (5 us), its tiles (4.2 us, 3.4 with half of the value columns) and
-// the join of splits. Measured, in us, as splits / splits with halves: one request of 65 entries 9.4 / 8.3; of 400, one 13.6 /
-// 11.6, two 13.3 / 10.9; of 2,048, one 39 / 32, two 25.7 / 20.7, four 18.3 / 14.9, eight 15.8; 9 of 2,048 (more clusters of 16
-// CTAs than the device holds), two 26.1 / 21.6, four 19.3 / 30.6; 32 of 2,048, one 41 / 34, two 27.9 / 65; 76 of 2,048, one 45 /
-// 100.
+// splits; false where the device could not be asked. A wave takes its start, its last softmax and its output (5 us), its tiles
+// (4.2 us, 3.4 with half of the value columns) and the join of splits. Measured, in us, as splits / splits with halves: one
+// request of 65 entries 9.4 / 8.3; of 400, one 13.6 / 11.6, two 13.3 / 10.9; of 2,048, one 39 / 32, two 25.7 / 20.7, four 18.3 /
+// 14.9, eight 15.8; 9 of 2,048 (more clusters of 16 CTAs than the device holds), two 26.1 / 21.6, four 19.3 / 30.6; 32 of 2,048,
+// one 41 / 34, two 27.9 / 65; 76 of 2,048, one 45 / 100.
 template <class F>
-void each_cut(int dev, int tiles, F f) {
+bool each_cut(int dev, int tiles, F f) {
   for (int halves = 0; halves < 2; ++halves)
     for (int lg = 0; lg + halves <= MAX_PAIRS_LOG && 1 << lg <= tiles; ++lg) {
       const int held = resident(dev, lg, halves);
+      if (held < 0) return false;
       const double join = lg == 0 ? 0. : halves ? 1.5 + 1.1 * lg : 2.6 + 1.3 * lg;
       if (held > 0) f(lg, halves, held, 5. + (((tiles - 1) >> lg) + 1) * (halves ? 3.4 : 4.2) + join);
     }
+  return true;
 }
-// The cut of one grid with the shortest expected time, which goes to *us.
-Cut cut_of(int dev, int32_t batch, int tiles, double* us) {
-  Cut best = {0, 0};
-  each_cut(dev, tiles, [&](int lg, int halves, int held, double wave) {
+// The cut of one grid with the shortest expected time, which goes to *us; no splits where the device holds no pair, and false
+// where it could not be asked.
+bool cut_of(int dev, int32_t batch, int tiles, Cut* best, double* us) {
+  *best = {0, 0};
+  return each_cut(dev, tiles, [&](int lg, int halves, int held, double wave) {
     const double cost = (batch + held - 1) / held * wave;
-    if (best.splits == 0 || cost < *us) *us = cost, best = {1 << lg, halves};
+    if (best->splits == 0 || cost < *us) *us = cost, *best = {1 << lg, halves};
   });
-  return best;
 }
 // A call is one grid, or two where the requests of a last, partly filled wave do better with a cut of their own (a second grid
 // costs GRID_US: with 1.5 77 requests of 300 took 27.1 us in place of 26.4). 80 of 2,048 62.5 us from 81.3, 160 106 from 124,
@@ -805,25 +815,22 @@ struct Plan {
   Cut cut[2];
 };
 constexpr double GRID_US = 3;
-Plan plan_of(int32_t batch, int32_t k) {
+int plan_of(int dev, int32_t batch, int32_t k, Plan* plan) {
+  if (dev < 0 || dev >= 64) return HS_ERR_UNSUPPORTED;
   const int tiles = (k + NK - 1) / NK;
-  Plan plan = {batch, {{0, 0}, {0, 0}}};
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) {
-    cudaGetLastError();
-    return plan;
-  }
+  *plan = {batch, {{0, 0}, {0, 0}}};
   double least = 0;
-  plan.cut[0] = cut_of(dev, batch, tiles, &least);
-  each_cut(dev, tiles, [&](int lg, int halves, int held, double wave) {
+  if (!cut_of(dev, batch, tiles, &plan->cut[0], &least)) return HS_ERR_CUDA;
+  each_cut(dev, tiles, [&](int lg, int halves, int held, double wave) {  // (every answer is cached by now)
     const int32_t waves = batch / held, rest = batch - waves * held;
     if (waves == 0 || rest == 0 || waves * wave + GRID_US >= least) return;
     double us = 0;
-    const Cut last = cut_of(dev, rest, tiles, &us);
+    Cut last;
+    cut_of(dev, rest, tiles, &last, &us);
     us += waves * wave + GRID_US;
-    if (us < least) least = us, plan = {waves * held, {{1 << lg, halves}, last}};
+    if (us < least) least = us, *plan = {waves * held, {{1 << lg, halves}, last}};
   });
-  return plan;
+  return plan->cut[0].splits < 1 ? HS_ERR_UNSUPPORTED : HS_OK;
 }
 
 int launch_part(Decode4Args a, int32_t batch, const Cut& cut, const void* q, hs_stream_t stream) {
@@ -851,8 +858,9 @@ int launch_part(Decode4Args a, int32_t batch, const Cut& cut, const void* q, hs_
 
 int launch(hs_pool* p, int32_t batch, const void* q, const int32_t* idx, int32_t k, const RowSource& src, float sm_scale,
            void* out, int32_t out_type, float* lse, hs_stream_t stream) {
-  const Plan plan = plan_of(batch, k);
-  if (plan.cut[0].splits < 1) return HS_ERR_UNSUPPORTED;
+  Plan plan;
+  int rc = plan_of(p->device, batch, k, &plan);  // (the pool's device is the current one: see check)
+  if (rc != HS_OK) return rc;
   Decode4Args a;
   std::memset(&a, 0, sizeof(a));
   a.idx = idx;
@@ -864,7 +872,7 @@ int launch(hs_pool* p, int32_t batch, const void* q, const int32_t* idx, int32_t
   a.lse = lse;
   a.err = p->err;
   hs_attention_waits(&a.wait_limit, &a.stall);
-  const int rc = launch_part(a, plan.first, plan.cut[0], q, stream);
+  rc = launch_part(a, plan.first, plan.cut[0], q, stream);
   if (rc != HS_OK || plan.first == batch) return rc;
   const size_t heads = (size_t)plan.first * HEADS;
   a.idx += (size_t)plan.first * (size_t)k;
