@@ -56,6 +56,7 @@
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <atomic>
 #include <cstdint>
 #include <cstring>
@@ -699,14 +700,16 @@ __global__ void __launch_bounds__(NTHREADS, 1) hs_mla_decode_kernel(const MlaArg
   }
 }
 
-// How many clusters of four CTAs (a request's two key halves) the current device holds at once, cached per device.
+// How many clusters of four CTAs (a request's two key halves) the current device holds at once, cached per device; -1 where it
+// could not be asked: not cached, so that equal calls are split alike before and after.
 int four_cta_clusters_resident() {
   static std::atomic<int> cache[64];  // 0: not yet asked, else the count + 1
   int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) {
+  if (cudaGetDevice(&dev) != cudaSuccess) {
     cudaGetLastError();
-    return 0;
+    return -1;
   }
+  if (dev < 0 || dev >= 64) return 0;
   const int c = cache[dev].load(std::memory_order_relaxed);
   if (c) return c - 1;
   cudaLaunchConfig_t cfg = {};
@@ -720,10 +723,12 @@ int four_cta_clusters_resident() {
   attr.val.clusterDim.z = 1;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
+  // (without the attribute, as long as no call has set it, the answer is 0)
   int n = 0;
-  if (cudaOccupancyMaxActiveClusters(&n, hs_mla_decode_kernel, &cfg) != cudaSuccess) {
+  if (cudaFuncSetAttribute(hs_mla_decode_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_BYTES) != cudaSuccess ||
+      cudaOccupancyMaxActiveClusters(&n, hs_mla_decode_kernel, &cfg) != cudaSuccess) {
     cudaGetLastError();
-    n = 0;
+    return -1;
   }
   cache[dev].store(n + 1, std::memory_order_relaxed);
   return n;
@@ -742,7 +747,9 @@ int launch_mla(hs_pool* p, int32_t batch, MlaArgs a, cudaStream_t s) {
   // Split each request's keys in two (a cluster of four CTAs) when every request's cluster fits on the device at
   // once; the per-block chain of dependent steps, not a bandwidth, bounds a CTA pair, so twice the SMs take half
   // the blocks each.
-  a.nsplit = four_cta_clusters_resident() >= batch ? 2 : 1;
+  const int held = four_cta_clusters_resident();
+  if (held < 0) return HS_ERR_CUDA;
+  a.nsplit = held >= batch ? 2 : 1;
   a.wait_limit = g_wait_limit.load(std::memory_order_relaxed);
   a.stall = g_stall.load(std::memory_order_relaxed);
   cudaLaunchConfig_t cfg = {};
@@ -829,6 +836,8 @@ extern "C" int hs_mla_decode_history(hs_pool* pool, int32_t layer, int32_t batch
 extern "C" int hs_debug_attention(uint32_t wait_limit, int32_t stall, int32_t* split_max_batch) {
   g_wait_limit.store(wait_limit ? wait_limit : WAIT_LIMIT, std::memory_order_relaxed);
   g_stall.store(stall ? 1 : 0, std::memory_order_relaxed);
-  if (split_max_batch) *split_max_batch = four_cta_clusters_resident();
-  return HS_OK;
+  if (!split_max_batch) return HS_OK;
+  const int held = four_cta_clusters_resident();
+  *split_max_batch = std::max(held, 0);
+  return held < 0 ? HS_ERR_CUDA : HS_OK;
 }

@@ -67,3 +67,36 @@ def test_cluster_sizes_that_the_device_does_not_take_are_remembered(run):
 def test_a_device_that_holds_no_pair(run):
     got = run("q.fake_clusters(16, 0)\ngot = [seen(decode), seen(decode)]")
     assert got[0][:2] == got[1][:2] == [-5, []] and got[0][2] > 0 and got[1][2] == 0
+
+
+BF16 = """
+q.fake_ask_first(1)
+
+
+def attend(batch=2):
+    block = pool(row_bytes=1152, max_batch=200)
+    return hs.load().hs_mla_decode(ctypes.addressof(block), 0, batch, A, A, 100, A, 10, 0.1, A, A, 0)
+
+
+def debug():
+    n = ctypes.c_int32(-1)
+    rc = hs.load().hs_debug_attention(0, 0, ctypes.byref(n))
+    return [rc, n.value] if rc == 0 else [rc]
+"""
+
+
+def test_debug_attention_before_any_attention(run):
+    """What it says is what hs_mla_decode does, whichever is called first."""
+    assert run(BF16 + "got = [debug(), seen(attend)[:2], debug()]") == [[0, 76], [0, [8]], [0, 76]]
+    assert run(BF16 + "got = [seen(attend)[:2], debug()]") == [[0, [8]], [0, 76]]
+
+
+def test_a_failed_query_does_not_change_how_later_bf16_calls_are_split(run):
+    good = run(BF16 + "got = [seen(attend), seen(attend, 76), seen(attend, 77)]")
+    assert [g[:2] for g in good] == [[0, [8]], [0, [304]], [0, [154]]]  # clusters of four CTAs, as many as fit, then pairs
+    for at in range(1, good[0][2] + 1):
+        got = run(BF16 + f"q.fake_fail_query({at}, 999)\ngot = [seen(attend), seen(attend)]")
+        assert got[0][0] in (-2, -5) and got[0][1] == [] and got[0][3] == 0, at
+        assert got[1][:2] == [0, [8]], at
+    got = run(BF16 + "q.fake_fail_query(2, 999)\ngot = [debug(), debug(), seen(attend)[:2]]")
+    assert got == [[-2], [0, 76], [0, [8]]]
