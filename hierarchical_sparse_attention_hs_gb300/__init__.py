@@ -432,12 +432,26 @@ def _entries(what: str, batch: int, entries, k: int):
     return at
 
 
+def _has_rows(t, row_bytes: int) -> bool:
+    """Whether the last dimensions of a tensor, as few as hold a row, hold whole rows of these bytes. (One dimension is plain
+    memory, and of a pool that was not made here the rows are not known.)"""
+    if t.dim() < 2 or not row_bytes or t.nbytes == t.size(0) * row_bytes:
+        return True
+    n = t.element_size()
+    for d in reversed(t.shape[1:]):
+        n *= d
+        if n >= row_bytes:
+            break
+    return n >= row_bytes and n % row_bytes == 0
+
+
 def _resident(what: str, pool: int, rows, count: int):
     if rows is None or isinstance(rows, int):
         return rows
     row_bytes = _pool_row_bytes.get(pool, 0)
-    if rows.nbytes < count * row_bytes or not rows.is_contiguous():
-        raise ValueError(f"{what} takes contiguous resident rows, {count} of {row_bytes} bytes")
+    if rows.nbytes < count * row_bytes or not rows.is_contiguous() or not _has_rows(rows, row_bytes):
+        raise ValueError(f"{what} takes contiguous resident rows, {count} of {row_bytes} bytes, not {tuple(rows.shape)} of "
+                         f"{rows.dtype}")
     return rows.data_ptr()
 
 
