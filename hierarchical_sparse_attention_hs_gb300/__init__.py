@@ -425,6 +425,15 @@ def _tensor(t, dtype, nbytes: int):
     return t.dtype is dtype and t.nbytes >= nbytes and t.is_contiguous() and t.data_ptr()
 
 
+def _refuse_host(what: str, entries, *tensors) -> None:
+    """For a call with a tensor in host memory, which only a list may be, and only page-locked."""
+    host = [t is not None and not isinstance(t, int) and not t.is_cuda for t in (entries, *tensors)]
+    if any(host[1:]):
+        raise ValueError(f"{what} takes tensors in device memory")
+    if host[0] and not entries.is_pinned():
+        raise ValueError(f"{what} takes a list in device memory or in page-locked host memory")
+
+
 def _entries(what: str, batch: int, entries, k: int):
     at = _tensor(entries, (_dtypes or _load_dtypes())[2], batch * k * 4)
     if at is False:
@@ -435,7 +444,7 @@ def _entries(what: str, batch: int, entries, k: int):
 def _has_rows(t, row_bytes: int) -> bool:
     """Whether the last dimensions of a tensor, as few as hold a row, hold whole rows of these bytes. (One dimension is plain
     memory, and of a pool that was not made here the rows are not known.)"""
-    if t.dim() < 2 or not row_bytes or t.nbytes == t.size(0) * row_bytes:
+    if t.dim() < 2 or t.numel() == 0 or not row_bytes:
         return True
     n = t.element_size()
     for d in reversed(t.shape[1:]):
@@ -448,8 +457,9 @@ def _has_rows(t, row_bytes: int) -> bool:
 def _resident(what: str, pool: int, rows, count: int):
     if rows is None or isinstance(rows, int):
         return rows
-    row_bytes = _pool_row_bytes.get(pool, 0)
-    if rows.nbytes < count * row_bytes or not rows.is_contiguous() or not _has_rows(rows, row_bytes):
+    row_bytes, nbytes = _pool_row_bytes.get(pool, 0), rows.nbytes
+    want = count * row_bytes
+    if nbytes < want or not rows.is_contiguous() or nbytes != want and not _has_rows(rows, row_bytes):
         raise ValueError(f"{what} takes contiguous resident rows, {count} of {row_bytes} bytes, not {tuple(rows.shape)} of "
                          f"{rows.dtype}")
     return rows.data_ptr()
@@ -466,19 +476,29 @@ def _values(what: str, batch: int, k: int, dst, dst_type: int):
     return at
 
 
+# In the calls below an address that is not what was passed is a tensor's.
+
+
 def hs_gather_values(pool: int, layer: int, batch: int, out_slots, k: int, resident_rows, resident_count: int, dst,
                      dst_type: int, stream=None) -> None:
     entries = _entries("hs_gather_values", batch, out_slots, k)
     rows = _resident("hs_gather_values", pool, resident_rows, resident_count)
     values = _values("hs_gather_values", batch, k, dst, dst_type)
-    _check((_lib or load()).hs_gather_values(pool, layer, batch, entries, k, rows, resident_count, values, dst_type,
-                                             _stream(stream)), "hs_gather_values")
+    lib = _lib or load()
+    if (entries is not out_slots and not out_slots.is_cuda or rows is not resident_rows and not resident_rows.is_cuda or
+            values is not dst and not dst.is_cuda):
+        _refuse_host("hs_gather_values", out_slots, resident_rows, dst)
+    _check(lib.hs_gather_values(pool, layer, batch, entries, k, rows, resident_count, values, dst_type, _stream(stream)),
+           "hs_gather_values")
 
 
 def hs_gather_values_history(pool: int, layer: int, batch: int, topk_idx, k: int, dst, dst_type: int, stream=None) -> None:
     entries = _entries("hs_gather_values_history", batch, topk_idx, k)
     values = _values("hs_gather_values_history", batch, k, dst, dst_type)
-    _check((_lib or load()).hs_gather_values_history(pool, layer, batch, entries, k, values, dst_type, _stream(stream)),
+    lib = _lib or load()
+    if entries is not topk_idx and not topk_idx.is_cuda or values is not dst and not dst.is_cuda:
+        _refuse_host("hs_gather_values_history", topk_idx, dst)
+    _check(lib.hs_gather_values_history(pool, layer, batch, entries, k, values, dst_type, _stream(stream)),
            "hs_gather_values_history")
 
 
@@ -497,17 +517,25 @@ def hs_mla_decode_int4(pool: int, layer: int, batch: int, q, out_slots, k: int, 
                        sm_scale: float, out, out_type: int, lse, stream=None) -> None:
     entries = _entries("hs_mla_decode_int4", batch, out_slots, k)
     rows = _resident("hs_mla_decode_int4", pool, resident_rows, resident_count)
-    q, out, lse = _heads("hs_mla_decode_int4", batch, q, out, out_type, lse)
-    _check((_lib or load()).hs_mla_decode_int4(pool, layer, batch, q, entries, k, rows, resident_count, sm_scale, out, out_type,
-                                               lse, _stream(stream)), "hs_mla_decode_int4")
+    at = _heads("hs_mla_decode_int4", batch, q, out, out_type, lse)
+    lib = _lib or load()
+    if (entries is not out_slots and not out_slots.is_cuda or rows is not resident_rows and not resident_rows.is_cuda or
+            at[0] is not q and not q.is_cuda or at[1] is not out and not out.is_cuda or at[2] is not lse and not lse.is_cuda):
+        _refuse_host("hs_mla_decode_int4", out_slots, resident_rows, q, out, lse)
+    _check(lib.hs_mla_decode_int4(pool, layer, batch, at[0], entries, k, rows, resident_count, sm_scale, at[1], out_type, at[2],
+                                  _stream(stream)), "hs_mla_decode_int4")
 
 
 def hs_mla_decode_int4_history(pool: int, layer: int, batch: int, q, topk_idx, k: int, sm_scale: float, out, out_type: int,
                                lse, stream=None) -> None:
     entries = _entries("hs_mla_decode_int4_history", batch, topk_idx, k)
-    q, out, lse = _heads("hs_mla_decode_int4_history", batch, q, out, out_type, lse)
-    _check((_lib or load()).hs_mla_decode_int4_history(pool, layer, batch, q, entries, k, sm_scale, out, out_type, lse,
-                                                       _stream(stream)), "hs_mla_decode_int4_history")
+    at = _heads("hs_mla_decode_int4_history", batch, q, out, out_type, lse)
+    lib = _lib or load()
+    if (entries is not topk_idx and not topk_idx.is_cuda or at[0] is not q and not q.is_cuda or
+            at[1] is not out and not out.is_cuda or at[2] is not lse and not lse.is_cuda):
+        _refuse_host("hs_mla_decode_int4_history", topk_idx, q, out, lse)
+    _check(lib.hs_mla_decode_int4_history(pool, layer, batch, at[0], entries, k, sm_scale, at[1], out_type, at[2],
+                                          _stream(stream)), "hs_mla_decode_int4_history")
 
 
 def hs_get_error(pool: int, clear: bool = False) -> int:

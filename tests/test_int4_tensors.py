@@ -62,3 +62,41 @@ def test_resident_rows_of_a_pool_of_fp8_rows(calls, monkeypatch):
     for rows in (bytes_of(9, 656), bytes_of(9, 41, 16), bytes_of(2, 8, 656)):
         values(rows, 9)
     assert len(calls) == 3
+
+
+def test_tensors_in_ordinary_host_memory(calls):
+    """Their addresses would go to a kernel that reads device memory."""
+    on = lambda t: bytes_of(t.nbytes).view(t.dtype).view(t.shape)  # noqa: E731
+    idx = torch.zeros(2, 3, dtype=torch.int32)
+    dst, q = torch.zeros(2, 3, 576, dtype=torch.bfloat16), torch.zeros(2, 128, 576, dtype=torch.bfloat16)
+    out, lse, rows = torch.zeros(2, 128, 512, dtype=torch.bfloat16), torch.zeros(2, 128), torch.zeros(9, 416, dtype=torch.uint8)
+    host = dict(idx=idx, rows=rows, dst=dst, q=q, out=out, lse=lse)
+    fine = {n: on(t) for n, t in host.items()}
+    forms = dict(
+        values=(lambda a: hs.hs_gather_values(POOL, 0, 2, a["idx"], 3, a["rows"], 9, a["dst"], 0, 0), ("idx", "rows", "dst")),
+        values_history=(lambda a: hs.hs_gather_values_history(POOL, 0, 2, a["idx"], 3, a["dst"], 0, 0), ("idx", "dst")),
+        decode=(lambda a: hs.hs_mla_decode_int4(POOL, 0, 2, a["q"], a["idx"], 3, a["rows"], 9, 0.1, a["out"], 0, a["lse"], 0),
+                ("idx", "rows", "q", "out", "lse")),
+        decode_history=(lambda a: hs.hs_mla_decode_int4_history(POOL, 0, 2, a["q"], a["idx"], 3, 0.1, a["out"], 0, a["lse"], 0),
+                        ("idx", "q", "out", "lse")))
+    for name, (call, takes) in forms.items():
+        call(fine)
+        assert len(calls) == 1, name
+        for t in takes:
+            with pytest.raises(ValueError, match="memory"):
+                call({**fine, t: host[t]})
+        call({**fine, **{t: 1 << 20 for t in takes}})
+        assert len(calls) == 2, name
+        calls.clear()
+
+
+def test_a_page_locked_list(calls):
+    """A list may be page-locked host memory."""
+    class Locked(torch.Tensor):
+        def is_pinned(self):
+            return True
+
+    idx = torch.zeros(1, 3, dtype=torch.int32).as_subclass(Locked)
+    hs.hs_gather_values(POOL, 0, 1, idx, 3, None, 0, 1 << 20, 0, 0)
+    hs.hs_mla_decode_int4_history(POOL, 0, 1, 1 << 20, idx, 3, 0.1, 1 << 20, 0, 1 << 20, 0)
+    assert [a[3] if n == "hs_gather_values" else a[4] for n, a in calls] == [idx.data_ptr()] * 2
