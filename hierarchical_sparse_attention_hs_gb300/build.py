@@ -16,7 +16,7 @@ SOURCES = [os.path.join(HERE, "csrc", n) for n in ("hs_resolve.cu", "hs_attentio
                                                    "hs_decode4.cu")]
 HEADERS = [os.path.join(ROOT, "include", "hs.h")] + [
     os.path.join(HERE, "csrc", n) for n in ("hs_block.cuh", "hs_pool.hpp", "hs_internal.hpp", "hs_load.cuh",
-                                        "hs_tcgen05.cuh", "hs_rows.cuh", "hs_source.hpp", "hs_pair.cuh")]
+                                        "hs_tcgen05.cuh", "hs_rows.cuh", "hs_source.hpp", "hs_pair.cuh", "hs_ring.hpp")]
 BUILD_DIR = os.path.join(HERE, "_build")
 LIB_PATH = os.path.join(BUILD_DIR, "libhs.so")
 ARCH_FLAGS = ["-gencode", "arch=compute_103a,code=sm_103a"]

@@ -65,6 +65,7 @@
 #include "hs_internal.hpp"
 #include "hs_load.cuh"
 #include "hs_pair.cuh"
+#include "hs_ring.hpp"
 #include "hs_rows.cuh"
 #include "hs_source.hpp"
 
@@ -77,17 +78,14 @@ constexpr int NK = 256;            // rows of a tile
 constexpr int QH = HEADS / 2;      // heads of a CTA
 constexpr int KH = NK / 2;         // rows of a CTA's K half
 constexpr int DVH = LATENT / 2;    // value columns of a CTA
-constexpr int SEG = 64;            // a softmax thread's rows
-constexpr int NSEG = NK / SEG;
-constexpr int KBLK = WIDTH / 64;   // 64-column blocks of a row: K stages of a tile
-constexpr int ROPE_AT = 4;         // the K stage of the rotary keys
+static_assert(SEG * NSEG == NK, "a softmax thread's rows of a tile are a segment");
+static_assert(KBLK * 64 == WIDTH, "a stage's columns");
 constexpr int BLK_BYTES = 64 * 128;      // 64 rows x 64 columns
 constexpr int STAGE_BYTES = 2 * BLK_BYTES;
-constexpr int NSTAGE = 5;          // stages of the ring
 constexpr int OFF_Q = 0;
 constexpr int OFF_RING = OFF_Q + KBLK * BLK_BYTES;
 constexpr int OFF_P = OFF_RING + NSTAGE * STAGE_BYTES;
-constexpr int SOFTMAX_WARPS = 8, MMA_WARP = 8, LOAD_WARP0 = 9, LOADERS = 8, KEY_WARP = LOAD_WARP0 + LOADERS, KEY_WARPS = 2,
+constexpr int SOFTMAX_WARPS = 8, MMA_WARP = 8, LOAD_WARP0 = 9, KEY_WARP = LOAD_WARP0 + LOADERS,
               THREADS = (KEY_WARP + KEY_WARPS) * 32;
 static_assert(THREADS <= 640, "96 registers a thread: five warps a scheduler");
 // A loader's two jobs as their rows are in memory, 64 bytes of codes (row r: 16-byte chunk j at j ^ (r / 2 % 4)) and eight scales
@@ -155,18 +153,6 @@ __device__ __forceinline__ float2 ld_peer2(uint32_t addr) {
   return v;
 }
 
-// A split's tiles, and where their stages lie in the order K(0) K(1) V(0) K(2) V(1) ... V(n - 1): K's rotary keys in the
-// middle of its latents (stage ROPE_AT). Of the list's last tile only the first `last_segs` segments hold entries: the others
-// are not multiplied with V. (lv, here and below: 1 with the value columns in halves.)
-template <int lv>
-struct Tiles {
-  static constexpr int vstages = (2 * NSEG) >> lv;  // V stages of a whole tile
-  int first, n;      // the split's first tile, and how many it has
-  int last_segs;     // segments of its last tile
-  __device__ __forceinline__ int segs(int t) const { return t == n - 1 ? last_segs : NSEG; }
-  __device__ __forceinline__ int k_stage(int t) const { return t == 0 ? 0 : t * (KBLK + vstages) - vstages; }
-  __device__ __forceinline__ int v_stage(int t) const { return (t + 1) * (KBLK + vstages) - vstages + (t == n - 1 ? 0 : KBLK); }
-};
 // 32 latents of a row, unpacked into four of the eight 16-byte chunks of a stage's row, from chunk ch on: as bf16 for the
 // scores, as halves at 2^-6 for the values.
 template <bool K>
@@ -208,8 +194,8 @@ __global__ void __launch_bounds__(THREADS, 1) hs_decode4_kernel(const Decode4Arg
 
   if (t == 0) {
     for (int i = 0; i < NBAR; ++i) bar_init(bar + i, 1);
-    // one arrival for each softmax warp of the pair; four of each CTA's loaders for a stage
-    for (int i = 0; i < NSTAGE; ++i) bar_init(bar + B_FULL + i, 8);
+    // one arrival for each softmax warp of the pair
+    for (int i = 0; i < NSTAGE; ++i) bar_init(bar + B_FULL + i, FULL);
     for (int i = 0; i < 2; ++i) bar_init(bar + B_SFREE + i, 2 * SOFTMAX_WARPS);
     bar_init(bar + B_PFULL, 2 * SOFTMAX_WARPS);
     for (int i = 0; i < 2; ++i) bar_init(bar + B_MX + i, NSEG);  // the warps that hold the same heads
@@ -281,7 +267,7 @@ __global__ void __launch_bounds__(THREADS, 1) hs_decode4_kernel(const Decode4Arg
         if (g >= 1) {
           ok = wait(B_PFULL, (unsigned)(g - 1) & 1u);
           tc_fence_after();
-          const int nv = (2 * tiles.segs(g - 1)) >> lv, two = 1 - lv;
+          const int nv = tiles.v_stages(g - 1), two = 1 - lv;
           for (int c = 0; c < nv && ok; ++c) {
             // 64 rows: a block of P; 128 of the CTA's value columns, 16 rows a step
             ok = wait(B_FULL + st, ph);
@@ -337,7 +323,7 @@ __global__ void __launch_bounds__(THREADS, 1) hs_decode4_kernel(const Decode4Arg
       copies_wait<0>();
       fence_proxy_async();
       __syncwarp();
-      if (lane == 0) arrive_lead(lead + (B_FULL + slot) * 8, 2);
+      if (lane == 0) arrive_lead(lead + (B_FULL + slot) * 8, KEY_ARRIVE);
     }
     copies_wait<0>();
     __syncwarp();
@@ -346,7 +332,8 @@ __global__ void __launch_bounds__(THREADS, 1) hs_decode4_kernel(const Decode4Arg
     //      four, then on the other two 128s; of V on two segments, then on the other two (of half of the columns on all four).
     //      Two jobs' words are on their way.
     ok = !a.stall || __all_sync(0xffffffffu, bar_wait(bar + B_STALL, 0, abort_flag, lim));
-    const int r8 = lane & 7, qd = lane >> 3, wl = warp - LOAD_WARP0, grp = wl >> 2;
+    const Loader<lv> loader{warp - LOAD_WARP0};
+    const int r8 = lane & 7, qd = lane >> 3, wl = loader.wl, grp = loader.group();
     if (wl == 0 && lane == 0 && ok) {
       if (rank == 0) bar_arrive_expect(bar + B_QFULL, 2 * KBLK * BLK_BYTES);
       for (int i = 0; i < KBLK; i += 3)
@@ -360,8 +347,8 @@ __global__ void __launch_bounds__(THREADS, 1) hs_decode4_kernel(const Decode4Arg
       return tile < tiles.n && i < a.k ? ld_fresh(list + i) : -1;
     };
     auto at = [&](int32_t e) { return reinterpret_cast<Address>(row_at(a.src, b, e, ROW_INT4)); };
-    // a loader's rows of K, the first of its segments of V, its columns of either, and its stage among a tile's V
-    const int krow = (int)rank * KH + (wl & 3) * 32, vseg = lv ? wl >> 1 : grp, vrow = vseg * SEG + (wl & 1) * 32;
+    // a loader's rows of K and of its first segment of V
+    const int krow = (int)rank * KH + loader.k_row(), vrow = loader.segment(0) * SEG + loader.v_row();
     // The words of 128 columns from `col` on, on their way into buffer `par`: four lanes a row; where there is no row its scales
     // are zeros (and the numbers may be anything).
     uint8_t* const raw = smem + OFF_RAW + wl * 2 * RAW_JOB;
@@ -397,7 +384,6 @@ __global__ void __launch_bounds__(THREADS, 1) hs_decode4_kernel(const Decode4Arg
       if (n >= NSTAGE && ok)
         ok = __all_sync(0xffffffffu, bar_wait(bar + B_EMPTY + n % NSTAGE, (unsigned)(n / NSTAGE - 1) & 1u, abort_flag, lim));
     };
-    // a stage is full with eight arrivals, four for each CTA
     auto full = [&](int stage, uint32_t count) { arrive_lead(lead + (B_FULL + stage % NSTAGE) * 8, count); };
     // 32 rows by 128 columns of K into stages n and n + 1, or of V into stage n, the upper 64 columns behind the lower
     auto put = [&](auto k, const uint4 (&codes)[4], const uint32_t (&scales)[4], int n) {
@@ -406,20 +392,19 @@ __global__ void __launch_bounds__(THREADS, 1) hs_decode4_kernel(const Decode4Arg
       if (K) need(n + 1);
       if (!ok) return;
       uint8_t* const dst = smem + OFF_RING + (K ? n + (qd >> 1) : n) % NSTAGE * STAGE_BYTES +
-                           ((K ? (wl & 3) * 32 : (qd >> 1) * SEG + (wl & 1) * 32) + r8) * 128;
+                           ((K ? loader.k_row() : (qd >> 1) * SEG + loader.v_row()) + r8) * 128;
 #pragma unroll
       for (int i = 0; i < 4; ++i) unpack<K>(dst + i * 1024, r8, (qd & 1) * 4, codes[i], scales[i]);
       fence_proxy_async();
       __syncwarp();
       if (lane == 0) {
-        full(n, K ? 1 : 2);
-        if (K) full(n + 1, 1);
+        full(n, K ? K_ARRIVE : V_ARRIVE);
+        if (K) full(n + 1, K_ARRIVE);
       }
     };
     const std::true_type K;
     const std::false_type V;
-    const int kcol = grp * 128, vcol = (int)rank * DVH + (lv ? half : wl >> 1 & 1) * 128;
-    const int vstage = lv ? vseg : 2 * grp + (wl >> 1 & 1);
+    const int kcol = grp * 128, vcol = (int)rank * DVH + half * 128 + loader.v_col();
     uint4 w[4];
     uint32_t sc[4];
     Address krows = at(entry(0, krow));
@@ -446,7 +431,7 @@ __global__ void __launch_bounds__(THREADS, 1) hs_decode4_kernel(const Decode4Arg
           read(par, w, sc);
           load(par, v ? at(h > lv ? ev1 : ev0) : past && !k_next ? 0 : krows, v ? vcol : past && t > 0 ? kcol : kcol + 256 * h);
           if (lv && h == 0 && t > 0) ev0 = entry(t, vrow);
-          put(K, w, sc, n + (ROPE_AT + 1) * h + 2 * grp);
+          put(K, w, sc, n + loader.k_stage(h));
         }
         if (!ok) break;
         if (t > 0 && !lv) {
@@ -455,14 +440,14 @@ __global__ void __launch_bounds__(THREADS, 1) hs_decode4_kernel(const Decode4Arg
         }
       }
       if (t > 0) {
-        const int n = tiles.v_stage(t - 1) + vstage, segs = tiles.segs(t - 1);
+        const int n = tiles.v_stage(t - 1), segs = tiles.segs(t - 1);
 #pragma unroll 1
-        for (int h = 0; h < 2 - lv && ok; ++h) {
+        for (int h = 0; h < loader.v_jobs && ok; ++h) {
           const int par = h ^ odd;  // the job's buffer
           copies_wait<1>();
           read(par, w, sc);
           load(par, k_next ? krows : lv || t == tiles.n ? 0 : at(h ? ev1 : ev0), k_next ? kcol + 256 * (h | lv) : vcol);
-          if (vseg + 2 * h < segs) put(V, w, sc, n + 4 * h);
+          if (loader.segment(h) < segs) put(V, w, sc, n + loader.v_stage(h));
         }
       }
     }
