@@ -11,7 +11,10 @@ Default run: every workload. The headline (the top-level value, roofline, noio, 
 largest one, the shared-selection workload (8 requests x 78 layers, context 1,048,576, one top-k 2048 selection
 per request and step shared by all layers) with hs_prefetch(l+1) on a second stream overlapped with
 hs_resolve(l). The other workloads, and the shared one with a single hs_resolve_shared per step, are in
-``per_workload`` with the same fields. ``--workload NAME`` measures one workload.
+``per_workload``. ``--workload NAME`` measures one workload.
+
+Output: one JSON line on stdout, short enough for readers that keep the last 3,000 characters of a run (``brief``), and the
+same with every field of every leg and workload, tens of thousands of characters, on stderr.
 
 Timing: W warm-up steps, then K steps, each bracketed by CUDA events on the launching stream with a 256 MiB L2
 flush between steps (outside the events), barrier + synchronize around the whole region, max over ranks. A GPU-side
@@ -1154,6 +1157,40 @@ def gpu_measure(args, env: Env) -> dict:
     return line
 
 
+LINE_MOST = 2800  # characters of the printed line
+# what the printed line keeps of its objects (of per_workload: the values alone)
+BRIEF = {
+    "roofline": ("bound", "achieved", "peak", "unit", "frac", "hbm_frac", "hbm_frac_of_nominal", "traffic", "kernel",
+                 "kernel_ms_per_launch", "launches"),
+    "noio": ("value", "unit", "ms_per_step"),
+    "e2e": ("value", "unit", "h2d_bytes_per_step", "d2h_bytes_per_step", "ms_per_step", "out_slots_match_device_path"),
+    "cpu_baseline": ("value", "unit", "cores", "kind"),
+    "headline": ("repeats",),
+    "attention": ("kernel", "ms_per_launch", "frac", "error"),
+}
+
+
+def brief(line: dict) -> dict:
+    """The line without texts, lists and inner objects, its inner numbers to nine digits; what is still too long loses extras."""
+    def short(v):
+        if isinstance(v, float):
+            return float(f"{v:.9g}")
+        return v[:60] if isinstance(v, str) else [short(x) for x in v] if isinstance(v, list) else v
+
+    out = dict(line)
+    for key, names in BRIEF.items():
+        if isinstance(line.get(key), dict):
+            out[key] = {n: short(line[key][n]) for n in names if n in line[key]}
+    if "repeats" in (out.get("headline") or {}):
+        out["headline"] = {"repeats": {"values": short(line["headline"]["repeats"]["values"])}}
+    if line.get("per_workload"):
+        out["per_workload"] = {n: short(r.get("value", r.get("error"))) for n, r in line["per_workload"].items()}
+    for key in ("per_workload", "attention", "headline", "noio"):
+        if len(json.dumps(out)) > LINE_MOST:
+            out.pop(key, None)
+    return out
+
+
 def run_gpu(args, measure_fn=None) -> int:
     """One rank: set up the process group (gloo, for the barrier and the max over ranks), measure, and print the
     line on rank 0. `measure_fn(args, env) -> dict` is the GPU work (replaced by a stub in CPU tests)."""
@@ -1161,7 +1198,8 @@ def run_gpu(args, measure_fn=None) -> int:
     env = Env(args, dist, world, rank, local)
     line = (measure_fn or gpu_measure)(args, env)
     if rank == 0:
-        print(json.dumps(line), flush=True)
+        print(json.dumps(line), file=sys.stderr, flush=True)
+        print(json.dumps(brief(line)), flush=True)
     if dist:
         dist.destroy_process_group()
     return 0
