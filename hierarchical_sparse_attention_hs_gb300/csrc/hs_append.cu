@@ -21,8 +21,9 @@
 // 2.8 us; 2,047 with 128 heads 18.5 us from fp32 (5.8 TB/s) and 13.5 from bf16; 131,071 without queries 50 us into bf16 rows
 // (6.1 TB/s) and 49.6 into fp8 rows (4.8 TB/s; 50.1 and 339 instructions a row before the norm's products went two an
 // instruction, which take 38 us where every scheduler issues one a cycle: 0.73 were measured); 131,071 into 4-bit rows 51.8
-// with a norm and 44.4 without (4.7 TB/s), issue too; 4,096 into host memory 17.5 us for fp8 rows and 26 for bf16, 153 and
-// 180 GB/s of writes over the link.
+// with a norm and 44.4 without (4.7 TB/s), issue too (the lanes are those of bf16 rows, so the two that share a block of 16 both
+// work out its scale), from fp32 57.5 and 56.4 (6.3 TB/s, HBM); 4,096 into host memory 17.5 us for fp8 rows and 26 for bf16,
+// 153 and 180 GB/s of writes over the link.
 
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>

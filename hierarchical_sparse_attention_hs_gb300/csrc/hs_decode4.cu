@@ -27,15 +27,20 @@
 // Warp roles per CTA: 0-7 softmax (warp w: TMEM lanes 32 (w % 4) .. +31, that is head lane % 64 and half lane / 64 of the
 // tile's rows, and rows 64 (w / 4) .. +63 of that half), 8 the issuer (the pair's first CTA issues for both), 9-16 the
 // loaders, which unpack latents, 17 and 18 the rotary keys. K and V pass through one ring of 16 KB stages in the order in which
-// the MMAs read them: a K stage is 64 columns of the CTA's 128 rows, a V stage 128 of its value columns of 64 rows, both 128
-// rows of 128 bytes, 128-byte swizzle; each feeds four MMAs, 256 cycles. The rows' words come into shared memory as they are,
-// by asynchronous copies a job ahead (through registers they were waited for as soon as they were asked for), and are unpacked
-// from there.
+// the MMAs read them (hs_ring.hpp): a K stage is 64 columns of the CTA's 128 rows, a V stage 128 of its value columns of 64
+// rows, both 128 rows of 128 bytes, 128-byte swizzle; each feeds four MMAs, 256 cycles. The rows' words come into shared memory
+// as they are, by asynchronous copies a job ahead (through registers they were waited for as soon as they were asked for), and
+// are unpacked from there.
 //
 // Measured on one GB300 (replayed graphs): a tile takes 4.1 us, 7,700 cycles, of which its MMAs are 4,352 at their full rate.
 // Shared memory is what it waits for: 2,200 cycles of stores of unpacked rows, 1,100 of the words' way through it, and 96 of
 // its 128 bytes a cycle that MMAs of this shape read while they run, 3,300 or more. 32 requests of 2,048 entries 27.8 us (657
-// TFLOP/s; four tiles a pair, the start, the join), one 14.4, seven 16.3, five of 16,384 45.5, one of 65 8.3.
+// TFLOP/s; four tiles a pair, the start, the join), one 14.4, seven 16.3, five of 16,384 45.5, one of 65 8.3. Outputs in fp32 0.1 to
+// 0.6 us more; the list in mapped host memory, which each role of a CTA reads for itself, 0.9 us more for one request of 2,048, 6.6
+// for 32; rows in host memory 26 and 313 us (87 GB/s of rows for 32 requests).
+//
+// Where it leaves SMs idle: a list is cut into at most eight splits, since they join within one cluster, so a request has at most
+// 16 of 152 SMs (five of 16,384: 80), and splits are powers of two (40 requests of 2,048: one split each, 80 SMs, 39.9 us).
 //
 // Steps that brought it there, for 32 requests of 2,048: lanes that load a row each 62 us; eight rows by four lanes 40; copies
 // into shared memory, scores in bf16, queries by TMA 34; jobs of 32 rows in a fixed order, the keys by warps of their own
@@ -45,9 +50,9 @@
 //
 // Not kept: eleven loaders with 96 registers or fewer that take jobs in turn, 30.2 (and a wait that could be lapped); all
 // loaders on one stage pair, 16 rows each, 36; rows brought into L2 by bulk prefetches, whose issue took a warp 2,000 cycles
-// for 32; first copies ahead of the cluster's start, 29.2 against 28.9 (programmatic launch hides that start already); the
-// second tile's prefetch behind the first tile's keys, 29.5; a job's copies started after the job before is unpacked, 29.5
-// against 28.2; waits as calls of a function 28.7; the join by bulk copies into the CTA that sums a head, 31.
+// for 32; first copies ahead of the cluster's start, 29.2 against 28.9 (programmatic launch hides that start already); a job's
+// copies started after the job before is unpacked, 29.5 against 28.2; waits as calls of a function 28.7; the join by bulk copies
+// into the CTA that sums a head, 31.
 //
 // Waits are bounded: on running out a role sets the abort flag, which ends every role, and the HS_DEVERR_TIMEOUT bit.
 
@@ -490,7 +495,7 @@ __global__ void __launch_bounds__(THREADS, 1) hs_decode4_kernel(const Decode4Arg
       if (!ok) break;
       tc_fence_after();
       // The scores are read twice, 32 at a time: for the maximum, and once the four threads of a head agree on it. (Holding
-      // all 64 across the exchange takes more registers than 16 warps leave.)
+      // all 64 across the exchange takes more registers than 19 warps leave.)
       const uint32_t scol = trow + TMEM_S + (uint32_t)((g & 1) * KH + sub * SEG);
       uint32_t sv[32];
       float mb = -INFINITY;

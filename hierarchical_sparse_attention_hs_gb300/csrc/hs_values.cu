@@ -11,7 +11,10 @@
 // so that every store instruction of a warp fills 512 consecutive bytes, and every load of codes 128 (4-bit) to 512.
 //
 // Measured on one GB300 (reads and writes over the time): 131,072 4-bit rows into bf16 32.9 us, 6.25 TB/s, 0.92 of the
-// measured copy; 65,536 fp8 rows into fp32 33.6 us, 5.8 TB/s; 771 rows 2.2 us, a launch's own cost.
+// measured copy, into fp32 58.4 (6.1 TB/s); 65,536 fp8 rows into fp32 33.6 us, 5.8 TB/s, into bf16 20.5; 65,536 bf16 rows into
+// bf16 26.7, into fp32 36.3 (6.25 TB/s); 771 rows 2.2 us, a launch's own cost. Out of host memory, whose link gives 211 GB/s:
+// 32,768 4-bit rows into bf16 84 us (163 GB/s; into fp32 101, where a warp's loads of codes are half as wide), 16,384 fp8 rows
+// 66 (162 GB/s; into fp32 78), 16,384 bf16 rows 93 into any type (204 GB/s).
 
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>

@@ -466,7 +466,8 @@ int hs_mla_prefix_workspace_bound(hs_pool *pool, int32_t batch, int32_t max_leng
  *     on a barrier that nothing completes, so that wait runs out before any tensor-core work or row copy of the kernel is
  *     issued, and the abort path runs with nothing in flight. 0 restores normal operation.
  *   split_max_batch: if non-NULL, receives the largest batch for which hs_mla_decode splits a request's keys over
- *     two CTA pairs on the current device (larger batches run one pair per request).
+ *     two CTA pairs on the current device (larger batches run one pair per request). Where the device cannot be asked it
+ *     receives 0 and the call returns HS_ERR_CUDA; the settings above hold all the same.
  * Applies to the hs_mla_decode / hs_mla_decode_history / hs_mla_decode_int4 (and its history form) / hs_mla_prefix calls made
  * after it.
  */
